@@ -270,6 +270,123 @@ moe_status moe_stack_forward_host(moe_stack *stack, const void *x_host, void *ou
                                   void *stream);
 moe_status moe_stack_destroy(moe_stack *stack);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the layer: routing from logits, the residual addition and
+ * norm in front of it, and products with 4-bit weights. They keep no state:
+ * calls on different streams may overlap as long as their buffers (and, for
+ * moe_route_logits, their workspaces) differ, and all of them can be captured
+ * into a graph. Strides count elements, and rows may lie further apart than
+ * their length. Unless stated otherwise a pointer has the alignment of its
+ * elements only. Buffers belong to the current device.
+ * ------------------------------------------------------------------------- */
+typedef enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_F32 = 2, MOE_T_E4M3 = 3 } moe_dtype;
+
+/* Routing. With l the logits of a token,
+ *   p = softmax(l) or 1 / (1 + exp(-l)),   c = p + bias (bias NULL: c = p)
+ *   group score (n_groups > 1): the best c of the group, or the sum of its two
+ *     best (of the one, where only one is left); the topk_groups best are kept
+ *   ids = the top_k best c within the kept groups, by descending c
+ *   w[j] = scale * p[ids[j]], divided by the sum of the chosen p if renormalise
+ * Ties go to the lower index, group or expert. The choice is that of scores
+ * in 64-bit arithmetic. An expert whose logit is NaN or -inf takes no part in
+ * the softmax and is never chosen; nor is one whose bias is; +inf counts as
+ * the largest finite float. Where fewer than top_k experts are left the
+ * remaining slots hold id -1, weight 0 and pos -1.
+ * Limits: E <= 512, top_k <= 16, n_groups <= 32 and dividing E, the kept
+ * groups holding at least top_k experts, T <= 524288. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rule;
+typedef struct {
+    int E, top_k;
+    moe_score score;
+    const float *bias;           /* [E] fp32 (device) or NULL; steers the choice, not the weights */
+    int n_groups, topk_groups;   /* 1, 1: no groups */
+    moe_group_rule group_rule;
+    int renormalise;
+    float scale;
+} moe_route_desc;
+
+/* Bytes of device workspace moe_route_logits needs for T tokens. No GPU work. */
+moe_status moe_route_logits_workspace_size(const moe_route_desc *desc, int T, size_t *bytes);
+
+/* logits [T, E] in bf16, f16 or fp32, row_stride elements from row to row.
+ * ids [T, top_k] and w [T, top_k] are required; counts [E], offsets [E+1],
+ * perm [T*top_k] and pos [T, top_k] as in moe_route, each optional (NULL).
+ * Entries of perm past offsets[E] are set to -1. The workspace (4-byte
+ * aligned) may be NULL when none of the four is asked for; it needs no
+ * initialisation and carries nothing from one call to the next. T = 0 only
+ * zeroes counts and offsets. */
+moe_status moe_route_logits(const moe_route_desc *desc, const void *logits, moe_dtype type, int64_t row_stride, int T,
+                            int32_t *ids, float *w, int32_t *counts, int32_t *offsets, int32_t *perm, int32_t *pos,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/* Makes moe_route and moe_forward* on this layer choose experts as `desc`
+ * says, from the layer's own router logits (router_bias included); NULL
+ * restores the softmax top-k. E and top_k must be the layer's. desc is copied;
+ * its bias must stay valid. Such a forward runs the router, the choice and the
+ * expert kernels as separate launches. A token left with fewer than top_k
+ * experts sets the error word that moe_get_device_status() reports as
+ * MOE_ERR_DEVICE, and its output is undefined. Stacks of layers run the
+ * softmax top-k only: moe_stack_create and moe_stack_forward return
+ * MOE_ERR_UNSUPPORTED while one of their layers has a router set. */
+moe_status moe_layer_set_router(moe_layer *layer, const moe_route_desc *desc);
+
+/* Residual addition and RMSNorm:
+ *   s = round(x + res)   (to `type`; s = x without res)
+ *   y = s / sqrt(mean(s^2) + eps) * gain
+ * out_type = type: out = round(y). out_type = MOE_T_E4M3: for every `group`
+ * columns (0: the whole row) scale = max|y| / 448 (1 for a group of zeros) and
+ * out = E4M3(y / scale). fp32 arithmetic; the norm is of the rounded sum, as
+ * moe_rmsnorm after moe_forward_residual. A row of zeros gives zeros (eps = 0
+ * included). sum or out may be the same buffer as x or res, with the same
+ * stride; any other overlap is not allowed. d <= 16384, group dividing d. */
+typedef struct {
+    const void *x;       /* [T, d] bf16, f16 or fp32 */
+    const void *res;     /* [T, d] of the same type, or NULL */
+    const void *gain;    /* [d] of the same type, or NULL */
+    void *sum;           /* [T, d] of the same type: s, or NULL */
+    void *out;           /* [T, d] */
+    float *scales;       /* [T, d / group] for E4M3 output, else NULL */
+    int64_t x_stride, res_stride, sum_stride, out_stride, scales_stride;
+    int T, d, group;
+    moe_dtype type, out_type;
+    float eps;
+} moe_norm_args;
+moe_status moe_add_rmsnorm(const moe_norm_args *args, void *stream);
+
+/* y = x W^T + bias for M <= 64 tokens and 4-bit weights W [N, K], two codes
+ * per byte, the low nibble holding the lower contraction index:
+ *   MOE_W4_NVFP4: w = e2m1 * e4m3 * g, as moe_quantize_nvfp4 writes them
+ *     (group 16, s [N, K/16], g one fp32);
+ *   MOE_W4_INT4: w = (code - z) * s, codes 0..15, group 32, 64 or 128,
+ *     s [N, K/group] bf16 or f16, z [N, K/group] bytes, NULL: 8 everywhere.
+ * x [M, K] is bf16, f16, or E4M3 with scales x_scales [M, K/x_group], x_group
+ * a multiple of 128 or 0 (one scale per token), as moe_add_rmsnorm writes
+ * them. y [M, N] is bf16, f16 or fp32. Products and sums are fp32; more than 32
+ * tokens read the weights twice. K a multiple of 32 and of the group,
+ * K <= 32768; q 16-byte aligned, s 2-byte aligned; y overlaps no input. */
+typedef enum { MOE_W4_NVFP4 = 0, MOE_W4_INT4 = 1 } moe_w4_fmt;
+typedef struct {
+    moe_w4_fmt fmt;
+    int M, N, K, group;
+    const uint8_t *q;    /* [N, K/2] */
+    const void *s;
+    moe_dtype s_type;    /* INT4 */
+    const float *g;      /* NVFP4: [1] */
+    const uint8_t *z;    /* INT4 */
+    const void *x;
+    moe_dtype x_type;
+    int64_t x_stride;
+    const float *x_scales;
+    int64_t x_scales_stride;
+    int x_group;
+    const float *bias;   /* [N] fp32 or NULL */
+    void *y;
+    moe_dtype y_type;
+    int64_t y_stride;
+} moe_w4_args;
+moe_status moe_linear_w4(const moe_w4_args *args, void *stream);
+
 moe_status moe_layer_destroy(moe_layer *layer);
 
 const char *moe_status_string(moe_status s);

@@ -1,0 +1,678 @@
+"""The operators around the layer on the GPU, each against a plain
+implementation in 64 bits: routing from logits, residual + RMSNorm with its
+8-bit output, products with 4-bit weights, and the three together with the
+layer. Tolerances count roundings (half a step each) as stated beside them."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32, "e4m3": torch.float8_e4m3fn}
+INF, NAN, LOWEST = math.inf, math.nan, -3.4028234663852886e38
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+def ref_route(logits, k, score, bias, groups, keep, rule, renorm, scale):
+    """The definition, token by token in 64 bits."""
+    L = logits.float().cpu().numpy().astype(np.float64)
+    T, E = L.shape
+    big = float(np.finfo(np.float32).max)
+    b = None if bias is None else np.minimum(bias.cpu().numpy().astype(np.float64), big)
+    ids, w = np.full((T, k), -1), np.zeros((T, k))
+    idx = np.arange(E)
+    for t in range(T):
+        live = ~(np.isnan(L[t]) | (L[t] == -np.inf))
+        if not live.any():
+            continue
+        l = np.where(live, np.minimum(L[t], big), 0.0)
+        with np.errstate(over="ignore"):
+            p = 1 / (1 + np.exp(-l)) if score == "sigmoid" else np.exp(l - l[live].max())
+        p = np.where(live, p, 0.0)
+        if score == "softmax":
+            p /= p.sum()
+        on = live if b is None else live & ~(np.isnan(b) | (b == -np.inf))
+        by = l if b is None else p + np.where(on, b, 0.0)
+        if keep < groups:
+            n = E // groups
+            tot = np.full(groups, -np.inf)
+            for g in range(groups):
+                v = (by if b is not None or rule == "max" else p)[g * n:(g + 1) * n][on[g * n:(g + 1) * n]]
+                if v.size:
+                    v = -np.sort(-v)
+                    tot[g] = v[0] if rule == "max" else v[:2].sum()
+            kept = np.lexsort((np.arange(groups), -tot))[:keep]
+            on = on & np.isin(idx // n, kept)
+        o = idx[on][np.lexsort((idx[on], -by[on]))][:k]
+        if not o.size:
+            continue
+        ids[t, :o.size] = o
+        if not renorm:
+            got = p[o]
+        elif score == "softmax":
+            got = np.exp(l[o] - l[o].max())
+            got = got / got.sum()
+        else:                                              # log of the sigmoid: no underflow
+            ls = np.where(l[o] < 0, l[o], 0) - np.log1p(np.exp(-np.abs(l[o])))
+            got = np.exp(ls - ls.max())
+            got = got / got.sum()
+        w[t, :o.size] = got * scale
+    return ids, w
+
+
+def ref_permute(ids, E):
+    counts = np.bincount(ids[ids >= 0], minlength=E)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    perm, pos = np.full(ids.size, -1), np.full(ids.shape, -1)
+    tt, jj = np.nonzero(ids >= 0)
+    o = np.lexsort((tt, ids[tt, jj]))
+    perm[:o.size] = tt[o]
+    pos[tt[o], jj[o]] = np.arange(o.size)
+    return counts, offsets, perm, pos
+
+
+def check_route(got, logits, k, **kw):
+    a = dict(score="softmax", bias=None, n_groups=1, topk_groups=1, group_rule="max", renormalise=True, scale=1.0)
+    a.update(kw)
+    E = logits.shape[1]
+    ids, w = ref_route(logits, k, a["score"], a["bias"], a["n_groups"], a["topk_groups"], a["group_rule"],
+                       a["renormalise"], a["scale"])
+    np.testing.assert_array_equal(got["ids"].cpu().numpy(), ids)
+    # a weight: exp's argument off by up to 2^-24 of |l - l_max| < 104 (below that the weight is 0 or subnormal), and
+    # fewer than 60 other roundings of the exponentials, their sum, the quotient and the scale: under 170 * 2^-24
+    np.testing.assert_allclose(got["w"].cpu().numpy(), w, rtol=170 * 2.0 ** -24, atol=1e-37 * a["scale"])
+    for name, r in zip(("counts", "offsets", "perm", "pos"), ref_permute(ids, E)):
+        if got.get(name) is not None:
+            np.testing.assert_array_equal(got[name].cpu().numpy(), r, err_msg=name)
+
+
+ROUTES = [
+    # T, E, k, type, options
+    (1, 1, 1, "f32", {}),
+    (1, 256, 8, "f32", dict(score="sigmoid", bias=True, n_groups=8, topk_groups=4, group_rule="top2", scale=2.5)),
+    (2, 8, 2, "bf16", {}),
+    (5, 37, 16, "f16", dict(renormalise=False, scale=16.0)),
+    (33, 128, 8, "bf16", {}),
+    (64, 64, 6, "f16", dict(n_groups=8, topk_groups=3, renormalise=False)),
+    (31, 60, 4, "f32", dict(n_groups=4, topk_groups=2, group_rule="top2")),
+    (77, 160, 6, "bf16", dict(n_groups=8, topk_groups=3, renormalise=False, scale=16.0)),
+    (100, 300, 10, "f32", dict(score="sigmoid", bias=True)),
+    (65, 512, 16, "f32", dict(score="sigmoid", bias=True, n_groups=32, topk_groups=5, group_rule="top2")),
+    (40, 384, 8, "bf16", dict(score="softmax", bias=True, renormalise=False)),
+    (40, 500, 7, "f16", dict(score="softmax", bias=True, n_groups=5, topk_groups=2)),
+    (129, 96, 3, "bf16", dict(score="sigmoid", n_groups=32, topk_groups=7, group_rule="top2")),
+    (50, 32, 4, "f32", dict(n_groups=32, topk_groups=9, group_rule="top2")),     # groups of one expert
+    (1000, 256, 8, "f32", dict(score="sigmoid", bias=True, n_groups=8, topk_groups=4, group_rule="top2")),
+    (17000, 20, 3, "f32", dict(score="sigmoid", bias=True)),                     # chunks of more than 32 tokens
+]
+
+
+@pytest.mark.parametrize("T,E,k,dt,opt", ROUTES)
+def test_route_logits(gpu_lib, T, E, k, dt, opt):
+    g = gen(T * 1000 + E)
+    logits = (2 * torch.randn(T, E, generator=g, device="cuda")).to(DT[dt])
+    opt = dict(opt)
+    if opt.get("bias"):
+        opt["bias"] = 0.3 * torch.randn(E, generator=g, device="cuda")
+    check_route(gpu_lib.route_logits(logits, k, **opt), logits, k, **opt)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("rule", ["max", "top2"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,groups,keep", [(64, 8, 3), (64, 1, 1), (240, 6, 2)])
+def test_route_ties_masks_and_extremes(gpu_lib, score, rule, biased, E, groups, keep):
+    """Equal logits, masked experts (all of a row among them), the lowest float, infinities, NaN, far values."""
+    g = gen(E + groups)
+    rows = [torch.zeros(E, device="cuda"), torch.full((E,), LOWEST, device="cuda"), torch.full((E,), -INF, device="cuda"),
+            torch.full((E,), NAN, device="cuda"), torch.full((E,), INF, device="cuda")]
+    for _ in range(28):
+        r = (torch.randint(-3, 4, (E,), generator=g, device="cuda") * 0.5).float()      # many ties
+        n = torch.rand(E, generator=g, device="cuda")
+        for lo, v in ((0.1, -INF), (0.2, LOWEST), (0.25, NAN), (0.28, INF), (0.35, 100.0), (0.5, -100.0)):
+            r = torch.where((n < lo) & (n >= lo - 0.05), torch.tensor(v, device="cuda"), r)
+        rows.append(r)
+    few = torch.full((E,), -INF, device="cuda")
+    few[E // 2] = 1.0
+    rows += [few, torch.full((E,), -200.0, device="cuda") - torch.arange(E, device="cuda")]
+    logits = torch.stack(rows)
+    bias = None
+    if biased:
+        bias = torch.randint(-2, 3, (E,), generator=g, device="cuda").float() * 0.25
+        bias[3], bias[5], bias[7] = -INF, NAN, INF
+    opt = dict(score=score, bias=bias, n_groups=groups, topk_groups=keep, group_rule=rule)
+    check_route(gpu_lib.route_logits(logits, 6, **opt), logits, 6, **opt)
+    opt["renormalise"] = False
+    check_route(gpu_lib.route_logits(logits, 6, **opt), logits, 6, **opt)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
+def test_route_scores_nearer_than_fp32(gpu_lib, score, groups, keep):
+    """Biases that leave the scores of all experts within a few fp32 steps: 32-bit scores order them by chance."""
+    T, E, g = 96, 256, gen(7)
+    logits = torch.randn(1, E, generator=g, device="cuda").expand(T, E).clone()
+    logits += 1e-6 * torch.randn(T, E, generator=g, device="cuda")
+    p = torch.sigmoid(logits[0].double()) if score == "sigmoid" else torch.softmax(logits[0].double(), 0)
+    bias = (0.5 - p).float()
+    opt = dict(score=score, bias=bias, n_groups=groups, topk_groups=keep, group_rule="top2")
+    check_route(gpu_lib.route_logits(logits, 8, **opt), logits, 8, **opt)
+
+
+def test_route_strides_offsets_and_partial_outputs(gpu_lib):
+    g = gen(3)
+    for dt in ("bf16", "f16", "f32"):
+        for off, E, extra in ((0, 64, 64), (1, 63, 2), (3, 256, 5), (2, 130, 4)):
+            buf = torch.randn(50, off + E + extra, generator=g, device="cuda").to(DT[dt])
+            logits = buf[:, off:off + E]
+            check_route(gpu_lib.route_logits(logits, 5), logits, 5)
+    logits = torch.randn(40, 64, generator=g, device="cuda")
+    out = {"ids": torch.empty((40, 4), dtype=torch.int32, device="cuda"), "w": torch.empty((40, 4), device="cuda")}
+    check_route(gpu_lib.route_logits(logits, 4, out=out), logits, 4)
+    out["pos"] = torch.empty((40, 4), dtype=torch.int32, device="cuda")
+    check_route(gpu_lib.route_logits(logits, 4, out=out), logits, 4)
+
+
+def test_route_of_no_tokens(gpu_lib):
+    r = gpu_lib.route_logits(torch.empty((0, 16), device="cuda"), 2)
+    assert r["ids"].shape == (0, 2) and r["perm"].numel() == 0
+    assert (r["counts"] == 0).all() and (r["offsets"] == 0).all()
+
+
+def test_route_writes_only_its_outputs(gpu_lib):
+    """Guard words around every output stay as they were."""
+    T, E, k = 70, 48, 4
+    logits = torch.randn(T, E, device="cuda", generator=gen(1))
+    sizes = {"ids": T * k, "w": T * k, "counts": E, "offsets": E + 1, "perm": T * k, "pos": T * k}
+    pads, out = {}, {}
+    for n, s in sizes.items():
+        buf = torch.full((s + 64,), 77, dtype=torch.float32 if n == "w" else torch.int32, device="cuda")
+        pads[n] = buf
+        v = buf[32:32 + s]
+        out[n] = v.view(T, k) if n in ("ids", "w", "pos") else v
+    check_route(gpu_lib.route_logits(logits, k, out=out), logits, k)
+    for n, buf in pads.items():
+        assert (buf[:32] == 77).all() and (buf[-32:] == 77).all(), n
+
+
+# ---------------------------------------------------------------------------
+# norm
+# ---------------------------------------------------------------------------
+def check_norm(moe, x, res, gain, eps=1e-6, out_dtype=None, group=0, **kw):
+    rounded = x.double() if res is None else (x.float() + res.float()).to(x.dtype).double()
+    out, s, scales = moe.add_rmsnorm(x, res, gain, eps=eps, out_dtype=out_dtype, group=group, **kw)
+    if res is not None:
+        assert torch.equal(s.view(torch.uint8), (x.float() + res.float()).to(x.dtype).view(torch.uint8)) or \
+            torch.equal(torch.nan_to_num(s.float(), nan=1.25), torch.nan_to_num(rounded.float(), nan=1.25))
+    T, d = x.shape
+    ms = rounded.square().mean(1, keepdim=True) + eps
+    y = torch.where(ms == 0, rounded, rounded / ms.sqrt()) * (1.0 if gain is None else gain.double())
+    # fp32: the sum of d <= 16384 squares by up to 64 + 5 + 31 additions in a row, its root and quotient, three
+    # products: under 64 roundings of the result once the root has halved the sum's
+    rel = 64 * 2.0 ** -24
+    if out_dtype != torch.float8_e4m3fn:
+        fi = torch.finfo(x.dtype)
+        tol = y.abs() * (fi.eps / 2 + rel) + fi.smallest_normal * fi.eps
+        got = out.double()
+        y = torch.where(y.abs() > fi.max, torch.sign(y) * INF, y)
+        assert torch.equal(torch.isnan(got), torch.isnan(y))
+        fine = torch.isfinite(y)
+        assert torch.equal(got[~fine & ~torch.isnan(y)], y[~fine & ~torch.isnan(y)])
+        assert ((got - y).abs()[fine] <= tol[fine]).all()
+        return out, s, scales
+    n = group or d
+    amax = y.view(T, d // n, n).abs().amax(2)
+    want = torch.where(amax == 0, torch.ones_like(amax), amax / 448)
+    assert torch.equal(torch.isnan(scales), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    assert ((scales.double() - want).abs()[ok] <= want[ok] * rel).all()
+    v = (y.view(T, d // n, n) / want[:, :, None]).view(T, d)
+    q = out.float().double()
+    assert torch.equal(torch.isnan(q), torch.isnan(v))
+    ok = ~torch.isnan(v)
+    # E4M3: half a step is 2^-4 of the value, 2^-10 among the subnormals
+    assert ((q - v).abs()[ok] <= (v.abs() * (2.0 ** -4 + 2 * rel)).clamp_min(2.0 ** -10 * (1 + 1e-5))[ok]).all()
+    return out, s, scales
+
+
+NORMS = [(1, 8), (3, 16), (9, 64), (17, 128), (5, 200), (4, 264), (8, 520), (2, 1000), (3, 1024), (2, 1536), (5, 2048),
+         (3, 4096), (2, 5000), (2, 8192), (3, 12288), (2, 16384), (1, 1), (4, 7), (3, 100), (2, 129), (2, 1001), (1, 4097),
+         (2, 16383)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,d", NORMS)
+def test_norm(gpu_lib, dt, T, d):
+    g = gen(d)
+    x = torch.randn(T, d, generator=g, device="cuda").to(DT[dt])
+    res = (3 * torch.randn(T, d, generator=g, device="cuda")).to(DT[dt])
+    gain = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(DT[dt])
+    check_norm(gpu_lib, x, res, gain)
+    check_norm(gpu_lib, x, None, None, eps=1e-2)
+    check_norm(gpu_lib, x, res, gain, out_dtype=torch.float8_e4m3fn)
+    for group in (2, 4, 8, 16, 24, 32, 64, 100, 128, 256, 512):
+        if d % group == 0 and d // group <= 4096 and group < d:
+            check_norm(gpu_lib, x, res, gain, out_dtype=torch.float8_e4m3fn, group=group)
+
+
+@pytest.mark.parametrize("d", [64, 1000, 4096, 4099])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_norm_of_special_rows(gpu_lib, d, e4m3):
+    """Zeros, one NaN, one infinity, squares past the ends of fp32's range, the largest values."""
+    g = gen(d)
+    for dt in ("bf16", "f32", "f16"):
+        x = torch.randn(12, d, generator=g, device="cuda")
+        x[0] = 0
+        x[1, d // 2] = NAN
+        x[2, 0] = INF
+        x[3] *= 1e-4 if dt == "f16" else 1e-30
+        x[4] *= 1e3 if dt == "f16" else 1e30
+        x[5] = torch.finfo(DT[dt]).max * torch.sign(x[5])
+        x[6, 1:] = 0
+        x[7] *= torch.finfo(DT[dt]).smallest_normal
+        x = x.to(DT[dt])
+        for eps in (0.0, 1e-6):
+            for group in (0, 32):
+                if group and (not e4m3 or d % group):
+                    continue
+                check_norm(gpu_lib, x, None, None, eps=eps, out_dtype=torch.float8_e4m3fn if e4m3 else None, group=group)
+
+
+def test_norm_strides_and_aliases(gpu_lib):
+    g = gen(5)
+    for dt in ("bf16", "f32"):
+        for off, d, ld in ((0, 256, 512), (1, 256, 300), (8, 264, 272), (3, 1001, 1010)):
+            bx, br, bs, bo = (torch.randn(6, ld, generator=g, device="cuda").to(DT[dt]) for _ in range(4))
+            x, res, s, o = (b[:, off:off + d] for b in (bx, br, bs, bo))
+            ks, ko = bs.clone(), bo.clone()
+            check_norm(gpu_lib, x, res, None, sum_out=s, out=o)
+            for now, was in ((bs, ks), (bo, ko)):              # columns outside the rows untouched
+                assert torch.equal(now[:, :off], was[:, :off]) and torch.equal(now[:, off + d:], was[:, off + d:])
+            q = torch.zeros(6, ld, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)[:, off:off + d]
+            sc = torch.zeros(6, 9, device="cuda")[:, 2:3]
+            check_norm(gpu_lib, x, res, None, out_dtype=torch.float8_e4m3fn, out=q, scales=sc)
+        x = torch.randn(7, 512, generator=g, device="cuda").to(DT[dt])
+        res = torch.randn(7, 512, generator=g, device="cuda").to(DT[dt])
+        want, ws, _ = gpu_lib.add_rmsnorm(x, res)
+        x1, r1 = x.clone(), res.clone()
+        gpu_lib.add_rmsnorm(x1, r1, sum_out=r1, out=x1)        # in place on both
+        assert torch.equal(x1, want) and torch.equal(r1, ws)
+
+
+def test_norm_agrees_with_rmsnorm(gpu_lib):
+    """Without gain and residual: the norm the library had, up to one rounding of its output."""
+    x = torch.randn(9, 4096, device="cuda", generator=gen(2)).to(torch.bfloat16)
+    a, b = gpu_lib.rmsnorm(x).float(), gpu_lib.add_rmsnorm(x)[0].float()
+    assert ((a - b).abs() <= a.abs() * 2.0 ** -7).all()
+
+
+def test_norm_of_no_rows(gpu_lib):
+    out, s, sc = gpu_lib.add_rmsnorm(torch.empty((0, 64), device="cuda"), out_dtype=torch.float8_e4m3fn)
+    assert out.shape == (0, 64) and sc.shape == (0, 1) and s is None
+
+
+# ---------------------------------------------------------------------------
+# 4-bit products
+# ---------------------------------------------------------------------------
+E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def make_w4(fmt, N, K, group, zeros, sdt, g):
+    q = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    codes = torch.stack((q & 15, q >> 4), 2).view(N, K)
+    if fmt == "nvfp4":
+        s = torch.randint(0, 0x7F, (N, K // 16), generator=g, device="cuda", dtype=torch.uint8)   # every finite scale
+        gs = torch.full((1,), 0.37e-2, device="cuda")
+        table = torch.tensor(E2M1 + [-v for v in E2M1], device="cuda", dtype=torch.float64)
+        W = (table[codes.int()].view(N, -1, 16) * s.view(torch.float8_e4m3fn).double()[:, :, None]).view(N, K) * gs.double()
+        return (q, s, gs), W
+    s = (torch.rand(N, K // group, generator=g, device="cuda") + 0.1).to(DT[sdt])
+    z = torch.randint(0, 16, (N, K // group), generator=g, device="cuda", dtype=torch.uint8) if zeros else None
+    zz = z.double() if zeros else torch.full((N, K // group), 8.0, device="cuda", dtype=torch.float64)
+    W = ((codes.double().view(N, -1, group) - zz[:, :, None]) * s.double()[:, :, None]).view(N, K)
+    return (q, s, z), W
+
+
+def call_w4(moe, fmt, x, w, **kw):
+    return (moe.linear_nvfp4 if fmt == "nvfp4" else moe.linear_int4)(x, *w, **kw)
+
+
+def check_w4(moe, fmt, x, w, W, x_scales=None, bias=None, **kw):
+    y = call_w4(moe, fmt, x, w, x_scales=x_scales, bias=bias, **kw)
+    xd = x.double()
+    if x_scales is not None:
+        xd = (xd.view(x.shape[0], x_scales.shape[1], -1) * x_scales.double()[:, :, None]).view(x.shape)
+    ref = xd @ W.t()
+    size = xd.abs() @ W.abs().t()
+    if bias is not None:
+        ref, size = ref + bias.double(), size + bias.double().abs()
+    # a product of 16 and its accumulator meet in the tensor core with each term cut at 2^-23 of the largest: 17 of
+    # those for each of 8 products in a row, then one addition and up to three products per 128 columns, up to 8
+    # K-parts, the tensor scale and the bias
+    K = x.shape[1]
+    tol = size * (8 * 17 + 4 * (K // 128 + 1) + 16) * 2.0 ** -23
+    fi = torch.finfo(y.dtype)
+    tol = tol + ref.abs() * fi.eps / 2 + (fi.smallest_normal * fi.eps if y.dtype != torch.float32 else 0)
+    assert torch.isfinite(y).all()
+    bad = (y.double() - ref).abs() > tol
+    assert not bad.any(), (bad.nonzero()[:4].tolist(), (y.double() - ref)[bad][:4].tolist(), tol[bad][:4].tolist())
+    return y
+
+
+W4S = [
+    # M, N, K
+    (1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 40, 128), (1, 100, 160), (8, 129, 256), (9, 33, 384), (16, 64, 1024),
+    (5, 300, 1152), (17, 31, 512), (32, 130, 640), (33, 70, 256), (64, 48, 2048), (1, 5000, 256), (4, 2500, 1536),
+    (7, 64, 12288), (64, 20, 8192),
+]
+
+
+@pytest.mark.parametrize("M,N,K", W4S)
+@pytest.mark.parametrize("fmt,group", [("nvfp4", 16), ("int4", 32), ("int4", 64), ("int4", 128)])
+def test_linear_w4(gpu_lib, M, N, K, fmt, group):
+    if K % group:
+        pytest.skip("the group does not divide K")
+    g = gen(M * N + K)
+    for xdt, ydt, sdt, zeros in (("bf16", "f32", "bf16", True), ("f16", "f32", "f16", False), ("bf16", "bf16", "f16", True),
+                                 ("f16", "f16", "bf16", True)):
+        w, W = make_w4(fmt, N, K, group, zeros, sdt, g)
+        x = torch.randn(M, K, generator=g, device="cuda").to(DT[xdt])
+        if ydt == "f16":
+            x = x * 2.0 ** -6 if fmt == "nvfp4" else x      # stay inside f16
+        bias = torch.randn(N, generator=g, device="cuda") if zeros else None
+        check_w4(gpu_lib, fmt, x, w, W, bias=bias, out_dtype=DT[ydt])
+
+
+@pytest.mark.parametrize("M,N,K,xgroup", [(1, 64, 256, 128), (3, 50, 1024, 256), (8, 33, 1152, 128), (16, 40, 2048, 1024),
+                                          (20, 65, 384, 0), (2, 40, 160, 0), (40, 100, 640, 128)])
+@pytest.mark.parametrize("fmt,group", [("nvfp4", 16), ("int4", 32), ("int4", 128)])
+def test_linear_w4_8bit_inputs(gpu_lib, M, N, K, xgroup, fmt, group):
+    if K % group:
+        pytest.skip("the group does not divide K")
+    g = gen(M + N + K)
+    w, W = make_w4(fmt, N, K, group, True, "bf16", g)
+    x = torch.randint(0, 256, (M, K), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.where((x & 0x7F) == 0x7F, x - 1, x).view(torch.float8_e4m3fn)                     # every finite value
+    xs = torch.exp(torch.randn(M, K // (xgroup or K), generator=g, device="cuda"))
+    check_w4(gpu_lib, fmt, x, w, W, x_scales=xs, out_dtype=torch.float32)
+    check_w4(gpu_lib, fmt, x, w, W, x_scales=xs)
+
+
+def test_linear_w4_wide_range_of_x(gpu_lib):
+    """bf16 inputs of very different sizes in one block, and at the ends of the type's range."""
+    g = gen(11)
+    M, N, K = 6, 48, 512
+    (q, s, gs), W = make_w4("nvfp4", N, K, 16, False, None, g)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    x[1] *= torch.exp2(torch.randint(-40, 1, (K,), generator=g, device="cuda").float())
+    x[2] *= 1e30
+    x[3] *= 1e-33
+    x[4] = 0
+    x[5, :128] = 0
+    x = x.to(torch.bfloat16)
+    y = gpu_lib.linear_nvfp4(x, q, s, gs, out_dtype=torch.float32).double()
+    ref, size = x.double() @ W.t(), x.double().abs() @ W.abs().t()
+    # as check_w4, and 2^-40 of each block's largest input
+    big = x.double().abs().view(M, 4, 128).amax(2).repeat_interleave(128, 1) @ W.abs().t()
+    assert ((y - ref).abs() <= size * 200 * 2.0 ** -23 + big * 2.0 ** -40 + 1e-44).all()
+
+
+def test_linear_w4_infinities_stay_in_their_row(gpu_lib):
+    g = gen(12)
+    (q, s, gs), W = make_w4("nvfp4", 32, 256, 16, False, None, g)
+    x = torch.randn(4, 256, generator=g, device="cuda").to(torch.bfloat16)
+    clean = gpu_lib.linear_nvfp4(x, q, s, gs)
+    x2 = x.clone()
+    x2[1, 7], x2[2, 130] = INF, NAN
+    y = gpu_lib.linear_nvfp4(x2, q, s, gs)
+    assert torch.equal(y[[0, 3]], clean[[0, 3]])
+    assert not torch.isfinite(y[1]).any() and torch.isnan(y[2]).all()
+
+
+def test_linear_w4_strides_and_bounds(gpu_lib):
+    """Rows of x and y with other strides and offsets; nothing outside y is written."""
+    g = gen(13)
+    for fmt, group in (("nvfp4", 16), ("int4", 64)):
+        for M, N, K, xo, yo in ((3, 37, 320, 1, 3), (11, 64, 256, 8, 1), (1, 200, 128, 3, 5)):
+            w, W = make_w4(fmt, N, K, group, True, "f16", g)
+            x = torch.randn(M, K + 19, generator=g, device="cuda").to(torch.float16)[:, xo:xo + K]
+            by = torch.full((M, N + 9), 7.0, device="cuda")
+            y = by[:, yo:yo + N]
+            check_w4(gpu_lib, fmt, x, w, W, out=y)
+            assert (by[:, :yo] == 7).all() and (by[:, yo + N:] == 7).all()
+            xs = torch.rand(M, 5, generator=g, device="cuda")[:, 1:2]
+            x8 = torch.randn(M, K + 19, generator=g, device="cuda").to(torch.float8_e4m3fn)[:, xo:xo + K]
+            check_w4(gpu_lib, fmt, x8, w, W, x_scales=xs)
+
+
+def test_linear_takes_the_quantiser_output(gpu_lib):
+    W = 0.02 * torch.randn(1, 96, 512, generator=gen(14), device="cuda").to(torch.bfloat16)
+    q, s, gs = gpu_lib.quantize_nvfp4(W)
+    table = torch.tensor(E2M1 + [-v for v in E2M1], device="cuda", dtype=torch.float64)
+    codes = torch.stack((q[0] & 15, q[0] >> 4), 2).view(96, 512)
+    Wq = (table[codes.int()].view(96, -1, 16) * s[0].view(torch.float8_e4m3fn).double()[:, :, None]).view(96, 512) * gs.double()
+    x = torch.randn(3, 512, generator=gen(15), device="cuda").to(torch.bfloat16)
+    check_w4(gpu_lib, "nvfp4", x, (q[0], s[0], gs), Wq)
+
+
+def test_linear_of_no_tokens(gpu_lib):
+    (q, s, gs), _ = make_w4("nvfp4", 32, 64, 16, False, None, gen(16))
+    assert gpu_lib.linear_nvfp4(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), q, s, gs).shape == (0, 32)
+
+
+# ---------------------------------------------------------------------------
+# refusals of the bindings, streams, graphs
+# ---------------------------------------------------------------------------
+def test_bindings_refuse(gpu_lib):
+    moe = gpu_lib
+    x = torch.zeros(4, 64, device="cuda")
+    b = x.to(torch.bfloat16)
+    (q, s, gs), _ = make_w4("nvfp4", 32, 64, 16, False, None, gen(17))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for call in (
+        lambda: moe.route_logits(x[0], 2), lambda: moe.route_logits(x.double(), 2), lambda: moe.route_logits(x.t(), 2),
+        lambda: moe.route_logits(x, 2, score="tanh"), lambda: moe.route_logits(x, 2, bias=torch.zeros(63, device="cuda")),
+        lambda: moe.route_logits(x, 2, bias=torch.zeros(64)), lambda: moe.route_logits(x, 2, out={}),
+        lambda: moe.route_logits(x, 2, out={"ids": torch.empty(4, 3, **i32), "w": torch.empty(4, 2, device="cuda")}),
+        lambda: moe.route_logits(x[:1].expand(4, 64), 2),
+        lambda: moe.add_rmsnorm(x, b), lambda: moe.add_rmsnorm(x, gain=torch.ones(63, device="cuda")),
+        lambda: moe.add_rmsnorm(x, out_dtype=torch.bfloat16), lambda: moe.add_rmsnorm(x, group=32),
+        lambda: moe.add_rmsnorm(x, out_dtype=torch.float8_e4m3fn, group=48), lambda: moe.add_rmsnorm(x.t()),
+        lambda: moe.add_rmsnorm(x, scales=torch.empty(4, 1, device="cuda")),
+        lambda: moe.add_rmsnorm(x, out=torch.empty(4, 63, device="cuda")),
+        lambda: moe.linear_nvfp4(x, q, s, gs), lambda: moe.linear_nvfp4(b, q[:, :16], s, gs),
+        lambda: moe.linear_nvfp4(b, q, s[:, :2], gs), lambda: moe.linear_nvfp4(b, q, s, gs.double()),
+        lambda: moe.linear_nvfp4(b, q, s, gs, x_scales=torch.ones(4, 1, device="cuda")),
+        lambda: moe.linear_nvfp4(b.to(torch.float8_e4m3fn), q, s, gs),
+        lambda: moe.linear_nvfp4(b, q, s, gs, out=torch.empty(4, 32, dtype=torch.int32, device="cuda")),
+        lambda: moe.linear_nvfp4(b, q.t().contiguous().t(), s, gs), lambda: moe.linear_nvfp4(b, q, s, gs, bias=gs),
+        lambda: moe.linear_int4(b, q, s),
+    ):
+        with pytest.raises(ValueError):
+            call()
+    for call in (
+        lambda: moe.route_logits(x, 17), lambda: moe.route_logits(x, 2, n_groups=3), lambda: moe.route_logits(x, 2, scale=NAN),
+        lambda: moe.add_rmsnorm(x, eps=-1.0), lambda: moe.add_rmsnorm(torch.zeros(1, 20000, device="cuda")),
+        lambda: moe.linear_nvfp4(b.repeat(17, 1), q, s, gs),
+        lambda: moe.linear_int4(b, q, torch.ones(32, 4, dtype=torch.bfloat16, device="cuda")),
+    ):
+        with pytest.raises(moe.MoeError):
+            call()
+
+
+def test_streams_and_graphs(gpu_lib):
+    """Each operator on a side stream and captured into a graph that is replayed on new inputs."""
+    moe, g = gpu_lib, gen(21)
+    T, d, N = 40, 512, 96
+    w, W = make_w4("nvfp4", N, d, 16, False, None, g)
+    x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    res = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+
+    def step():
+        q, s, sc = moe.add_rmsnorm(x, res, out_dtype=torch.float8_e4m3fn, group=128)
+        y = moe.linear_nvfp4(q, *w, x_scales=sc, out_dtype=torch.float32)
+        return s, y, moe.route_logits(y, 4, score="sigmoid", n_groups=8, topk_groups=2)
+
+    def same(a, b):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        for n in b[2]:
+            assert torch.equal(a[2][n], b[2][n]), n
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    out = moe.route_logits(want[1], 4, stream=side)
+    side.synchronize()
+    same(got, want)
+    check_route(out, want[1], 4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in (1, 2):
+        x.copy_(torch.randn(T, d, generator=gen(seed), device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = (held[0].clone(), held[1].clone(), {n: v.clone() for n, v in held[2].items()})
+        same(got, step())
+
+
+# ---------------------------------------------------------------------------
+# with the layer
+# ---------------------------------------------------------------------------
+def make_layer(moe, d, I, E, k, max_tokens, g, fmt="bf16"):
+    wr = (0.3 * torch.randn(E, d, generator=g, device="cuda")).to(torch.bfloat16)
+    gate, up = ((0.05 * torch.randn(E, I, d, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2))
+    down = (0.05 * torch.randn(E, d, I, generator=g, device="cuda")).to(torch.bfloat16)
+    if fmt == "bf16":
+        layer = moe.MoeLayer(wr, w_gate=gate, w_up=up, w_down=down, top_k=k, max_tokens=max_tokens)
+    else:
+        nv = {}
+        for n, m in (("gate", gate), ("up", up), ("down", down)):
+            nv["q_" + n], nv["s_" + n], nv["g_" + n] = moe.quantize_nvfp4(m)
+        table = torch.tensor(E2M1 + [-v for v in E2M1], device="cuda")
+
+        def wide(n):
+            q, s, gs = nv["q_" + n], nv["s_" + n], nv["g_" + n]
+            c = torch.stack((q & 15, q >> 4), 3).flatten(2)
+            v = table[c.int()].unflatten(2, (-1, 16)) * s.view(torch.float8_e4m3fn).float()[..., None]
+            return v.flatten(2) * gs[:, None, None]
+        gate, up, down = wide("gate"), wide("up"), wide("down")
+        layer = moe.MoeLayer(wr, nvfp4=nv, top_k=k, max_tokens=max_tokens)
+    return layer, wr, gate, up, down
+
+
+def ref_experts(x, ids, w, gate, up, down):
+    """sum_j w_j * expert(ids_j) in fp64 from the routing given."""
+    out = torch.zeros(x.shape, dtype=torch.float64, device="cuda")
+    for e in ids.unique().tolist():
+        t, j = (ids == e).nonzero(as_tuple=True)
+        h = torch.nn.functional.silu(x[t].double() @ gate[e].double().t()) * (x[t].double() @ up[e].double().t())
+        out.index_add_(0, t, (h @ down[e].double().t()) * w[t, j].double()[:, None])
+    return out
+
+
+ROUTER = dict(score="sigmoid", n_groups=8, topk_groups=3, group_rule="top2", scale=2.5)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("d", [256, 320])
+def test_layer_with_its_own_router(gpu_lib, fmt, d):
+    if fmt == "nvfp4" and d % 256:
+        pytest.skip("NVFP4 layers take d a multiple of 256")
+    moe, g, I, E, k = gpu_lib, gen(31), 256, 64, 6
+    layer, wr, gate, up, down = make_layer(moe, d, I, E, k, 300, g, fmt)
+    bias = 0.2 * torch.randn(E, generator=g, device="cuda")
+    for T in (1, 5, 16, 17, 32, 33, 100, 300):
+        x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+        before = layer.forward(x).clone()
+        before_r = layer.route(x)
+        layer.set_router(bias=bias, **ROUTER)
+        r = layer.route(x)
+        logits = x.double() @ wr.double().t()
+        ids, w = ref_route(logits.float(), k, "sigmoid", bias, 8, 3, "top2", True, 2.5)
+        # tokens whose choice turns on less than the fp32 logits' error keep the right to differ: their ids are
+        # compared as a share only (a wrong rule changes nearly all)
+        same = (r["ids"].cpu().numpy() == ids).all(1)
+        assert same.mean() >= 0.97, same.mean()
+        # logits of size ~10 off by up to 2^-24 * sqrt(d) * 10 ~ 1e-5
+        np.testing.assert_allclose(r["w"].cpu().numpy()[same], w[same], rtol=1e-3, atol=1e-6)
+        for name, v in zip(("counts", "offsets", "perm", "pos"), ref_permute(r["ids"].cpu().numpy(), E)):
+            np.testing.assert_array_equal(r[name].cpu().numpy(), v, err_msg=name)
+        res = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+        y = layer.forward(x).clone()
+        yr = layer.forward(x, res=res).clone()
+        assert layer.device_status() == moe.MOE_OK
+        ref = ref_experts(x, r["ids"].long(), r["w"], gate, up, down)
+        tol = 2e-2 if fmt == "bf16" else 5e-2               # the layer's own bar
+        for got, want in ((y, ref), (yr, ref + res.double())):
+            err = (got.double() - want).abs().amax(1) / want.abs().amax(1)
+            assert err.max() <= tol, (T, err.max())
+        layer.clear_router()
+        assert torch.equal(layer.forward(x), before)
+        after_r = layer.route(x)
+        for n in before_r:
+            assert torch.equal(after_r[n], before_r[n]), n
+
+
+def test_layer_router_without_enough_experts_is_reported(gpu_lib):
+    moe, g = gpu_lib, gen(33)
+    layer, *_ = make_layer(moe, 256, 128, 64, 4, 64, g)
+    bias = torch.full((64,), -INF, device="cuda")
+    bias[5] = bias[9] = 0.0
+    for T in (3, 40):
+        x = torch.randn(T, 256, generator=g, device="cuda").to(torch.bfloat16)
+        layer.set_router(score="sigmoid", bias=bias)
+        layer.forward(x)
+        assert layer.device_status() == moe.MOE_ERR_DEVICE
+        layer.clear_router()
+        layer.forward(x)
+        assert layer.device_status() == moe.MOE_OK
+
+
+def test_router_refusals(gpu_lib):
+    moe, g = gpu_lib, gen(34)
+    layers = [make_layer(moe, 256, 128, 64, 4, 8, g)[0] for _ in range(2)]
+    with pytest.raises(moe.MoeError):
+        layers[0].set_router(n_groups=5)
+    with pytest.raises(ValueError):
+        layers[0].set_router(bias=torch.zeros(63, device="cuda"))
+    stack = moe.MoeStack(layers)
+    x = torch.randn(2, 256, generator=g, device="cuda").to(torch.bfloat16)
+    want = stack.forward(x).clone()
+    layers[1].set_router(score="sigmoid")
+    with pytest.raises(moe.MoeError):
+        stack.forward(x)
+    with pytest.raises(moe.MoeError):
+        moe.MoeStack(layers)
+    layers[1].clear_router()
+    assert torch.equal(stack.forward(x), want)
+
+
+def test_a_block_of_the_operators(gpu_lib):
+    """Residual + norm in 8 bits -> 4-bit projection -> residual + norm -> the layer with sigmoid routing -> residual."""
+    moe, g, T, d, E, k = gpu_lib, gen(35), 12, 256, 64, 4
+    layer, wr, gate, up, down = make_layer(moe, d, 128, E, k, 16, g)
+    layer.set_router(**ROUTER)
+    gain = (1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16)
+    (q, s, gs), W = make_w4("nvfp4", d, d, 16, False, None, g)
+    gs = gs / 30
+    W = W / 30
+    x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    res = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    n8, s1, sc = check_norm(moe, x, res, gain, out_dtype=torch.float8_e4m3fn, group=128)
+    p = check_w4(moe, "nvfp4", n8, (q, s, gs), W, x_scales=sc)
+    n2, s2, _ = check_norm(moe, p, s1, gain)
+    out = layer.forward(n2, res=s2)
+    r = layer.route_records(T)
+    ref = ref_experts(n2, r["ids"].long(), r["w"], gate, up, down) + s2.double()
+    assert ((out.double() - ref).abs().amax(1) / ref.abs().amax(1)).max() <= 2e-2

@@ -23,6 +23,10 @@ HEADER = os.path.join(_build.ROOT, "include", "moe.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_TIMEOUT = range(6)
 MOE_W_BF16, MOE_W_NVFP4 = 0, 1
+MOE_T_BF16, MOE_T_F16, MOE_T_F32, MOE_T_E4M3 = range(4)
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_W4_NVFP4, MOE_W4_INT4 = 0, 1
 MOE_DECODE_AUTO, MOE_DECODE_CUDA_CORES, MOE_DECODE_TENSOR_CORES = 0, 1, 2
 
 
@@ -43,6 +47,35 @@ class MoeLayerDesc(ctypes.Structure):
         ("g_gate", ctypes.c_void_p), ("g_up", ctypes.c_void_p), ("g_down", ctypes.c_void_p),
         ("expert_out_norm", ctypes.c_int),
         ("gate_up_interleaved", ctypes.c_int),
+    ]
+
+
+class MoeRouteDesc(ctypes.Structure):
+    _fields_ = [
+        ("E", ctypes.c_int), ("top_k", ctypes.c_int), ("score", ctypes.c_int), ("bias", ctypes.c_void_p),
+        ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int), ("group_rule", ctypes.c_int),
+        ("renormalise", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class MoeNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("res", ctypes.c_void_p), ("gain", ctypes.c_void_p), ("sum", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64), ("res_stride", ctypes.c_int64), ("sum_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64), ("scales_stride", ctypes.c_int64),
+        ("T", ctypes.c_int), ("d", ctypes.c_int), ("group", ctypes.c_int),
+        ("type", ctypes.c_int), ("out_type", ctypes.c_int), ("eps", ctypes.c_float),
+    ]
+
+
+class MoeW4Args(ctypes.Structure):
+    _fields_ = [
+        ("fmt", ctypes.c_int), ("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("group", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("s_type", ctypes.c_int), ("g", ctypes.c_void_p),
+        ("z", ctypes.c_void_p), ("x", ctypes.c_void_p), ("x_type", ctypes.c_int), ("x_stride", ctypes.c_int64),
+        ("x_scales", ctypes.c_void_p), ("x_scales_stride", ctypes.c_int64), ("x_group", ctypes.c_int),
+        ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_type", ctypes.c_int), ("y_stride", ctypes.c_int64),
     ]
 
 
@@ -90,6 +123,12 @@ def load(path: str | None = None):
             "moe_stack_forward": ([vp, vp, vp, i, f, vp, vp], st),
             "moe_stack_forward_host": ([vp, vp, vp, i, f, vp], st),
             "moe_stack_destroy": ([vp], st),
+            "moe_route_logits_workspace_size": ([ctypes.POINTER(MoeRouteDesc), i, ctypes.POINTER(ctypes.c_size_t)], st),
+            "moe_route_logits": ([ctypes.POINTER(MoeRouteDesc), vp, i, ctypes.c_int64, i, vp, vp, vp, vp, vp, vp, vp,
+                                  ctypes.c_size_t, vp], st),
+            "moe_layer_set_router": ([vp, ctypes.POINTER(MoeRouteDesc)], st),
+            "moe_add_rmsnorm": ([ctypes.POINTER(MoeNormArgs), vp], st),
+            "moe_linear_w4": ([ctypes.POINTER(MoeW4Args), vp], st),
             "moe_status_string": ([st], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -216,6 +255,19 @@ class MoeLayer:
         _check(load().moe_debug_hold_grid_barrier(self._h, 1 if hold else 0, _stream(stream)),
                "moe_debug_hold_grid_barrier")
 
+    def set_router(self, *, score="softmax", bias=None, n_groups=1, topk_groups=1, group_rule="max",
+                   renormalise=True, scale=1.0):
+        """Choose the layer's experts as ``route_logits`` does, from the layer's own
+        router logits; see ``clear_router``. ``bias``: [E] fp32 CUDA tensor or None."""
+        desc = _route_desc(self.E, self.k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale)
+        _check(load().moe_layer_set_router(self._h, ctypes.byref(desc)), "moe_layer_set_router")
+        self._router_bias = bias
+
+    def clear_router(self):
+        """Back to the softmax top-k."""
+        _check(load().moe_layer_set_router(self._h, None), "moe_layer_set_router")
+        self._router_bias = None
+
     def forward(self, x, out=None, res=None, stream=None):
         _require_cuda(x, out, res)
         T = x.shape[0]
@@ -331,3 +383,221 @@ def quantize_nvfp4(W, stream=None):
     _check(load().moe_quantize_nvfp4(_ptr(W), n, rows, K, _ptr(q), _ptr(s), _ptr(g), _stream(stream)),
            "moe_quantize_nvfp4")
     return q, s, g
+
+
+# -- operators around the layer -------------------------------------------------
+_DTYPE = {torch.bfloat16: MOE_T_BF16, torch.float16: MOE_T_F16, torch.float32: MOE_T_F32,
+          torch.float8_e4m3fn: MOE_T_E4M3}
+_SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_GROUP_RULE = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+
+
+def _tensor(name, t, dtype, shape, device, contiguous=True):
+    """Checks one tensor argument (None passes): type, shape, device, and rows whose
+    elements are adjacent (contiguous=False) or the whole tensor contiguous."""
+    if t is None:
+        return
+    if t.dtype is not dtype and t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the first argument on {device}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    else:
+        _row_stride(name, t)
+
+
+def _row_stride(name, t):
+    """Elements from one row of a 2-D tensor to the next (rows contiguous, not overlapping)."""
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    if rows <= 1:
+        return max(cols, 1)
+    if s0 < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return s0
+
+
+def _input(name, t, types):
+    """The first argument of a call: a 2-D CUDA tensor of one of `types`."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    if t.dtype not in types:
+        raise ValueError(f"{name}: type {t.dtype} is not supported")
+    return t.device
+
+
+def _run(device, stream, call):
+    """call(stream handle) with `device` current; stream None: the device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(_stream(stream))
+    return call(_stream(stream))
+
+
+def _route_desc(E, top_k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale):
+    if score not in _SCORE or group_rule not in _GROUP_RULE:
+        raise ValueError(f"score is one of {sorted(_SCORE)}, group_rule one of {sorted(_GROUP_RULE)}")
+    if bias is not None and (not bias.is_cuda or bias.dtype != torch.float32 or tuple(bias.shape) != (E,)
+                             or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous fp32 CUDA tensor of one value per expert")
+    return MoeRouteDesc(E, top_k, _SCORE[score], _ptr(bias), n_groups, topk_groups, _GROUP_RULE[group_rule],
+                        1 if renormalise else 0, scale)
+
+
+_ROUTE_RECORDS = ("ids", "w", "counts", "offsets", "perm", "pos")
+
+
+def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_groups=1, group_rule="max",
+                 renormalise=True, scale=1.0, out=None, stream=None):
+    """Routing from given logits [T, E] (bf16, f16 or fp32; moe_route_logits).
+
+    Scores are softmax or sigmoid of the logits; ``bias`` [E] fp32 is added to them for the choice only; with
+    ``n_groups`` > 1 the choice is from the ``topk_groups`` groups with the best ``group_rule`` ("max", or "top2": the
+    sum of the two best). -> dict of ids, w [T, top_k], counts [E], offsets [E+1], perm [T*top_k], pos [T, top_k] as
+    ``MoeLayer.route``; slots without an expert left hold id -1, weight 0, pos -1. ``out``: such a dict to write to;
+    counts, offsets, perm and pos may be left out of it and are then not computed.
+    """
+    device = _input("logits", logits, (torch.bfloat16, torch.float16, torch.float32))
+    T, E = logits.shape
+    desc = _route_desc(E, top_k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale)
+    if bias is not None and bias.device != device:
+        raise ValueError(f"bias: on {bias.device}, logits on {device}")
+    if out is None:
+        i32 = {"dtype": torch.int32, "device": device}
+        out = {"ids": torch.empty((T, top_k), **i32), "w": torch.empty((T, top_k), dtype=torch.float32, device=device),
+               "counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32),
+               "perm": torch.empty(T * top_k, **i32), "pos": torch.empty((T, top_k), **i32)}
+    else:
+        if out.get("ids") is None or out.get("w") is None:
+            raise ValueError("out must hold ids and w")
+        shapes = {"ids": (T, top_k), "w": (T, top_k), "counts": (E,), "offsets": (E + 1,), "perm": (T * top_k,),
+                  "pos": (T, top_k)}
+        for n, shape in shapes.items():
+            _tensor(n, out.get(n), torch.float32 if n == "w" else torch.int32, shape, device)
+    lib = load()
+    size = ctypes.c_size_t(0)
+    _check(lib.moe_route_logits_workspace_size(ctypes.byref(desc), T, ctypes.byref(size)), "moe_route_logits")
+    stride = _row_stride("logits", logits)
+
+    def call(st):
+        # scratch from torch's allocator on the stream the kernels run on: captured graphs and streams each get their own
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=device)
+        return lib.moe_route_logits(ctypes.byref(desc), _ptr(logits), _DTYPE[logits.dtype], stride, T,
+                                    *(_ptr(out.get(n)) for n in _ROUTE_RECORDS), _ptr(ws), size.value, st)
+
+    _check(_run(device, stream, call), "moe_route_logits")
+    return out
+
+
+def add_rmsnorm(x, res=None, gain=None, *, eps=1e-6, out_dtype=None, group=0, sum_out=None, out=None, scales=None,
+                stream=None):
+    """Residual addition and RMSNorm (moe_add_rmsnorm): s = x + res, y = s / sqrt(mean(s^2) + eps) * gain.
+
+    x, res [T, d] and gain [d] share one type (bf16, f16 or fp32); rows may lie further apart than d elements.
+    ``out_dtype`` torch.float8_e4m3fn (or an ``out`` of that type) gives E4M3 with one fp32 scale per ``group`` columns
+    (0: per row). -> (out, s or None without res, scales or None). ``sum_out``, ``out``, ``scales``: buffers to write
+    to; sum_out and out may be x or res themselves.
+    """
+    device = _input("x", x, (torch.bfloat16, torch.float16, torch.float32))
+    T, d = x.shape
+    if out is not None:
+        if out_dtype is not None and out_dtype != out.dtype:
+            raise ValueError("out_dtype and out differ")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = x.dtype
+    if out_dtype not in (x.dtype, torch.float8_e4m3fn):
+        raise ValueError(f"out_dtype {out_dtype} is not supported for {x.dtype} inputs")
+    e4m3 = out_dtype == torch.float8_e4m3fn
+    if group < 0 or (group and (not e4m3 or d % group)):
+        raise ValueError("group divides d, and needs E4M3 output")
+    if e4m3:
+        cols = d // (group or d) if d else 0
+        if scales is None:
+            scales = torch.empty((T, cols), dtype=torch.float32, device=device)
+    elif scales is not None:
+        raise ValueError("scales need E4M3 output")
+    if out is None:
+        out = torch.empty((T, d), dtype=out_dtype, device=device)
+    if sum_out is None and res is not None:
+        sum_out = torch.empty((T, d), dtype=x.dtype, device=device)
+    _tensor("res", res, x.dtype, x.shape, device, False)
+    _tensor("gain", gain, x.dtype, (d,), device)
+    _tensor("sum_out", sum_out, x.dtype, x.shape, device, False)
+    _tensor("out", out, out_dtype, x.shape, device, False)
+    if e4m3:
+        _tensor("scales", scales, torch.float32, (T, cols), device, False)
+    args = MoeNormArgs(_ptr(x), _ptr(res), _ptr(gain), _ptr(sum_out), _ptr(out), _ptr(scales),
+                       _row_stride("x", x), _row_stride("res", res) if res is not None else 0,
+                       _row_stride("sum_out", sum_out) if sum_out is not None else 0, _row_stride("out", out),
+                       _row_stride("scales", scales) if e4m3 else 0, T, d, group, _DTYPE[x.dtype],
+                       _DTYPE[out_dtype], eps)
+    _check(_run(device, stream, lambda st: load().moe_add_rmsnorm(ctypes.byref(args), st)), "moe_add_rmsnorm")
+    return out, sum_out, scales
+
+
+def _linear_w4(fmt, x, q, s, g, z, x_scales, bias, out, out_dtype, stream):
+    device = _input("x", x, (torch.bfloat16, torch.float16, torch.float8_e4m3fn))
+    M, K = x.shape
+    if q.dim() != 2 or s.dim() != 2:
+        raise ValueError("q and s must be 2-D")
+    N = q.shape[0]
+    if fmt == MOE_W4_NVFP4:
+        group, s_type = 16, torch.uint8
+    else:
+        group, s_type = K // s.shape[1] if s.shape[1] else 0, s.dtype
+        if s_type not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"s: type {s_type} is not supported")
+    if group < 1 or K % group:
+        raise ValueError("s: one scale per group of columns expected")
+    _tensor("q", q, torch.uint8, (N, K // 2), device)
+    _tensor("s", s, s_type, (N, K // group), device)
+    _tensor("g", g, torch.float32, (1,), device)
+    _tensor("zeros", z, torch.uint8, (N, K // group), device)
+    _tensor("bias", bias, torch.float32, (N,), device)
+    x_group = 0
+    if x.dtype == torch.float8_e4m3fn:
+        if x_scales is None or x_scales.dim() != 2 or not x_scales.shape[1] or K % x_scales.shape[1]:
+            raise ValueError("E4M3 x needs x_scales [M, groups]")
+        x_group = K // x_scales.shape[1] if x_scales.shape[1] > 1 else 0
+        _tensor("x_scales", x_scales, torch.float32, (M, x_scales.shape[1]), device, False)
+    elif x_scales is not None:
+        raise ValueError("x_scales belong to E4M3 x")
+    if out is None:
+        out_dtype = out_dtype or (torch.bfloat16 if x.dtype == torch.float8_e4m3fn else x.dtype)
+        out = torch.empty((M, N), dtype=out_dtype, device=device)
+    elif out_dtype is not None and out_dtype != out.dtype:
+        raise ValueError("out_dtype and out differ")
+    if out.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise ValueError(f"out: type {out.dtype} is not supported")
+    _tensor("out", out, out.dtype, (M, N), device, False)
+    args = MoeW4Args(fmt, M, N, K, group, _ptr(q), _ptr(s), _DTYPE.get(s_type, 0), _ptr(g), _ptr(z), _ptr(x),
+                     _DTYPE[x.dtype], _row_stride("x", x), _ptr(x_scales),
+                     _row_stride("x_scales", x_scales) if x_scales is not None else 0, x_group, _ptr(bias), _ptr(out),
+                     _DTYPE[out.dtype], _row_stride("out", out))
+    _check(_run(device, stream, lambda st: load().moe_linear_w4(ctypes.byref(args), st)), "moe_linear_w4")
+    return out
+
+
+def linear_nvfp4(x, q, s, g, *, x_scales=None, bias=None, out=None, out_dtype=None, stream=None):
+    """x W^T + bias for NVFP4 weights as ``quantize_nvfp4`` writes one tensor: q [N, K/2] and s [N, K/16] (uint8),
+    g [1] fp32 (moe_linear_w4).
+
+    x [M, K], M <= 64: bf16, f16, or E4M3 with x_scales [M, groups] fp32 as ``add_rmsnorm`` writes them (one group per
+    row, or groups of a multiple of 128 columns). The result is bf16, f16 or fp32 (default: x's type, bf16 for E4M3).
+    """
+    return _linear_w4(MOE_W4_NVFP4, x, q, s, g, None, x_scales, bias, out, out_dtype, stream)
+
+
+def linear_int4(x, q, s, zeros=None, *, x_scales=None, bias=None, out=None, out_dtype=None, stream=None):
+    """x W^T + bias for integer codes: w = (code - zero) * scale, q [N, K/2] uint8 (low nibble first), s [N, K/group]
+    bf16 or f16 with groups of 32, 64 or 128 columns, zeros [N, K/group] uint8 or None for 8 everywhere
+    (moe_linear_w4). x and the result as in ``linear_nvfp4``."""
+    return _linear_w4(MOE_W4_INT4, x, q, s, None, zeros, x_scales, bias, out, out_dtype, stream)

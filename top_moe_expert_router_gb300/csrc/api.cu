@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "ops_api.h"
 
 struct moe_layer {
     moe::LayerDev L;
@@ -17,6 +18,8 @@ struct moe_layer {
     int decode_path = MOE_DECODE_AUTO;
     bool mma_maps_ok = false;            // the tensor-core decode kernel's tensor maps are encoded
     std::vector<unsigned char> mma_maps;  // host copy, passed by value at launch
+    bool has_router = false;              // experts are chosen as `router` says (moe_layer_set_router)
+    moe_route_desc router{};
     bool y_bf16 = false;  // the last forward left the expert outputs in bf16 over ws.xperm
     // profiling: events [forward][kernel boundary]
     std::vector<cudaEvent_t> prof_events;
@@ -81,6 +84,49 @@ void prof_mark(moe_layer *ly, int i, cudaStream_t st) {
 // 256 (down-projection N tile) and I a multiple of 128 (gate/up N tile).
 bool prefill_supported(const LayerDev &L) { return L.d % 256 == 0 && L.I % 128 == 0; }
 
+// The experts of the T tokens whose router logits lie in ws.logits (nsplit
+// slices over K), as the layer's router description says: the records of the
+// softmax routing are written over, the used experts and tile offsets too.
+cudaError_t launch_layer_router(const moe_layer *ly, int T, int nsplit, cudaStream_t st, int *launches) {
+    const LayerDev &L = ly->L;
+    const Workspace &ws = ly->ws;
+    RouteArgs a = route_args(ly->router);
+    a.logits = ws.logits;
+    a.type = MOE_T_F32;
+    a.stride = L.E;
+    a.nsplit = nsplit;
+    a.split_stride = (int64_t)L.max_T * L.E;
+    a.T = T;
+    a.ids = ws.ids;
+    a.w = ws.w;
+    a.counts = ws.counts;
+    a.offsets = ws.offsets;
+    a.perm = ws.perm;
+    a.pos = ws.pos;
+    a.chunk_cnt = ws.chunk_base;
+    a.perm_fill = 0;                    // rows past the last pair are gathered (and never read back)
+    a.uniq = ws.uniq;
+    a.tile_off = ws.tile_off;
+    a.n_uniq = &ws.ctrl->n_uniq;
+    a.n_tiles = &ws.ctrl->n_tiles_gu;
+    return launch_route_logits(a, st, launches);
+}
+
+// Routing of one chunk of a forward (small: T <= 32, the GEMV router).
+cudaError_t launch_routing(moe_layer *ly, const uint16_t *x, int T, bool small, cudaStream_t st, int *launches) {
+    const LayerDev &L = ly->L;
+    if (small) {
+        cudaError_t e = launch_route_small(L, ly->ws, x, T, st);
+        ++*launches;
+        if (e == cudaSuccess && ly->has_router) e = launch_layer_router(ly, T, 1, st, launches);
+        return e;
+    }
+    if (!ly->has_router) return launch_route_large(L, ly->ws, x, T, st, launches);
+    cudaError_t e = launch_router_gemm(L, ly->ws, x, T, st);
+    ++*launches;
+    return e == cudaSuccess ? launch_layer_router(ly, T, router_ksplit(L.d), st, launches) : e;
+}
+
 // Large-batch forward: tensor-core router, top-k, permutation, row gather,
 // grouped gate/up GEMM with SwiGLU, grouped down GEMM, combine.
 moe_status forward_prefill(moe_layer *ly, const uint16_t *x, const uint16_t *res, uint16_t *out, int T,
@@ -89,7 +135,7 @@ moe_status forward_prefill(moe_layer *ly, const uint16_t *x, const uint16_t *res
     int launches = 0;
     prof_mark(ly, 0, st);
     const bool fp4 = L.fmt == MOE_W_NVFP4;
-    cudaError_t e = launch_route_large(L, ly->ws, x, T, st, &launches);
+    cudaError_t e = launch_routing(ly, x, T, false, st, &launches);
     if (e == cudaSuccess) e = fp4 ? launch_gather_rows_f16(L, ly->ws, x, T, st) : launch_gather_rows(L, ly->ws, x, T, st);
     ++launches;
     prof_mark(ly, 1, st);
@@ -130,8 +176,8 @@ moe_status forward_impl(moe_layer *ly, const uint16_t *x, const uint16_t *res, u
     const int tdec = decode_max_tokens(L.d);
     if (T > tdec && prefill_supported(L)) return forward_prefill(ly, x, res, out, T, st);
     ly->y_bf16 = false;
-    const bool mma = T <= 16 && use_mma(ly, T);
-    if (T <= tdec || mma) {
+    const bool mma = T <= 16 && !ly->has_router && use_mma(ly, T);
+    if ((T <= tdec && !ly->has_router) || mma) {
         // the whole layer in one persistent launch
         prof_mark(ly, 0, st);
         cudaError_t e = mma ? launch_decode_mma(L, ly->ws, ly->mma_maps.data(), x, res, out, T, st)
@@ -149,8 +195,7 @@ moe_status forward_impl(moe_layer *ly, const uint16_t *x, const uint16_t *res, u
     for (int t0 = 0; t0 < T; t0 += tdec) {
         const int n = T - t0 < tdec ? T - t0 : tdec;
         const uint16_t *xc = x + (size_t)t0 * L.d;
-        cudaError_t e = launch_route_small(L, ly->ws, xc, n, st);
-        ++launches;
+        cudaError_t e = launch_routing(ly, xc, n, true, st, &launches);
         if (e == cudaSuccess) e = launch_decode_gateup(L, ly->ws, xc, n, st);
         ++launches;
         if (e == cudaSuccess) e = launch_decode_down(L, ly->ws, xc, n, st);
@@ -249,20 +294,26 @@ moe_status moe_set_decode_path(moe_layer *ly, int path) {
     return MOE_OK;
 }
 
+moe_status moe_layer_set_router(moe_layer *ly, const moe_route_desc *desc) {
+    if (!ly) return MOE_ERR_INVALID_ARG;
+    if (!desc) {
+        ly->has_router = false;
+        return MOE_OK;
+    }
+    const moe_status s = check_route_desc(desc);
+    if (s != MOE_OK) return s;
+    if (desc->E != ly->L.E || desc->top_k != ly->L.k) return MOE_ERR_INVALID_ARG;
+    ly->router = *desc;
+    ly->has_router = true;
+    return MOE_OK;
+}
+
 moe_status moe_route(moe_layer *ly, const void *x, int T, int32_t *ids, float *w, int32_t *counts,
                      int32_t *offsets, int32_t *perm, int32_t *pos, void *stream) {
     if (!ly || !x || !aligned16(x) || T < 1 || T > ly->L.max_T) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    const LayerDev &L = ly->L;
-    const Workspace &ws = ly->ws;
     int launches = 0;
-    cudaError_t e;
-    if (T <= 32) {
-        e = launch_route_small(L, ws, (const uint16_t *)x, T, st);
-        launches = 1;
-    } else {
-        e = launch_route_large(L, ws, (const uint16_t *)x, T, st, &launches);
-    }
+    const cudaError_t e = launch_routing(ly, (const uint16_t *)x, T, T <= 32, st, &launches);
     ly->last_launches = launches;
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     return copy_records(ly, T, ids, w, counts, offsets, perm, pos, st);
@@ -374,6 +425,7 @@ moe_status moe_profile_end(moe_layer *ly, float *ms, int max_kernels, int *n_for
 struct moe_stack {
     moe_layer *first;  // its workspace holds the stack's weight records
     int n_layers;
+    moe_layer *layers[kMaxStack];
 };
 
 moe_status moe_stack_create(moe_layer *const *layers, int n_layers, moe_stack **out) {
@@ -387,7 +439,7 @@ moe_status moe_stack_create(moe_layer *const *layers, int n_layers, moe_stack **
         if (!ly) return MOE_ERR_INVALID_ARG;
         const LayerDev &L = ly->L;
         if (L.d != L0.d || L.E != L0.E || L.k != L0.k || L.I != L0.I || L.fmt != L0.fmt) return MOE_ERR_INVALID_ARG;
-        if (L.expert_norm) return MOE_ERR_UNSUPPORTED;
+        if (L.expert_norm || ly->has_router) return MOE_ERR_UNSUPPORTED;
         w[(size_t)l] = L.weights();
     }
     if (cudaMemcpy(layers[0]->ws.stack, w.data(), sizeof(LayerW) * (size_t)n_layers, cudaMemcpyHostToDevice) !=
@@ -407,7 +459,10 @@ moe_status moe_stack_create(moe_layer *const *layers, int n_layers, moe_stack **
             return MOE_ERR_CUDA;
         if (!ok) layers[0]->mma_maps_ok = false;
     }
-    *out = new moe_stack{layers[0], n_layers};
+    moe_stack *sk = new (std::nothrow) moe_stack{layers[0], n_layers, {}};
+    if (!sk) return MOE_ERR_INVALID_ARG;
+    for (int l = 0; l < n_layers; ++l) sk->layers[l] = layers[l];
+    *out = sk;
     return MOE_OK;
 }
 
@@ -416,6 +471,8 @@ moe_status moe_stack_forward(moe_stack *sk, const void *x, void *out, int T, flo
     if (!sk || !x || !out || !aligned16(x) || !aligned16(out) || (layer_out && !aligned16(layer_out)) || T < 1 ||
         T > 8 || T > sk->first->L.max_T || !(eps >= 0.f))
         return MOE_ERR_INVALID_ARG;
+    for (int l = 0; l < sk->n_layers; ++l)
+        if (sk->layers[l]->has_router) return MOE_ERR_UNSUPPORTED;
     moe_layer *ly = sk->first;
     const cudaError_t e =
         use_mma(ly, T) ? launch_decode_mma_stack(ly->L, ly->ws, sk->n_layers, eps, (const uint16_t *)x, (uint16_t *)out,
