@@ -392,52 +392,56 @@ _SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 _GROUP_RULE = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
 
 
-def _tensor(name, t, dtype, shape, device, contiguous=True):
-    """Checks one tensor argument (None passes): type, shape, device, and rows whose
-    elements are adjacent (contiguous=False) or the whole tensor contiguous."""
+# The current stream's handle without the Stream object around it: these calls take a few microseconds on the GPU, and
+# the object costs about three on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _tensor(name, t, dtype, shape, index, contiguous=True):
+    """Checks one tensor argument (None passes): type, shape, device, and the whole tensor contiguous unless its rows
+    are looked at by _row_stride."""
     if t is None:
         return
-    if t.dtype is not dtype and t.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the first argument on {device}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    else:
-        _row_stride(name, t)
+    if t.dtype != dtype or t.shape != shape or t.get_device() != index or (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{name}: a {'contiguous ' if contiguous else ''}{dtype} tensor of shape {tuple(shape)} on "
+                         f"cuda:{index} expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _row_stride(name, t):
-    """Elements from one row of a 2-D tensor to the next (rows contiguous, not overlapping)."""
+    """Elements from one row of a 2-D tensor to the next (rows contiguous, not overlapping); 0 for None."""
+    if t is None:
+        return 0
     rows, cols = t.shape
     s0, s1 = t.stride()
     if cols > 1 and s1 != 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
     if rows <= 1:
-        return max(cols, 1)
+        return cols or 1
     if s0 < cols:
         raise ValueError(f"{name}: rows overlap")
     return s0
 
 
 def _input(name, t, types):
-    """The first argument of a call: a 2-D CUDA tensor of one of `types`."""
+    """The first argument of a call: a 2-D CUDA tensor of one of `types`. -> its device's index"""
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     if t.dtype not in types:
         raise ValueError(f"{name}: type {t.dtype} is not supported")
-    return t.device
+    return t.get_device()
 
 
-def _run(device, stream, call):
-    """call(stream handle) with `device` current; stream None: the device's current stream."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return call(_stream(stream))
-    return call(_stream(stream))
+def _run(fn, index, stream, args, what):
+    """fn(*args, stream handle) with device `index` current; stream None: that device's current stream."""
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        s = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            s = fn(*args, st)
+    if s != MOE_OK:
+        raise MoeError(s, what)
 
 
 def _route_desc(E, top_k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale):
@@ -450,6 +454,7 @@ def _route_desc(E, top_k, score, bias, n_groups, topk_groups, group_rule, renorm
                         1 if renormalise else 0, scale)
 
 
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 _ROUTE_RECORDS = ("ids", "w", "counts", "offsets", "perm", "pos")
 
 
@@ -463,36 +468,37 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
     ``MoeLayer.route``; slots without an expert left hold id -1, weight 0, pos -1. ``out``: such a dict to write to;
     counts, offsets, perm and pos may be left out of it and are then not computed.
     """
-    device = _input("logits", logits, (torch.bfloat16, torch.float16, torch.float32))
+    index = _input("logits", logits, _FLOATS)
     T, E = logits.shape
     desc = _route_desc(E, top_k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale)
-    if bias is not None and bias.device != device:
-        raise ValueError(f"bias: on {bias.device}, logits on {device}")
+    if bias is not None and bias.get_device() != index:
+        raise ValueError(f"bias: on {bias.device}, logits on {logits.device}")
     if out is None:
-        i32 = {"dtype": torch.int32, "device": device}
-        out = {"ids": torch.empty((T, top_k), **i32), "w": torch.empty((T, top_k), dtype=torch.float32, device=device),
+        i32 = {"dtype": torch.int32, "device": logits.device}
+        out = {"ids": torch.empty((T, top_k), **i32),
+               "w": torch.empty((T, top_k), dtype=torch.float32, device=logits.device),
                "counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32),
                "perm": torch.empty(T * top_k, **i32), "pos": torch.empty((T, top_k), **i32)}
+        recs = [out[n] for n in _ROUTE_RECORDS]
     else:
-        if out.get("ids") is None or out.get("w") is None:
+        recs = [out.get(n) for n in _ROUTE_RECORDS]
+        if recs[0] is None or recs[1] is None:
             raise ValueError("out must hold ids and w")
-        shapes = {"ids": (T, top_k), "w": (T, top_k), "counts": (E,), "offsets": (E + 1,), "perm": (T * top_k,),
-                  "pos": (T, top_k)}
-        for n, shape in shapes.items():
-            _tensor(n, out.get(n), torch.float32 if n == "w" else torch.int32, shape, device)
-    lib = load()
+        pairs = (T, top_k)
+        for n, t, shape in zip(_ROUTE_RECORDS, recs, (pairs, pairs, (E,), (E + 1,), (T * top_k,), pairs)):
+            _tensor(n, t, torch.float32 if n == "w" else torch.int32, shape, index)
+    lib = _lib or load()
     size = ctypes.c_size_t(0)
-    _check(lib.moe_route_logits_workspace_size(ctypes.byref(desc), T, ctypes.byref(size)), "moe_route_logits")
-    stride = _row_stride("logits", logits)
-
-    def call(st):
-        # scratch from torch's allocator on the stream the kernels run on: captured graphs and streams each get their own
+    ref = ctypes.byref(desc)
+    _check(lib.moe_route_logits_workspace_size(ref, T, ctypes.byref(size)), "moe_route_logits")
+    ws = None
+    if size.value:
+        # scratch from torch's allocator on the stream the kernels run on: every stream and captured graph has its own
         with torch.cuda.stream(stream):
-            ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=device)
-        return lib.moe_route_logits(ctypes.byref(desc), _ptr(logits), _DTYPE[logits.dtype], stride, T,
-                                    *(_ptr(out.get(n)) for n in _ROUTE_RECORDS), _ptr(ws), size.value, st)
-
-    _check(_run(device, stream, call), "moe_route_logits")
+            ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
+    _run(lib.moe_route_logits, index, stream,
+         (ref, logits.data_ptr(), _DTYPE[logits.dtype], _row_stride("logits", logits), T, *map(_ptr, recs), _ptr(ws),
+          size.value), "moe_route_logits")
     return out
 
 
@@ -505,46 +511,45 @@ def add_rmsnorm(x, res=None, gain=None, *, eps=1e-6, out_dtype=None, group=0, su
     (0: per row). -> (out, s or None without res, scales or None). ``sum_out``, ``out``, ``scales``: buffers to write
     to; sum_out and out may be x or res themselves.
     """
-    device = _input("x", x, (torch.bfloat16, torch.float16, torch.float32))
+    index = _input("x", x, _FLOATS)
     T, d = x.shape
+    dtype = x.dtype
     if out is not None:
         if out_dtype is not None and out_dtype != out.dtype:
             raise ValueError("out_dtype and out differ")
         out_dtype = out.dtype
     elif out_dtype is None:
-        out_dtype = x.dtype
-    if out_dtype not in (x.dtype, torch.float8_e4m3fn):
-        raise ValueError(f"out_dtype {out_dtype} is not supported for {x.dtype} inputs")
+        out_dtype = dtype
     e4m3 = out_dtype == torch.float8_e4m3fn
+    if not e4m3 and out_dtype != dtype:
+        raise ValueError(f"out_dtype {out_dtype} is not supported for {dtype} inputs")
     if group < 0 or (group and (not e4m3 or d % group)):
         raise ValueError("group divides d, and needs E4M3 output")
+    if out is None:
+        out = torch.empty((T, d), dtype=out_dtype, device=x.device)
     if e4m3:
         cols = d // (group or d) if d else 0
         if scales is None:
-            scales = torch.empty((T, cols), dtype=torch.float32, device=device)
+            scales = torch.empty((T, cols), dtype=torch.float32, device=x.device)
+        _tensor("scales", scales, torch.float32, (T, cols), index, False)
     elif scales is not None:
         raise ValueError("scales need E4M3 output")
-    if out is None:
-        out = torch.empty((T, d), dtype=out_dtype, device=device)
     if sum_out is None and res is not None:
-        sum_out = torch.empty((T, d), dtype=x.dtype, device=device)
-    _tensor("res", res, x.dtype, x.shape, device, False)
-    _tensor("gain", gain, x.dtype, (d,), device)
-    _tensor("sum_out", sum_out, x.dtype, x.shape, device, False)
-    _tensor("out", out, out_dtype, x.shape, device, False)
-    if e4m3:
-        _tensor("scales", scales, torch.float32, (T, cols), device, False)
-    args = MoeNormArgs(_ptr(x), _ptr(res), _ptr(gain), _ptr(sum_out), _ptr(out), _ptr(scales),
-                       _row_stride("x", x), _row_stride("res", res) if res is not None else 0,
-                       _row_stride("sum_out", sum_out) if sum_out is not None else 0, _row_stride("out", out),
-                       _row_stride("scales", scales) if e4m3 else 0, T, d, group, _DTYPE[x.dtype],
+        sum_out = torch.empty((T, d), dtype=dtype, device=x.device)
+    _tensor("res", res, dtype, x.shape, index, False)
+    _tensor("gain", gain, dtype, (d,), index)
+    _tensor("sum_out", sum_out, dtype, x.shape, index, False)
+    _tensor("out", out, out_dtype, x.shape, index, False)
+    args = MoeNormArgs(x.data_ptr(), _ptr(res), _ptr(gain), _ptr(sum_out), out.data_ptr(), _ptr(scales),
+                       _row_stride("x", x), _row_stride("res", res), _row_stride("sum_out", sum_out),
+                       _row_stride("out", out), _row_stride("scales", scales), T, d, group, _DTYPE[dtype],
                        _DTYPE[out_dtype], eps)
-    _check(_run(device, stream, lambda st: load().moe_add_rmsnorm(ctypes.byref(args), st)), "moe_add_rmsnorm")
+    _run((_lib or load()).moe_add_rmsnorm, index, stream, (ctypes.byref(args),), "moe_add_rmsnorm")
     return out, sum_out, scales
 
 
 def _linear_w4(fmt, x, q, s, g, z, x_scales, bias, out, out_dtype, stream):
-    device = _input("x", x, (torch.bfloat16, torch.float16, torch.float8_e4m3fn))
+    index = _input("x", x, (torch.bfloat16, torch.float16, torch.float8_e4m3fn))
     M, K = x.shape
     if q.dim() != 2 or s.dim() != 2:
         raise ValueError("q and s must be 2-D")
@@ -557,32 +562,33 @@ def _linear_w4(fmt, x, q, s, g, z, x_scales, bias, out, out_dtype, stream):
             raise ValueError(f"s: type {s_type} is not supported")
     if group < 1 or K % group:
         raise ValueError("s: one scale per group of columns expected")
-    _tensor("q", q, torch.uint8, (N, K // 2), device)
-    _tensor("s", s, s_type, (N, K // group), device)
-    _tensor("g", g, torch.float32, (1,), device)
-    _tensor("zeros", z, torch.uint8, (N, K // group), device)
-    _tensor("bias", bias, torch.float32, (N,), device)
+    _tensor("q", q, torch.uint8, (N, K // 2), index)
+    _tensor("s", s, s_type, (N, K // group), index)
+    _tensor("g", g, torch.float32, (1,), index)
+    _tensor("zeros", z, torch.uint8, (N, K // group), index)
+    _tensor("bias", bias, torch.float32, (N,), index)
     x_group = 0
     if x.dtype == torch.float8_e4m3fn:
         if x_scales is None or x_scales.dim() != 2 or not x_scales.shape[1] or K % x_scales.shape[1]:
             raise ValueError("E4M3 x needs x_scales [M, groups]")
-        x_group = K // x_scales.shape[1] if x_scales.shape[1] > 1 else 0
-        _tensor("x_scales", x_scales, torch.float32, (M, x_scales.shape[1]), device, False)
+        cols = x_scales.shape[1]
+        x_group = K // cols if cols > 1 else 0
+        _tensor("x_scales", x_scales, torch.float32, (M, cols), index, False)
     elif x_scales is not None:
         raise ValueError("x_scales belong to E4M3 x")
     if out is None:
         out_dtype = out_dtype or (torch.bfloat16 if x.dtype == torch.float8_e4m3fn else x.dtype)
-        out = torch.empty((M, N), dtype=out_dtype, device=device)
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
     elif out_dtype is not None and out_dtype != out.dtype:
         raise ValueError("out_dtype and out differ")
-    if out.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+    if out.dtype not in _FLOATS:
         raise ValueError(f"out: type {out.dtype} is not supported")
-    _tensor("out", out, out.dtype, (M, N), device, False)
-    args = MoeW4Args(fmt, M, N, K, group, _ptr(q), _ptr(s), _DTYPE.get(s_type, 0), _ptr(g), _ptr(z), _ptr(x),
-                     _DTYPE[x.dtype], _row_stride("x", x), _ptr(x_scales),
-                     _row_stride("x_scales", x_scales) if x_scales is not None else 0, x_group, _ptr(bias), _ptr(out),
-                     _DTYPE[out.dtype], _row_stride("out", out))
-    _check(_run(device, stream, lambda st: load().moe_linear_w4(ctypes.byref(args), st)), "moe_linear_w4")
+    _tensor("out", out, out.dtype, (M, N), index, False)
+    args = MoeW4Args(fmt, M, N, K, group, q.data_ptr(), s.data_ptr(), _DTYPE.get(s_type, 0), _ptr(g), _ptr(z),
+                     x.data_ptr(), _DTYPE[x.dtype], _row_stride("x", x), _ptr(x_scales),
+                     _row_stride("x_scales", x_scales), x_group, _ptr(bias), out.data_ptr(), _DTYPE[out.dtype],
+                     _row_stride("out", out))
+    _run((_lib or load()).moe_linear_w4, index, stream, (ctypes.byref(args),), "moe_linear_w4")
     return out
 
 

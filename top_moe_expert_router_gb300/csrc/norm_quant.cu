@@ -2,7 +2,7 @@
 // or 32 bits or in E4M3 with a scale per group of columns:
 //   s = round(x + res)            (to the inputs' type; stored if asked for)
 //   y = s / sqrt(mean(s^2) + eps) * gain
-//   scale = max|y| over the group / 448 (1 for a group of zeros), q = E4M3(y / scale)
+//   scale = max|y| over the group / 448 (1 for a group of zeros), q = E4M3(y * (1 / scale))
 // The norm is of the rounded sum, so that the result is the same as that of
 // the addition and the norm called one after the other. Everything between
 // the loads and the one rounding at the end is in fp32, the row held in
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(Norm
                 const float scale = group_scale(row_amax);
                 if (tid == 0 && v == 0) sc[0] = scale;
 #pragma unroll
-                for (int i = 0; i < V; ++i) inv[i] = scale;
+                for (int i = 0; i < V; ++i) inv[i] = 1.f / scale;
             } else if (in_warp) {
                 float m8 = 0.f;
 #pragma unroll
@@ -238,25 +238,26 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(Norm
                 const float scale = group_scale(m8);
                 if (c < d && (tid & (lanes - 1)) == 0) sc[c / group] = scale;
 #pragma unroll
-                for (int i = 0; i < V; ++i) inv[i] = scale;
+                for (int i = 0; i < V; ++i) inv[i] = 1.f / scale;
             } else if (c < d) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    inv[i] = group_scale(__uint_as_float(am[(c + i) / group]));
-                    if ((c + i) % group == 0) sc[(c + i) / group] = inv[i];
+                    const float scale = group_scale(__uint_as_float(am[(c + i) / group]));
+                    if ((c + i) % group == 0) sc[(c + i) / group] = scale;
+                    inv[i] = 1.f / scale;
                 }
             }
             if (c < d) {
                 if constexpr (V == 1) {
-                    o[c] = (uint8_t)__nv_cvt_float_to_fp8(s[v][0] / inv[0], __NV_SATFINITE, __NV_E4M3);
+                    o[c] = (uint8_t)__nv_cvt_float_to_fp8(s[v][0] * inv[0], __NV_SATFINITE, __NV_E4M3);
                 } else {
                     uint32_t pk[V / 4];
 #pragma unroll
                     for (int i = 0; i < V; i += 4) {
                         const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                            make_float2(s[v][i] / inv[i], s[v][i + 1] / inv[i + 1]), __NV_SATFINITE, __NV_E4M3);
+                            make_float2(s[v][i] * inv[i], s[v][i + 1] * inv[i + 1]), __NV_SATFINITE, __NV_E4M3);
                         const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                            make_float2(s[v][i + 2] / inv[i + 2], s[v][i + 3] / inv[i + 3]), __NV_SATFINITE, __NV_E4M3);
+                            make_float2(s[v][i + 2] * inv[i + 2], s[v][i + 3] * inv[i + 3]), __NV_SATFINITE, __NV_E4M3);
                         pk[i / 4] = lo | (hi << 16);
                     }
                     if constexpr (V == 8) *reinterpret_cast<uint2 *>(o + c) = make_uint2(pk[0], pk[1]);
