@@ -19,22 +19,38 @@
 // ones lose at most 2^-40 of it. Products and sums are fp32; an INT4 group's
 // sum is multiplied by its scale, a 128-column block's by x's, in fp32.
 //
+// Structure. A CTA takes tiles of 64 or 128 rows: TMA streams their codes through
+// X K is split over a cluster of up to 8 CTAs
+// where there are few tiles; their sums meet in distributed shared
+// memory, added in rank order. What bounds it: with the loads by TMA the
+// shared-memory pipe (per warp and 128 columns: 16 cycles of codes, 18 of
+// TMA's writes, 16 of x for 8 tokens), which is why a warp takes 32 rows: the
+// B fragments are read once for two products.
+// Measured on the way (131072 x 4096 NVFP4, 4 tokens, 45 us of stream): loads
+// into registers one block ahead 92 us (waiting for one block's load waited
+// for later ones too), two batches of four blocks in turn 70 us, a ring of
+// 16-byte asynchronous copies 88 us (the L1's tag and data cycles: 82 % busy).
+//
 // The k order inside a 128-column block is free as long as both operands use
-// the same: each lane takes L consecutive codes of its row (one 16-, 8- or
-// 4-byte load), the four lanes of a row together one group of 4 L codes, and x
-// is staged in shared memory in that order, so that a lane's B fragments for
-// two products are one conflict-free 16-byte read.
+// the same. NVFP4: lane t of a row takes the row's 32 codes from 32 t on (one
+// 16-byte read, two block scales). INT4: of each 32 codes the eight from 8 t on
+// (ldmatrix), so that a product pair lies within one group. x is staged in
+// shared memory in that order: a lane's B fragments for two products are one
+// conflict-free 16-byte read.
 #include <math.h>
 
+#include <type_traits>
+
+#include "gemm.cuh"
 #include "ops.cuh"
 
 namespace moe {
 namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kXSmem = 96 * 1024;      // staged x of one pass over K
+constexpr int kCons = 8;               // warps: 4 along a tile's rows by the 2 blocks of a stage
+constexpr int kConsThreads = 32 * kCons;
+constexpr int kThreads = kConsThreads + 32;
 
 __device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -53,258 +69,313 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
     return o;
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t o;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o) : "r"(a), "r"(b), "r"(c));
+    return o;
+}
 
 // Four f16 pairs of a word's eight codes. NVFP4: codes (0,1), (2,3), (4,5),
-// (6,7) times the block scale `m`. INT4: codes (0,4), (1,5), (2,6), (3,7)
-// minus the zero point: 0x6400 | q is 1024 + q, and `m` is 1024 + z, twice.
-template <bool NVFP4>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t m, uint32_t o[4]) {
-    if constexpr (NVFP4) {
-        e2m1x8_to_f16x2(w, o);
+// (6,7) times the block scale, `m` twice that scale in f16.
+__device__ __forceinline__ void widen_fp4(uint32_t w, uint32_t m, uint32_t o[4]) {
+    e2m1x8_to_f16x2(w, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = hmul2(o[i], m);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = hsub2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, m);
-    }
+    for (int i = 0; i < 4; ++i) o[i] = hmul2(o[i], m);
 }
 
-__device__ __forceinline__ float scale_f32(const void *s, size_t i, moe_dtype t) {
-    const uint16_t h = __ldg((const uint16_t *)s + i);
-    return t == MOE_T_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+// INT4: codes (0,4), (1,5), (2,6), (3,7) minus the zero point. 0x6400 | q is
+// 1024 + q in f16 and 0x6400 | 16 q is 1024 + 16 q: m0 = 1024 + z is subtracted
+// from the first, m1 = -(64 + z) added to a sixteenth of the second: integers
+// below 2048, all exact.
+__device__ __forceinline__ void widen_int4(uint32_t w, uint32_t m0, uint32_t m1, uint32_t o[4]) {
+    const uint32_t w8 = w >> 8;
+    o[0] = hsub2((w & 0x000F000Fu) | 0x64006400u, m0);
+    o[1] = hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, m1);
+    o[2] = hsub2((w8 & 0x000F000Fu) | 0x64006400u, m0);
+    o[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, m1);
 }
 
-// Eight elements of x as fp32.
-__device__ __forceinline__ void load_x8(const W4Args &a, int64_t i, bool vec, float f[8]) {
-    if (a.x_type == MOE_T_E4M3) {
-        const uint8_t *p = (const uint8_t *)a.x + i;
-        uint32_t u[2];
+// Eight elements of x as they are loaded (E4M3: two words).
+template <typename T>
+__device__ __forceinline__ uint4 load_x8(const T *p, bool vec) {
+    uint32_t u[4] = {0u, 0u, 0u, 0u};
+    if constexpr (sizeof(T) == 1) {
         if (vec) {
             const uint2 v = __ldg((const uint2 *)p);
-            u[0] = v.x, u[1] = v.y;
-        } else {
-            u[0] = u[1] = 0u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j >> 2] |= (uint32_t)__ldg(p + j) << (8 * (j & 3));
+            return make_uint4(v.x, v.y, 0u, 0u);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t h = e4m3x2_to_f16x2((uint16_t)(u[j >> 1] >> (16 * (j & 1))));
-            f[2 * j] = __half2float(__ushort_as_half((uint16_t)h));
-            f[2 * j + 1] = __half2float(__ushort_as_half((uint16_t)(h >> 16)));
-        }
-        return;
-    }
-    const uint16_t *p = (const uint16_t *)a.x + i;
-    uint32_t u[4];
-    if (vec) {
-        const uint4 v = __ldg((const uint4 *)p);
-        u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+        for (int j = 0; j < 8; ++j) u[j >> 2] |= (uint32_t)__ldg(p + j) << (8 * (j & 3));
     } else {
+        if (vec) return __ldg((const uint4 *)p);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = (uint32_t)__ldg(p + 2 * j) | ((uint32_t)__ldg(p + 2 * j + 1) << 16);
+        for (int j = 0; j < 8; ++j) u[j >> 1] |= (uint32_t)__ldg(p + j) << (16 * (j & 1));
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (a.x_type == MOE_T_BF16) {
-            f[2 * j] = bf16lo(u[j]);
-            f[2 * j + 1] = bf16hi(u[j]);
-        } else {
-            f[2 * j] = __half2float(__ushort_as_half((uint16_t)u[j]));
-            f[2 * j + 1] = __half2float(__ushort_as_half((uint16_t)(u[j] >> 16)));
-        }
-    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
+
+// Units of 16 bytes from one product pair's staged x to the next: 2 modulo 8,
+// so that the stores of half a warp (four product pairs, two lanes' columns a
+// quarter) fall on different banks.
+__device__ __host__ __forceinline__ int pair_stride(int mt) { return 4 * mt + ((mt & 1) ? 6 : 2); }
 
 // Stages 128-column blocks kb0 .. kb0 + nkb - 1 of tokens m0 .. m0 + mt - 1:
-// xh[((kb * 4 + sp) * mt + m) * 4 + t] holds the eight elements that lane t of
-// a row multiplies in product pair sp, xsc[kb * mt + m] the block's scale.
-template <bool NVFP4, int L>
-__device__ __forceinline__ void stage_x(const W4Args &a, uint4 *xh, float *xsc, int m0, int mt, int kb0, int nkb,
-                                        bool vec) {
-    const int units = mt * nkb * 16;             // 16 threads (half a warp) per token and block
-    for (int u = threadIdx.x; u < ((units + 31) & ~31); u += kThreads) {
-        const bool in = u < units;
-        const int j = u & 15, mb = in ? u >> 4 : 0;
-        const int kb = mb % nkb, m = mb / nkb;
-        const int k = (kb0 + kb) * 128 + 8 * j;
-        float f[8];
-        if (in && k < a.K) {
-            load_x8(a, (int64_t)(m0 + m) * a.x_ld + k, vec, f);
-        } else {
+// xh[(kb * 4 + sp) * pair_stride + m * 4 + t] holds the eight elements that lane
+// t of a row multiplies in product pair sp, xsc[kb * mt + m] the block's scale.
+// Half a warp per token and block; the loads of U come first.
+template <bool NVFP4, moe_dtype XT>
+__device__ __forceinline__ void stage_x_type(const W4Args &a, uint4 *xh, float *xsc, int m0, int mt, int kb0, int nkb,
+                                             bool vec) {
+    constexpr int U = XT == MOE_T_BF16 ? 4 : 8, slots = kConsThreads / 16, L = NVFP4 ? 32 : 8;
+    using T = typename std::conditional<XT == MOE_T_E4M3, uint8_t, uint16_t>::type;
+    const int j = threadIdx.x & 15, n = mt * nkb, ps = pair_stride(mt);
+    const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+    const int gi = j / (L / 2), t = (j % (L / 2)) / (L / 8), sp = gi * (L / 8) + j % (L / 8);
+    const int dm = slots / nkb, dk = slots % nkb;
+    int m = (threadIdx.x >> 4) / nkb, kb = (threadIdx.x >> 4) % nkb;
+    const T *p = (const T *)a.x + (int64_t)(m0 + m) * a.x_ld + (kb0 + kb) * 128 + 8 * j;
+    const int64_t dp = (int64_t)dm * a.x_ld + dk * 128, wrap = a.x_ld - (int64_t)nkb * 128;
+    const int kmax = (a.K - 8 * j + 127) / 128 - kb0;  // this thread's columns of block kb exist below kmax
+    for (int i0 = threadIdx.x >> 4; i0 < n; i0 += U * slots) {
+        uint4 raw[U];
+        float sc[U];
+        int ms[U], ks[U];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = 0.f;
+        for (int u = 0; u < U; ++u) {
+            ms[u] = m;
+            ks[u] = kb;
+            const bool in = i0 + u * slots < n && kb < kmax;
+            raw[u] = in ? load_x8(p, vec) : make_uint4(0u, 0u, 0u, 0u);
+            sc[u] = 1.f;
+            if (XT == MOE_T_E4M3 && j == 0 && in) {
+                const int gb = kb0 + kb;
+                sc[u] = __ldg(a.xs + (int64_t)(m0 + m) * a.xs_ld + (a.xgroup == 128 ? gb : gb * 128 / a.xgroup));
+            }
+            m += dm;
+            kb += dk;
+            p += dp;
+            if (kb >= nkb) {
+                kb -= nkb;
+                ++m;
+                p += wrap;
+            }
         }
-        float inv = 1.f;
-        if (a.x_type == MOE_T_BF16) {
-            float big = 0.f;                     // largest finite magnitude of the block
 #pragma unroll
-            for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(f[i]) < INFINITY ? fabsf(f[i]) : 0.f);
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * slots >= n) break;
+            uint32_t h[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+            if constexpr (XT == MOE_T_E4M3) {
+                const uint32_t lo = h[0], hi = h[1];
+                h[0] = e4m3x2_to_f16x2((uint16_t)lo);
+                h[1] = e4m3x2_to_f16x2((uint16_t)(lo >> 16));
+                h[2] = e4m3x2_to_f16x2((uint16_t)hi);
+                h[3] = e4m3x2_to_f16x2((uint16_t)(hi >> 16));
+            }
+            if constexpr (XT == MOE_T_BF16) {
+                // the block's largest magnitude, as bf16 bits
+                uint32_t b2 = 0u;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-            const uint32_t e = max(__float_as_uint(big) >> 23, 15u);
-            const float mul = big > 0.f ? __uint_as_float((268u - e) << 23) : 1.f;  // 2^(14 - exponent)
-            inv = big > 0.f ? __uint_as_float((e - 14u) << 23) : 1.f;
+                for (int i = 0; i < 4; ++i) b2 = __vmaxu2(b2, h[i] & 0x7FFF7FFFu);
+                uint32_t big = max(b2 & 0xFFFFu, b2 >> 16);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= mul;
-        } else if (a.x_type == MOE_T_E4M3) {
-            if (in && k < a.K) inv = __ldg(a.xs + (int64_t)(m0 + m) * a.xs_ld + k / a.xgroup);
-        }
-        if (!in) continue;
-        uint32_t h[4];
+                for (int o = 8; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(half, big, o));
+                if (big >= 0x7F80u) {            // infinities or NaN in the block: the largest finite one
+                    big = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t e = (h[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+                        big = max(big, e < 0x7F80u ? e : 0u);
+                    }
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(half, big, o));
+                }
+                const uint32_t e = max(big >> 7, 15u);
+                const float mul = big ? __uint_as_float((268u - e) << 23) : 1.f;  // 2^(14 - exponent)
+                sc[u] = big ? __uint_as_float((e - 14u) << 23) : 1.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 v = __floats2half2_rn(bf16lo(h[i]) * mul, bf16hi(h[i]) * mul);
+                    h[i] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+            }
             // NVFP4: in order; INT4: the pairs (i, i + 4)
-            const __half2 v = NVFP4 ? __floats2half2_rn(f[2 * i], f[2 * i + 1]) : __floats2half2_rn(f[i], f[i + 4]);
-            h[i] = *reinterpret_cast<const uint32_t *>(&v);
+            uint4 o = make_uint4(h[0], h[1], h[2], h[3]);
+            if constexpr (!NVFP4)
+                o = make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
+                               __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632));
+            xh[(ks[u] * 4 + sp) * ps + ms[u] * 4 + t] = o;
+            if (j == 0) xsc[ks[u] * mt + ms[u]] = sc[u];
         }
-        const int gi = j / (L / 2), t = (j % (L / 2)) / (L / 8), sp = gi * (L / 8) + j % (L / 8);
-        xh[((size_t)(kb * 4 + sp) * mt + m) * 4 + t] = make_uint4(h[0], h[1], h[2], h[3]);
-        if (j == 0) xsc[kb * mt + m] = inv;
     }
 }
 
-// CTA: wr warps along the rows (16 each) by kWarps / wr along K; up to 8 NT tokens.
-template <int NT, bool NVFP4, int L>
-__global__ void __launch_bounds__(kThreads) linear_w4_kernel(W4Args a, int wr, int kb_pass, int vec) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int wk = kWarps / wr, rw = warp % wr, kw = warp / wr;
-    const int m0 = blockIdx.y * 8 * NT, mt = min(8 * NT, a.M - m0);
-    const int row0 = blockIdx.x * 16 * wr;
-    const int r_lo = min(row0 + rw * 16 + g, a.N - 1), r_hi = min(row0 + rw * 16 + g + 8, a.N - 1);
-    const int nkb = (a.K + 127) / 128;
-    uint4 *xh = reinterpret_cast<uint4 *>(smem);
-    float *xsc = reinterpret_cast<float *>(smem + (size_t)kb_pass * mt * 256);
-    const uint8_t *q_lo = a.q + (size_t)r_lo * (a.K / 2), *q_hi = a.q + (size_t)r_hi * (a.K / 2);
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+template <bool NVFP4>
+__device__ __forceinline__ void stage_x(const W4Args &a, uint4 *xh, float *xsc, int m0, int mt, int kb0, int nkb,
+                                        bool vec) {
+    if (a.x_type == MOE_T_BF16) stage_x_type<NVFP4, MOE_T_BF16>(a, xh, xsc, m0, mt, kb0, nkb, vec);
+    else if (a.x_type == MOE_T_F16) stage_x_type<NVFP4, MOE_T_F16>(a, xh, xsc, m0, mt, kb0, nkb, vec);
+    else stage_x_type<NVFP4, MOE_T_E4M3>(a, xh, xsc, m0, mt, kb0, nkb, vec);
+}
 
-    for (int p0 = 0; p0 < nkb; p0 += kb_pass) {
-        const int np = min(kb_pass, nkb - p0);
-        if (p0 > 0) __syncthreads();
-        stage_x<NVFP4, L>(a, xh, xsc, m0, mt, p0, np, vec != 0);
-        __syncthreads();
-        for (int kb = kw; kb < np; kb += wk) {
-            const int k0 = (p0 + kb) * 128;
-            uint32_t w[2][4];
-            uint32_t mul[2][4];                  // per product pair: NVFP4 block scale, INT4 1024 + zero point
-            float sc[2][4];                      // INT4: the group's scale
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ldmatrix4(uint32_t a) {
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// A tile has 64 MT rows, 16 MT per warp. A ring stage: two 128-column blocks
+// of the tile's codes, [block][row][64 B] (INT4: with TMA's 64-byte swizzle),
+// and with TS NVFP4's scales, [row][16 B].
+template <int MT>
+constexpr int kRows = 64 * MT;
+template <int MT>
+constexpr int kCodes = 2 * kRows<MT> * 64;
+template <int MT, bool TS>
+constexpr int kStage = kCodes<MT> + (TS ? kRows<MT> * 16 : 0);
+
+// A lane's scales of its warp's block where they do not come with the stage:
+// rows 8 j + g of the warp's 16 MT. NVFP4: v[j], the two block scales. INT4:
+// scale | zero point << 16 of the block's 128 / G groups, spread over the four
+// lanes of a row: item 4 j' + t of the warp's 2 MT rows by 128 / G groups.
+template <int MT, bool NVFP4, int G>
+struct Scales {
+    static constexpr int per_row = NVFP4 ? 4 : 128 / G;
+    static constexpr int NV = (2 * MT * per_row + 3) / 4;
+    uint32_t v[NV];
+};
+
+template <int MT, bool NVFP4, int G>
+__device__ __forceinline__ void load_scales(const W4Args &a, int row, int kb, int lane, Scales<MT, NVFP4, G> &s) {
+    using S = Scales<MT, NVFP4, G>;
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint8_t *q = h ? q_hi : q_lo;
-                const int r = h ? r_hi : r_lo;
-                if constexpr (L == 32) {
-                    const int k = k0 + 32 * t;
-                    const uint4 v = k < a.K ? __ldg((const uint4 *)(q + k / 2)) : make_uint4(0, 0, 0, 0);
-                    w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
-                } else if constexpr (L == 16) {
+    for (int j = 0; j < S::NV; ++j) {
+        // rows past N and columns past K: others of the array, for products that are zero or not stored
+        const int item = 4 * j + t, jj = NVFP4 ? j : item / S::per_row;
+        const size_t r = min(row + 8 * jj + g, a.N - 1);
+        if constexpr (NVFP4) {
+            const int k = min(128 * kb + 32 * t, a.K - 32);
+            s.v[j] = __ldg((const uint16_t *)((const uint8_t *)a.s + r * (a.K / 16) + (k >> 4)));
+        } else {
+            const int ng = a.K / G, gi = min(kb * S::per_row + item % S::per_row, ng - 1);
+            s.v[j] = __ldg((const uint16_t *)a.s + r * ng + gi) | (a.z ? (uint32_t)__ldg(a.z + r * ng + gi) : 8u) << 16;
+        }
+    }
+}
+
+__device__ __forceinline__ float s_value(uint32_t h, moe_dtype t) {
+    return t == MOE_T_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
+}
+
+// acc += a warp's 16 MT rows by block b of a stage. xb, xs: the block's staged
+// x and its scales (16-byte units; product pair sp of token n at sp * ps + tok[n]).
+template <int NT, int MT, bool NVFP4, int G, bool TS>
+__device__ __forceinline__ void mul_block(const W4Args &a, uint32_t stage, int b, int wrow, int lane,
+                                          const Scales<MT, NVFP4, G> &sc, const uint4 *xb, const float *xs, int ps,
+                                          const int (&tok)[NT], const int (&col)[NT][2], float (&acc)[MT][NT][4]) {
+    using S = Scales<MT, NVFP4, G>;
+    const int g = lane >> 2, t = lane & 3;
+    float x0[NT], x1[NT];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = k0 + 64 * i + 16 * t;
-                        const uint2 v = k < a.K ? __ldg((const uint2 *)(q + k / 2)) : make_uint2(0, 0);
-                        w[h][2 * i] = v.x, w[h][2 * i + 1] = v.y;
-                    }
-                } else {
+    for (int n = 0; n < NT; ++n) {
+        x0[n] = xs[col[n][0]];
+        x1[n] = xs[col[n][1]];
+    }
+    uint32_t w[2 * MT][4];
+    uint32_t s2[2 * MT];                         // NVFP4: the lane's two block scales of each row, in f16
+    const uint32_t base = stage + b * (kRows<MT> * 64) + wrow * 64;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = k0 + 32 * i + 8 * t;
-                        w[h][i] = k < a.K ? __ldg((const uint32_t *)(q + k / 2)) : 0u;
-                    }
-                }
-                if constexpr (NVFP4) {
-                    const int k = k0 + 32 * t;
-                    const uint32_t s2 =
-                        k < a.K ? e4m3x2_to_f16x2(__ldg((const uint16_t *)((const uint8_t *)a.s + (size_t)r * (a.K / 16) + k / 16)))
-                                : 0u;
-                    mul[h][0] = mul[h][1] = (s2 & 0xFFFFu) * 0x10001u;
-                    mul[h][2] = mul[h][3] = (s2 >> 16) * 0x10001u;
-                } else {
-                    constexpr int per = L / 8;   // product pairs per group
+    for (int j = 0; j < 2 * MT; ++j) {
+        uint4 v;
+        if constexpr (NVFP4) {
+            v = lds128(base + (8 * j + g) * 64 + 16 * t);
+            const uint32_t u = TS ? lds16(stage + kCodes<MT> + (wrow + 8 * j + g) * 16 + 8 * b + 2 * t) : sc.v[j];
+            s2[j] = e4m3x2_to_f16x2((uint16_t)u);
+        } else {
+            // matrix i: 16-byte chunk i of eight rows, lane l naming row l & 7 of matrix l >> 3
+            const int r = 8 * j + (lane & 7);
+            v = ldmatrix4(base + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4));
+        }
+        w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+    }
+    constexpr int per = NVFP4 ? 4 : G / 32;      // product pairs of one partial sum
 #pragma unroll
-                    for (int i = 0; i < 4; i += per) {
-                        const int k = k0 + i * 32;
-                        const size_t at = (size_t)r * (a.K / (4 * L)) + k / (4 * L);
-                        const float s = k < a.K ? scale_f32(a.s, at, a.s_type) : 0.f;
-                        const uint32_t z = a.z && k < a.K ? __ldg(a.z + at) : 8u;
-                        // 1024 + z, exact in f16 for any byte
+    for (int gi = 0; gi < 4 / per; ++gi) {
+        float sf[2 * MT];
+        uint32_t z0[2 * MT], z1[2 * MT];
+        if constexpr (!NVFP4) {
 #pragma unroll
-                        for (int jj = 0; jj < per; ++jj) {
-                            sc[h][i + jj] = s;
-                            mul[h][i + jj] = (0x6400u + z) * 0x10001u;
-                        }
-                    }
-                }
+            for (int j = 0; j < 2 * MT; ++j) {
+                const int item = j * S::per_row + gi;
+                const uint32_t u = __shfl_sync(kFull, sc.v[item / 4], (lane & ~3) | (item & 3));
+                sf[j] = s_value(u & 0xFFFFu, a.s_type);
+                z0[j] = (0x6400u + (u >> 16)) * 0x10001u;
+                const __half2 zh = __half2half2(__int2half_rn(-64 - (int)(u >> 16)));
+                z1[j] = *reinterpret_cast<const uint32_t *>(&zh);
             }
-            float blk[NT][4];
+        }
+        float part[MT][NT][4];
+#pragma unroll
+        for (int h = 0; h < MT; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) blk[n][i] = 0.f;
-            float grp[NT][4];
+                for (int e = 0; e < 4; ++e) part[h][n][e] = 0.f;
 #pragma unroll
-            for (int sp = 0; sp < 4; ++sp) {
-                uint32_t lo[4], hi[4];
-                widen<NVFP4>(w[0][sp], mul[0][sp], lo);
-                widen<NVFP4>(w[1][sp], mul[1][sp], hi);
-                constexpr int per = L / 8;
+        for (int sp = gi * per; sp < (gi + 1) * per; ++sp) {
+            uint32_t f[2 * MT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    uint4 b = make_uint4(0, 0, 0, 0);
-                    const int m = n * 8 + g;
-                    if (m < mt) b = xh[((size_t)(kb * 4 + sp) * mt + m) * 4 + t];
-                    if constexpr (NVFP4) {
-                        mma16816(blk[n], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                        mma16816(blk[n], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-                    } else {
-                        if (sp % per == 0) grp[n][0] = grp[n][1] = grp[n][2] = grp[n][3] = 0.f;
-                        mma16816(grp[n], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                        mma16816(grp[n], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-                        if (sp % per == per - 1) {
-                            blk[n][0] = fmaf(grp[n][0], sc[0][sp], blk[n][0]);
-                            blk[n][1] = fmaf(grp[n][1], sc[0][sp], blk[n][1]);
-                            blk[n][2] = fmaf(grp[n][2], sc[1][sp], blk[n][2]);
-                            blk[n][3] = fmaf(grp[n][3], sc[1][sp], blk[n][3]);
-                        }
-                    }
-                }
+            for (int j = 0; j < 2 * MT; ++j) {
+                // NVFP4: codes 0..15 of the lane are its first block of 16, 16..31 the second
+                if constexpr (NVFP4) widen_fp4(w[j][sp], __byte_perm(s2[j], 0, sp < 2 ? 0x1010 : 0x3232), f[j]);
+                else widen_int4(w[j][sp], z0[j], z1[j], f[j]);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int m = n * 8 + 2 * t;
-                const float x0 = m < mt ? xsc[kb * mt + m] : 0.f, x1 = m + 1 < mt ? xsc[kb * mt + m + 1] : 0.f;
-                acc[n][0] = fmaf(blk[n][0], x0, acc[n][0]);
-                acc[n][1] = fmaf(blk[n][1], x1, acc[n][1]);
-                acc[n][2] = fmaf(blk[n][2], x0, acc[n][2]);
-                acc[n][3] = fmaf(blk[n][3], x1, acc[n][3]);
+                const uint4 x = xb[sp * ps + tok[n]];
+#pragma unroll
+                for (int h = 0; h < MT; ++h) {
+                    mma16816(part[h][n], f[2 * h][0], f[2 * h + 1][0], f[2 * h][1], f[2 * h + 1][1], x.x, x.y);
+                    mma16816(part[h][n], f[2 * h][2], f[2 * h + 1][2], f[2 * h][3], f[2 * h + 1][3], x.z, x.w);
+                }
             }
         }
-    }
-    // the K-warps' sums, added in their order; then the tensor scale and the bias
-    __syncthreads();
-    const int rows = 16 * wr;
-    constexpr int MP = 8 * NT + 1;               // odd: rows fall on different banks
-    float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float *r = red + ((size_t)kw * rows + rw * 16 + g) * MP + n * 8 + 2 * t;
-        r[0] = acc[n][0];
-        r[1] = acc[n][1];
-        r[8 * MP] = acc[n][2];
-        r[8 * MP + 1] = acc[n][3];
+        for (int h = 0; h < MT; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[h][n][0] = fmaf(part[h][n][0], NVFP4 ? x0[n] : sf[2 * h] * x0[n], acc[h][n][0]);
+                acc[h][n][1] = fmaf(part[h][n][1], NVFP4 ? x1[n] : sf[2 * h] * x1[n], acc[h][n][1]);
+                acc[h][n][2] = fmaf(part[h][n][2], NVFP4 ? x0[n] : sf[2 * h + 1] * x0[n], acc[h][n][2]);
+                acc[h][n][3] = fmaf(part[h][n][3], NVFP4 ? x1[n] : sf[2 * h + 1] * x1[n], acc[h][n][3]);
+            }
     }
-    __syncthreads();
-    const float gs = NVFP4 ? __ldg(a.g) : 1.f;
-    for (int i = tid; i < rows * mt; i += kThreads) {
-        const int r = i % rows, m = i / rows, n = row0 + r;
-        if (n >= a.N) continue;
+}
+
+// y of a tile's rows that this part owns, from the sums of all parts.
+__device__ __forceinline__ void store_tile(const W4Args &a, const float *sums, int parts, int own, int part, int mp, int m0,
+                                        int mt, int row0, int rows, float gs, bool failed) {
+    const int first = part * own, n_own = min(own, rows - first);
+    for (int e = threadIdx.x; e < own * mt; e += kConsThreads) {
+        const int m = e / own, r = e - m * own, n = row0 + first + r;
+        if (r >= n_own || n >= a.N) continue;
+        const float *at = sums + r * mp + m;
         float v = 0.f;
-        for (int k = 0; k < wk; ++k) v += red[((size_t)k * rows + r) * MP + m];
-        v *= gs;
+        for (int p = 0; p < parts; ++p) v += at[2 * p * own * mp] + at[(2 * p + 1) * own * mp];
+        v = failed ? NAN : v * gs;
         if (a.bias) v += __ldg(a.bias + n);
         const int64_t o = (int64_t)(m0 + m) * a.y_ld + n;
         if (a.y_type == MOE_T_F32) ((float *)a.y)[o] = v;
@@ -313,32 +384,262 @@ __global__ void __launch_bounds__(kThreads) linear_w4_kernel(W4Args a, int wr, i
     }
 }
 
-template <int NT, bool NVFP4, int L>
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// mbarrier wait that gives up after kWaitLimitNs (or once another warp has)
+// and says so in *bad; the outputs are then NaN.
+__device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, volatile int *bad) {
+    if (mbar_try_wait(bar, parity)) return;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
+        if ((it & 255u) == 0 && (*bad || global_ns() - t0 > kWaitLimitNs)) {
+            *bad = 1;
+            return;
+        }
+}
+
+struct Shape {
+    int parts;      // CTAs of a cluster, along K
+    int st_pass;    // stages whose x is staged at a time
+    int ring;       // stages in flight
+    int bars;       // offset of the barriers in shared memory
+    int vec;
+};
+
+// blockIdx.x: the part of K; .y: the first row tile (then every gridDim.y-th);
+// .z: the token block. x is staged once where the CTA's part of it fits.
+template <int NT, int MT, bool NVFP4, int G, bool TS>
+__global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_constant__ CUtensorMap tq,
+                                                                const __grid_constant__ CUtensorMap ts, const W4Args a,
+                                                                const Shape sh) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    constexpr int MP = 8 * NT + 1;               // odd: rows fall on different banks
+    constexpr int kR = kRows<MT>, kSt = kStage<MT, TS>;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int m0 = blockIdx.z * 8 * NT, mt = min(8 * NT, a.M - m0);
+    const int tiles = (a.N + kR - 1) / kR, parts = sh.parts, part = blockIdx.x;
+    const int nst = (a.K + 255) / 256;
+    const int s0 = (int)((int64_t)part * nst / parts), s1 = (int)((int64_t)(part + 1) * nst / parts);
+    const int R = sh.ring, ps = pair_stride(mt), own = (kR + parts - 1) / parts;
+    // ring | two buffers of the tile's sums | x | x's scales | barriers
+    float *red = reinterpret_cast<float *>(smem + (size_t)R * kSt);
+    uint4 *xh = reinterpret_cast<uint4 *>(red + (parts * 4 * own * MP + 3) / 4 * 4);
+    float *xsc = reinterpret_cast<float *>(xh + (size_t)sh.st_pass * 8 * ps);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + sh.bars);
+    uint64_t *empty = full + 8;
+    volatile int *bad = reinterpret_cast<volatile int *>(empty + 8);
+    if (tid == 0) {
+        for (int i = 0; i < R; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kCons);
+        }
+        *bad = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+
+    if (warp == kCons) {
+        // producer: every tile's stages in order; the cluster barrier of a
+        // tile is passed before the next one is arrived at
+        int i = 0;
+        for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+            if (lane == 0)
+                for (int st = s0; st < s1; ++st, ++i) {
+                    const int slot = i % R;
+                    if (i >= R) wait_full(&empty[slot], ((i / R) - 1) & 1, bad);
+                    if (*bad) break;
+                    unsigned char *dst = smem + (size_t)slot * kSt;
+                    mbar_arrive_expect_tx(&full[slot], TS ? kSt : kCodes<MT>);
+                    tma_load_2d(dst, &tq, st * 128, tile * kR, &full[slot]);
+                    tma_load_2d(dst + kR * 64, &tq, st * 128 + 64, tile * kR, &full[slot]);
+                    if (TS) tma_load_2d(dst + kCodes<MT>, &ts, st * 16, tile * kR, &full[slot]);
+                }
+            __syncwarp();
+            if (parts > 1) {
+                if (tile != (int)blockIdx.y) cluster_wait();
+                cluster_arrive();
+            }
+        }
+        if (parts > 1) {
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
+    }
+
+    const int g = lane >> 2, t = lane & 3, wrow = (warp & 3) * 16 * MT, b = warp >> 2;
+    // tokens past mt repeat the last one: an output column depends on its own token only
+    int tok[NT], col[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        tok[n] = min(n * 8 + g, mt - 1) * 4 + t;
+        col[n][0] = min(n * 8 + 2 * t, mt - 1);
+        col[n][1] = min(n * 8 + 2 * t + 1, mt - 1);
+    }
+    const float gs = NVFP4 ? __ldg(a.g) : 1.f;
+    Scales<MT, NVFP4, G> sc;                     // loaded by the lanes one stage ahead unless they come with it
+    if (!TS) load_scales<MT, NVFP4, G>(a, blockIdx.y * kR + wrow, 2 * s0 + b, lane, sc);
+    bool staged = false;
+    int buf = 0, i = 0;
+    for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y, buf ^= 1) {
+        float acc[MT][NT][4];
+#pragma unroll
+        for (int h = 0; h < MT; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.f;
+        for (int p0 = s0; p0 < s1; p0 += sh.st_pass) {
+            const int pe = min(p0 + sh.st_pass, s1);
+            if (!staged) {
+                named_bar(1, kConsThreads);
+                stage_x<NVFP4>(a, xh, xsc, m0, mt, 2 * p0, 2 * (pe - p0), sh.vec != 0);
+                named_bar(1, kConsThreads);
+                staged = s1 - s0 <= sh.st_pass;
+            }
+            for (int st = p0; st < pe; ++st, ++i) {
+                const int slot = i % R;
+                const Scales<MT, NVFP4, G> cur = sc;
+                if (!TS) {
+                    const bool more = st + 1 < s1;
+                    const int nt = more ? tile : tile + (int)gridDim.y;
+                    if (nt < tiles) load_scales<MT, NVFP4, G>(a, nt * kR + wrow, 2 * (more ? st + 1 : s0) + b, lane, sc);
+                }
+                wait_full(&full[slot], (i / R) & 1, bad);
+                const int xb = 2 * (st - p0) + b;
+                mul_block<NT, MT, NVFP4, G, TS>(a, smem_u32(smem + (size_t)slot * kSt), b, wrow, lane, cur,
+                                        xh + xb * 4 * ps, xsc + xb * mt, ps, tok, col, acc);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot]);
+            }
+        }
+        // The sums meet at the part that owns the row, 1 / parts of the tile's:
+        // [source part][K-warp][own row], added there in that order; then the
+        // tensor scale and the bias. The barrier also tells that every CTA is
+        // done reading the other buffer's last tile.
+        const uint32_t sums = smem_u32(red) + buf * (parts * 2 * own * MP * 4);
+#pragma unroll
+        for (int h = 0; h < MT; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int r = wrow + 16 * h + g + 4 * e, p = r / own;
+                const uint32_t at = sums + (((part * 2 + b) * own + r - p * own) * MP + 2 * t) * 4;
+                if (parts > 1) {
+                    uint32_t ra;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(at), "r"(p));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (n * 8 + 2 * t >= mt) continue;
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra + n * 32), "f"(acc[h][n][e]) : "memory");
+                        if (n * 8 + 2 * t + 1 >= mt) continue;
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra + n * 32 + 4), "f"(acc[h][n][e + 1]) : "memory");
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + n * 32), "f"(acc[h][n][e]) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + n * 32 + 4), "f"(acc[h][n][e + 1]) : "memory");
+                    }
+                }
+            }
+        if (parts > 1) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            named_bar(1, kConsThreads);
+        }
+        store_tile(a, red + buf * (parts * 2 * own * MP), parts, own, part, MP, m0, mt, tile * kR, kR, gs, *bad != 0);
+    }
+    if (parts > 1) {                             // no CTA leaves while another may still write to it
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+bool code_map(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+              bool swizzle) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, int MT, bool NVFP4, int G, bool TS>
 cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     static std::atomic<uint64_t> attr_set{0};
-    const cudaError_t e = set_smem_limit_once((const void *)linear_w4_kernel<NT, NVFP4, L>, 200 * 1024, attr_set);
+    const auto kern = linear_w4_kernel<NT, MT, NVFP4, G, TS>;
+    cudaError_t e = set_smem_limit_once((const void *)kern, 226 * 1024, attr_set);
     if (e != cudaSuccess) return e;
-    const int mt = a.M < 8 * NT ? a.M : 8 * NT;
-    const int nkb = (a.K + 127) / 128;
-    int kb_pass = kXSmem / (mt * 256);
-    if (kb_pass > nkb) kb_pass = nkb;
-    int wr = 8;
-    while (wr > 1 && (a.N + 16 * wr - 1) / (16 * wr) < 304) wr /= 2;
-    const size_t xb = (size_t)kb_pass * mt * 260;
-    const size_t rb = (size_t)kWarps * 16 * (8 * NT + 1) * 4;
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    CUtensorMap tq, ts;
+    constexpr int R = kRows<MT>;
+    if (!code_map(&tq, a.q, a.N, a.K / 2, 64, R, !NVFP4)) return cudaErrorInvalidValue;
+    Shape sh{};
+    ts = tq;
+    if (TS && !code_map(&ts, a.s, a.N, a.K / 16, 16, R, false)) return cudaErrorInvalidValue;
+    const int mt = a.M < 8 * NT ? a.M : 8 * NT, mb = (a.M + 8 * NT - 1) / (8 * NT);
+    const int nst = (a.K + 255) / 256, tiles = (a.N + R - 1) / R, slots = 2 * sms;
+    // K in 1 to 8 parts: the fewest stages that one of the 2 * sms CTAs at a
+    // time takes, a tile's start and sum counted as kTile stages
+    constexpr int kTile = 4;
+    sh.parts = 1;
+    int64_t best = INT64_MAX;
+    for (int p = 1; p <= 8 && 2 * p <= nst + 1; ++p) {
+        const int64_t per = ((int64_t)tiles * p * mb + slots - 1) / slots * ((nst + p - 1) / p + kTile);
+        if (per < best) {
+            best = per;
+            sh.parts = p;
+        }
+    }
+    // each CTA stages its part of x once and walks the row tiles
+    int gy = slots / (sh.parts * mb);
+    gy = gy < 1 ? 1 : gy > tiles ? tiles : gy;
+    const int part_st = (nst + sh.parts - 1) / sh.parts;
+    constexpr int kSt = kStage<MT, TS>, kHalf = 113 * 1024 - 1024;
+    const int kRed = (sh.parts * 4 * ((R + sh.parts - 1) / sh.parts) * (8 * NT + 1) + 3) / 4 * 16;
+    const int xst = 8 * pair_stride(mt) * 16 + 8 * mt;  // bytes of x and its scales for one stage
+    sh.st_pass = (kHalf - kRed - 2 * kSt - 256) / xst;
+    if (sh.st_pass > part_st) sh.st_pass = part_st;
+    sh.ring = (kHalf - kRed - 256 - sh.st_pass * xst) / kSt;
+    if (sh.ring > 8) sh.ring = 8;
     const int es = a.x_type == MOE_T_E4M3 ? 1 : 2;
-    const int vec = (uintptr_t)a.x % (8 * es) == 0 && (a.x_ld * es) % (8 * es) == 0;
-    const dim3 grid((a.N + 16 * wr - 1) / (16 * wr), (a.M + 8 * NT - 1) / (8 * NT));
-    linear_w4_kernel<NT, NVFP4, L><<<grid, kThreads, xb > rb ? xb : rb, st>>>(a, wr, kb_pass, vec);
-    return cudaGetLastError();
+    sh.vec = (uintptr_t)a.x % (8 * es) == 0 && (a.x_ld * es) % (8 * es) == 0;
+    sh.bars = (sh.ring * kSt + kRed + sh.st_pass * xst + 7) / 8 * 8;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sh.parts, gy, mb);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sh.bars + 16 * 8 + 8;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = sh.parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tq, ts, a, sh);
 }
 
 template <int NT>
 cudaError_t launch_fmt(const W4Args &a, cudaStream_t st) {
-    if (a.nvfp4) return launch_one<NT, true, 32>(a, st);
-    if (a.group == 128) return launch_one<NT, false, 32>(a, st);
-    if (a.group == 64) return launch_one<NT, false, 16>(a, st);
-    return launch_one<NT, false, 8>(a, st);
+    constexpr int MT = NT == 1 ? 2 : 1;  // more tokens: the sums of 32 rows would not fit in the registers
+    if (a.nvfp4) {
+        // TMA takes the scales where their rows are multiples of 16 bytes
+        if (a.K % 256 == 0 && (uintptr_t)a.s % 16 == 0) return launch_one<NT, MT, true, 16, true>(a, st);
+        return launch_one<NT, MT, true, 16, false>(a, st);
+    }
+    if (a.group == 128) return launch_one<NT, MT, false, 128, false>(a, st);
+    if (a.group == 64) return launch_one<NT, MT, false, 64, false>(a, st);
+    return launch_one<NT, MT, false, 32, false>(a, st);
 }
 
 }  // namespace
