@@ -293,7 +293,7 @@ typedef enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_F32 = 2, MOE_T_E4M3 = 3 } mo
  * the largest finite float. Where fewer than top_k experts are left the
  * remaining slots hold id -1, weight 0 and pos -1.
  * Limits: E <= 512, top_k <= 16, n_groups <= 32 and dividing E, the kept
- * groups holding at least top_k experts, T <= 524288. */
+ * groups holding at least top_k experts, T <= 262144. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rule;
 typedef struct {
@@ -306,13 +306,13 @@ typedef struct {
     float scale;
 } moe_route_desc;
 
-/* Bytes of device workspace moe_route_logits needs for T tokens. No GPU work. */
+/* Bytes of device workspace moe_route_logits needs for T tokens (0 for few). No GPU work. */
 moe_status moe_route_logits_workspace_size(const moe_route_desc *desc, int T, size_t *bytes);
 
 /* logits [T, E] in bf16, f16 or fp32, row_stride elements from row to row.
  * ids [T, top_k] and w [T, top_k] are required; counts [E], offsets [E+1],
  * perm [T*top_k] and pos [T, top_k] as in moe_route, each optional (NULL).
- * Entries of perm past offsets[E] are set to -1. The workspace (4-byte
+ * Entries of perm past offsets[E] are set to -1. The workspace (16-byte
  * aligned) may be NULL when none of the four is asked for; it needs no
  * initialisation and carries nothing from one call to the next. T = 0 only
  * zeroes counts and offsets. */

@@ -111,7 +111,10 @@ ROUTES = [
     (129, 96, 3, "bf16", dict(score="sigmoid", n_groups=32, topk_groups=7, group_rule="top2")),
     (50, 32, 4, "f32", dict(n_groups=32, topk_groups=9, group_rule="top2")),     # groups of one expert
     (1000, 256, 8, "f32", dict(score="sigmoid", bias=True, n_groups=8, topk_groups=4, group_rule="top2")),
-    (17000, 20, 3, "f32", dict(score="sigmoid", bias=True)),                     # chunks of more than 32 tokens
+    (256, 256, 8, "bf16", {}),                                                   # the most tokens of one launch
+    (257, 256, 8, "bf16", {}),
+    (8193, 96, 4, "f16", dict(n_groups=6, topk_groups=2)),                       # chunks of more than 32 tokens
+    (17000, 20, 3, "f32", dict(score="sigmoid", bias=True)),
 ]
 
 

@@ -44,7 +44,7 @@ def test_route_arguments_rejected(lib):
     d = _route_desc()
     size = ctypes.c_size_t()
 
-    def call(desc=d, logits=P, t=moe.MOE_T_F32, stride=256, T=4, ids=P, w=P, counts=P, offsets=P, perm=P, pos=P, ws=P,
+    def call(desc=d, logits=P, t=moe.MOE_T_F32, stride=256, T=4096, ids=P, w=P, counts=P, offsets=P, perm=P, pos=P, ws=P,
              n=1 << 30):
         return lib.moe_route_logits(ctypes.byref(desc) if desc else None, logits, t, stride, T, ids, w, counts,
                                     offsets, perm, pos, ws, n, None)
@@ -52,13 +52,13 @@ def test_route_arguments_rejected(lib):
     assert lib.moe_route_logits_workspace_size(None, 4, ctypes.byref(size)) == BAD
     assert lib.moe_route_logits_workspace_size(ctypes.byref(d), 4, None) == BAD
     assert lib.moe_route_logits_workspace_size(ctypes.byref(d), -1, ctypes.byref(size)) == BAD
-    assert lib.moe_route_logits_workspace_size(ctypes.byref(d), 524289, ctypes.byref(size)) == UNS
+    assert lib.moe_route_logits_workspace_size(ctypes.byref(d), 262145, ctypes.byref(size)) == UNS
     assert lib.moe_route_logits_workspace_size(ctypes.byref(d), 0, ctypes.byref(size)) == OK
-    assert lib.moe_route_logits_workspace_size(ctypes.byref(d), 4, ctypes.byref(size)) == OK and size.value >= 1024
+    assert lib.moe_route_logits_workspace_size(ctypes.byref(d), 4096, ctypes.byref(size)) == OK and size.value >= 1024
     assert call(desc=None) == BAD
     assert call(logits=None) == BAD and call(ids=None) == BAD and call(w=None) == BAD
     assert call(t=moe.MOE_T_E4M3) == UNS and call(t=9) == UNS
-    assert call(stride=255) == BAD and call(T=-1) == BAD and call(T=524289) == UNS
+    assert call(stride=255) == BAD and call(T=-1) == BAD and call(T=262145) == UNS
     assert call(logits=P + 2) == BAD and call(ids=P + 1) == BAD and call(w=P + 2) == BAD and call(perm=P + 2) == BAD
     assert call(ws=None) == BAD and call(n=16) == BAD and call(ws=P + 2) == BAD
 

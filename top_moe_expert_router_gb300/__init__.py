@@ -494,8 +494,11 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
     ws = None
     if size.value:
         # scratch from torch's allocator on the stream the kernels run on: every stream and captured graph has its own
-        with torch.cuda.stream(stream):
+        if stream is None:
             ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
     _run(lib.moe_route_logits, index, stream,
          (ref, logits.data_ptr(), _DTYPE[logits.dtype], _row_stride("logits", logits), T, *map(_ptr, recs), _ptr(ws),
           size.value), "moe_route_logits")

@@ -103,7 +103,7 @@ cudaError_t launch_layer_router(const moe_layer *ly, int T, int nsplit, cudaStre
     a.offsets = ws.offsets;
     a.perm = ws.perm;
     a.pos = ws.pos;
-    a.chunk_cnt = ws.chunk_base;
+    a.chunk_cnt = reinterpret_cast<uint16_t *>(ws.chunk_base);
     a.perm_fill = 0;                    // rows past the last pair are gathered (and never read back)
     a.uniq = ws.uniq;
     a.tile_off = ws.tile_off;

@@ -17,8 +17,9 @@ namespace moe {
 constexpr int kRouteMaxE = 512;
 constexpr int kRouteMaxK = 16;
 constexpr int kRouteMaxGroups = 32;
-constexpr int kRouteMaxT = 1 << 19;
-constexpr int kRouteMaxChunks = 512;
+constexpr int kRouteMaxT = 1 << 18;
+constexpr int kRouteMaxChunks = 256;
+constexpr int kRouteFusedChunks = 8;   // batches of up to 8 times 32 tokens run as one launch
 
 struct RouteArgs {
     const void *logits;      // [T, E], rows `stride` elements apart; nsplit slices to be summed in order
@@ -35,22 +36,26 @@ struct RouteArgs {
     int32_t *ids;            // [T, k]
     float *w;
     int32_t *counts, *offsets, *perm, *pos;  // any may be null
-    int32_t *chunk_cnt;      // [ceil(T / chunk), E] scratch
+    uint16_t *chunk_cnt;     // scratch of route_scratch_bytes, 16-byte aligned
     int chunk;               // tokens per CTA, a multiple of 32 (set by the launcher)
     int32_t perm_fill;       // written to the rows of perm past the last pair
     // of a layer's workspace (null otherwise): used experts, 128-row tile offsets and their counts
     int32_t *uniq, *tile_off, *n_uniq, *n_tiles;
+    uint32_t group_inv;      // ceil(2^22 / (E / groups)) (this and the next two set by the launcher)
+    int lanes_per_group;     // a power of two, at most 32 / groups
     bool vec;                // a lane's logits may be read as 16-byte (or smaller) vectors
 };
 
+// Tokens of a chunk of the permutation launch.
 inline int route_chunk_tokens(int T) {
     int c = 32;
     while ((T + c - 1) / c > kRouteMaxChunks) c *= 2;
     return c;
 }
+// The counts of every 32 tokens, 16 bits each, in rows of E rounded up to 8.
 inline size_t route_scratch_bytes(int T, int E) {
-    const int c = route_chunk_tokens(T);
-    return sizeof(int32_t) * (size_t)((T + c - 1) / c) * E;
+    const int rows = (T + 31) / 32;
+    return rows <= kRouteFusedChunks ? 0 : sizeof(uint16_t) * (size_t)rows * ((E + 7) & ~7);
 }
 
 // route_logits.cu; T >= 1. *launches (may be null) is advanced by the launches made.

@@ -70,8 +70,9 @@ moe_status moe_route_logits(const moe_route_desc *desc, const void *logits, moe_
     if (T < 0) return MOE_ERR_INVALID_ARG;
     if (T > kRouteMaxT) return MOE_ERR_UNSUPPORTED;
     for (const void *p : {(const void *)counts, (const void *)offsets, (const void *)perm, (const void *)pos,
-                          (const void *)ids, (const void *)w, (const void *)workspace})
+                          (const void *)ids, (const void *)w})
         if (misaligned(p, 4)) return MOE_ERR_INVALID_ARG;
+    if (misaligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) {
         if (counts && cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)desc->E, st) != cudaSuccess)
@@ -94,8 +95,9 @@ moe_status moe_route_logits(const moe_route_desc *desc, const void *logits, moe_
     a.perm = perm;
     a.pos = pos;
     if (counts || offsets || perm || pos) {
-        if (!workspace || ws_bytes < route_scratch_bytes(T, desc->E)) return MOE_ERR_INVALID_ARG;
-        a.chunk_cnt = (int32_t *)workspace;
+        const size_t need = route_scratch_bytes(T, desc->E);
+        if (need && (!workspace || ws_bytes < need)) return MOE_ERR_INVALID_ARG;
+        a.chunk_cnt = (uint16_t *)workspace;
     }
     return status_of(launch_route_logits(a, st, nullptr));
 }
