@@ -18,7 +18,7 @@ constexpr int kRouteMaxE = 512;
 constexpr int kRouteMaxK = 16;
 constexpr int kRouteMaxGroups = 32;
 constexpr int kRouteMaxT = 1 << 18;
-constexpr int kRouteMaxChunks = 256;
+constexpr int kRouteMaxChunks = 304;   // two CTAs on each of 152 SMs
 constexpr int kRouteFusedChunks = 8;   // batches of up to 8 times 32 tokens run as one launch
 
 struct RouteArgs {
@@ -37,24 +37,25 @@ struct RouteArgs {
     float *w;
     int32_t *counts, *offsets, *perm, *pos;  // any may be null
     uint16_t *chunk_cnt;     // scratch of route_scratch_bytes, 16-byte aligned
-    int chunk;               // tokens per CTA, a multiple of 32 (set by the launcher)
+    int chunk;               // tokens per CTA (set by the launcher)
     int32_t perm_fill;       // written to the rows of perm past the last pair
     // of a layer's workspace (null otherwise): used experts, 128-row tile offsets and their counts
     int32_t *uniq, *tile_off, *n_uniq, *n_tiles;
-    uint32_t group_inv;      // ceil(2^22 / (E / groups)) (this and the next two set by the launcher)
+    uint32_t group_inv;      // ceil(2^22 / (E / groups)) (this and the next four set by the launcher)
     int lanes_per_group;     // a power of two, at most 32 / groups
+    bool direct;             // the groups are whole lanes: lanes_per_group of them each
+    bool vec_bias;           // the bias may be read as 16-byte vectors
     bool vec;                // a lane's logits may be read as 16-byte (or smaller) vectors
 };
 
-// Tokens of a chunk of the permutation launch.
+// Tokens of a chunk: 32, or a multiple of 16 that makes kRouteMaxChunks of them.
 inline int route_chunk_tokens(int T) {
-    int c = 32;
-    while ((T + c - 1) / c > kRouteMaxChunks) c *= 2;
-    return c;
+    const int c = (T + kRouteMaxChunks - 1) / kRouteMaxChunks;
+    return c <= 32 ? 32 : (c + 15) / 16 * 16;
 }
-// The counts of every 32 tokens, 16 bits each, in rows of E rounded up to 8.
+// The counts of every chunk, 16 bits each, in rows of E rounded up to 8.
 inline size_t route_scratch_bytes(int T, int E) {
-    const int rows = (T + 31) / 32;
+    const int c = route_chunk_tokens(T), rows = (T + c - 1) / c;
     return rows <= kRouteFusedChunks ? 0 : sizeof(uint16_t) * (size_t)rows * ((E + 7) & ~7);
 }
 

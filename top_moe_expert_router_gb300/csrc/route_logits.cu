@@ -21,11 +21,12 @@
 // logits, which needs no score at all.
 //
 // One warp per token; lane l holds the EPL consecutive experts from l * EPL
-// on. A lane packs its slot into the low 4 bits of each 32-bit key and sorts
-// its keys by minima and maxima alone (two instructions a comparator); a pick
-// is one warp maximum of the lanes' heads without the slot, the lowest lane
-// among equals, and a shift of that lane's list. The 4 bits count in the error
-// bound; they are zeros anyway in the keys of 16-bit logits.
+// on. The (k + 1)-th largest of the lanes' maxima is a lower bound of the
+// (k + 1)-th best expert: the few experts that reach it (about 13 for k = 8) are
+// gathered one to a lane, in order of their ids, and ranked by comparing each
+// with all. That takes half the instructions of k rounds of "best of all".
+// The kernel is bound by its instructions: about 450 a token without scores,
+// 900 with a bias and groups.
 #include <math.h>
 
 #include "ops.cuh"
@@ -34,9 +35,9 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
-constexpr int kSelThreads = 1024;
-constexpr int kSelSmem = 32 * (2 * kRouteMaxE + 2) * 4;               // 32 warps' scores
-constexpr int kPermSmem = 2 * kRouteMaxE * (kRouteMaxT / kRouteMaxChunks / 32) * 4;  // both tables at the largest chunk
+constexpr int kSelThreads = 1024, kPermThreads = 512;
+constexpr int kSelSmem = 32 * (2 * kRouteMaxE + 192) * 4;              // 32 warps' scores
+constexpr int kPermSmem = 2 * kRouteMaxE * ((kRouteMaxT / kRouteMaxChunks + 47) / 32) * 4;  // both tables at the largest chunk
 
 __device__ __forceinline__ float load_logit(const void *p, int64_t i, moe_dtype t) {
     if (t == MOE_T_F32) return __ldg((const float *)p + i);
@@ -123,10 +124,12 @@ __device__ __forceinline__ void load_clean(const RouteArgs &a, int64_t row, int 
     for (int i = 0; i < EPL; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], 3.402823466e38f) : -INFINITY;
 }
 
-// What a choice leaves in lane j < k: the j-th pick.
+// What a choice leaves in a lane: an expert, its logit and its place among the
+// picks (the first k count).
 struct Pick {
-    int id;        // -1: none left
-    float l;       // its logit
+    int id;        // -1: none
+    float l;
+    int rank;
 };
 
 // The logit of expert e of a row (lane by lane), cleaned as in the kernel.
@@ -136,23 +139,65 @@ __device__ __forceinline__ float one_logit(const RouteArgs &a, int64_t row, int 
     return fminf(l, 3.402823466e38f);
 }
 
-// Sorts key[0 .. N) in descending order.
-template <int N>
-__device__ __forceinline__ void sort_desc(uint32_t (&key)[N]) {
-    // odd-even merge sort (Batcher)
+// The `want`-th largest of the lanes' largest keys: at most the want-th largest
+// key of all. 1 where fewer lanes have any.
+template <int EPL>
+__device__ __forceinline__ uint32_t lane_bound(const uint32_t (&key)[EPL], int want) {
+    uint32_t top = key[0];
 #pragma unroll
-    for (int p = 1; p < N; p *= 2)
+    for (int i = 1; i < EPL; ++i) top = max(top, key[i]);
+    uint32_t m = 0u;
+    for (int j = 0; j < want;) {
+        m = __reduce_max_sync(kFull, top);
+        if (m == 0u) return 1u;
+        const bool hit = top == m;
+        j += __popc(__ballot_sync(kFull, hit));
+        if (hit) top = 0u;
+    }
+    return m;
+}
+
+// Gathers the experts whose keys reach `bound`, ids ascending, one to a lane
+// (key 0: none), and returns how many they are; over 32 (many equal keys),
+// nothing is gathered.
+template <int EPL>
+__device__ __forceinline__ int gather_from(const uint32_t (&key)[EPL], uint32_t bound, int lane, uint2 *cand,
+                                           uint32_t *my_key, int *my_id) {
+    int cnt = 0;
 #pragma unroll
-        for (int k = p; k >= 1; k /= 2)
+    for (int i = 0; i < EPL; ++i) cnt += key[i] >= bound ? 1 : 0;
+    int incl = cnt;
 #pragma unroll
-            for (int j = k % p; j + k < N; j += 2 * k)
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    const int n = __shfl_sync(kFull, incl, 31);
+    *my_key = 0u;
+    *my_id = -1;
+    if (n > 32) return n;
+    __syncwarp();
+    uint2 *at = cand + (incl - cnt);
 #pragma unroll
-                for (int i = 0; i < k; ++i)
-                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-                        const uint32_t x = key[i + j], y = key[i + j + k];
-                        key[i + j] = max(x, y);
-                        key[i + j + k] = min(x, y);
-                    }
+    for (int i = 0; i < EPL; ++i)
+        if (key[i] >= bound) *at++ = make_uint2(key[i], (uint32_t)(lane * EPL + i));
+    __syncwarp();
+    if (lane < n) {
+        const uint2 v = cand[lane];
+        *my_key = v.x;
+        *my_id = (int)v.y;
+    }
+    return n;
+}
+
+// The place of a lane's key among n gathered ones; ties to the lower lane.
+__device__ __forceinline__ int rank_of(uint32_t key, int n, int lane) {
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const uint32_t o = __shfl_sync(kFull, key, j);
+        rank += o > key - (j < lane ? 1u : 0u) ? 1 : 0;
+    }
+    return rank;
 }
 
 // The scores of a lane's experts in 32 bits (c), which of them may be chosen,
@@ -198,39 +243,60 @@ __device__ __forceinline__ Scored score_lane(const RouteArgs &a, const float (&l
         for (int i = 0; i < EPL; ++i) c[i] *= inv_z;
     }
     if (a.bias) {
+        float b[EPL];
+        if (a.vec_bias && EPL >= 4 && e0 < a.E) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if ((r.on >> i) & 1u) {
-                const float b = __ldg(a.bias + e0 + i);
-                if (b > -INFINITY) c[i] += fminf(b, 3.402823466e38f);
-                else r.on &= ~(1u << i);                  // also NaN
+            for (int i = 0; i + 3 < EPL; i += 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(a.bias + e0 + i));
+                b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) b[i] = e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            c[i] += fminf(b[i], 3.402823466e38f);
+            // fminf takes NaN for the other operand
+            if (!(b[i] > -INFINITY)) r.on &= ~(1u << i);
+        }
     }
     return r;
 }
 
-// The two best of every group: lpg lanes (a power of two, 32 / groups at most)
-// walk each group and all of them end with its result (element e lies at
-// e + e / 32: groups a multiple of 32 apart would share a bank).
+// The two best of every group, with the lpg lanes of a group (a power of two).
+// Where the groups are whole lanes (a.direct) those lanes hold the group
+// themselves; else 32 / groups lanes or fewer walk it in shared memory (element
+// e lies at e + e / 32: groups a multiple of 32 apart would share a bank).
 template <int EPL, typename S>
 __device__ __forceinline__ void group_best(const RouteArgs &a, const S (&c)[EPL], uint32_t on, int lane, S *buf, S &b1,
                                            S &b2) {
     const int e0 = lane * EPL, gs = a.E / a.groups, lpg = a.lanes_per_group, sub = lane & (lpg - 1), g = lane / lpg;
     constexpr int kPad = sizeof(S) == 4 ? 5 : 31;         // no padding for doubles: the room is E of them
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-        if (e0 + i < a.E) buf[e0 + i + ((e0 + i) >> kPad)] = ((on >> i) & 1u) ? c[i] : (S)-INFINITY;
-    __syncwarp();
     b1 = b2 = (S)-INFINITY;
-    if (g < a.groups)
-        for (int i = sub; i < gs; i += lpg) {
-            const int e = g * gs + i;
-            const S v = buf[e + (e >> kPad)];
+    if (a.direct) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const S v = ((on >> i) & 1u) ? c[i] : (S)-INFINITY;
             const S low = b1 < v ? b1 : v;
             b2 = b2 > low ? b2 : low;
             b1 = b1 > v ? b1 : v;
         }
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (e0 + i < a.E) buf[e0 + i + ((e0 + i) >> kPad)] = ((on >> i) & 1u) ? c[i] : (S)-INFINITY;
+        __syncwarp();
+        if (g < a.groups)
+            for (int i = sub; i < gs; i += lpg) {
+                const int e = g * gs + i;
+                const S v = buf[e + (e >> kPad)];
+                const S low = b1 < v ? b1 : v;
+                b2 = b2 > low ? b2 : low;
+                b1 = b1 > v ? b1 : v;
+            }
+    }
     for (int o = lpg >> 1; o > 0; o >>= 1) {
         const S v1 = __shfl_xor_sync(kFull, b1, o), v2 = __shfl_xor_sync(kFull, b2, o);
         const S low = b1 < v1 ? b1 : v1;
@@ -256,7 +322,9 @@ __device__ __forceinline__ bool group_kept(const RouteArgs &a, S score, bool any
 }
 
 template <int EPL>
-__device__ __forceinline__ uint32_t in_kept_groups(const RouteArgs &a, uint32_t on, uint32_t mask, int e0) {
+__device__ __forceinline__ uint32_t in_kept_groups(const RouteArgs &a, uint32_t on, bool kept, int e0) {
+    if (a.direct) return kept ? on : 0u;
+    const uint32_t mask = __ballot_sync(kFull, kept);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const uint32_t gi = ((uint32_t)(e0 + i) * a.group_inv) >> 22;  // (e0 + i) / group size
@@ -265,47 +333,20 @@ __device__ __forceinline__ uint32_t in_kept_groups(const RouteArgs &a, uint32_t 
     return on;
 }
 
-// The n largest packed keys of the warp in order: lane j gets the j-th (0: none) and its expert.
-template <int EPL>
-__device__ __forceinline__ uint32_t pick_packed(const float (&c)[EPL], uint32_t on, int n, int lane, int *id) {
-    uint32_t key[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? (order_key(c[i]) & ~15u) | (15u - i) : 0u;
-    sort_desc<EPL>(key);
-    uint32_t mine = 0u;
-    *id = -1;
-    for (int j = 0; j < n; ++j) {
-        const uint32_t m = __reduce_max_sync(kFull, key[0] >> 4);
-        if (m == 0u) break;
-        const int win = __ffs(__ballot_sync(kFull, (key[0] >> 4) == m)) - 1;
-        const uint32_t h = __shfl_sync(kFull, key[0], win);
-        if (lane == j) {
-            mine = h;
-            *id = win * EPL + 15 - (int)(h & 15u);
-        }
-        if (lane == win) {
-#pragma unroll
-            for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
-            key[EPL - 1] = 0u;
-        }
-    }
-    return mine;
-}
-
-// A packed key stands for a score within 2^-19 of it above.
-constexpr float kPackSlack = 0x1p-19f;
-
 // The choice in 32 bits; *close (warp-uniform) says that some comparison was
-// within the error of what was compared. buf: room for E + E / 32 floats.
+// within the error of what was compared (*near_groups: of the groups), or that
+// over 32 experts tied. buf: room
+// for E + E / 32 floats, and for 32 pairs.
 template <int EPL>
 __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)[EPL], float lmax, int64_t row, int lane,
-                                            float *buf, bool *close) {
+                                            float *buf, bool *close, bool *near_groups) {
     const int e0 = lane * EPL;
     const bool staged = a.keep < a.groups, by_logit = a.bias == nullptr;
     float c[EPL];
     const Scored sc = score_lane<EPL>(a, l, lmax, e0, !by_logit || (staged && a.top2), c);
     uint32_t on = sc.on;
     bool near = false;
+    *near_groups = false;
     if (staged) {
         float b1, b2;
         group_best<EPL, float>(a, c, on, lane, buf, b1, b2);
@@ -315,46 +356,49 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
         if (!by_logit || a.top2) {
             // the border: the worst kept group against the best one left out;
             // two scores make a group's, each rounded once more with its bias
-            float lo = kept ? score : INFINITY;
-            float hi = is_group && !kept ? score : -INFINITY;
-            float mag = any ? fabsf(b1) + (b2 > -INFINITY ? fabsf(b2) : 0.f) : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-                mag = fmaxf(mag, __shfl_xor_sync(kFull, mag, o));
-            }
-            near = hi > -INFINITY && !(lo - hi > 4.f * sc.err + 0x1p-22f * mag);
+            const uint32_t lo = ~__reduce_max_sync(kFull, kept ? ~order_key(score) : 0u);
+            const uint32_t hi = __reduce_max_sync(kFull, is_group && any && !kept ? order_key(score) : 0u);
+            const uint32_t mag = __reduce_max_sync(
+                kFull, any ? __float_as_uint(fabsf(b1) + (b2 > -INFINITY ? fabsf(b2) : 0.f)) : 0u);
+            *near_groups = hi != 0u && !(key_value(lo) - key_value(hi) > 4.f * sc.err + 0x1p-22f * __uint_as_float(mag));
         }
-        on = in_kept_groups<EPL>(a, on, __ballot_sync(kFull, kept), e0);
+        on = in_kept_groups<EPL>(a, on, kept, e0);
         if (by_logit) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] = l[i];
         }
     }
-    Pick r{-1, -INFINITY};
-    const uint32_t mine = pick_packed<EPL>(c, on, a.k + 1, lane, &r.id);  // one more: the border
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? order_key(c[i]) : 0u;
+    uint32_t mine;
+    Pick r{-1, -INFINITY, 0};
+    const int n = gather_from<EPL>(key, lane_bound<EPL>(key, a.k + 1), lane, reinterpret_cast<uint2 *>(buf), &mine, &r.id);
+    near |= n > 32;
+    r.rank = rank_of(mine, min(n, 32), lane);
     if (r.id >= 0) r.l = one_logit(a, row, r.id);
-    const uint32_t next = __shfl_down_sync(kFull, mine, 1);
-    if (by_logit) {
-        // equal but for the slot: ties in 16-bit types, anything in fp32
-        near |= lane < a.k && next && a.type == MOE_T_F32 && (next >> 4) == (mine >> 4);
-    } else {
-        // the score again, without the packed slot; what was not picked lies
-        // below the border's key and its slack
-        float v = 0.f;
-        if (r.id >= 0) {
-            v = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-r.l)) : __expf(r.l - lmax) * (sc.err * 0x1p18f);
-            v += fminf(__ldg(a.bias + r.id), 3.402823466e38f);
+    if (!by_logit) {
+        // each pick against the next one, the last against the border
+        __syncwarp();
+        if (r.id >= 0) buf[r.rank] = key_value(mine);
+        __syncwarp();
+        if (r.id >= 0 && r.rank < a.k && r.rank + 1 < n) {
+            const float v = key_value(mine), x = buf[r.rank + 1];
+            near |= !(v - x > 2.f * sc.err + 0x1p-22f * fmaxf(fabsf(v), fabsf(x)));
         }
-        const float nv = __shfl_down_sync(kFull, v, 1);
-        const float x = lane < a.k - 1 ? nv : key_value(next & ~15u);
-        const float mag = fmaxf(fabsf(v), fabsf(x));
-        near |= lane < a.k && next && !(v - x > 2.f * sc.err + mag * (lane < a.k - 1 ? 0x1p-22f : kPackSlack + 0x1p-22f));
     }
-    *close = __any_sync(kFull, near);
-    if (lane >= a.k) r.id = -1;
+    *close = __any_sync(kFull, near) || *near_groups;
     return r;
+}
+
+// The softmax's sum in 64 bits (1 where no expert is live).
+template <int EPL>
+__device__ __forceinline__ double sum64(const float (&l)[EPL], float lmax) {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s += l[i] > -INFINITY ? exp((double)l[i] - (double)lmax) : 0.0;
+    s = warp_add(s);
+    return s > 0.0 ? s : 1.0;
 }
 
 // A score in 64 bits.
@@ -365,95 +409,42 @@ __device__ __forceinline__ double score64(const RouteArgs &a, float l, float lma
     return a.bias ? p + (double)fminf(__ldg(a.bias + e), 3.402823466e38f) : p;
 }
 
-// The choice in 64 bits, of those scores that can matter: in 32 bits first, a
-// score that lies further below a group's second best, or below the k-th pick,
-// than the errors allow is left out. buf: room for E doubles.
+// The choice in 64 bits of every expert, for tokens where over 32 of them tie
+// or nearly do. buf: room for E doubles.
 template <int EPL>
-__device__ __forceinline__ Pick choose_exact(const RouteArgs &a, const float (&l)[EPL], float lmax, int lane, float *buf) {
+__device__ __noinline__ Pick choose_general(const RouteArgs &a, int64_t row, float lmax, int lane, float *buf) {
     const int e0 = lane * EPL;
-    const bool staged = a.keep < a.groups;
-    const bool by_logit = a.bias == nullptr;              // the picks' order needs no score
+    const bool staged = a.keep < a.groups, by_logit = a.bias == nullptr;
+    float l[EPL], c[EPL];
+    load_clean<EPL>(a, row, e0, l);
     const bool scored = !by_logit || (staged && a.top2);
-    float c[EPL];
-    const Scored sc = score_lane<EPL>(a, l, lmax, e0, scored, c);
-    uint32_t on = sc.on;
-    double z = 1.0;
-    if (scored && !a.sigmoid) {
-        double s = 0.0;
+    uint32_t on = score_lane<EPL>(a, l, lmax, e0, scored, c).on;
+    double z = 1.0, d[EPL];
+    if (scored && !a.sigmoid) z = sum64<EPL>(l, lmax);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s += l[i] > -INFINITY ? exp((double)l[i] - (double)lmax) : 0.0;
-        s = warp_add(s);
-        if (s > 0.0) z = s;
-    }
-    double d[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) d[i] = l[i];
-    uint32_t have = 0u;
-    auto compute = [&](uint32_t need) {
-        need &= ~have;
-        have |= need;
-        while (__any_sync(kFull, need != 0u)) {
-            const int at = need ? __ffs(need) - 1 : 0;
-            float la = 0.f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i == at) la = l[i];
-            const double v = score64(a, la, lmax, z, need ? e0 + at : 0);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (need && i == at) d[i] = v;
-            need &= need - 1u;
-        }
-    };
+    for (int i = 0; i < EPL; ++i) d[i] = scored ? score64(a, l[i], lmax, z, min(e0 + i, a.E - 1)) : (double)l[i];
     if (staged) {
-        float f1, f2;
-        group_best<EPL, float>(a, c, on, lane, buf, f1, f2);
-        uint32_t need = on;
-        if (scored) {
-            const float thr = a.top2 ? f2 : f1;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const uint32_t gi = ((uint32_t)min(e0 + i, a.E - 1) * a.group_inv) >> 22;
-                const float tg = __shfl_sync(kFull, thr, (gi * a.lanes_per_group) & 31);
-                if (tg - c[i] > 2.f * sc.err + 0x1p-21f * fmaxf(fabsf(tg), fabsf(c[i]))) need &= ~(1u << i);
-            }
-            compute(need);
-        }
         double b1, b2;
-        group_best<EPL, double>(a, d, need, lane, reinterpret_cast<double *>(buf), b1, b2);
-        const double score = a.top2 && b2 > -INFINITY ? b1 + b2 : b1;
-        const bool kept = group_kept(a, score, b1 > -INFINITY, lane);
-        on = in_kept_groups<EPL>(a, on, __ballot_sync(kFull, kept), e0);
-    }
-    if (by_logit) {
+        group_best<EPL, double>(a, d, on, lane, reinterpret_cast<double *>(buf), b1, b2);
+        const bool kept = group_kept(a, a.top2 && b2 > -INFINITY ? b1 + b2 : b1, b1 > -INFINITY, lane);
+        on = in_kept_groups<EPL>(a, on, kept, e0);
+        if (by_logit) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) d[i] = c[i] = l[i];
-    } else {
-        int id;
-        const uint32_t mine = pick_packed<EPL>(c, on, a.k, lane, &id);
-        const uint32_t last = __shfl_sync(kFull, mine, a.k - 1);
-        if (last) {                                       // fewer than k are left: all of them
-            const float x = key_value(last & ~15u);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (x - c[i] > 2.f * sc.err + (kPackSlack + 0x1p-21f) * fmaxf(fabsf(x), fabsf(c[i]))) on &= ~(1u << i);
+            for (int i = 0; i < EPL; ++i) d[i] = l[i];
         }
-        compute(on);
     }
     uint64_t key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? key_of(d[i]) : 0ull;
-    Pick r{-1, -INFINITY};
+    Pick r{-1, -INFINITY, lane};
     for (int j = 0; j < a.k; ++j) {
         uint64_t bk = key[0];
         int bi = 0;
-        float lw = l[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i)
             if (key[i] > bk) {
                 bk = key[i];
                 bi = i;
-                lw = l[i];
             }
         const uint64_t m = warp_max(bk);
         if (m == 0) break;
@@ -462,38 +453,116 @@ __device__ __forceinline__ Pick choose_exact(const RouteArgs &a, const float (&l
         for (int i = 0; i < EPL; ++i)
             if (i == bi && lane == win) key[i] = 0;
         const int id = __shfl_sync(kFull, e0 + bi, win);
-        lw = __shfl_sync(kFull, lw, win);
-        if (lane == j) r = Pick{id, lw};
+        if (lane == j) r.id = id;
+    }
+    if (r.id >= 0) r.l = one_logit(a, row, r.id);
+    return r;
+}
+
+// The choice in 64 bits, of those scores that can matter: one that lies further
+// below its group's second best, or below the k-th pick, in 32 bits than the
+// errors allow is left out; the others are gathered one to a lane. buf: room for
+// E + E / 32 floats, and for 32 doubles and 32 words behind 32 pairs.
+template <int EPL>
+__device__ __noinline__ Pick choose_exact(const RouteArgs &a, int64_t row, float lmax, int lane, float *buf,
+                                          bool near_groups) {
+    const int e0 = lane * EPL, gs = a.E / a.groups;
+    const bool staged = a.keep < a.groups, by_logit = a.bias == nullptr;
+    const bool scored = !by_logit || (staged && a.top2);
+    float l[EPL], c[EPL];
+    load_clean<EPL>(a, row, e0, l);
+    const Scored sc = score_lane<EPL>(a, l, lmax, e0, scored, c);
+    uint32_t on = sc.on, key[EPL], mine;
+    uint2 *cand = reinterpret_cast<uint2 *>(buf);
+    double z = 1.0;
+    if (scored && !a.sigmoid) z = sum64<EPL>(l, lmax);
+    Pick r{-1, -INFINITY, lane};
+    if (staged) {
+        float f1, f2;
+        group_best<EPL, float>(a, c, on, lane, buf, f1, f2);
+        if (!near_groups) {                               // the 32-bit choice of the groups stands
+            const float score = a.top2 && f2 > -INFINITY ? f1 + f2 : f1;
+            on = in_kept_groups<EPL>(a, on, group_kept(a, score, f1 > -INFINITY, lane), e0);
+        } else {
+            const float thr = a.top2 ? f2 : f1;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const uint32_t gi = ((uint32_t)min(e0 + i, a.E - 1) * a.group_inv) >> 22;
+                const float tg = __shfl_sync(kFull, thr, (gi * a.lanes_per_group) & 31);
+                const bool below = tg - c[i] > 2.f * sc.err + 0x1p-21f * fmaxf(fabsf(tg), fabsf(c[i]));
+                key[i] = ((on >> i) & 1u) && !below ? 1u : 0u;
+            }
+            const int n = gather_from<EPL>(key, 1u, lane, cand, &mine, &r.id);
+            if (n > 32) return choose_general<EPL>(a, row, lmax, lane, buf);
+            double *val = reinterpret_cast<double *>(buf + 64);
+            int *grp = reinterpret_cast<int *>(buf + 128);
+            if (r.id >= 0) {
+                val[lane] = score64(a, one_logit(a, row, r.id), lmax, z, r.id);
+                grp[lane] = r.id / gs;
+            }
+            __syncwarp();
+            double b1 = -INFINITY, b2 = -INFINITY;       // lane g: group g
+            for (int j = 0; j < n; ++j) {
+                const double v = val[j];
+                if (grp[j] == lane) {
+                    if (v > b1) b2 = b1, b1 = v;
+                    else if (v > b2) b2 = v;
+                }
+            }
+            const double score = a.top2 && b2 > -INFINITY ? b1 + b2 : b1;
+            int rank = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const double o = __shfl_sync(kFull, score, g);
+                rank += o > score || (o == score && g < lane) ? 1 : 0;
+            }
+            const uint32_t mask = __ballot_sync(kFull, lane < a.groups && rank < a.keep && b1 > -INFINITY);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const uint32_t gi = ((uint32_t)(e0 + i) * a.group_inv) >> 22;
+                if (e0 + i >= a.E || !((mask >> (gi & 31u)) & 1u)) on &= ~(1u << i);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? order_key(by_logit ? l[i] : c[i]) : 0u;
+    uint32_t bound = lane_bound<EPL>(key, a.k);
+    if (!by_logit && bound > 1u) {
+        const float x = key_value(bound);
+        bound = order_key(x - (2.f * sc.err + 0x1p-20f * fabsf(x)));
+    }
+    const int n = gather_from<EPL>(key, bound, lane, cand, &mine, &r.id);
+    if (n > 32) return choose_general<EPL>(a, row, lmax, lane, buf);
+    if (r.id >= 0) r.l = one_logit(a, row, r.id);
+    if (by_logit) {
+        r.rank = rank_of(mine, n, lane);
+        return r;
+    }
+    const uint64_t k64 = r.id >= 0 ? key_of(score64(a, r.l, lmax, z, r.id)) : 0ull;
+    r.rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const uint64_t o = __shfl_sync(kFull, k64, j);
+        r.rank += o > k64 - (j < lane ? 1ull : 0ull) ? 1 : 0;
     }
     return r;
 }
 
-// Out of line: few tokens take it, and it loads its logits again so that the
-// caller's stay in registers.
-template <int EPL>
-__device__ __noinline__ Pick choose_again(const RouteArgs &a, int64_t row, float lmax, int lane, float *lbuf) {
-    float l[EPL];
-    load_clean<EPL>(a, row, lane * EPL, l);
-    return choose_exact<EPL>(a, l, lmax, lane, lbuf);
-}
-
-// The weight of lane j's pick (lanes >= k or without a pick: 0).
+// The weight of a lane's pick (`on`: it is one of the first k).
 template <int EPL>
 __device__ __forceinline__ float pick_weight(const RouteArgs &a, const float (&l)[EPL], float lmax, const Pick &r,
-                                             int lane) {
-    const bool on = r.id >= 0;
+                                             bool on) {
     float w = 0.f;
     if (a.renorm) {
-        float top = on ? r.l : -INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        // relative to the largest chosen score: at most 1, and their sum is
+        // taken in fixed point, 2^-27, where it is 1 to 16
+        const float top = key_value(__reduce_max_sync(kFull, on ? order_key(r.l) : 0u));
         // sigmoid(l) = exp(l) to within exp(-60) below -60: the quotient is
         // then that of the exponentials, which does not underflow
-        if (on) w = a.sigmoid && top >= -60.f ? 1.f / (1.f + expf(-r.l)) : expf(r.l - top);
-        const float s = warp_add(w);
-        if (on) w = w / s;
+        if (on)
+            w = a.sigmoid && top >= -60.f ? __fdividef(1.f + expf(-top), 1.f + expf(-r.l)) : expf(r.l - top);
+        const uint32_t s = __reduce_add_sync(kFull, __float2uint_rn(w * 0x1p27f));
+        w *= __fdividef(0x1p27f, (float)s);
     } else if (a.sigmoid) {
-        if (on) w = 1.f / (1.f + expf(-r.l));
+        if (on) w = __fdividef(1.f, 1.f + expf(-r.l));
     } else {
         float s = 0.f;
 #pragma unroll
@@ -505,31 +574,41 @@ __device__ __forceinline__ float pick_weight(const RouteArgs &a, const float (&l
 }
 
 // ids and weights of a chunk's tokens, one warp per token, and the chunk's
-// count of every expert in cnt. lbuf: 2 E + 2 floats per warp.
+// count of every expert in cnt. lbuf: 2 E + 192 floats per warp.
 template <int EPL>
 __device__ __forceinline__ void select_chunk(const RouteArgs &a, int c, int32_t *cnt, float *lbuf) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = 0;
     __syncthreads();
     const int t0 = c * a.chunk, t1 = min(t0 + a.chunk, a.T);
-    lbuf += warp * (2 * a.E + 2);
+    lbuf += warp * (2 * a.E + 192);
     for (int t = t0 + warp; t < t1; t += nw) {
         const int64_t row = (int64_t)t * a.stride;
         float l[EPL];
         load_clean<EPL>(a, row, lane * EPL, l);
-        float lmax = l[0];
+        float lmax = 0.f;
+        if (!a.sigmoid) {                                 // the softmax's largest logit
+            uint32_t m = order_key(l[0]);
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) lmax = fmaxf(lmax, l[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) lmax = fmaxf(lmax, __shfl_xor_sync(kFull, lmax, o));
-        bool close;
-        Pick r = choose_fast<EPL>(a, l, lmax, row, lane, lbuf, &close);
-        if (close) r = choose_again<EPL>(a, row, lmax, lane, lbuf);
-        const float w = pick_weight<EPL>(a, l, lmax, r, lane);
-        if (lane < a.k) {
-            a.ids[(size_t)t * a.k + lane] = r.id;
-            a.w[(size_t)t * a.k + lane] = w;
-            if (r.id >= 0) atomicAdd(&cnt[r.id], 1);
+            for (int i = 1; i < EPL; ++i) m = max(m, order_key(l[i]));
+            lmax = key_value(__reduce_max_sync(kFull, m));
+        }
+        bool close, near_groups;
+        Pick r = choose_fast<EPL>(a, l, lmax, row, lane, lbuf, &close, &near_groups);
+        if (close) r = choose_exact<EPL>(a, row, lmax, lane, lbuf, near_groups);
+        const bool picked = r.id >= 0 && r.rank < a.k;
+        const float w = pick_weight<EPL>(a, l, lmax, r, picked);
+        int32_t *ids = a.ids + (size_t)t * a.k;
+        float *ws = a.w + (size_t)t * a.k;
+        if (picked) {
+            ids[r.rank] = r.id;
+            ws[r.rank] = w;
+            atomicAdd(&cnt[r.id], 1);
+        }
+        const int n_picked = __popc(__ballot_sync(kFull, picked));
+        if (lane < a.k && lane >= n_picked) {
+            ids[lane] = -1;
+            ws[lane] = 0.f;
         }
     }
 }
@@ -540,7 +619,6 @@ struct PermSmem {
     int32_t base[kRouteMaxE];      // those in earlier chunks
     int32_t own[kRouteMaxE];       // those of this chunk
     int32_t off[kRouteMaxE + 1];
-    int32_t part[2][kRouteMaxE];   // this CTA's share of the counts' sums: all, earlier clusters'
     int32_t wsum[kSelThreads / 32];
 };
 
@@ -570,7 +648,7 @@ __device__ __forceinline__ int block_scan(int v, int32_t *wsum, int *total) {
 // The chunk's tokens per expert as bitmaps bm[E][words] (cleared by the
 // caller), the pairs in earlier words (bm + E * words), and the chunk's counts.
 __device__ __forceinline__ void chunk_bitmaps(const RouteArgs &a, int c, PermSmem &sm, uint32_t *bm) {
-    const int tid = threadIdx.x, nth = blockDim.x, E = a.E, words = a.chunk / 32;
+    const int tid = threadIdx.x, nth = blockDim.x, E = a.E, words = (a.chunk + 31) / 32;
     const int t0 = c * a.chunk, nt = max(0, min(a.chunk, a.T - t0));
     const int32_t *ids = a.ids + (size_t)t0 * a.k;
     for (int i = tid; i < nt * a.k; i += nth) {
@@ -589,15 +667,9 @@ __device__ __forceinline__ void chunk_bitmaps(const RouteArgs &a, int c, PermSme
     }
 }
 
-// The rows of a chunk's pairs, from sm.tot and sm.base. Expert e's rows are
-// offsets[e] .., its tokens ascending: row = offsets[e] + (pairs in earlier
-// chunks) + (tokens of e earlier in the chunk), the last from the bitmaps, so
-// the result does not depend on the order of threads.
-__device__ __forceinline__ void place_chunk(const RouteArgs &a, int c, int nch, PermSmem &sm, const uint32_t *bm) {
-    const int tid = threadIdx.x, nth = blockDim.x, E = a.E, words = a.chunk / 32;
-    const uint32_t *before = bm + E * words;
-    const int t0 = c * a.chunk, nt = max(0, min(a.chunk, a.T - t0));
-    const int32_t *ids = a.ids + (size_t)t0 * a.k;
+// offsets from sm.tot (every thread of the CTA, after its own writes of tot); returns the total.
+__device__ __forceinline__ int expert_offsets(const RouteArgs &a, PermSmem &sm) {
+    const int tid = threadIdx.x, nth = blockDim.x, E = a.E;
     __syncthreads();
     int run = 0, total;
     for (int e0 = 0; e0 < E; e0 += nth) {
@@ -608,6 +680,18 @@ __device__ __forceinline__ void place_chunk(const RouteArgs &a, int c, int nch, 
     }
     if (tid == 0) sm.off[E] = run;
     __syncthreads();
+    return run;
+}
+
+// The rows of a chunk's pairs. Expert e's rows are offsets[e] .., its tokens
+// ascending: row = offsets[e] + (pairs in earlier chunks) + (tokens of e earlier
+// in the chunk), the last from the bitmaps, so the result does not depend on
+// the order of threads.
+__device__ __forceinline__ void place_chunk(const RouteArgs &a, int c, const PermSmem &sm, const uint32_t *bm) {
+    const int tid = threadIdx.x, nth = blockDim.x, words = (a.chunk + 31) / 32;
+    const uint32_t *before = bm + a.E * words;
+    const int t0 = c * a.chunk, nt = max(0, min(a.chunk, a.T - t0));
+    const int32_t *ids = a.ids + (size_t)t0 * a.k;
     for (int i = tid; i < nt * a.k; i += nth) {
         const int e = __ldcg(ids + i), t = i / a.k;
         int row = -1;
@@ -618,16 +702,22 @@ __device__ __forceinline__ void place_chunk(const RouteArgs &a, int c, int nch, 
         }
         if (a.pos) a.pos[(size_t)t0 * a.k + i] = row;
     }
+}
+
+// The rest of the outputs, by CTA `b` of `nb`: the rows of perm past the last
+// pair; the first CTA the counts, the offsets and a layer's tables.
+__device__ __forceinline__ void finish_route(const RouteArgs &a, int b, int nb, int pairs, PermSmem &sm) {
+    const int tid = threadIdx.x, nth = blockDim.x, E = a.E;
     if (a.perm)
-        for (int64_t i = run + (int64_t)c * nth + tid; i < (int64_t)a.T * a.k; i += (int64_t)nch * nth)
+        for (int64_t i = pairs + (int64_t)b * nth + tid; i < (int64_t)a.T * a.k; i += (int64_t)nb * nth)
             a.perm[i] = a.perm_fill;
-    if (c != 0) return;
+    if (b != 0) return;
     for (int e = tid; e <= E; e += nth) {
         if (a.counts && e < E) a.counts[e] = sm.tot[e];
         if (a.offsets) a.offsets[e] = sm.off[e];
     }
     if (!a.uniq) return;
-    int nu = 0, ntile = 0;
+    int nu = 0, ntile = 0, total;
     for (int e0 = 0; e0 < E; e0 += nth) {
         const int e = e0 + tid, n = e < E ? sm.tot[e] : 0;
         const int u = block_scan(n > 0 ? 1 : 0, sm.wsum, &total);
@@ -654,10 +744,10 @@ __device__ __forceinline__ int ld_cluster(const int32_t *p, int rank) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// Large batches, first launch: the choice, and the counts of every 32 tokens
-// in rows of `ep` (E rounded up to 8).
+// Large batches, first launch: the choice, and the counts of every chunk in
+// rows of `ep` (E rounded up to 8).
 template <int EPL>
-__global__ void __launch_bounds__(kSelThreads) route_select_kernel(RouteArgs a, int ep) {
+__global__ void __launch_bounds__(kSelThreads) route_select_kernel(const __grid_constant__ RouteArgs a, int ep) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int32_t cnt[kRouteMaxE];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -668,69 +758,60 @@ __global__ void __launch_bounds__(kSelThreads) route_select_kernel(RouteArgs a, 
         a.chunk_cnt[(size_t)blockIdx.x * ep + e] = e < a.E ? (uint16_t)cnt[e] : (uint16_t)0;
 }
 
-// Second launch, clusters of 8 CTAs, a chunk of tokens each: every CTA sums an
-// eighth of the count rows (all of them, and those before its cluster), the
-// CTAs add up their sums and their own chunks' counts through distributed
-// shared memory, and each places its pairs.
-__global__ void __launch_bounds__(kSelThreads) route_permute_kernel(RouteArgs a, int rows, int ep) {
+// Second launch: every CTA sums the count rows of all chunks and of those before
+// its own, and places its chunk's pairs. All CTAs read the same rows at once, so
+// their latency counts: with 512 threads a thread's loads (8 at 4096 tokens of
+// 256 experts) are one batch, 2 us, with 256 threads two, 4 to 8 us. (Sums split
+// over a cluster of 8 and joined through distributed shared memory: 4 us longer,
+// two barriers and 16 remote loads a thread.)
+__global__ void __launch_bounds__(kPermThreads) route_permute_kernel(const __grid_constant__ RouteArgs a, int rows, int ep) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ PermSmem sm;
+    __shared__ __align__(16) int32_t sums[2][8 * kPermThreads];  // [all, before][row group][ep]
     uint32_t *bm = reinterpret_cast<uint32_t *>(smem);
-    const int tid = threadIdx.x, E = a.E, c = blockIdx.x, rank = c & 7, words = a.chunk / 32;
-    for (int i = tid; i < E * words; i += kSelThreads) bm[i] = 0u;
-    for (int e = tid; e < E; e += kSelThreads) sm.part[0][e] = sm.part[1][e] = 0;
+    const int tid = threadIdx.x, E = a.E, words = (a.chunk + 31) / 32, c = blockIdx.x;
+    for (int i = tid; i < E * words; i += kPermThreads) bm[i] = 0u;
     __syncthreads();
     pdl_wait();
-    {
-        const int nv = ep / 8, v = tid % nv, per = kSelThreads / nv;
-        const int first = (int)((int64_t)rank * rows / 8), last = (int)((int64_t)(rank + 1) * rows / 8);
-        const int before = (c - rank) * words;           // rows ahead of this cluster's chunks
+    const int nv = ep / 8, per = kPermThreads / nv;      // row groups of nv threads, 8 experts each
+    if (tid < per * nv) {
         int all[8], pre[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) all[i] = pre[i] = 0;
-        if (tid < per * nv) {
-#pragma unroll 4
-            for (int r = first + tid / nv; r < last; r += per) {
-                const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(a.chunk_cnt + (size_t)r * ep) + v);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll 8
+        for (int r = tid / nv; r < rows; r += per) {
+            const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(a.chunk_cnt + (size_t)r * ep) + tid % nv);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int n = (w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-                    all[i] += n;
-                    pre[i] += r < before ? n : 0;
-                }
+            for (int i = 0; i < 8; ++i) {
+                const int n = (w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+                all[i] += n;
+                pre[i] += r < c ? n : 0;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (all[i]) {
-                    atomicAdd(&sm.part[0][8 * v + i], all[i]);
-                    if (pre[i]) atomicAdd(&sm.part[1][8 * v + i], pre[i]);
-                }
         }
+        int4 *s0 = reinterpret_cast<int4 *>(sums[0] + 8 * tid), *s1 = reinterpret_cast<int4 *>(sums[1] + 8 * tid);
+        s0[0] = make_int4(all[0], all[1], all[2], all[3]), s0[1] = make_int4(all[4], all[5], all[6], all[7]);
+        s1[0] = make_int4(pre[0], pre[1], pre[2], pre[3]), s1[1] = make_int4(pre[4], pre[5], pre[6], pre[7]);
     }
-    chunk_bitmaps(a, c, sm, bm);
-    cluster_arrive();
-    cluster_wait();
-    for (int e = tid; e < E; e += kSelThreads) {
-        int tot = 0, base = 0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            tot += ld_cluster(&sm.part[0][e], q);
-            base += ld_cluster(&sm.part[1][e], q);
-            if (q < rank) base += ld_cluster(&sm.own[e], q);
+    chunk_bitmaps(a, c, sm, bm);                         // (a barrier within)
+    for (int e = tid; e < E; e += kPermThreads) {
+        int all = 0, pre = 0;
+        for (int g = 0; g < per; ++g) {
+            all += sums[0][g * ep + e];
+            pre += sums[1][g * ep + e];
         }
-        sm.tot[e] = tot;
-        sm.base[e] = base;
+        sm.tot[e] = all;
+        sm.base[e] = pre;
     }
-    cluster_arrive();
-    place_chunk(a, c, gridDim.x, sm, bm);
-    cluster_wait();                                      // no CTA leaves while another may read its sums
+    const int total = expert_offsets(a, sm);
+    place_chunk(a, c, sm, bm);
+    finish_route(a, c, rows, total, sm);
 }
 
 // Small batches: both steps in one launch, the chunks of one cluster, which
 // read each other's counts through distributed shared memory.
 template <int EPL>
-__global__ void __launch_bounds__(kSelThreads) route_fused_kernel(RouteArgs a, int nch) {
+__global__ void __launch_bounds__(kSelThreads) route_fused_kernel(const __grid_constant__ RouteArgs a, int nch) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int32_t cnt[kRouteMaxE];
     __shared__ PermSmem sm;
@@ -759,20 +840,22 @@ __global__ void __launch_bounds__(kSelThreads) route_fused_kernel(RouteArgs a, i
         sm.base[e] = base;
     }
     if (nch > 1) cluster_arrive();
-    place_chunk(a, c, nch, sm, bm);
+    const int total = expert_offsets(a, sm);
+    place_chunk(a, c, sm, bm);
+    finish_route(a, c, nch, total, sm);
     if (nch > 1) cluster_wait();                         // no CTA leaves while another may read its counts
 }
 
 template <int EPL>
 cudaError_t launch_epl(RouteArgs a, cudaStream_t st, int *launches) {
     const bool permute = a.counts || a.offsets || a.perm || a.pos || a.uniq;
-    const int rows = (a.T + 31) / 32;
-    const size_t per_warp = (size_t)(2 * a.E + 2) * 4;
+    a.chunk = route_chunk_tokens(a.T);
+    const int rows = (a.T + a.chunk - 1) / a.chunk;
+    const size_t per_warp = (size_t)(2 * a.E + 192) * 4;
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
     cfg.stream = st;
-    a.chunk = 32;
     cfg.gridDim = dim3(rows);
     if (launches) ++*launches;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -794,8 +877,8 @@ cudaError_t launch_epl(RouteArgs a, cudaStream_t st, int *launches) {
     static std::atomic<uint64_t> set_sel{0}, set_perm{0};
     cudaError_t e = set_smem_limit_once((const void *)route_select_kernel<EPL>, kSelSmem, set_sel);
     if (e != cudaSuccess) return e;
-    // one token per warp while the SMs hold all chunks; then half as many warps, two CTAs on an SM
-    const int warps = rows <= 152 ? 32 : 16;
+    // one token per warp while every chunk has an SM; then half as many warps, two CTAs on an SM
+    const int warps = rows <= kRouteMaxChunks / 2 ? 32 : 16;
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = warps * per_warp;
     cfg.numAttrs = 0;
@@ -803,15 +886,11 @@ cudaError_t launch_epl(RouteArgs a, cudaStream_t st, int *launches) {
     if (e != cudaSuccess || !permute) return e;
     e = set_smem_limit_once((const void *)route_permute_kernel, kPermSmem, set_perm);
     if (e != cudaSuccess) return e;
-    a.chunk = route_chunk_tokens(a.T);
-    const int nch = (a.T + a.chunk - 1) / a.chunk;
-    cfg.gridDim = dim3((nch + 7) / 8 * 8);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)2 * a.E * (a.chunk / 32) * 4;
-    attr[0].val.clusterDim.x = 8;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 2;
+    cfg.blockDim = dim3(kPermThreads);
+    cfg.dynamicSmemBytes = (size_t)2 * a.E * ((a.chunk + 31) / 32) * 4;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
     if (launches) ++*launches;
     return cudaLaunchKernelEx(&cfg, route_permute_kernel, a, rows, ep);
 }
@@ -825,8 +904,11 @@ cudaError_t launch_route_logits(RouteArgs a, cudaStream_t st, int *launches) {
     a.vec = a.nsplit == 1 && a.E % epl == 0 && (uintptr_t)a.logits % align == 0 && (a.stride * size) % align == 0;
     const int gs = a.E / a.groups;
     a.group_inv = ((1u << 22) + gs - 1) / gs;
-    a.lanes_per_group = 1;
-    while (2 * a.lanes_per_group * a.groups <= 32) a.lanes_per_group *= 2;
+    const int lanes = gs / epl;
+    a.direct = gs % epl == 0 && (lanes & (lanes - 1)) == 0;
+    a.lanes_per_group = a.direct ? lanes : 1;
+    while (!a.direct && 2 * a.lanes_per_group * a.groups <= 32) a.lanes_per_group *= 2;
+    a.vec_bias = a.E % epl == 0 && (uintptr_t)a.bias % 16 == 0;
     return epl == 1   ? launch_epl<1>(a, st, launches)
            : epl == 2 ? launch_epl<2>(a, st, launches)
            : epl == 4 ? launch_epl<4>(a, st, launches)
