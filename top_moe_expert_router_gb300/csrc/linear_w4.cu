@@ -139,11 +139,10 @@ __device__ __forceinline__ void stage_x_type(const W4Args &a, uint4 *xh, float *
     for (int i0 = threadIdx.x >> 4; i0 < n; i0 += U * slots) {
         uint4 raw[U];
         float sc[U];
-        int ms[U], ks[U];
+        int to[U];                               // the block's first unit, and its scale's place
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            ms[u] = m;
-            ks[u] = kb;
+            to[u] = kb << 8 | m;
             const bool in = i0 + u * slots < n && kb < kmax;
             raw[u] = in ? load_x8(p, vec) : make_uint4(0u, 0u, 0u, 0u);
             sc[u] = 1.f;
@@ -203,8 +202,9 @@ __device__ __forceinline__ void stage_x_type(const W4Args &a, uint4 *xh, float *
             if constexpr (!NVFP4)
                 o = make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
                                __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632));
-            xh[(ks[u] * 4 + sp) * ps + ms[u] * 4 + t] = o;
-            if (j == 0) xsc[ks[u] * mt + ms[u]] = sc[u];
+            const int ku = to[u] >> 8, mu = to[u] & 255;
+            xh[(ku * 4 + sp) * ps + mu * 4 + t] = o;
+            if (j == 0) xsc[ku * mt + mu] = sc[u];
         }
     }
 }
@@ -220,6 +220,11 @@ __device__ __forceinline__ void stage_x(const W4Args &a, uint4 *xh, float *xsc, 
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -280,34 +285,31 @@ __device__ __forceinline__ float s_value(uint32_t h, moe_dtype t) {
     return t == MOE_T_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
 }
 
-// acc += a warp's 16 MT rows by block b of a stage. xb, xs: the block's staged
-// x and its scales (16-byte units; product pair sp of token n at sp * ps + tok[n]).
+// acc += a warp's 16 MT rows by one block. Shared-memory addresses: `codes` and
+// `scales` of this lane's first row, `x` of the block's staged x (product pair sp
+// of token n at x + sp * ps + tok[n]), `xs` of its scales (column n at xs + col[n]).
 template <int NT, int MT, bool NVFP4, int G, bool TS>
-__device__ __forceinline__ void mul_block(const W4Args &a, uint32_t stage, int b, int wrow, int lane,
-                                          const Scales<MT, NVFP4, G> &sc, const uint4 *xb, const float *xs, int ps,
-                                          const int (&tok)[NT], const int (&col)[NT][2], float (&acc)[MT][NT][4]) {
+__device__ __forceinline__ void mul_block(const W4Args &a, uint32_t codes, uint32_t scales, int lane,
+                                          const Scales<MT, NVFP4, G> &sc, uint32_t x, uint32_t xs, int ps,
+                                          const uint32_t (&tok)[NT], const uint32_t (&col)[NT][2],
+                                          float (&acc)[MT][NT][4]) {
     using S = Scales<MT, NVFP4, G>;
-    const int g = lane >> 2, t = lane & 3;
     float x0[NT], x1[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        x0[n] = xs[col[n][0]];
-        x1[n] = xs[col[n][1]];
+        x0[n] = lds_f32(xs + col[n][0]);
+        x1[n] = lds_f32(xs + col[n][1]);
     }
     uint32_t w[2 * MT][4];
     uint32_t s2[2 * MT];                         // NVFP4: the lane's two block scales of each row, in f16
-    const uint32_t base = stage + b * (kRows<MT> * 64) + wrow * 64;
 #pragma unroll
     for (int j = 0; j < 2 * MT; ++j) {
         uint4 v;
         if constexpr (NVFP4) {
-            v = lds128(base + (8 * j + g) * 64 + 16 * t);
-            const uint32_t u = TS ? lds16(stage + kCodes<MT> + (wrow + 8 * j + g) * 16 + 8 * b + 2 * t) : sc.v[j];
-            s2[j] = e4m3x2_to_f16x2((uint16_t)u);
+            v = lds128(codes + j * 512);
+            s2[j] = e4m3x2_to_f16x2((uint16_t)(TS ? lds16(scales + j * 128) : sc.v[j]));
         } else {
-            // matrix i: 16-byte chunk i of eight rows, lane l naming row l & 7 of matrix l >> 3
-            const int r = 8 * j + (lane & 7);
-            v = ldmatrix4(base + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4));
+            v = ldmatrix4(codes + j * 512);
         }
         w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
     }
@@ -345,11 +347,11 @@ __device__ __forceinline__ void mul_block(const W4Args &a, uint32_t stage, int b
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const uint4 x = xb[sp * ps + tok[n]];
+                const uint4 xv = lds128(x + sp * ps + tok[n]);
 #pragma unroll
                 for (int h = 0; h < MT; ++h) {
-                    mma16816(part[h][n], f[2 * h][0], f[2 * h + 1][0], f[2 * h][1], f[2 * h + 1][1], x.x, x.y);
-                    mma16816(part[h][n], f[2 * h][2], f[2 * h + 1][2], f[2 * h][3], f[2 * h + 1][3], x.z, x.w);
+                    mma16816(part[h][n], f[2 * h][0], f[2 * h + 1][0], f[2 * h][1], f[2 * h + 1][1], xv.x, xv.y);
+                    mma16816(part[h][n], f[2 * h][2], f[2 * h + 1][2], f[2 * h][3], f[2 * h + 1][3], xv.z, xv.w);
                 }
             }
         }
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
                                                                 const __grid_constant__ CUtensorMap ts, const W4Args a,
                                                                 const Shape sh) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    constexpr int MP = 8 * NT + 1;               // odd: rows fall on different banks
+    constexpr int MP = 8 * NT + 2;               // even, for stores of two columns
     constexpr int kR = kRows<MT>, kSt = kStage<MT, TS>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int m0 = blockIdx.z * 8 * NT, mt = min(8 * NT, a.M - m0);
@@ -438,6 +440,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
         fence_barrier_init();
     }
     __syncthreads();
+    // launched ahead of the end of the kernel before it; lets the next one do the same
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_wait();
 
     if (warp == kCons) {
         // producer: every tile's stages in order; the cluster barrier of a
@@ -471,18 +476,25 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
 
     const int g = lane >> 2, t = lane & 3, wrow = (warp & 3) * 16 * MT, b = warp >> 2;
     // tokens past mt repeat the last one: an output column depends on its own token only
-    int tok[NT], col[NT][2];
+    uint32_t tok[NT], col[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        tok[n] = min(n * 8 + g, mt - 1) * 4 + t;
-        col[n][0] = min(n * 8 + 2 * t, mt - 1);
-        col[n][1] = min(n * 8 + 2 * t + 1, mt - 1);
+        tok[n] = (min(n * 8 + g, mt - 1) * 4 + t) * 16;
+        col[n][0] = min(n * 8 + 2 * t, mt - 1) * 4;
+        col[n][1] = min(n * 8 + 2 * t + 1, mt - 1) * 4;
     }
+    // NVFP4: the row's codes from 32 t on. INT4, ldmatrix: lane l names row l & 7
+    // of matrix l >> 3, which is 16-byte chunk l >> 3 of eight rows.
+    const uint32_t code_at = b * (kR * 64) + (NVFP4 ? (wrow + g) * 64 + 16 * t
+                                                    : (wrow + (lane & 7)) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+    const uint32_t scale_at = kCodes<MT> + (wrow + g) * 16 + 8 * b + 2 * t;
+    const uint32_t ring = smem_u32(smem), x_at = smem_u32(xh) + b * 4 * ps * 16, xs_at = smem_u32(xsc) + b * mt * 4;
     const float gs = NVFP4 ? __ldg(a.g) : 1.f;
     Scales<MT, NVFP4, G> sc;                     // loaded by the lanes one stage ahead unless they come with it
     if (!TS) load_scales<MT, NVFP4, G>(a, blockIdx.y * kR + wrow, 2 * s0 + b, lane, sc);
     bool staged = false;
-    int buf = 0, i = 0;
+    int buf = 0, slot = 0;
+    uint32_t phase = 0;
     for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y, buf ^= 1) {
         float acc[MT][NT][4];
 #pragma unroll
@@ -499,20 +511,26 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
                 named_bar(1, kConsThreads);
                 staged = s1 - s0 <= sh.st_pass;
             }
-            for (int st = p0; st < pe; ++st, ++i) {
-                const int slot = i % R;
-                const Scales<MT, NVFP4, G> cur = sc;
+            uint32_t x = x_at, xs = xs_at;
+            for (int st = p0; st < pe; ++st) {
+                Scales<MT, NVFP4, G> cur;
                 if (!TS) {
+                    cur = sc;
                     const bool more = st + 1 < s1;
                     const int nt = more ? tile : tile + (int)gridDim.y;
                     if (nt < tiles) load_scales<MT, NVFP4, G>(a, nt * kR + wrow, 2 * (more ? st + 1 : s0) + b, lane, sc);
                 }
-                wait_full(&full[slot], (i / R) & 1, bad);
-                const int xb = 2 * (st - p0) + b;
-                mul_block<NT, MT, NVFP4, G, TS>(a, smem_u32(smem + (size_t)slot * kSt), b, wrow, lane, cur,
-                                        xh + xb * 4 * ps, xsc + xb * mt, ps, tok, col, acc);
+                wait_full(&full[slot], phase, bad);
+                const uint32_t stage = ring + slot * kSt;
+                mul_block<NT, MT, NVFP4, G, TS>(a, stage + code_at, stage + scale_at, lane, cur, x, xs, ps * 16, tok, col, acc);
+                x += 8 * ps * 16;
+                xs += 2 * mt * 4;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[slot]);
+                if (++slot == R) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
         }
         // The sums meet at the part that owns the row, 1 / parts of the tile's:
@@ -526,22 +544,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
             for (int e = 0; e < 4; e += 2) {
                 const int r = wrow + 16 * h + g + 4 * e, p = r / own;
                 const uint32_t at = sums + (((part * 2 + b) * own + r - p * own) * MP + 2 * t) * 4;
-                if (parts > 1) {
-                    uint32_t ra;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(at), "r"(p));
+                uint32_t ra = at;
+                if (parts > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(at), "r"(p));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (n * 8 + 2 * t >= mt) continue;
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra + n * 32), "f"(acc[h][n][e]) : "memory");
-                        if (n * 8 + 2 * t + 1 >= mt) continue;
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra + n * 32 + 4), "f"(acc[h][n][e + 1]) : "memory");
-                    }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + n * 32), "f"(acc[h][n][e]) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + n * 32 + 4), "f"(acc[h][n][e + 1]) : "memory");
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    if (n * 8 + 2 * t >= mt) continue;
+                    if (parts > 1)
+                        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(ra + n * 32), "f"(acc[h][n][e]), "f"(acc[h][n][e + 1]) : "memory");
+                    else
+                        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ra + n * 32), "f"(acc[h][n][e]), "f"(acc[h][n][e + 1]) : "memory");
                 }
             }
         if (parts > 1) {
@@ -605,7 +616,7 @@ cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     gy = gy < 1 ? 1 : gy > tiles ? tiles : gy;
     const int part_st = (nst + sh.parts - 1) / sh.parts;
     constexpr int kSt = kStage<MT, TS>, kHalf = 113 * 1024 - 1024;
-    const int kRed = (sh.parts * 4 * ((R + sh.parts - 1) / sh.parts) * (8 * NT + 1) + 3) / 4 * 16;
+    const int kRed = (sh.parts * 4 * ((R + sh.parts - 1) / sh.parts) * (8 * NT + 2) + 3) / 4 * 16;
     const int xst = 8 * pair_stride(mt) * 16 + 8 * mt;  // bytes of x and its scales for one stage
     sh.st_pass = (kHalf - kRed - 2 * kSt - 256) / xst;
     if (sh.st_pass > part_st) sh.st_pass = part_st;
@@ -619,13 +630,18 @@ cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sh.bars + 16 * 8 + 8;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = sh.parts;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    // The start overlaps the end of the kernel before where a CTA takes one
+    // tile (0.5 us of 6 to 14); CTAs that stay would share their SM with it
+    // (131072 x 4096, 4 tokens: 62 -> 70 us).
+    cfg.numAttrs = gy == tiles ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, tq, ts, a, sh);
 }
 
