@@ -375,6 +375,8 @@ W4S = [
     (1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 40, 128), (1, 100, 160), (8, 129, 256), (9, 33, 384), (16, 64, 1024),
     (5, 300, 1152), (17, 31, 512), (32, 130, 640), (33, 70, 256), (64, 48, 2048), (1, 5000, 256), (4, 2500, 1536),
     (7, 64, 12288), (64, 20, 8192),
+    # many tiles: pairs of CTAs share runs of them
+    (3, 39000, 512), (8, 45001, 256), (1, 39040, 160), (12, 20000, 384), (20, 20011, 256),
 ]
 
 

@@ -19,17 +19,20 @@
 // ones lose at most 2^-40 of it. Products and sums are fp32; an INT4 group's
 // sum is multiplied by its scale, a 128-column block's by x's, in fp32.
 //
-// Structure. A CTA takes tiles of 64 or 128 rows: TMA streams their codes through
-// X K is split over a cluster of up to 8 CTAs
-// where there are few tiles; their sums meet in distributed shared
-// memory, added in rank order. What bounds it: with the loads by TMA the
-// shared-memory pipe (per warp and 128 columns: 16 cycles of codes, 18 of
-// TMA's writes, 16 of x for 8 tokens), which is why a warp takes 32 rows: the
-// B fragments are read once for two products.
+// Structure. A CTA takes tiles of 64 or 128 rows: a producer warp streams their
+// codes by TMA through a ring of 256-column stages; four warps along the rows by
+// two along a stage's columns widen and multiply them, 32 rows a warp up to 8
+// tokens (x is read once for two products), 16 above. K is split over a cluster
+// of up to 8 CTAs where there are few tiles; their sums meet in distributed
+// shared memory, added in rank order. What bounds it: the large sizes, the issue
+// of about 18 instructions per 256 weights (the stream leaves 22 at full issue);
+// the small ones, staging x and joining the parts.
 // Measured on the way (131072 x 4096 NVFP4, 4 tokens, 45 us of stream): loads
 // into registers one block ahead 92 us (waiting for one block's load waited
 // for later ones too), two batches of four blocks in turn 70 us, a ring of
-// 16-byte asynchronous copies 88 us (the L1's tag and data cycles: 82 % busy).
+// 16-byte asynchronous copies 88 us (the L1's tag and data cycles: 82 % busy);
+// now 60 us. 256-row tiles on one CTA of 16 warps took 63 us, pairs of CTAs that
+// share a run of tiles, to end together, 64 us.
 //
 // The k order inside a 128-column block is free as long as both operands use
 // the same. NVFP4: lane t of a row takes the row's 32 codes from 32 t on (one
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
                                                                 const __grid_constant__ CUtensorMap ts, const W4Args a,
                                                                 const Shape sh) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    constexpr int MP = 8 * NT + 2;               // even, for stores of two columns
+    constexpr int MP = 8 * NT + 2;               // even for stores of two columns, and rows on different banks
     constexpr int kR = kRows<MT>, kSt = kStage<MT, TS>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int m0 = blockIdx.z * 8 * NT, mt = min(8 * NT, a.M - m0);
@@ -442,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
     __syncthreads();
     // launched ahead of the end of the kernel before it; lets the next one do the same
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (parts > 1) cluster_arrive();             // this CTA runs: its shared memory may be written to
     pdl_wait();
 
     if (warp == kCons) {
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
                 }
             __syncwarp();
             if (parts > 1) {
-                if (tile != (int)blockIdx.y) cluster_wait();
+                cluster_wait();                  // the start's, or the tile's before
                 cluster_arrive();
             }
         }
@@ -538,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
         // tensor scale and the bias. The barrier also tells that every CTA is
         // done reading the other buffer's last tile.
         const uint32_t sums = smem_u32(red) + buf * (parts * 2 * own * MP * 4);
+        if (parts > 1 && tile == (int)blockIdx.y) cluster_wait();  // every CTA of the cluster runs
 #pragma unroll
         for (int h = 0; h < MT; ++h)
 #pragma unroll
@@ -599,13 +604,18 @@ cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     if (TS && !code_map(&ts, a.s, a.N, a.K / 16, 16, R, false)) return cudaErrorInvalidValue;
     const int mt = a.M < 8 * NT ? a.M : 8 * NT, mb = (a.M + 8 * NT - 1) / (8 * NT);
     const int nst = (a.K + 255) / 256, tiles = (a.N + R - 1) / R, slots = 2 * sms;
+    constexpr int kSt = kStage<MT, TS>, kHalf = 112 * 1024, kBars = 16 * 8 + 16;
+    const int xst = 8 * pair_stride(mt) * 16 + 8 * mt;  // bytes of x and its scales for one stage
+    auto sums_bytes = [&](int p) { return (p * 4 * ((R + p - 1) / p) * (8 * NT + 2) * 4 + 15) / 16 * 16; };
     // K in 1 to 8 parts: the fewest stages that one of the 2 * sms CTAs at a
-    // time takes, a tile's start and sum counted as kTile stages
-    constexpr int kTile = 4;
+    // time takes, a tile's start and sum counted as four, and half as many again
+    // where x does not fit beside two stages and is staged anew for every tile
     sh.parts = 1;
     int64_t best = INT64_MAX;
     for (int p = 1; p <= 8 && 2 * p <= nst + 1; ++p) {
-        const int64_t per = ((int64_t)tiles * p * mb + slots - 1) / slots * ((nst + p - 1) / p + kTile);
+        const int st = (nst + p - 1) / p;
+        int64_t per = ((int64_t)tiles * p * mb + slots - 1) / slots * (st + 4);
+        if (st * xst + sums_bytes(p) + 2 * kSt + kBars > kHalf) per += per / 2;
         if (per < best) {
             best = per;
             sh.parts = p;
@@ -615,16 +625,14 @@ cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     int gy = slots / (sh.parts * mb);
     gy = gy < 1 ? 1 : gy > tiles ? tiles : gy;
     const int part_st = (nst + sh.parts - 1) / sh.parts;
-    constexpr int kSt = kStage<MT, TS>, kHalf = 113 * 1024 - 1024;
-    const int kRed = (sh.parts * 4 * ((R + sh.parts - 1) / sh.parts) * (8 * NT + 2) + 3) / 4 * 16;
-    const int xst = 8 * pair_stride(mt) * 16 + 8 * mt;  // bytes of x and its scales for one stage
-    sh.st_pass = (kHalf - kRed - 2 * kSt - 256) / xst;
+    const int sums = sums_bytes(sh.parts);
+    sh.st_pass = (kHalf - sums - 2 * kSt - kBars) / xst;
     if (sh.st_pass > part_st) sh.st_pass = part_st;
-    sh.ring = (kHalf - kRed - 256 - sh.st_pass * xst) / kSt;
+    sh.ring = (kHalf - sums - kBars - sh.st_pass * xst) / kSt;
     if (sh.ring > 8) sh.ring = 8;
     const int es = a.x_type == MOE_T_E4M3 ? 1 : 2;
     sh.vec = (uintptr_t)a.x % (8 * es) == 0 && (a.x_ld * es) % (8 * es) == 0;
-    sh.bars = (sh.ring * kSt + kRed + sh.st_pass * xst + 7) / 8 * 8;
+    sh.bars = (sh.ring * kSt + sums + sh.st_pass * xst + 7) / 8 * 8;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(sh.parts, gy, mb);
     cfg.blockDim = dim3(kThreads);
