@@ -314,7 +314,8 @@ moe_status moe_route_logits_workspace_size(const moe_route_desc *desc, int T, si
  * perm [T*top_k] and pos [T, top_k] as in moe_route, each optional (NULL).
  * Entries of perm past offsets[E] are set to -1. The workspace (16-byte
  * aligned) may be NULL when none of the four is asked for; it needs no
- * initialisation and carries nothing from one call to the next. T = 0 only
+ * initialisation and carries nothing from one call to the next; up to 256
+ * tokens need none. T = 0 only
  * zeroes counts and offsets. */
 moe_status moe_route_logits(const moe_route_desc *desc, const void *logits, moe_dtype type, int64_t row_stride, int T,
                             int32_t *ids, float *w, int32_t *counts, int32_t *offsets, int32_t *perm, int32_t *pos,

@@ -412,15 +412,15 @@ def _row_stride(name, t):
     """Elements from one row of a 2-D tensor to the next (rows contiguous, not overlapping); 0 for None."""
     if t is None:
         return 0
-    rows, cols = t.shape
     s0, s1 = t.stride()
+    rows, cols = t.shape
+    if s1 == 1 and s0 >= cols and rows > 1:
+        return s0
     if cols > 1 and s1 != 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
-    if rows <= 1:
-        return cols or 1
-    if s0 < cols:
+    if rows > 1 and s0 < cols:
         raise ValueError(f"{name}: rows overlap")
-    return s0
+    return s0 if rows > 1 else cols or 1
 
 
 def _input(name, t, types):
@@ -456,6 +456,7 @@ def _route_desc(E, top_k, score, bias, n_groups, topk_groups, group_rule, renorm
 
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 _ROUTE_RECORDS = ("ids", "w", "counts", "offsets", "perm", "pos")
+_ROUTE_TYPES = (torch.int32, torch.float32, torch.int32, torch.int32, torch.int32, torch.int32)
 
 
 def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_groups=1, group_rule="max",
@@ -485,13 +486,16 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
         if recs[0] is None or recs[1] is None:
             raise ValueError("out must hold ids and w")
         pairs = (T, top_k)
-        for n, t, shape in zip(_ROUTE_RECORDS, recs, (pairs, pairs, (E,), (E + 1,), (T * top_k,), pairs)):
-            _tensor(n, t, torch.float32 if n == "w" else torch.int32, shape, index)
+        for n, t, dtype, shape in zip(_ROUTE_RECORDS, recs, _ROUTE_TYPES,
+                                      (pairs, pairs, (E,), (E + 1,), (T * top_k,), pairs)):
+            if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+                                  or not t.is_contiguous()):
+                _tensor(n, t, dtype, shape, index)
     lib = _lib or load()
-    size = ctypes.c_size_t(0)
     ref = ctypes.byref(desc)
-    _check(lib.moe_route_logits_workspace_size(ref, T, ctypes.byref(size)), "moe_route_logits")
-    ws = None
+    size, ws = ctypes.c_size_t(0), None
+    if T > 256:                                    # fewer tokens need none
+        _check(lib.moe_route_logits_workspace_size(ref, T, ctypes.byref(size)), "moe_route_logits")
     if size.value:
         # scratch from torch's allocator on the stream the kernels run on: every stream and captured graph has its own
         if stream is None:
@@ -500,8 +504,8 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
             with torch.cuda.stream(stream):
                 ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
     _run(lib.moe_route_logits, index, stream,
-         (ref, logits.data_ptr(), _DTYPE[logits.dtype], _row_stride("logits", logits), T, *map(_ptr, recs), _ptr(ws),
-          size.value), "moe_route_logits")
+         (ref, logits.data_ptr(), _DTYPE[logits.dtype], _row_stride("logits", logits), T,
+          *[None if t is None else t.data_ptr() for t in recs], _ptr(ws), size.value), "moe_route_logits")
     return out
 
 

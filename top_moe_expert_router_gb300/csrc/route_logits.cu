@@ -333,20 +333,22 @@ __device__ __forceinline__ uint32_t in_kept_groups(const RouteArgs &a, uint32_t 
     return on;
 }
 
+constexpr int kAll = -1, kGroups = -2;
+
 // The choice in 32 bits; *close (warp-uniform) says that some comparison was
-// within the error of what was compared (*near_groups: of the groups), or that
-// over 32 experts tied. buf: room
+// within the error of what was compared, or that over 32 experts tied; *again
+// then: kGroups, the groups' border was close; n (>= 0), only some of the n
+// gathered experts were, which no other can reach; kAll, anything else. buf: room
 // for E + E / 32 floats, and for 32 pairs.
 template <int EPL>
 __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)[EPL], float lmax, int64_t row, int lane,
-                                            float *buf, bool *close, bool *near_groups) {
+                                            float *buf, bool *close, int *again) {
     const int e0 = lane * EPL;
     const bool staged = a.keep < a.groups, by_logit = a.bias == nullptr;
     float c[EPL];
     const Scored sc = score_lane<EPL>(a, l, lmax, e0, !by_logit || (staged && a.top2), c);
     uint32_t on = sc.on;
-    bool near = false;
-    *near_groups = false;
+    bool near = false, near_groups = false;
     if (staged) {
         float b1, b2;
         group_best<EPL, float>(a, c, on, lane, buf, b1, b2);
@@ -360,7 +362,7 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
             const uint32_t hi = __reduce_max_sync(kFull, is_group && any && !kept ? order_key(score) : 0u);
             const uint32_t mag = __reduce_max_sync(
                 kFull, any ? __float_as_uint(fabsf(b1) + (b2 > -INFINITY ? fabsf(b2) : 0.f)) : 0u);
-            *near_groups = hi != 0u && !(key_value(lo) - key_value(hi) > 4.f * sc.err + 0x1p-22f * __uint_as_float(mag));
+            near_groups = hi != 0u && !(key_value(lo) - key_value(hi) > 4.f * sc.err + 0x1p-22f * __uint_as_float(mag));
         }
         on = in_kept_groups<EPL>(a, on, kept, e0);
         if (by_logit) {
@@ -373,8 +375,10 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
     for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? order_key(c[i]) : 0u;
     uint32_t mine;
     Pick r{-1, -INFINITY, 0};
-    const int n = gather_from<EPL>(key, lane_bound<EPL>(key, a.k + 1), lane, reinterpret_cast<uint2 *>(buf), &mine, &r.id);
+    const uint32_t bound = lane_bound<EPL>(key, a.k + 1);
+    const int n = gather_from<EPL>(key, bound, lane, reinterpret_cast<uint2 *>(buf), &mine, &r.id);
     near |= n > 32;
+    bool within = false;
     r.rank = rank_of(mine, min(n, 32), lane);
     if (r.id >= 0) r.l = one_logit(a, row, r.id);
     if (!by_logit) {
@@ -386,8 +390,14 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
             const float v = key_value(mine), x = buf[r.rank + 1];
             near |= !(v - x > 2.f * sc.err + 0x1p-22f * fmaxf(fabsf(v), fabsf(x)));
         }
+        // what was not gathered lies below the bound
+        if (n > 0 && n <= 32) {
+            const float v = buf[min(n, a.k) - 1], x = key_value(bound);
+            within = bound == 1u || v - x > 2.f * sc.err + 0x1p-22f * fmaxf(fabsf(v), fabsf(x));
+        }
     }
-    *close = __any_sync(kFull, near) || *near_groups;
+    *close = __any_sync(kFull, near) || near_groups;
+    *again = near_groups ? kGroups : within ? n : kAll;
     return r;
 }
 
@@ -546,6 +556,17 @@ __device__ __noinline__ Pick choose_exact(const RouteArgs &a, int64_t row, float
     return r;
 }
 
+// The places of n gathered experts by their scores in 64 bits.
+__device__ __noinline__ int rank_exact(const RouteArgs &a, int id, float l, int n, int lane) {
+    const uint64_t k64 = id >= 0 ? key_of(score64(a, l, 0.f, 1.0, id)) : 0ull;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const uint64_t o = __shfl_sync(kFull, k64, j);
+        rank += o > k64 - (j < lane ? 1ull : 0ull) ? 1 : 0;
+    }
+    return rank;
+}
+
 // The weight of a lane's pick (`on`: it is one of the first k).
 template <int EPL>
 __device__ __forceinline__ float pick_weight(const RouteArgs &a, const float (&l)[EPL], float lmax, const Pick &r,
@@ -593,9 +614,13 @@ __device__ __forceinline__ void select_chunk(const RouteArgs &a, int c, int32_t 
             for (int i = 1; i < EPL; ++i) m = max(m, order_key(l[i]));
             lmax = key_value(__reduce_max_sync(kFull, m));
         }
-        bool close, near_groups;
-        Pick r = choose_fast<EPL>(a, l, lmax, row, lane, lbuf, &close, &near_groups);
-        if (close) r = choose_exact<EPL>(a, row, lmax, lane, lbuf, near_groups);
+        bool close;
+        int again;
+        Pick r = choose_fast<EPL>(a, l, lmax, row, lane, lbuf, &close, &again);
+        if (close) {
+            if (again >= 0 && a.sigmoid) r.rank = rank_exact(a, r.id, r.l, again, lane);
+            else r = choose_exact<EPL>(a, row, lmax, lane, lbuf, again == kGroups);
+        }
         const bool picked = r.id >= 0 && r.rank < a.k;
         const float w = pick_weight<EPL>(a, l, lmax, r, picked);
         int32_t *ids = a.ids + (size_t)t * a.k;
