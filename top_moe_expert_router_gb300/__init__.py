@@ -432,9 +432,13 @@ def _input(name, t, types):
     return t.get_device()
 
 
-def _run(fn, index, stream, args, what):
-    """fn(*args, stream handle) with device `index` current; stream None: that device's current stream."""
-    st = _raw_stream(index) if stream is None else stream.cuda_stream
+def _handle(index, stream):
+    """The stream's handle; None: device `index`'s current stream."""
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _run(fn, index, st, args, what):
+    """fn(*args, stream handle) with device `index` current."""
     if index == torch.cuda.current_device():
         s = fn(*args, st)
     else:
@@ -494,18 +498,20 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
     lib = _lib or load()
     ref = ctypes.byref(desc)
     size, ws = ctypes.c_size_t(0), None
-    if T > 256:                                    # fewer tokens need none
+    if T > 256 and any(t is not None for t in recs[2:]):   # fewer tokens, or the choice alone, need none
         _check(lib.moe_route_logits_workspace_size(ref, T, ctypes.byref(size)), "moe_route_logits")
+    st = _handle(index, stream)
     if size.value:
         # scratch from torch's allocator on the stream the kernels run on: every stream and captured graph has its own
-        if stream is None:
-            ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
-        else:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
-    _run(lib.moe_route_logits, index, stream,
-         (ref, logits.data_ptr(), _DTYPE[logits.dtype], _row_stride("logits", logits), T,
-          *[None if t is None else t.data_ptr() for t in recs], _ptr(ws), size.value), "moe_route_logits")
+        # (without a tensor around it, which costs as much as the two launches)
+        ws = torch.cuda.caching_allocator_alloc(size.value, index, st)
+    try:
+        _run(lib.moe_route_logits, index, st,
+             (ref, logits.data_ptr(), _DTYPE[logits.dtype], _row_stride("logits", logits), T,
+              *[None if t is None else t.data_ptr() for t in recs], ws, size.value), "moe_route_logits")
+    finally:
+        if ws is not None:
+            torch.cuda.caching_allocator_delete(ws)
     return out
 
 
@@ -551,7 +557,7 @@ def add_rmsnorm(x, res=None, gain=None, *, eps=1e-6, out_dtype=None, group=0, su
                        _row_stride("x", x), _row_stride("res", res), _row_stride("sum_out", sum_out),
                        _row_stride("out", out), _row_stride("scales", scales), T, d, group, _DTYPE[dtype],
                        _DTYPE[out_dtype], eps)
-    _run((_lib or load()).moe_add_rmsnorm, index, stream, (ctypes.byref(args),), "moe_add_rmsnorm")
+    _run((_lib or load()).moe_add_rmsnorm, index, _handle(index, stream), (ctypes.byref(args),), "moe_add_rmsnorm")
     return out, sum_out, scales
 
 
@@ -595,7 +601,7 @@ def _linear_w4(fmt, x, q, s, g, z, x_scales, bias, out, out_dtype, stream):
                      x.data_ptr(), _DTYPE[x.dtype], _row_stride("x", x), _ptr(x_scales),
                      _row_stride("x_scales", x_scales), x_group, _ptr(bias), out.data_ptr(), _DTYPE[out.dtype],
                      _row_stride("out", out))
-    _run((_lib or load()).moe_linear_w4, index, stream, (ctypes.byref(args),), "moe_linear_w4")
+    _run((_lib or load()).moe_linear_w4, index, _handle(index, stream), (ctypes.byref(args),), "moe_linear_w4")
     return out
 
 
