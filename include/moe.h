@@ -288,7 +288,8 @@ typedef enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_F32 = 2, MOE_T_E4M3 = 3 } mo
  *   ids = the top_k best c within the kept groups, by descending c
  *   w[j] = scale * p[ids[j]], divided by the sum of the chosen p if renormalise
  * Ties go to the lower index, group or expert. The choice is that of scores
- * in 64-bit arithmetic. An expert whose logit is NaN or -inf takes no part in
+ * in 64-bit arithmetic, without a bias that of the logits (which order the
+ * scores; sums of two best always are of scores). An expert whose logit is NaN or -inf takes no part in
  * the softmax and is never chosen; nor is one whose bias is; +inf counts as
  * the largest finite float. Where fewer than top_k experts are left the
  * remaining slots hold id -1, weight 0 and pos -1.
@@ -315,8 +316,8 @@ moe_status moe_route_logits_workspace_size(const moe_route_desc *desc, int T, si
  * Entries of perm past offsets[E] are set to -1. The workspace (16-byte
  * aligned) may be NULL when none of the four is asked for; it needs no
  * initialisation and carries nothing from one call to the next; up to 256
- * tokens need none. T = 0 only
- * zeroes counts and offsets. */
+ * tokens need none. The outputs overlap neither each other nor the inputs. T = 0
+ * only zeroes counts and offsets. */
 moe_status moe_route_logits(const moe_route_desc *desc, const void *logits, moe_dtype type, int64_t row_stride, int T,
                             int32_t *ids, float *w, int32_t *counts, int32_t *offsets, int32_t *perm, int32_t *pos,
                             void *workspace, size_t ws_bytes, void *stream);
@@ -336,11 +337,14 @@ moe_status moe_layer_set_router(moe_layer *layer, const moe_route_desc *desc);
  *   s = round(x + res)   (to `type`; s = x without res)
  *   y = s / sqrt(mean(s^2) + eps) * gain
  * out_type = type: out = round(y). out_type = MOE_T_E4M3: for every `group`
- * columns (0: the whole row) scale = max|y| / 448 (1 for a group of zeros) and
- * out = E4M3(y / scale). fp32 arithmetic; the norm is of the rounded sum, as
- * moe_rmsnorm after moe_forward_residual. A row of zeros gives zeros (eps = 0
- * included). sum or out may be the same buffer as x or res, with the same
- * stride; any other overlap is not allowed. d <= 16384, group dividing d. */
+ * columns (0: the whole row) scale = max|y| / 448 (1 where that is no normal
+ * float: a group of zeros) and out = E4M3(y / scale). fp32 arithmetic; the norm
+ * is of the rounded sum, as moe_rmsnorm after moe_forward_residual. A row of
+ * zeros gives zeros (eps = 0 included); a row with an infinity or NaN gives what
+ * the formula does, zeros and NaN, and no other row is touched. sum, or out of
+ * the inputs' type, may be the same buffer as x or res, with the same stride;
+ * any other overlap is not allowed. d <= 16384, group dividing d, at most 4096
+ * groups. */
 typedef struct {
     const void *x;       /* [T, d] bf16, f16 or fp32 */
     const void *res;     /* [T, d] of the same type, or NULL */
@@ -365,7 +369,7 @@ moe_status moe_add_rmsnorm(const moe_norm_args *args, void *stream);
  * a multiple of 128 or 0 (one scale per token), as moe_add_rmsnorm writes
  * them. y [M, N] is bf16, f16 or fp32. Products and sums are fp32; more than 32
  * tokens read the weights twice. K a multiple of 32 and of the group,
- * K <= 32768; q 16-byte aligned, s 2-byte aligned; y overlaps no input. */
+ * K <= 32768, N <= 2^30; q 16-byte aligned, s 2-byte aligned; y overlaps no input. */
 typedef enum { MOE_W4_NVFP4 = 0, MOE_W4_INT4 = 1 } moe_w4_fmt;
 typedef struct {
     moe_w4_fmt fmt;

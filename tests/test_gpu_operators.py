@@ -184,6 +184,20 @@ def test_route_strides_offsets_and_partial_outputs(gpu_lib):
     check_route(gpu_lib.route_logits(logits, 4, out=out), logits, 4)
 
 
+@pytest.mark.parametrize("T,E,k", [(262144, 16, 3), (262144, 512, 16)])
+def test_route_largest(gpu_lib, T, E, k):
+    """The most tokens, and the most experts and picks, against a stable sort of the logits."""
+    logits = torch.randn(T, E, generator=gen(T + E), device="cuda")
+    got = gpu_lib.route_logits(logits, k)
+    val, order = torch.sort(logits.double(), dim=1, descending=True, stable=True)
+    ids = order[:, :k].int()
+    assert torch.equal(got["ids"], ids)
+    w = torch.softmax(val[:, :k], 1)
+    assert ((got["w"] - w).abs() <= w * 170 * 2.0 ** -24).all()       # as in check_route
+    for name, r in zip(("counts", "offsets", "perm", "pos"), ref_permute(ids.cpu().numpy(), E)):
+        np.testing.assert_array_equal(got[name].cpu().numpy(), r, err_msg=name)
+
+
 def test_route_of_no_tokens(gpu_lib):
     r = gpu_lib.route_logits(torch.empty((0, 16), device="cuda"), 2)
     assert r["ids"].shape == (0, 2) and r["perm"].numel() == 0
@@ -375,8 +389,9 @@ W4S = [
     (1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 40, 128), (1, 100, 160), (8, 129, 256), (9, 33, 384), (16, 64, 1024),
     (5, 300, 1152), (17, 31, 512), (32, 130, 640), (33, 70, 256), (64, 48, 2048), (1, 5000, 256), (4, 2500, 1536),
     (7, 64, 12288), (64, 20, 8192),
-    # many tiles: pairs of CTAs share runs of them
-    (3, 39000, 512), (8, 45001, 256), (1, 39040, 160), (12, 20000, 384), (20, 20011, 256),
+    # many tiles: every CTA walks several; the last ones stage their tokens anew for each
+    (3, 39000, 512), (8, 45001, 256), (1, 39040, 160), (12, 20000, 384), (20, 20011, 256), (30, 20011, 4096),
+    (64, 40, 32768), (64, 20011, 512),
 ]
 
 
@@ -468,6 +483,40 @@ def test_linear_takes_the_quantiser_output(gpu_lib):
     check_w4(gpu_lib, "nvfp4", x, (q[0], s[0], gs), Wq)
 
 
+def test_offsets_past_32_bits(gpu_lib):
+    """Rows that lie more than 2^32 elements apart, and weights of more than 2^32 bytes."""
+    g = gen(27)
+    T, ld = 18, 1 << 28                                    # the last row starts at 2^32 + 2^28
+    big = torch.zeros(T * ld, dtype=torch.bfloat16, device="cuda")
+    rows = big.as_strided((T, 320), (ld, 1))
+    rows.copy_(torch.randn(T, 320, generator=g, device="cuda"))
+    check_route(gpu_lib.route_logits(rows, 4), rows, 4)
+    w, W = make_w4("nvfp4", 50, 320, 16, False, None, g)
+    check_w4(gpu_lib, "nvfp4", rows, w, W)
+    out = big[1 << 20:].as_strided((T, 320), (ld, 1))
+    check_norm(gpu_lib, rows, None, None, out=out)
+    check_w4(gpu_lib, "nvfp4", out, w, W, out=big[2 << 20:].as_strided((T, 50), (ld, 1)))
+    del big, rows, out
+    N, K, last = (1 << 18) + 77, 32768, 300
+    for fmt, group in (("nvfp4", 16), ("int4", 128)):
+        (q, s, z), W = make_w4(fmt, last, K, group, True, "bf16", g)
+        bq = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+        bs = torch.zeros(N, K // group, dtype=s.dtype, device="cuda")
+        bq[-last:], bs[-last:] = q, s
+        if fmt == "int4":
+            bz = torch.zeros(N, K // group, dtype=torch.uint8, device="cuda")
+            bz[-last:] = z
+            z = bz
+        x = torch.randn(2, K, generator=g, device="cuda").to(torch.bfloat16)
+        y = call_w4(gpu_lib, fmt, x, (bq, bs, z), out_dtype=torch.float32)
+        small = call_w4(gpu_lib, fmt, x, (q, s, z if fmt == "nvfp4" else z[-last:]), out_dtype=torch.float32)
+        ref, size = x.double() @ W.t(), x.double().abs() @ W.abs().t()
+        tol = size * (8 * 17 + 4 * (K // 128 + 1) + 16) * 2.0 ** -23 + ref.abs() * 2.0 ** -24   # as in check_w4
+        assert ((y[:, -last:] - ref).abs() <= tol).all() and ((small - ref).abs() <= tol).all()
+        assert (y[:, :-last] == 0).all()
+        del bq, bs, y
+
+
 def test_linear_of_no_tokens(gpu_lib):
     (q, s, gs), _ = make_w4("nvfp4", 32, 64, 16, False, None, gen(16))
     assert gpu_lib.linear_nvfp4(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), q, s, gs).shape == (0, 32)
@@ -506,7 +555,7 @@ def test_bindings_refuse(gpu_lib):
     for call in (
         lambda: moe.route_logits(x, 17), lambda: moe.route_logits(x, 2, n_groups=3), lambda: moe.route_logits(x, 2, scale=NAN),
         lambda: moe.add_rmsnorm(x, eps=-1.0), lambda: moe.add_rmsnorm(torch.zeros(1, 20000, device="cuda")),
-        lambda: moe.linear_nvfp4(b.repeat(17, 1), q, s, gs),
+        lambda: moe.linear_nvfp4(b.repeat(17, 1), q, s, gs), lambda: moe.add_rmsnorm(x, b.float(), sum_out=x, out=x),
         lambda: moe.linear_int4(b, q, torch.ones(32, 4, dtype=torch.bfloat16, device="cuda")),
     ):
         with pytest.raises(moe.MoeError):

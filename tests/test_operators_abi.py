@@ -69,7 +69,7 @@ def test_set_router_rejects(lib):
 
 
 def _norm(**kw):
-    a = moe.MoeNormArgs(P, P, P, P, P, P, 4096, 4096, 4096, 4096, 32, 4, 4096, 128, moe.MOE_T_BF16, moe.MOE_T_E4M3,
+    a = moe.MoeNormArgs(P, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, 4096, 4096, 4096, 4096, 32, 4, 4096, 128, moe.MOE_T_BF16, moe.MOE_T_E4M3,
                         1e-6)
     for k, v in kw.items():
         setattr(a, k, v)
@@ -85,6 +85,9 @@ def _norm(**kw):
     (dict(res_stride=0), BAD), (dict(sum_stride=7), BAD), (dict(scales_stride=31), BAD),
     (dict(x=P + 1), BAD), (dict(res=P + 1), BAD), (dict(gain=P + 1), BAD), (dict(sum=P + 1), BAD),
     (dict(scales=P + 2), BAD),
+    (dict(sum=5 * P), BAD), (dict(out=P), BAD), (dict(out=2 * P), BAD),                     # sum is out; codes in place
+    (dict(sum=2 * P, sum_stride=4100), BAD), (dict(sum=P, x_stride=4100), BAD),             # in place, other rows
+    (dict(out_type=moe.MOE_T_BF16, group=0, out=P, out_stride=4100), BAD),
 ])
 def test_norm_arguments_rejected(lib, kw, want):
     if kw == dict(d=8192, group=1):            # 8192 groups: more than the kernel keeps
@@ -111,7 +114,7 @@ def _w4(**kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(M=-1), BAD), (dict(M=65), UNS), (dict(N=0), BAD), (dict(K=0), BAD), (dict(K=1000), UNS),
-    (dict(K=65536), UNS), (dict(fmt=2), UNS), (dict(group=16), UNS), (dict(group=256), UNS), (dict(K=1056), BAD),
+    (dict(K=65536), UNS), (dict(N=(1 << 30) + 1, y_stride=1 << 31), UNS), (dict(fmt=2), UNS), (dict(group=16), UNS), (dict(group=256), UNS), (dict(K=1056), BAD),
     (dict(fmt=moe.MOE_W4_NVFP4), UNS), (dict(fmt=moe.MOE_W4_NVFP4, group=16, g=None), BAD),
     (dict(s_type=moe.MOE_T_F32), UNS), (dict(x_type=moe.MOE_T_F32), UNS), (dict(y_type=moe.MOE_T_E4M3), UNS),
     (dict(x_group=64), UNS), (dict(x_group=384), BAD), (dict(x_group=-128), BAD), (dict(x_scales=None), BAD),

@@ -260,6 +260,8 @@ class MoeLayer:
         """Choose the layer's experts as ``route_logits`` does, from the layer's own
         router logits; see ``clear_router``. ``bias``: [E] fp32 CUDA tensor or None."""
         desc = _route_desc(self.E, self.k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale)
+        if bias is not None and bias.device != self.workspace.device:
+            raise ValueError(f"bias: on {bias.device}, the layer on {self.workspace.device}")
         _check(load().moe_layer_set_router(self._h, ctypes.byref(desc)), "moe_layer_set_router")
         self._router_bias = bias
 

@@ -372,7 +372,7 @@ __device__ __forceinline__ void mul_block(const W4Args &a, uint32_t codes, uint3
 
 // y of a tile's rows that this part owns, from the sums of all parts.
 __device__ __forceinline__ void store_tile(const W4Args &a, const float *sums, int parts, int own, int part, int mp, int m0,
-                                        int mt, int row0, int rows, float gs, bool failed) {
+                                        int mt, int row0, int rows, float gs) {
     const int first = part * own, n_own = min(own, rows - first);
     for (int e = threadIdx.x; e < own * mt; e += kConsThreads) {
         const int m = e / own, r = e - m * own, n = row0 + first + r;
@@ -380,7 +380,7 @@ __device__ __forceinline__ void store_tile(const W4Args &a, const float *sums, i
         const float *at = sums + r * mp + m;
         float v = 0.f;
         for (int p = 0; p < parts; ++p) v += at[2 * p * own * mp] + at[(2 * p + 1) * own * mp];
-        v = failed ? NAN : v * gs;
+        v *= gs;
         if (a.bias) v += __ldg(a.bias + n);
         const int64_t o = (int64_t)(m0 + m) * a.y_ld + n;
         if (a.y_type == MOE_T_F32) ((float *)a.y)[o] = v;
@@ -393,7 +393,7 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // mbarrier wait that gives up after kWaitLimitNs (or once another warp has)
-// and says so in *bad; the outputs are then NaN.
+// and says so in *bad; the tile's outputs are then NaN.
 __device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, volatile int *bad) {
     if (mbar_try_wait(bar, parity)) return;
     const unsigned long long t0 = global_ns();
@@ -543,6 +543,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
         // done reading the other buffer's last tile.
         const uint32_t sums = smem_u32(red) + buf * (parts * 2 * own * MP * 4);
         if (parts > 1 && tile == (int)blockIdx.y) cluster_wait();  // every CTA of the cluster runs
+        if (*bad) {                              // a wait that gave up: the rows' owners store NaN
+#pragma unroll
+            for (int h = 0; h < MT; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[h][n][e] = NAN;
+        }
 #pragma unroll
         for (int h = 0; h < MT; ++h)
 #pragma unroll
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
         } else {
             named_bar(1, kConsThreads);
         }
-        store_tile(a, red + buf * (parts * 2 * own * MP), parts, own, part, MP, m0, mt, tile * kR, kR, gs, *bad != 0);
+        store_tile(a, red + buf * (parts * 2 * own * MP), parts, own, part, MP, m0, mt, tile * kR, kR, gs);
     }
     if (parts > 1) {                             // no CTA leaves while another may still write to it
         cluster_arrive();

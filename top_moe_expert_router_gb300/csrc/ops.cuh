@@ -91,6 +91,7 @@ struct W4Args {
 };
 constexpr int kW4MaxM = 64;
 constexpr int kW4MaxK = 32768;
+constexpr int kW4MaxN = 1 << 30;
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st);
 
 #ifdef __CUDACC__

@@ -119,6 +119,14 @@ moe_status moe_add_rmsnorm(const moe_norm_args *n, void *stream) {
     if (n->x_stride < n->d || n->out_stride < n->d || (n->res && n->res_stride < n->d) ||
         (n->sum && n->sum_stride < n->d) || (e4m3 && n->scales_stride < n->d / group))
         return MOE_ERR_INVALID_ARG;
+    // in place means the same rows; the E4M3 codes of one would lie over another's elements
+    if (n->sum == n->out) return MOE_ERR_INVALID_ARG;
+    struct { const void *in; int64_t ld; } in[2] = {{n->x, n->x_stride}, {n->res, n->res_stride}};
+    for (const auto &i : in) {
+        if (!i.in) continue;
+        if (n->out == i.in && (e4m3 || (n->T > 1 && n->out_stride != i.ld))) return MOE_ERR_INVALID_ARG;
+        if (n->sum == i.in && n->T > 1 && n->sum_stride != i.ld) return MOE_ERR_INVALID_ARG;
+    }
     NormArgs a{};
     a.x = n->x;
     a.res = n->res;
@@ -142,8 +150,8 @@ moe_status moe_add_rmsnorm(const moe_norm_args *n, void *stream) {
 
 moe_status moe_linear_w4(const moe_w4_args *l, void *stream) {
     if (!l || l->M < 0 || l->N < 1 || l->K < 1) return MOE_ERR_INVALID_ARG;
-    if ((l->fmt != MOE_W4_NVFP4 && l->fmt != MOE_W4_INT4) || l->M > kW4MaxM || l->K > kW4MaxK || l->K % 32)
-        return MOE_ERR_UNSUPPORTED;
+    if (l->fmt != MOE_W4_NVFP4 && l->fmt != MOE_W4_INT4) return MOE_ERR_UNSUPPORTED;
+    if (l->M > kW4MaxM || l->N > kW4MaxN || l->K > kW4MaxK || l->K % 32) return MOE_ERR_UNSUPPORTED;
     if (l->x_type != MOE_T_BF16 && l->x_type != MOE_T_F16 && l->x_type != MOE_T_E4M3) return MOE_ERR_UNSUPPORTED;
     if (!is_float_type(l->y_type)) return MOE_ERR_UNSUPPORTED;
     const bool nvfp4 = l->fmt == MOE_W4_NVFP4;
