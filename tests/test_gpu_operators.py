@@ -115,6 +115,10 @@ ROUTES = [
     (257, 256, 8, "bf16", {}),
     (8193, 96, 4, "f16", dict(n_groups=6, topk_groups=2)),                       # chunks of more than 32 tokens
     (17000, 20, 3, "f32", dict(score="sigmoid", bias=True)),
+    (140, 272, 8, "f32", dict(score="sigmoid", n_groups=8, topk_groups=3)),      # the kept experts in few lanes
+    (84, 343, 16, "bf16", dict(renormalise=False)),
+    (90, 300, 16, "f32", dict(score="softmax", bias=True, n_groups=6, topk_groups=1, group_rule="top2")),
+    (1225, 455, 11, "f16", dict(score="softmax", bias=True)),
 ]
 
 
@@ -262,7 +266,7 @@ def check_norm(moe, x, res, gain, eps=1e-6, out_dtype=None, group=0, **kw):
 
 NORMS = [(1, 8), (3, 16), (9, 64), (17, 128), (5, 200), (4, 264), (8, 520), (2, 1000), (3, 1024), (2, 1536), (5, 2048),
          (3, 4096), (2, 5000), (2, 8192), (3, 12288), (2, 16384), (1, 1), (4, 7), (3, 100), (2, 129), (2, 1001), (1, 4097),
-         (2, 16383)]
+         (2, 16383), (3, 130), (5, 602), (7, 1102), (2, 2050), (3, 4100), (2, 8194), (2, 16382), (600, 514), (3, 2001), (2, 8193)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])

@@ -38,39 +38,55 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// V consecutive elements as they lie in memory, by 16-byte accesses (V = 1: by itself).
+// What V elements are accessed as: 2 to 16 bytes at a time.
+template <int B>
+struct Words { using type = uint4; };
+template <>
+struct Words<8> { using type = uint2; };
+template <>
+struct Words<4> { using type = uint32_t; };
+template <typename T, int V>
+constexpr int kAccess = V * (int)sizeof(T) < 16 ? V * (int)sizeof(T) : 16;
+
+// V consecutive elements as they lie in memory (V = 1: by itself, widened).
 template <typename T, int V>
 struct Packed {
-    static constexpr int N = V == 1 ? 1 : V * (int)sizeof(T) / 16;
-    uint4 u[N];                                  // V = 1: the value in u[0].x
+    static constexpr int W = V == 1 ? 1 : V * (int)sizeof(T) / 4;
+    uint32_t u[W];
     __device__ __forceinline__ void load(const T *p) {
         if constexpr (V == 1) {
-            u[0].x = __float_as_uint(to_f32<T>(*p));
+            u[0] = __float_as_uint(to_f32<T>(*p));
         } else {
+            constexpr int A = kAccess<T, V>;
+            using U = typename Words<A>::type;
 #pragma unroll
-            for (int i = 0; i < N; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
+            for (int i = 0; i < 4 * W / A; ++i) {
+                const U v = reinterpret_cast<const U *>(p)[i];
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+#pragma unroll
+                for (int j = 0; j < A / 4; ++j) u[i * (A / 4) + j] = w[j];
+            }
         }
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < W; ++i) u[i] = 0u;
     }
     __device__ __forceinline__ void get(float f[V]) const {
         if constexpr (V == 1) {
-            f[0] = __uint_as_float(u[0].x);
+            f[0] = __uint_as_float(u[0]);
         } else {
-            constexpr int per = 16 / sizeof(T);
+            constexpr int per = 4 / sizeof(T);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            for (int i = 0; i < W; ++i) {
 #pragma unroll
                 for (int j = 0; j < per; ++j) {
                     if constexpr (sizeof(T) == 4) {
-                        f[i * per + j] = __uint_as_float(w[j]);
+                        f[i] = __uint_as_float(u[i]);
                     } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                        f[i * per + j] = (j & 1) ? bf16hi(w[j >> 1]) : bf16lo(w[j >> 1]);
+                        f[i * per + j] = j ? bf16hi(u[i]) : bf16lo(u[i]);
                     } else {
-                        f[i * per + j] = __half2float(__ushort_as_half((uint16_t)(w[j >> 1] >> (16 * (j & 1)))));
+                        f[i * per + j] = __half2float(__ushort_as_half((uint16_t)(u[i] >> (16 * j))));
                     }
                 }
             }
@@ -82,14 +98,15 @@ __device__ __forceinline__ void store_vec(T *p, const float f[V]) {
     if constexpr (V == 1) {
         *p = from_f32<T>(f[0]);
     } else {
-        constexpr int per = 16 / sizeof(T);
+        constexpr int A = kAccess<T, V>, per = A / (int)sizeof(T);
+        using U = typename Words<A>::type;
 #pragma unroll
         for (int i = 0; i < V; i += per) {
-            uint4 u;
+            U u;
             T *e = reinterpret_cast<T *>(&u);
 #pragma unroll
             for (int j = 0; j < per; ++j) e[j] = from_f32<T>(f[i + j]);
-            *reinterpret_cast<uint4 *>(p + i) = u;
+            *reinterpret_cast<U *>(p + i) = u;
         }
     }
 }
@@ -311,6 +328,9 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) add_rmsnorm_kernel(Norm
                 if (c < d) {
                     if constexpr (V == 1) {
                         o[v * TPR] = (uint8_t)__nv_cvt_float_to_fp8(s[v][0], __NV_SATFINITE, __NV_E4M3);
+                    } else if constexpr (V == 2) {
+                        *reinterpret_cast<uint16_t *>(o + v * TPR * V) =
+                            (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(s[v][0], s[v][1]), __NV_SATFINITE, __NV_E4M3);
                     } else {
                         uint32_t pk[V / 4];
 #pragma unroll
@@ -331,7 +351,7 @@ template <typename T, bool E4M3, int TPR, int V, int NV>
 cudaError_t launch_one(const NormArgs &a, cudaStream_t st) {
     constexpr int ROWS = TPR == 32 ? 8 : 1;
     // the next row (x and res) and the gain in registers while they take at most 48
-    constexpr bool PF = V > 1 && NV * V * (int)sizeof(T) <= 64;
+    constexpr bool PF = V > 1 && NV <= 8 && NV * V * (int)sizeof(T) <= 64;
     const auto kern = add_rmsnorm_kernel<T, E4M3, TPR, V, NV, PF>;
     const int ng = a.d / a.group;
     const size_t smem = E4M3 && ng > 1 ? (size_t)ROWS * ng * 4 : 0;
@@ -353,10 +373,17 @@ template <typename T, bool E4M3, int V>
 cudaError_t launch_shape(const NormArgs &a, cudaStream_t st) {
     // one warp per row up to 4 vectors a lane, then one CTA per row
     const int nv = (a.d + V - 1) / V;
-    if constexpr (V == 1) {
+    if constexpr (V <= 2) {
+        // rows off the 16-byte boundaries (12361 x 1102 fp32: 36 us by pairs; by single
+        // elements with 1024 threads of 16 each it took 250)
         if (nv <= 128) return launch_one<T, E4M3, 32, V, 4>(a, st);
+        if (nv <= 512) return launch_one<T, E4M3, 128, V, 4>(a, st);
         if (nv <= 1024) return launch_one<T, E4M3, 256, V, 4>(a, st);
-        return launch_one<T, E4M3, 1024, V, 16>(a, st);
+        if (nv <= 2048) return launch_one<T, E4M3, 256, V, 8>(a, st);
+        if (nv <= 4096) return launch_one<T, E4M3, 512, V, 8>(a, st);
+        if constexpr (V == 1)
+            if (nv > 8192) return launch_one<T, E4M3, 1024, V, 16>(a, st);
+        return launch_one<T, E4M3, 512, V, 16>(a, st);
     }
     if (nv <= 32) return launch_one<T, E4M3, 32, V, 1>(a, st);
     if (nv <= 64) return launch_one<T, E4M3, 32, V, 2>(a, st);
@@ -370,15 +397,18 @@ cudaError_t launch_shape(const NormArgs &a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_type(const NormArgs &a, cudaStream_t st) {
-    constexpr int V = 8;
     const int es = sizeof(T);
-    auto row16 = [&](const void *p, int64_t ld, int size) {
-        return !p || ((uintptr_t)p % 16 == 0 && (ld * size) % 16 == 0);
+    // whether every row of every array starts on a boundary of v elements, up to 16 bytes
+    auto fits = [&](int v) {
+        auto row = [&](const void *p, int64_t ld, int size) {
+            const int b = v * size < 16 ? v * size : 16;
+            return !p || ((uintptr_t)p % b == 0 && (ld * size) % b == 0);
+        };
+        return a.d % v == 0 && row(a.x, a.x_ld, es) && row(a.res, a.res_ld, es) && row(a.sum, a.sum_ld, es) &&
+               row(a.gain, 0, es) && row(a.out, a.out_ld, a.e4m3 ? 1 : es);
     };
-    const bool vec = a.d % V == 0 && row16(a.x, a.x_ld, es) && row16(a.res, a.res_ld, es) &&
-                     row16(a.sum, a.sum_ld, es) && row16(a.gain, 0, es) &&
-                     (a.e4m3 ? (uintptr_t)a.out % 8 == 0 && a.out_ld % 8 == 0 : row16(a.out, a.out_ld, es));
-    if (vec) return a.e4m3 ? launch_shape<T, true, V>(a, st) : launch_shape<T, false, V>(a, st);
+    if (fits(8)) return a.e4m3 ? launch_shape<T, true, 8>(a, st) : launch_shape<T, false, 8>(a, st);
+    if (fits(2)) return a.e4m3 ? launch_shape<T, true, 2>(a, st) : launch_shape<T, false, 2>(a, st);
     return a.e4m3 ? launch_shape<T, true, 1>(a, st) : launch_shape<T, false, 1>(a, st);
 }
 

@@ -24,7 +24,9 @@
 // on. The (k + 1)-th largest of the lanes' maxima is a lower bound of the
 // (k + 1)-th best expert: the few experts that reach it (about 13 for k = 8) are
 // gathered one to a lane, in order of their ids, and ranked by comparing each
-// with all. That takes half the instructions of k rounds of "best of all".
+// with all. That takes half the instructions of k rounds of "best of all". Where
+// over 32 reach it (the live experts lie in few lanes) they are spread first: 140
+// tokens of 272 experts, 3 of 8 groups kept, 42 -> 15 us.
 // The kernel is bound by its instructions: about 450 a token without scores,
 // 900 with a bias and groups.
 #include <math.h>
@@ -190,6 +192,63 @@ __device__ __forceinline__ int gather_from(const uint32_t (&key)[EPL], uint32_t 
     return n;
 }
 
+// The rest of gather_spread: cand holds the live keys, behind them (at cand + E)
+// room for 32 pairs.
+struct Gathered {
+    uint32_t bound, key;
+    int n, id;
+};
+__device__ __noinline__ Gathered gather_live(const uint2 *cand, uint2 *out, int live, int want, float slack, float rel,
+                                             int lane) {
+    uint32_t top[1] = {0u};
+    for (int p = lane; p < live; p += 32) top[0] = max(top[0], cand[p].x);
+    Gathered r;
+    r.bound = lane_bound<1>(top, want);
+    if (slack >= 0.f && r.bound > 1u) {
+        const float x = key_value(r.bound);
+        r.bound = order_key(x - (slack + rel * fabsf(x)));
+    }
+    r.n = 0;
+    for (int p0 = 0; p0 < live; p0 += 32) {
+        const uint2 v = p0 + lane < live ? cand[p0 + lane] : make_uint2(0u, 0u);
+        const uint32_t hits = __ballot_sync(kFull, v.x >= r.bound);
+        const int to = r.n + __popc(hits & ((1u << lane) - 1u));
+        if (v.x >= r.bound && to < 32) out[to] = v;
+        r.n += __popc(hits);
+    }
+    __syncwarp();
+    const bool mine = r.n <= 32 && lane < r.n;
+    r.key = mine ? out[lane].x : 0u;
+    r.id = mine ? (int)out[lane].y : -1;
+    return r;
+}
+
+// gather_from for keys that lie in few lanes (kept groups, or E much below 32
+// EPL), where the lanes' maxima say little: the live keys are first spread over
+// all lanes, item 32 j + lane in order of the ids. The bound: the `want`-th largest
+// of those lanes' maxima, less slack + rel |bound| where slack is not negative.
+// cand: room for E pairs and 32 more.
+template <int EPL>
+__device__ __forceinline__ Gathered gather_spread(const RouteArgs &a, const uint32_t (&key)[EPL], int want, float slack,
+                                                  float rel, int lane, uint2 *cand) {
+    int cnt = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) cnt += key[i] != 0u ? 1 : 0;
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncwarp();
+    uint2 *at = cand + (incl - cnt);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (key[i] != 0u) *at++ = make_uint2(key[i], (uint32_t)(lane * EPL + i));
+    __syncwarp();
+    return gather_live(cand, cand + a.E, __shfl_sync(kFull, incl, 31), want, slack, rel, lane);
+}
+
 // The place of a lane's key among n gathered ones; ties to the lower lane.
 __device__ __forceinline__ int rank_of(uint32_t key, int n, int lane) {
     int rank = 0;
@@ -209,7 +268,11 @@ __device__ __forceinline__ int rank_of(uint32_t key, int n, int lane) {
 // most 0.64 * 2^-23; with the sum's and the reciprocal's roundings under
 // 2.2 * 2^-23: 2^-21 is allowed. Softmax: likewise t exp(-t) of a term's
 // argument, and about 25 roundings of the sum: 2^-18 of the largest score 1 / z
-// is allowed. The bias adds a rounding of 2^-24 of the sum.
+// is allowed, and for one expert own_err of that: relative to its score p =
+// exp(-t) / z, its term's (2 + 1.2 t) 2^-23, z's (a mean of the same over the
+// terms, under 10 * 2^-23 for 512 of them, and 25 roundings) and those of the
+// quotient: under (27 + 1.2 t) 2^-23 of p. The bias adds a rounding of 2^-24 of
+// the sum.
 struct Scored {
     uint32_t on;
     float err;
@@ -262,6 +325,11 @@ __device__ __forceinline__ Scored score_lane(const RouteArgs &a, const float (&l
         }
     }
     return r;
+}
+
+__device__ __forceinline__ float own_err(const RouteArgs &a, float err, float l, float lmax) {
+    const float t = lmax - l;
+    return a.sigmoid ? err : err * __expf(-t) * (1.f + 0.04f * t) + 1e-37f;
 }
 
 // The two best of every group, with the lpg lanes of a group (a power of two).
@@ -375,8 +443,13 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
     for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? order_key(c[i]) : 0u;
     uint32_t mine;
     Pick r{-1, -INFINITY, 0};
-    const uint32_t bound = lane_bound<EPL>(key, a.k + 1);
-    const int n = gather_from<EPL>(key, bound, lane, reinterpret_cast<uint2 *>(buf), &mine, &r.id);
+    uint32_t bound = lane_bound<EPL>(key, a.k + 1);
+    uint2 *cand = reinterpret_cast<uint2 *>(buf);
+    int n = gather_from<EPL>(key, bound, lane, cand, &mine, &r.id);
+    if (EPL > 1 && n > 32) {
+        const Gathered s = gather_spread<EPL>(a, key, a.k + 1, -1.f, 0.f, lane, cand);
+        bound = s.bound, mine = s.key, n = s.n, r.id = s.id;
+    }
     near |= n > 32;
     bool within = false;
     r.rank = rank_of(mine, min(n, 32), lane);
@@ -384,11 +457,12 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
     if (!by_logit) {
         // each pick against the next one, the last against the border
         __syncwarp();
-        if (r.id >= 0) buf[r.rank] = key_value(mine);
+        const float own = own_err(a, sc.err, r.l, lmax);
+        if (r.id >= 0) buf[r.rank] = key_value(mine), buf[32 + r.rank] = own;
         __syncwarp();
         if (r.id >= 0 && r.rank < a.k && r.rank + 1 < n) {
             const float v = key_value(mine), x = buf[r.rank + 1];
-            near |= !(v - x > 2.f * sc.err + 0x1p-22f * fmaxf(fabsf(v), fabsf(x)));
+            near |= !(v - x > own + buf[33 + r.rank] + 0x1p-22f * fmaxf(fabsf(v), fabsf(x)));
         }
         // what was not gathered lies below the bound
         if (n > 0 && n <= 32) {
@@ -401,21 +475,37 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
     return r;
 }
 
+// One copy of the code, and loops that stay loops: the 64-bit steps run for few
+// tokens, by warps that find none of it in the instruction cache (1225 tokens of
+// 455 experts, some decided in 64 bits: 41 us with the sum unrolled over 16 experts
+// a lane, 32 us so, 19 us where no token is close).
+__device__ __noinline__ double exp64(double x) { return exp(x); }
+
 // The softmax's sum in 64 bits (1 where no expert is live).
-template <int EPL>
-__device__ __forceinline__ double sum64(const float (&l)[EPL], float lmax) {
+__device__ __noinline__ double sum64(const RouteArgs &a, int64_t row, float lmax, int lane) {
     double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s += l[i] > -INFINITY ? exp((double)l[i] - (double)lmax) : 0.0;
+    auto load = [&](int e) {
+        if (e >= a.E) return -INFINITY;
+        float l = load_logit(a.logits, row + e, a.type);
+        for (int i = 1; i < a.nsplit; ++i) l += ((const float *)a.logits)[row + i * a.split_stride + e];
+        return l;
+    };
+    float next = load(lane);
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32) {
+        const float l = next;
+        next = load(e + 32);
+        if (l > -INFINITY) s += exp64((double)fminf(l, 3.402823466e38f) - (double)lmax);
+    }
     s = warp_add(s);
     return s > 0.0 ? s : 1.0;
 }
 
 // A score in 64 bits.
 __device__ __forceinline__ double score64(const RouteArgs &a, float l, float lmax, double z, int e) {
-    double p = l;
-    if (a.sigmoid) p = 1.0 / (1.0 + exp(-(double)l));
-    else p = exp((double)l - (double)lmax) / z;
+    double p;
+    const double x = exp64(a.sigmoid ? -(double)l : (double)l - (double)lmax);
+    p = a.sigmoid ? 1.0 / (1.0 + x) : x / z;
     return a.bias ? p + (double)fminf(__ldg(a.bias + e), 3.402823466e38f) : p;
 }
 
@@ -430,7 +520,7 @@ __device__ __noinline__ Pick choose_general(const RouteArgs &a, int64_t row, flo
     const bool scored = !by_logit || (staged && a.top2);
     uint32_t on = score_lane<EPL>(a, l, lmax, e0, scored, c).on;
     double z = 1.0, d[EPL];
-    if (scored && !a.sigmoid) z = sum64<EPL>(l, lmax);
+    if (scored && !a.sigmoid) z = sum64(a, row, lmax, lane);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) d[i] = scored ? score64(a, l[i], lmax, z, min(e0 + i, a.E - 1)) : (double)l[i];
     if (staged) {
@@ -485,7 +575,7 @@ __device__ __noinline__ Pick choose_exact(const RouteArgs &a, int64_t row, float
     uint32_t on = sc.on, key[EPL], mine;
     uint2 *cand = reinterpret_cast<uint2 *>(buf);
     double z = 1.0;
-    if (scored && !a.sigmoid) z = sum64<EPL>(l, lmax);
+    if (scored && !a.sigmoid) z = sum64(a, row, lmax, lane);
     Pick r{-1, -INFINITY, lane};
     if (staged) {
         float f1, f2;
@@ -535,12 +625,9 @@ __device__ __noinline__ Pick choose_exact(const RouteArgs &a, int64_t row, float
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? order_key(by_logit ? l[i] : c[i]) : 0u;
-    uint32_t bound = lane_bound<EPL>(key, a.k);
-    if (!by_logit && bound > 1u) {
-        const float x = key_value(bound);
-        bound = order_key(x - (2.f * sc.err + 0x1p-20f * fabsf(x)));
-    }
-    const int n = gather_from<EPL>(key, bound, lane, cand, &mine, &r.id);
+    const Gathered s = gather_spread<EPL>(a, key, a.k, by_logit ? -1.f : 2.f * sc.err, 0x1p-20f, lane, cand);
+    const int n = s.n;
+    mine = s.key, r.id = s.id;
     if (n > 32) return choose_general<EPL>(a, row, lmax, lane, buf);
     if (r.id >= 0) r.l = one_logit(a, row, r.id);
     if (by_logit) {
@@ -557,8 +644,9 @@ __device__ __noinline__ Pick choose_exact(const RouteArgs &a, int64_t row, float
 }
 
 // The places of n gathered experts by their scores in 64 bits.
-__device__ __noinline__ int rank_exact(const RouteArgs &a, int id, float l, int n, int lane) {
-    const uint64_t k64 = id >= 0 ? key_of(score64(a, l, 0.f, 1.0, id)) : 0ull;
+__device__ __noinline__ int rank_exact(const RouteArgs &a, int64_t row, float lmax, int id, float l, int n, int lane) {
+    const double z = a.sigmoid ? 1.0 : sum64(a, row, lmax, lane);
+    const uint64_t k64 = id >= 0 ? key_of(score64(a, l, lmax, z, id)) : 0ull;
     int rank = 0;
     for (int j = 0; j < n; ++j) {
         const uint64_t o = __shfl_sync(kFull, k64, j);
@@ -618,7 +706,7 @@ __device__ __forceinline__ void select_chunk(const RouteArgs &a, int c, int32_t 
         int again;
         Pick r = choose_fast<EPL>(a, l, lmax, row, lane, lbuf, &close, &again);
         if (close) {
-            if (again >= 0 && a.sigmoid) r.rank = rank_exact(a, r.id, r.l, again, lane);
+            if (again >= 0) r.rank = rank_exact(a, row, lmax, r.id, r.l, again, lane);
             else r = choose_exact<EPL>(a, row, lmax, lane, lbuf, again == kGroups);
         }
         const bool picked = r.id >= 0 && r.rank < a.k;
