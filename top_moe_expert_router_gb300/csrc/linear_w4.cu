@@ -405,6 +405,7 @@ __device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, volati
 }
 
 struct Shape {
+    int tokens;     // of a token block
     int parts;      // CTAs of a cluster, along K
     int st_pass;    // stages whose x is staged at a time
     int ring;       // stages in flight
@@ -414,15 +415,15 @@ struct Shape {
 
 // blockIdx.x: the part of K; .y: the first row tile (then every gridDim.y-th);
 // .z: the token block. x is staged once where the CTA's part of it fits.
-template <int NT, int MT, bool NVFP4, int G, bool TS>
-__global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_constant__ CUtensorMap tq,
+template <int NT, int MT, int CPS, bool NVFP4, int G, bool TS>
+__global__ void __launch_bounds__(kThreads, CPS) linear_w4_kernel(const __grid_constant__ CUtensorMap tq,
                                                                 const __grid_constant__ CUtensorMap ts, const W4Args a,
                                                                 const Shape sh) {
     extern __shared__ __align__(1024) unsigned char smem[];
     constexpr int MP = 8 * NT + 2;               // even for stores of two columns, and rows on different banks
     constexpr int kR = kRows<MT>, kSt = kStage<MT, TS>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int m0 = blockIdx.z * 8 * NT, mt = min(8 * NT, a.M - m0);
+    const int m0 = blockIdx.z * sh.tokens, mt = min(sh.tokens, a.M - m0);
     const int tiles = (a.N + kR - 1) / kR, parts = sh.parts, part = blockIdx.x;
     const int nst = (a.K + 255) / 256;
     const int s0 = (int)((int64_t)part * nst / parts), s1 = (int)((int64_t)(part + 1) * nst / parts);
@@ -595,48 +596,81 @@ bool code_map(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, u
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, int MT, bool NVFP4, int G, bool TS>
+// Clusters of 1 to 8 CTAs with `smem` bytes each that the device holds at once, as
+// n[1 .. 8]; asked for once per kernel and device. (Fewer than the SMs suggest: a
+// cluster's CTAs lie in one group of SMs.)
+constexpr int kMaxDevices = 64;
+struct Clusters {
+    std::atomic<int> n[kMaxDevices][9];
+};
+cudaError_t resident_clusters(const void *kern, size_t smem, int dev, Clusters &known, int (&n)[9]) {
+    for (int p = 1; p <= 8; ++p) {
+        n[p] = dev < kMaxDevices ? known.n[dev][p].load(std::memory_order_relaxed) : 0;
+        if (n[p] > 0) continue;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(p, 1024);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = p;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n[p], kern, &cfg);
+        if (e != cudaSuccess) return e;
+        if (dev < kMaxDevices) known.n[dev][p].store(n[p], std::memory_order_relaxed);
+    }
+    return n[1] > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+template <int NT, int MT, int CPS, bool NVFP4, int G, bool TS>
 cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     static std::atomic<uint64_t> attr_set{0};
-    const auto kern = linear_w4_kernel<NT, MT, NVFP4, G, TS>;
+    const auto kern = linear_w4_kernel<NT, MT, CPS, NVFP4, G, TS>;
     cudaError_t e = set_smem_limit_once((const void *)kern, 226 * 1024, attr_set);
     if (e != cudaSuccess) return e;
-    int dev = 0, sms = 0;
+    int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     CUtensorMap tq, ts;
     constexpr int R = kRows<MT>;
     if (!code_map(&tq, a.q, a.N, a.K / 2, 64, R, !NVFP4)) return cudaErrorInvalidValue;
     Shape sh{};
     ts = tq;
     if (TS && !code_map(&ts, a.s, a.N, a.K / 16, 16, R, false)) return cudaErrorInvalidValue;
-    const int mt = a.M < 8 * NT ? a.M : 8 * NT, mb = (a.M + 8 * NT - 1) / (8 * NT);
-    const int nst = (a.K + 255) / 256, tiles = (a.N + R - 1) / R, slots = 2 * sms;
-    constexpr int kSt = kStage<MT, TS>, kHalf = 112 * 1024, kBars = 16 * 8 + 16;
+    const int mb = (a.M + 8 * NT - 1) / (8 * NT), mt = (a.M + mb - 1) / mb;
+    sh.tokens = mt;
+    const int nst = (a.K + 255) / 256, tiles = (a.N + R - 1) / R;
+    constexpr int kSt = kStage<MT, TS>, kRoom = CPS == 2 ? 112 * 1024 : 225 * 1024, kBars = 16 * 8 + 16;
     const int xst = 8 * pair_stride(mt) * 16 + 8 * mt;  // bytes of x and its scales for one stage
     auto sums_bytes = [&](int p) { return (p * 4 * ((R + p - 1) / p) * (8 * NT + 2) * 4 + 15) / 16 * 16; };
-    // K in 1 to 8 parts: the fewest stages that one of the 2 * sms CTAs at a
-    // time takes, a tile's start and sum counted as four, and half as many again
-    // where x does not fit beside two stages and is staged anew for every tile
+    static Clusters known;
+    int resident[9];
+    if ((e = resident_clusters((const void *)kern, kRoom, dev, known, resident)) != cudaSuccess) return e;
+    // K in 1 to 8 parts: the fewest stages that one of the resident CTAs takes, a
+    // tile's start and sum counted as four, and half as many again where x does not
+    // fit beside two stages and is staged anew for every tile
     sh.parts = 1;
     int64_t best = INT64_MAX;
     for (int p = 1; p <= 8 && 2 * p <= nst + 1; ++p) {
         const int st = (nst + p - 1) / p;
-        int64_t per = ((int64_t)tiles * p * mb + slots - 1) / slots * (st + 4);
-        if (st * xst + sums_bytes(p) + 2 * kSt + kBars > kHalf) per += per / 2;
+        if (resident[p] < 1) continue;
+        int64_t per = ((int64_t)tiles * mb + resident[p] - 1) / resident[p] * (st + 4);
+        if (st * xst + sums_bytes(p) + 2 * kSt + kBars > kRoom) per += per / 2;
         if (per < best) {
             best = per;
             sh.parts = p;
         }
     }
     // each CTA stages its part of x once and walks the row tiles
-    int gy = slots / (sh.parts * mb);
+    int gy = resident[sh.parts] / mb;
     gy = gy < 1 ? 1 : gy > tiles ? tiles : gy;
     const int part_st = (nst + sh.parts - 1) / sh.parts;
     const int sums = sums_bytes(sh.parts);
-    sh.st_pass = (kHalf - sums - 2 * kSt - kBars) / xst;
+    sh.st_pass = (kRoom - sums - 2 * kSt - kBars) / xst;
     if (sh.st_pass > part_st) sh.st_pass = part_st;
-    sh.ring = (kHalf - sums - kBars - sh.st_pass * xst) / kSt;
+    sh.ring = (kRoom - sums - kBars - sh.st_pass * xst) / kSt;
     if (sh.ring > 8) sh.ring = 8;
     const int es = a.x_type == MOE_T_E4M3 ? 1 : 2;
     sh.vec = (uintptr_t)a.x % (8 * es) == 0 && (a.x_ld * es) % (8 * es) == 0;
@@ -663,15 +697,19 @@ cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
 
 template <int NT>
 cudaError_t launch_fmt(const W4Args &a, cudaStream_t st) {
-    constexpr int MT = NT == 1 ? 2 : 1;  // more tokens: the sums of 32 rows would not fit in the registers
+    // 32 rows a warp, where their sums fit in the registers of two CTAs on an SM
+    // (up to 8 tokens) or of one (over 16); the latter also holds twice the x, which
+    // is then rarely staged anew for every tile (41 tokens, 7684 x 6816: 81 us with
+    // 16 rows and two CTAs, 40 us so).
+    constexpr int MT = NT == 2 ? 1 : 2, CPS = NT <= 2 ? 2 : 1;
     if (a.nvfp4) {
         // TMA takes the scales where their rows are multiples of 16 bytes
-        if (a.K % 256 == 0 && (uintptr_t)a.s % 16 == 0) return launch_one<NT, MT, true, 16, true>(a, st);
-        return launch_one<NT, MT, true, 16, false>(a, st);
+        if (a.K % 256 == 0 && (uintptr_t)a.s % 16 == 0) return launch_one<NT, MT, CPS, true, 16, true>(a, st);
+        return launch_one<NT, MT, CPS, true, 16, false>(a, st);
     }
-    if (a.group == 128) return launch_one<NT, MT, false, 128, false>(a, st);
-    if (a.group == 64) return launch_one<NT, MT, false, 64, false>(a, st);
-    return launch_one<NT, MT, false, 32, false>(a, st);
+    if (a.group == 128) return launch_one<NT, MT, CPS, false, 128, false>(a, st);
+    if (a.group == 64) return launch_one<NT, MT, CPS, false, 64, false>(a, st);
+    return launch_one<NT, MT, CPS, false, 32, false>(a, st);
 }
 
 }  // namespace
@@ -679,6 +717,7 @@ cudaError_t launch_fmt(const W4Args &a, cudaStream_t st) {
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st) {
     if (a.M <= 8) return launch_fmt<1>(a, st);
     if (a.M <= 16) return launch_fmt<2>(a, st);
+    if (a.M <= 24 || (a.M > 32 && a.M <= 48)) return launch_fmt<3>(a, st);
     return launch_fmt<4>(a, st);
 }
 
