@@ -395,7 +395,7 @@ W4S = [
     (7, 64, 12288), (64, 20, 8192),
     # many tiles: every CTA walks several; the last ones stage their tokens anew for each
     (3, 39000, 512), (8, 45001, 256), (1, 39040, 160), (12, 20000, 384), (20, 20011, 256), (30, 20011, 4096),
-    (64, 40, 32768), (64, 20011, 512),
+    (64, 40, 32768), (64, 20011, 512), (11, 4200, 4096), (25, 4100, 6816), (41, 700, 1056), (16, 5000, 12288),
 ]
 
 

@@ -695,13 +695,8 @@ cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, tq, ts, a, sh);
 }
 
-template <int NT>
+template <int NT, int MT, int CPS>
 cudaError_t launch_fmt(const W4Args &a, cudaStream_t st) {
-    // 32 rows a warp, where their sums fit in the registers of two CTAs on an SM
-    // (up to 8 tokens) or of one (over 16); the latter also holds twice the x, which
-    // is then rarely staged anew for every tile (41 tokens, 7684 x 6816: 81 us with
-    // 16 rows and two CTAs, 40 us so).
-    constexpr int MT = NT == 2 ? 1 : 2, CPS = NT <= 2 ? 2 : 1;
     if (a.nvfp4) {
         // TMA takes the scales where their rows are multiples of 16 bytes
         if (a.K % 256 == 0 && (uintptr_t)a.s % 16 == 0) return launch_one<NT, MT, CPS, true, 16, true>(a, st);
@@ -715,10 +710,19 @@ cudaError_t launch_fmt(const W4Args &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st) {
-    if (a.M <= 8) return launch_fmt<1>(a, st);
-    if (a.M <= 16) return launch_fmt<2>(a, st);
-    if (a.M <= 24 || (a.M > 32 && a.M <= 48)) return launch_fmt<3>(a, st);
-    return launch_fmt<4>(a, st);
+    // 32 rows a warp (each x fragment serves two products), where their sums fit in
+    // the registers of two CTAs on an SM (up to 8 tokens) or of one (over 16); one
+    // CTA also holds twice the x, which is then rarely staged anew for every tile
+    // (41 tokens, 7684 x 6816: 81 us with 16 rows and two CTAs, 40 us so).
+    if (a.M <= 8) return launch_fmt<1, 2, 2>(a, st);
+    // In between it is the length of a CTA's work that decides, since a lone CTA
+    // waits at every tile's start and sum. 16 tokens, two CTAs / one, us: 8192 x 4096
+    // INT4 17.4 / 15.5, 8192 x 4096 8-bit x 13.1 / 11.4, 32768 x 4096 f16 x 35.1 /
+    // 32.9; but 43485 x 2048 INT4 34.1 / 37.8, 2048 x 12288 11.6 / 12.7, 512 x 4096
+    // 5.3 / 5.8.
+    if (a.M <= 16) return a.K >= 4096 && a.N >= 4096 ? launch_fmt<2, 2, 1>(a, st) : launch_fmt<2, 1, 2>(a, st);
+    if (a.M <= 24 || (a.M > 32 && a.M <= 48)) return launch_fmt<3, 2, 1>(a, st);
+    return launch_fmt<4, 2, 1>(a, st);
 }
 
 }  // namespace moe
