@@ -328,8 +328,7 @@ __device__ __forceinline__ void mul_block(const W4Args &a, uint32_t codes, uint3
                 const uint32_t u = __shfl_sync(kFull, sc.v[item / 4], (lane & ~3) | (item & 3));
                 sf[j] = s_value(u & 0xFFFFu, a.s_type);
                 z0[j] = (0x6400u + (u >> 16)) * 0x10001u;
-                const __half2 zh = __half2half2(__int2half_rn(-64 - (int)(u >> 16)));
-                z1[j] = *reinterpret_cast<const uint32_t *>(&zh);
+                z1[j] = hsub2(0x63806380u, z0[j]);  // 960 - (1024 + z), exact
             }
         }
         float part[MT][NT][4];
@@ -714,7 +713,10 @@ cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st) {
     // the registers of two CTAs on an SM (up to 8 tokens) or of one (over 16); one
     // CTA also holds twice the x, which is then rarely staged anew for every tile
     // (41 tokens, 7684 x 6816: 81 us with 16 rows and two CTAs, 40 us so).
-    if (a.M <= 8) return launch_fmt<1, 2, 2>(a, st);
+    // Few rows: tiles of 64 where 8 parts of 128-row tiles would leave half of the
+    // CTAs' places empty (1 token, 2081 x 8960 NVFP4: 7.5 -> 6.2 us, 7 tokens, 415 x
+    // 9856 INT4: 8.6 -> 7.4; but 4096 x 4096 INT4 6.7 -> 7.3, 131072 x 4096 61 -> 73).
+    if (a.M <= 8) return a.N <= 128 * 152 / 8 ? launch_fmt<1, 1, 2>(a, st) : launch_fmt<1, 2, 2>(a, st);
     // In between it is the length of a CTA's work that decides, since a lone CTA
     // waits at every tile's start and sum. 16 tokens, two CTAs / one, us: 8192 x 4096
     // INT4 17.4 / 15.5, 8192 x 4096 8-bit x 13.1 / 11.4, 32768 x 4096 f16 x 35.1 /
