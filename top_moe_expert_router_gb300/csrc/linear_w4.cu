@@ -21,12 +21,12 @@
 //
 // Structure. A CTA takes tiles of 64 or 128 rows: a producer warp streams their
 // codes by TMA through a ring of 256-column stages; four warps along the rows by
-// two along a stage's columns widen and multiply them, 32 rows a warp up to 8
-// tokens (x is read once for two products), 16 above. K is split over a cluster
-// of up to 8 CTAs where there are few tiles; their sums meet in distributed
-// shared memory, added in rank order. What bounds it: the large sizes, the issue
-// of about 18 instructions per 256 weights (the stream leaves 22 at full issue);
-// the small ones, staging x and joining the parts.
+// two along a stage's columns widen and multiply them, 16 or 32 rows a warp (at 32
+// x is read once for two products). K is split over a cluster of up to 8 CTAs
+// where there are few tiles; their sums meet in distributed shared memory, added
+// in rank order. What bounds it: the large sizes, about 18 instructions per 256
+// weights that issue in 52 % of the slots while the ring, three stages beside x,
+// keeps DRAM 61 % busy; the small ones, staging x and joining the parts.
 // Measured on the way (131072 x 4096 NVFP4, 4 tokens, 45 us of stream): loads
 // into registers one block ahead 92 us (waiting for one block's load waited
 // for later ones too), two batches of four blocks in turn 70 us, a ring of

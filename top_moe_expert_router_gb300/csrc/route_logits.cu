@@ -27,8 +27,9 @@
 // with all. That takes half the instructions of k rounds of "best of all". Where
 // over 32 reach it (the live experts lie in few lanes) they are spread first: 140
 // tokens of 272 experts, 3 of 8 groups kept, 42 -> 15 us.
-// The kernel is bound by its instructions: about 450 a token without scores,
-// 900 with a bias and groups.
+// The kernel is bound by its instructions: 1300 a token for 160 experts in 8
+// groups (30011 tokens, 160 experts: 39 us of choice at 64 % of the issue slots,
+// 12 us of permutation).
 #include <math.h>
 
 #include "ops.cuh"
