@@ -26,10 +26,10 @@
 // gathered one to a lane, in order of their ids, and ranked by comparing each
 // with all. That takes half the instructions of k rounds of "best of all". Where
 // over 32 reach it (the live experts lie in few lanes) they are spread first: 140
-// tokens of 272 experts, 3 of 8 groups kept, 42 -> 15 us.
-// The kernel is bound by its instructions: 1300 a token for 160 experts in 8
-// groups (30011 tokens, 160 experts: 39 us of choice at 64 % of the issue slots,
-// 12 us of permutation).
+// tokens of 272 experts, 3 of 8 groups kept, 42 -> 14 us (always spreading where
+// few lanes are kept: 30011 tokens of 160 experts, 47 -> 51 us).
+// The kernel is bound by its instructions: 1060 a token for 160 experts in 8
+// groups (30011 tokens: 47 us, of it 12 of permutation; issue slots 59 % used).
 #include <math.h>
 
 #include "ops.cuh"
@@ -103,7 +103,13 @@ __device__ __forceinline__ void load_lane(const RouteArgs &a, int64_t row, int e
     }
 }
 
-// Order-preserving unsigned keys; 0 marks "no candidate".
+// Order-preserving unsigned keys; 0, that of -inf, marks "no candidate". Both
+// zeros have the same. Not for NaN.
+__device__ __forceinline__ uint32_t key_of(float f) {
+    const uint32_t u = __float_as_uint(f + 0.f);
+    return (u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) - 0x007FFFFFu;
+}
+__device__ __forceinline__ float value_of(uint32_t key) { return key_value(key + 0x007FFFFFu); }
 __device__ __forceinline__ uint64_t key_of(double f) {
     const uint64_t u = (uint64_t)__double_as_longlong(f == 0.0 ? 0.0 : f);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
@@ -119,12 +125,14 @@ __device__ __forceinline__ S warp_add(S v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
 }
-// load_lane, with NaN and -inf as -inf and +inf as the largest finite float.
+// NaN and -inf as -inf, +inf as the largest finite float (fmaxf takes NaN for the other operand).
+__device__ __forceinline__ float clean(float f) { return fminf(fmaxf(f, -INFINITY), 3.402823466e38f); }
+// load_lane, cleaned.
 template <int EPL>
 __device__ __forceinline__ void load_clean(const RouteArgs &a, int64_t row, int e0, float l[EPL]) {
     load_lane<EPL>(a, row, e0, l);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], 3.402823466e38f) : -INFINITY;
+    for (int i = 0; i < EPL; ++i) l[i] = clean(l[i]);
 }
 
 // What a choice leaves in a lane: an expert, its logit and its place among the
@@ -152,12 +160,11 @@ __device__ __forceinline__ uint32_t lane_bound(const uint32_t (&key)[EPL], int w
     uint32_t m = 0u;
     for (int j = 0; j < want;) {
         m = __reduce_max_sync(kFull, top);
-        if (m == 0u) return 1u;
-        const bool hit = top == m;
+        const bool hit = top == m;               // no key left: every lane, and the loop ends
         j += __popc(__ballot_sync(kFull, hit));
         if (hit) top = 0u;
     }
-    return m;
+    return max(m, 1u);
 }
 
 // Gathers the experts whose keys reach `bound`, ids ascending, one to a lane
@@ -206,8 +213,8 @@ __device__ __noinline__ Gathered gather_live(const uint2 *cand, uint2 *out, int 
     Gathered r;
     r.bound = lane_bound<1>(top, want);
     if (slack >= 0.f && r.bound > 1u) {
-        const float x = key_value(r.bound);
-        r.bound = order_key(x - (slack + rel * fabsf(x)));
+        const float x = value_of(r.bound);
+        r.bound = max(key_of(x - (slack + rel * fabsf(x))), 1u);
     }
     r.n = 0;
     for (int p0 = 0; p0 < live; p0 += 32) {
@@ -252,17 +259,14 @@ __device__ __forceinline__ Gathered gather_spread(const RouteArgs &a, const uint
 
 // The place of a lane's key among n gathered ones; ties to the lower lane.
 __device__ __forceinline__ int rank_of(uint32_t key, int n, int lane) {
-    int rank = 0;
-    for (int j = 0; j < n; ++j) {
-        const uint32_t o = __shfl_sync(kFull, key, j);
-        rank += o > key - (j < lane ? 1u : 0u) ? 1 : 0;
-    }
+    int rank = __popc(__match_any_sync(kFull, key) & ((1u << lane) - 1u));
+    for (int j = 0; j < n; ++j) rank += __shfl_sync(kFull, key, j) > key ? 1 : 0;
     return rank;
 }
 
-// The scores of a lane's experts in 32 bits (c), which of them may be chosen,
-// and a bound on the error of a score. `scored`: false where the order of the
-// logits serves.
+// The scores of a lane's experts in 32 bits (c; -inf: not to be chosen), and a
+// bound on the error of a score. `scored`: false where the order of the logits
+// serves.
 //
 // Errors. Sigmoid by the fast exponential and reciprocal: the exponent's
 // relative error of (2 + 1.2 |l|) 2^-23 enters the score times p (1 - p), at
@@ -274,37 +278,31 @@ __device__ __forceinline__ int rank_of(uint32_t key, int n, int lane) {
 // terms, under 10 * 2^-23 for 512 of them, and 25 roundings) and those of the
 // quotient: under (27 + 1.2 t) 2^-23 of p. The bias adds a rounding of 2^-24 of
 // the sum.
-struct Scored {
-    uint32_t on;
-    float err;
-};
 template <int EPL>
-__device__ __forceinline__ Scored score_lane(const RouteArgs &a, const float (&l)[EPL], float lmax, int e0, bool scored,
-                                             float (&c)[EPL]) {
-    Scored r{0u, 0.f};
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) r.on |= l[i] > -INFINITY ? 1u << i : 0u;
+__device__ __forceinline__ float score_lane(const RouteArgs &a, const float (&l)[EPL], float lmax, int e0, bool scored,
+                                            float (&c)[EPL]) {
     if (!scored) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) c[i] = l[i];
-        return r;
+        return 0.f;
     }
+    float err;
     if (a.sigmoid) {
-        r.err = 0x1p-21f;
+        err = 0x1p-21f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) c[i] = __fdividef(1.f, 1.f + __expf(-l[i]));
+        for (int i = 0; i < EPL; ++i) c[i] = l[i] > -INFINITY ? __fdividef(1.f, 1.f + __expf(-l[i])) : -INFINITY;
     } else {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            c[i] = ((r.on >> i) & 1u) ? __expf(l[i] - lmax) : 0.f;
+            c[i] = __expf(l[i] - lmax);          // (a token without any expert: NaN, and all -inf below)
             s += c[i];
         }
         s = warp_add(s);
         const float inv_z = s > 0.f ? 1.f / s : 1.f;
-        r.err = 0x1p-18f * inv_z;
+        err = 0x1p-18f * inv_z;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) c[i] *= inv_z;
+        for (int i = 0; i < EPL; ++i) c[i] = l[i] > -INFINITY ? c[i] * inv_z : -INFINITY;
     }
     if (a.bias) {
         float b[EPL];
@@ -319,13 +317,9 @@ __device__ __forceinline__ Scored score_lane(const RouteArgs &a, const float (&l
             for (int i = 0; i < EPL; ++i) b[i] = e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            c[i] += fminf(b[i], 3.402823466e38f);
-            // fminf takes NaN for the other operand
-            if (!(b[i] > -INFINITY)) r.on &= ~(1u << i);
-        }
+        for (int i = 0; i < EPL; ++i) c[i] += clean(b[i]);
     }
-    return r;
+    return err;
 }
 
 __device__ __forceinline__ float own_err(const RouteArgs &a, float err, float l, float lmax) {
@@ -333,46 +327,44 @@ __device__ __forceinline__ float own_err(const RouteArgs &a, float err, float l,
     return a.sigmoid ? err : err * __expf(-t) * (1.f + 0.04f * t) + 1e-37f;
 }
 
-// The two best of every group, with the lpg lanes of a group (a power of two).
-// Where the groups are whole lanes (a.direct) those lanes hold the group
-// themselves; else 32 / groups lanes or fewer walk it in shared memory (element
-// e lies at e + e / 32: groups a multiple of 32 apart would share a bank).
+// The best (a.top2: two best) of every group, with the lpg lanes of a group (a
+// power of two). Where the groups are whole lanes (a.direct) those lanes hold the
+// group themselves; else 32 / groups lanes or fewer walk it in shared memory
+// (element e lies at e + e / 32: groups a multiple of 32 apart would share a bank).
 template <int EPL, typename S>
-__device__ __forceinline__ void group_best(const RouteArgs &a, const S (&c)[EPL], uint32_t on, int lane, S *buf, S &b1,
-                                           S &b2) {
+__device__ __forceinline__ void group_best(const RouteArgs &a, const S (&c)[EPL], int lane, S *buf, S &b1, S &b2) {
     const int e0 = lane * EPL, gs = a.E / a.groups, lpg = a.lanes_per_group, sub = lane & (lpg - 1), g = lane / lpg;
-    constexpr int kPad = sizeof(S) == 4 ? 5 : 31;         // no padding for doubles: the room is E of them
-    b1 = b2 = (S)-INFINITY;
+    constexpr bool kPad = sizeof(S) == 4;        // doubles: room for E of them only
+    S m1 = (S)-INFINITY, m2 = (S)-INFINITY;
+    auto take = [&](S v) {
+        if (a.top2) {
+            const S low = m1 < v ? m1 : v;
+            m2 = m2 > low ? m2 : low;
+        }
+        m1 = m1 > v ? m1 : v;
+    };
     if (a.direct) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const S v = ((on >> i) & 1u) ? c[i] : (S)-INFINITY;
-            const S low = b1 < v ? b1 : v;
-            b2 = b2 > low ? b2 : low;
-            b1 = b1 > v ? b1 : v;
-        }
+        for (int i = 0; i < EPL; ++i) take(c[i]);
     } else {
         __syncwarp();
+        S *at = buf + e0 + (kPad ? e0 >> 5 : 0);  // EPL divides 32
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (e0 + i < a.E) buf[e0 + i + ((e0 + i) >> kPad)] = ((on >> i) & 1u) ? c[i] : (S)-INFINITY;
+            if (kPad || e0 + i < a.E) at[i] = c[i];
         __syncwarp();
         if (g < a.groups)
-            for (int i = sub; i < gs; i += lpg) {
-                const int e = g * gs + i;
-                const S v = buf[e + (e >> kPad)];
-                const S low = b1 < v ? b1 : v;
-                b2 = b2 > low ? b2 : low;
-                b1 = b1 > v ? b1 : v;
-            }
+            for (int e = g * gs + sub; e < g * gs + gs; e += lpg) take(buf[e + (kPad ? e >> 5 : 0)]);
     }
     for (int o = lpg >> 1; o > 0; o >>= 1) {
-        const S v1 = __shfl_xor_sync(kFull, b1, o), v2 = __shfl_xor_sync(kFull, b2, o);
-        const S low = b1 < v1 ? b1 : v1;
-        b2 = b2 > v2 ? b2 : v2;
-        b2 = b2 > low ? b2 : low;
-        b1 = b1 > v1 ? b1 : v1;
+        const S v = __shfl_xor_sync(kFull, m1, o);
+        if (a.top2) {
+            const S v2 = __shfl_xor_sync(kFull, m2, o);
+            m2 = m2 > v2 ? m2 : v2;
+        }
+        take(v);
     }
+    b1 = m1, b2 = m2;
 }
 
 // Whether this lane's group is among the `keep` best by `score`; the ballot has
@@ -390,16 +382,24 @@ __device__ __forceinline__ bool group_kept(const RouteArgs &a, S score, bool any
     return g < a.groups && rank < a.keep && any;
 }
 
+// Bits of a lane's experts that lie in kept groups.
 template <int EPL>
-__device__ __forceinline__ uint32_t in_kept_groups(const RouteArgs &a, uint32_t on, bool kept, int e0) {
-    if (a.direct) return kept ? on : 0u;
+__device__ __forceinline__ uint32_t in_kept_groups(const RouteArgs &a, bool kept, int e0) {
+    if (a.direct) return kept ? kFull : 0u;
+    const int gs = a.E / a.groups, lpg = a.lanes_per_group;
     const uint32_t mask = __ballot_sync(kFull, kept);
+    if (gs >= EPL) {                             // two groups at most
+        const int g = (int)(((uint32_t)e0 * a.group_inv) >> 22), rem = (g + 1) * gs - e0;
+        const uint32_t first = rem >= 32 ? kFull : (1u << rem) - 1u;
+        return (((mask >> ((g * lpg) & 31)) & 1u) ? first : 0u) | (((mask >> (((g + 1) * lpg) & 31)) & 1u) ? ~first : 0u);
+    }
+    uint32_t in = 0u;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const uint32_t gi = ((uint32_t)(e0 + i) * a.group_inv) >> 22;  // (e0 + i) / group size
-        if (e0 + i >= a.E || !((mask >> (gi * a.lanes_per_group)) & 1u)) on &= ~(1u << i);
+        in |= ((mask >> ((gi * lpg) & 31u)) & 1u) << i;
     }
-    return on;
+    return in;
 }
 
 constexpr int kAll = -1, kGroups = -2;
@@ -415,33 +415,30 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
     const int e0 = lane * EPL;
     const bool staged = a.keep < a.groups, by_logit = a.bias == nullptr;
     float c[EPL];
-    const Scored sc = score_lane<EPL>(a, l, lmax, e0, !by_logit || (staged && a.top2), c);
-    uint32_t on = sc.on;
+    const float err = score_lane<EPL>(a, l, lmax, e0, !by_logit || (staged && a.top2), c);
     bool near = false, near_groups = false;
     if (staged) {
         float b1, b2;
-        group_best<EPL, float>(a, c, on, lane, buf, b1, b2);
+        group_best<EPL, float>(a, c, lane, buf, b1, b2);
         const bool any = b1 > -INFINITY, is_group = lane / a.lanes_per_group < a.groups;
         const float score = a.top2 && b2 > -INFINITY ? b1 + b2 : b1;
         const bool kept = group_kept(a, score, any, lane);
         if (!by_logit || a.top2) {
             // the border: the worst kept group against the best one left out;
             // two scores make a group's, each rounded once more with its bias
-            const uint32_t lo = ~__reduce_max_sync(kFull, kept ? ~order_key(score) : 0u);
-            const uint32_t hi = __reduce_max_sync(kFull, is_group && any && !kept ? order_key(score) : 0u);
+            const uint32_t lo = ~__reduce_max_sync(kFull, kept ? ~key_of(score) : 0u);
+            const uint32_t hi = __reduce_max_sync(kFull, is_group && any && !kept ? key_of(score) : 0u);
             const uint32_t mag = __reduce_max_sync(
                 kFull, any ? __float_as_uint(fabsf(b1) + (b2 > -INFINITY ? fabsf(b2) : 0.f)) : 0u);
-            near_groups = hi != 0u && !(key_value(lo) - key_value(hi) > 4.f * sc.err + 0x1p-22f * __uint_as_float(mag));
+            near_groups = hi != 0u && !(value_of(lo) - value_of(hi) > 4.f * err + 0x1p-22f * __uint_as_float(mag));
         }
-        on = in_kept_groups<EPL>(a, on, kept, e0);
-        if (by_logit) {
+        const uint32_t in = in_kept_groups<EPL>(a, kept, e0);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = l[i];
-        }
+        for (int i = 0; i < EPL; ++i) c[i] = ((in >> i) & 1u) ? (by_logit ? l[i] : c[i]) : -INFINITY;
     }
     uint32_t key[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? order_key(c[i]) : 0u;
+    for (int i = 0; i < EPL; ++i) key[i] = key_of(c[i]);
     uint32_t mine;
     Pick r{-1, -INFINITY, 0};
     uint32_t bound = lane_bound<EPL>(key, a.k + 1);
@@ -458,17 +455,17 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
     if (!by_logit) {
         // each pick against the next one, the last against the border
         __syncwarp();
-        const float own = own_err(a, sc.err, r.l, lmax);
-        if (r.id >= 0) buf[r.rank] = key_value(mine), buf[32 + r.rank] = own;
+        const float own = own_err(a, err, r.l, lmax);
+        if (r.id >= 0) buf[r.rank] = value_of(mine), buf[32 + r.rank] = own;
         __syncwarp();
         if (r.id >= 0 && r.rank < a.k && r.rank + 1 < n) {
-            const float v = key_value(mine), x = buf[r.rank + 1];
+            const float v = value_of(mine), x = buf[r.rank + 1];
             near |= !(v - x > own + buf[33 + r.rank] + 0x1p-22f * fmaxf(fabsf(v), fabsf(x)));
         }
         // what was not gathered lies below the bound
         if (n > 0 && n <= 32) {
-            const float v = buf[min(n, a.k) - 1], x = key_value(bound);
-            within = bound == 1u || v - x > 2.f * sc.err + 0x1p-22f * fmaxf(fabsf(v), fabsf(x));
+            const float v = buf[min(n, a.k) - 1], x = value_of(bound);
+            within = bound == 1u || v - x > 2.f * err + 0x1p-22f * fmaxf(fabsf(v), fabsf(x));
         }
     }
     *close = __any_sync(kFull, near) || near_groups;
@@ -519,24 +516,22 @@ __device__ __noinline__ Pick choose_general(const RouteArgs &a, int64_t row, flo
     float l[EPL], c[EPL];
     load_clean<EPL>(a, row, e0, l);
     const bool scored = !by_logit || (staged && a.top2);
-    uint32_t on = score_lane<EPL>(a, l, lmax, e0, scored, c).on;
+    score_lane<EPL>(a, l, lmax, e0, scored, c);
     double z = 1.0, d[EPL];
     if (scored && !a.sigmoid) z = sum64(a, row, lmax, lane);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) d[i] = scored ? score64(a, l[i], lmax, z, min(e0 + i, a.E - 1)) : (double)l[i];
+    for (int i = 0; i < EPL; ++i) d[i] = scored && c[i] > -INFINITY ? score64(a, l[i], lmax, z, e0 + i) : (double)c[i];
     if (staged) {
         double b1, b2;
-        group_best<EPL, double>(a, d, on, lane, reinterpret_cast<double *>(buf), b1, b2);
+        group_best<EPL, double>(a, d, lane, reinterpret_cast<double *>(buf), b1, b2);
         const bool kept = group_kept(a, a.top2 && b2 > -INFINITY ? b1 + b2 : b1, b1 > -INFINITY, lane);
-        on = in_kept_groups<EPL>(a, on, kept, e0);
-        if (by_logit) {
+        const uint32_t in = in_kept_groups<EPL>(a, kept, e0);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) d[i] = l[i];
-        }
+        for (int i = 0; i < EPL; ++i) d[i] = ((in >> i) & 1u) ? (by_logit ? (double)l[i] : d[i]) : -INFINITY;
     }
     uint64_t key[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? key_of(d[i]) : 0ull;
+    for (int i = 0; i < EPL; ++i) key[i] = d[i] > -INFINITY ? key_of(d[i]) : 0ull;
     Pick r{-1, -INFINITY, lane};
     for (int j = 0; j < a.k; ++j) {
         uint64_t bk = key[0];
@@ -572,26 +567,26 @@ __device__ __noinline__ Pick choose_exact(const RouteArgs &a, int64_t row, float
     const bool scored = !by_logit || (staged && a.top2);
     float l[EPL], c[EPL];
     load_clean<EPL>(a, row, e0, l);
-    const Scored sc = score_lane<EPL>(a, l, lmax, e0, scored, c);
-    uint32_t on = sc.on, key[EPL], mine;
+    const float err = score_lane<EPL>(a, l, lmax, e0, scored, c);
+    uint32_t in = kFull, key[EPL], mine;
     uint2 *cand = reinterpret_cast<uint2 *>(buf);
     double z = 1.0;
     if (scored && !a.sigmoid) z = sum64(a, row, lmax, lane);
     Pick r{-1, -INFINITY, lane};
     if (staged) {
         float f1, f2;
-        group_best<EPL, float>(a, c, on, lane, buf, f1, f2);
+        group_best<EPL, float>(a, c, lane, buf, f1, f2);
         if (!near_groups) {                               // the 32-bit choice of the groups stands
             const float score = a.top2 && f2 > -INFINITY ? f1 + f2 : f1;
-            on = in_kept_groups<EPL>(a, on, group_kept(a, score, f1 > -INFINITY, lane), e0);
+            in = in_kept_groups<EPL>(a, group_kept(a, score, f1 > -INFINITY, lane), e0);
         } else {
             const float thr = a.top2 ? f2 : f1;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const uint32_t gi = ((uint32_t)min(e0 + i, a.E - 1) * a.group_inv) >> 22;
                 const float tg = __shfl_sync(kFull, thr, (gi * a.lanes_per_group) & 31);
-                const bool below = tg - c[i] > 2.f * sc.err + 0x1p-21f * fmaxf(fabsf(tg), fabsf(c[i]));
-                key[i] = ((on >> i) & 1u) && !below ? 1u : 0u;
+                const bool below = tg - c[i] > 2.f * err + 0x1p-21f * fmaxf(fabsf(tg), fabsf(c[i]));
+                key[i] = c[i] > -INFINITY && !below ? 1u : 0u;
             }
             const int n = gather_from<EPL>(key, 1u, lane, cand, &mine, &r.id);
             if (n > 32) return choose_general<EPL>(a, row, lmax, lane, buf);
@@ -617,16 +612,17 @@ __device__ __noinline__ Pick choose_exact(const RouteArgs &a, int64_t row, float
                 rank += o > score || (o == score && g < lane) ? 1 : 0;
             }
             const uint32_t mask = __ballot_sync(kFull, lane < a.groups && rank < a.keep && b1 > -INFINITY);
+            in = 0u;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const uint32_t gi = ((uint32_t)(e0 + i) * a.group_inv) >> 22;
-                if (e0 + i >= a.E || !((mask >> (gi & 31u)) & 1u)) on &= ~(1u << i);
+                in |= ((mask >> (gi & 31u)) & 1u) << i;
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = ((on >> i) & 1u) ? order_key(by_logit ? l[i] : c[i]) : 0u;
-    const Gathered s = gather_spread<EPL>(a, key, a.k, by_logit ? -1.f : 2.f * sc.err, 0x1p-20f, lane, cand);
+    for (int i = 0; i < EPL; ++i) key[i] = ((in >> i) & 1u) ? key_of(by_logit ? l[i] : c[i]) : 0u;
+    const Gathered s = gather_spread<EPL>(a, key, a.k, by_logit ? -1.f : 2.f * err, 0x1p-20f, lane, cand);
     const int n = s.n;
     mine = s.key, r.id = s.id;
     if (n > 32) return choose_general<EPL>(a, row, lmax, lane, buf);
@@ -664,7 +660,7 @@ __device__ __forceinline__ float pick_weight(const RouteArgs &a, const float (&l
     if (a.renorm) {
         // relative to the largest chosen score: at most 1, and their sum is
         // taken in fixed point, 2^-27, where it is 1 to 16
-        const float top = key_value(__reduce_max_sync(kFull, on ? order_key(r.l) : 0u));
+        const float top = value_of(__reduce_max_sync(kFull, on ? key_of(r.l) : 0u));
         // sigmoid(l) = exp(l) to within exp(-60) below -60: the quotient is
         // then that of the exponentials, which does not underflow
         if (on)
@@ -676,7 +672,7 @@ __device__ __forceinline__ float pick_weight(const RouteArgs &a, const float (&l
     } else {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s += l[i] > -INFINITY ? __expf(l[i] - lmax) : 0.f;  // within 2^-20 of the sum
+        for (int i = 0; i < EPL; ++i) s += __expf(l[i] - lmax);  // within 2^-20 of the sum
         s = warp_add(s);
         if (on) w = expf(r.l - lmax) / s;
     }
@@ -698,10 +694,10 @@ __device__ __forceinline__ void select_chunk(const RouteArgs &a, int c, int32_t 
         load_clean<EPL>(a, row, lane * EPL, l);
         float lmax = 0.f;
         if (!a.sigmoid) {                                 // the softmax's largest logit
-            uint32_t m = order_key(l[0]);
+            float m = l[0];
 #pragma unroll
-            for (int i = 1; i < EPL; ++i) m = max(m, order_key(l[i]));
-            lmax = key_value(__reduce_max_sync(kFull, m));
+            for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+            lmax = value_of(__reduce_max_sync(kFull, key_of(m)));
         }
         bool close;
         int again;
