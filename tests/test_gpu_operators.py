@@ -477,6 +477,16 @@ def test_linear_w4_strides_and_bounds(gpu_lib):
             check_w4(gpu_lib, fmt, x8, w, W, x_scales=xs)
 
 
+def test_linear_int4_zero_points_of_a_byte(gpu_lib):
+    """Zero points outside the codes' range."""
+    g = gen(28)
+    (q, s, z), W = make_w4("int4", 70, 384, 64, True, "f16", g)
+    big = torch.randint(0, 256, z.shape, generator=g, device="cuda", dtype=torch.uint8)
+    shift = (z.double() - big.double()) * s.double()
+    W = W + shift.repeat_interleave(64, 1)
+    check_w4(gpu_lib, "int4", torch.randn(5, 384, generator=g, device="cuda").to(torch.bfloat16), (q, s, big), W)
+
+
 def test_linear_takes_the_quantiser_output(gpu_lib):
     W = 0.02 * torch.randn(1, 96, 512, generator=gen(14), device="cuda").to(torch.bfloat16)
     q, s, gs = gpu_lib.quantize_nvfp4(W)
@@ -604,6 +614,37 @@ def test_streams_and_graphs(gpu_lib):
         same(got, step())
 
 
+def test_graphs_replayed_at_once(gpu_lib):
+    """Two graphs of every operator on two streams at the same time; the first calls of these kernels are captured ones."""
+    moe, streams, runs = gpu_lib, [torch.cuda.Stream() for _ in range(2)], []
+    for i, st in enumerate(streams):
+        g = gen(41 + i)
+        T, E, M, K, N = 3000 + 77 * i, 96, 19, 1024, 700
+        logits = torch.randn(T, E, generator=g, device="cuda")
+        x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+        w, _ = make_w4("int4", N, K, 64, True, "f16", g)
+        torch.cuda.synchronize()
+        graph, held = torch.cuda.CUDAGraph(), []
+        with torch.cuda.graph(graph, stream=st):
+            for _ in range(8):
+                n, s, _ = moe.add_rmsnorm(x, x)
+                held.append((moe.route_logits(logits, 5, n_groups=4, topk_groups=2), n, s, moe.linear_int4(n, *w)))
+        runs.append((graph, held, logits, x, w))
+    for _ in range(20):
+        for st, r in zip(streams, runs):
+            with torch.cuda.stream(st):
+                r[0].replay()
+    torch.cuda.synchronize()
+    for _, held, logits, x, w in runs:
+        n, s, _ = moe.add_rmsnorm(x, x)
+        want = (moe.route_logits(logits, 5, n_groups=4, topk_groups=2), n, s, moe.linear_int4(n, *w))
+        check_route(want[0], logits, 5, n_groups=4, topk_groups=2)
+        for h in held:
+            for name in want[0]:
+                assert torch.equal(h[0][name], want[0][name]), name
+            assert all(torch.equal(a, b) for a, b in zip(h[1:], want[1:]))
+
+
 # ---------------------------------------------------------------------------
 # with the layer
 # ---------------------------------------------------------------------------
@@ -680,6 +721,23 @@ def test_layer_with_its_own_router(gpu_lib, fmt, d):
         after_r = layer.route(x)
         for n in before_r:
             assert torch.equal(after_r[n], before_r[n]), n
+
+
+@pytest.mark.parametrize("E", [1, 2, 3, 5])
+def test_layer_with_few_experts_and_its_own_router(gpu_lib, E):
+    """Many chunks of few experts: their counts lie in rows of eight."""
+    g, T = gen(36), 9728
+    layer, wr, *_ = make_layer(gpu_lib, 256, 128, E, 1, T, g)
+    x = torch.randn(T, 256, generator=g, device="cuda").to(torch.bfloat16)
+    want = layer.route(x)
+    layer.set_router(score="sigmoid")                      # the same choice, by another path
+    got = layer.route(x)
+    for n in ("ids", "counts", "offsets", "perm", "pos"):
+        assert torch.equal(got[n], want[n]), n
+    assert (got["w"] == 1).all()
+    y = layer.forward(x).clone()
+    layer.clear_router()
+    assert torch.equal(layer.forward(x), y)
 
 
 def test_layer_router_without_enough_experts_is_reported(gpu_lib):
