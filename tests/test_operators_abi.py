@@ -63,6 +63,25 @@ def test_route_arguments_rejected(lib):
     assert call(ws=None) == BAD and call(n=16) == BAD and call(ws=P + 2) == BAD
 
 
+def test_packed_arguments_match_the_structures():
+    """The bytes that the bindings pass are those of the ctypes structures, field by field."""
+    for cls, pack in moe._PACK.items():
+        assert pack.size == ctypes.sizeof(cls)
+        vals = []
+        for i, (_, ctype) in enumerate(cls._fields_):
+            vals.append(i + 0.5 if ctype is ctypes.c_float else (1 << 40) + i if ctypes.sizeof(ctype) == 8 else i + 1)
+        got = cls.from_buffer_copy(pack.pack(*vals))
+        for (name, _), v in zip(cls._fields_, vals):
+            assert getattr(got, name) == v, (cls, name)
+
+
+@pytest.mark.parametrize("args", [(1 << 40, 8, "softmax", None, 1, 1, "max", True, 1.0),
+                                  (64, 8.5, "softmax", None, 1, 1, "max", True, 1.0)])
+def test_arguments_that_do_not_fit(args):
+    with pytest.raises(ValueError):
+        moe._route_desc(*args)
+
+
 def test_set_router_rejects(lib):
     assert lib.moe_layer_set_router(None, ctypes.byref(_route_desc())) == BAD
     assert lib.moe_layer_set_router(None, None) == BAD

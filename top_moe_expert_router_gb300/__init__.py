@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -262,7 +263,7 @@ class MoeLayer:
         desc = _route_desc(self.E, self.k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale)
         if bias is not None and bias.device != self.workspace.device:
             raise ValueError(f"bias: on {bias.device}, the layer on {self.workspace.device}")
-        _check(load().moe_layer_set_router(self._h, ctypes.byref(desc)), "moe_layer_set_router")
+        _check(load().moe_layer_set_router(self._h, MoeRouteDesc.from_buffer_copy(desc)), "moe_layer_set_router")
         self._router_bias = bias
 
     def clear_router(self):
@@ -398,22 +399,73 @@ _GROUP_RULE = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
 # the object costs about three on the host.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+# The argument structures as bytes, in a quarter of the time that a ctypes structure takes to fill.
+_PACK = {MoeRouteDesc: struct.Struct("@iiiPiiiif4x"), MoeNormArgs: struct.Struct("@6P5q5if"),
+         MoeW4Args: struct.Struct("@5iPPiPPPiqPqiPPiq")}
 
 
-def _tensor(name, t, dtype, shape, index, contiguous=True):
-    """Checks one tensor argument (None passes): type, shape, device, and the whole tensor contiguous unless its rows
-    are looked at by _row_stride."""
+def _packer(cls):
+    pack = _PACK[cls].pack
+
+    def packed(*fields):
+        try:
+            return pack(*fields)
+        except struct.error as e:
+            raise ValueError(f"{cls.__name__}: {e}") from None
+    return packed
+
+
+_pack_route, _pack_norm, _pack_w4 = (_packer(s) for s in (MoeRouteDesc, MoeNormArgs, MoeW4Args))
+_entries = None
+
+
+def _entry(i):
+    """route_logits', add_rmsnorm's or linear_w4's C entry, which takes its structure as bytes."""
+    global _entries
+    if _entries is None:
+        lib = load()
+        fns = [lib["moe_route_logits"], lib["moe_add_rmsnorm"], lib["moe_linear_w4"]]    # objects of their own
+        for fn, typed in zip(fns, (lib.moe_route_logits, lib.moe_add_rmsnorm, lib.moe_linear_w4)):
+            fn.argtypes = [ctypes.c_char_p, *typed.argtypes[1:]]
+            fn.restype = typed.restype
+        _entries = fns
+    return _entries[i]
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _refuse(name, t, dtype, shape, index, what=""):
+    raise ValueError(f"{name}: a {what}{dtype} tensor of shape {tuple(shape)} on cuda:{index} expected, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
+def _whole(name, t, dtype, shape, index):
+    """The address of a contiguous tensor argument, its type, shape and device checked; 0 for None."""
     if t is None:
-        return
-    if t.dtype != dtype or t.shape != shape or t.get_device() != index or (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{name}: a {'contiguous ' if contiguous else ''}{dtype} tensor of shape {tuple(shape)} on "
-                         f"cuda:{index} expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, index, "contiguous ")
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape, index):
+    """The address of a 2-D tensor argument, its type, shape and device checked, and the elements from one row to the
+    next; 0, 0 for None."""
+    if t is None:
+        return 0, 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(name, t, dtype, shape, index)
+    return t.data_ptr(), _row_stride(name, t)
 
 
 def _row_stride(name, t):
-    """Elements from one row of a 2-D tensor to the next (rows contiguous, not overlapping); 0 for None."""
-    if t is None:
-        return 0
+    """Elements from one row of a 2-D tensor to the next (rows contiguous, not overlapping)."""
+    if t.is_contiguous():
+        return t.shape[1] or 1
     s0, s1 = t.stride()
     rows, cols = t.shape
     if s1 == 1 and s0 >= cols and rows > 1:
@@ -441,7 +493,7 @@ def _handle(index, stream):
 
 def _run(fn, index, st, args, what):
     """fn(*args, stream handle) with device `index` current."""
-    if index == torch.cuda.current_device():
+    if index == _device():
         s = fn(*args, st)
     else:
         with torch.cuda.device(index):
@@ -451,13 +503,14 @@ def _run(fn, index, st, args, what):
 
 
 def _route_desc(E, top_k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale):
+    """A moe_route_desc as bytes."""
     if score not in _SCORE or group_rule not in _GROUP_RULE:
         raise ValueError(f"score is one of {sorted(_SCORE)}, group_rule one of {sorted(_GROUP_RULE)}")
-    if bias is not None and (not bias.is_cuda or bias.dtype != torch.float32 or tuple(bias.shape) != (E,)
+    if bias is not None and (not bias.is_cuda or bias.dtype is not torch.float32 or bias.shape != (E,)
                              or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous fp32 CUDA tensor of one value per expert")
-    return MoeRouteDesc(E, top_k, _SCORE[score], _ptr(bias), n_groups, topk_groups, _GROUP_RULE[group_rule],
-                        1 if renormalise else 0, scale)
+    return _pack_route(E, top_k, _SCORE[score], _addr(bias), n_groups, topk_groups, _GROUP_RULE[group_rule],
+                       1 if renormalise else 0, scale)
 
 
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
@@ -496,21 +549,22 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
                                       (pairs, pairs, (E,), (E + 1,), (T * top_k,), pairs)):
             if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != index
                                   or not t.is_contiguous()):
-                _tensor(n, t, dtype, shape, index)
-    lib = _lib or load()
-    ref = ctypes.byref(desc)
-    size, ws = ctypes.c_size_t(0), None
-    if T > 256 and any(t is not None for t in recs[2:]):   # fewer tokens, or the choice alone, need none
-        _check(lib.moe_route_logits_workspace_size(ref, T, ctypes.byref(size)), "moe_route_logits")
+                _refuse(n, t, dtype, shape, index, "contiguous ")
+    entry = _entry(0)
+    size, ws = 0, None
     st = _handle(index, stream)
-    if size.value:
+    row_stride = _row_stride("logits", logits)
+    if T > 256 and any(t is not None for t in recs[2:]):   # fewer tokens, or the choice alone, need none
+        need = ctypes.c_size_t(0)
+        _check(_lib.moe_route_logits_workspace_size(MoeRouteDesc.from_buffer_copy(desc), T, ctypes.byref(need)),
+               "moe_route_logits")
         # scratch from torch's allocator on the stream the kernels run on: every stream and captured graph has its own
         # (without a tensor around it, which costs as much as the two launches)
-        ws = torch.cuda.caching_allocator_alloc(size.value, index, st)
+        size = need.value
+        ws = torch.cuda.caching_allocator_alloc(size, index, st)
     try:
-        _run(lib.moe_route_logits, index, st,
-             (ref, logits.data_ptr(), _DTYPE[logits.dtype], _row_stride("logits", logits), T,
-              *[None if t is None else t.data_ptr() for t in recs], ws, size.value), "moe_route_logits")
+        _run(entry, index, st, (desc, logits.data_ptr(), _DTYPE[logits.dtype], row_stride, T,
+                                *[None if t is None else t.data_ptr() for t in recs], ws, size), "moe_route_logits")
     finally:
         if ws is not None:
             torch.cuda.caching_allocator_delete(ws)
@@ -546,20 +600,21 @@ def add_rmsnorm(x, res=None, gain=None, *, eps=1e-6, out_dtype=None, group=0, su
         cols = d // (group or d) if d else 0
         if scales is None:
             scales = torch.empty((T, cols), dtype=torch.float32, device=x.device)
-        _tensor("scales", scales, torch.float32, (T, cols), index, False)
+        scales_at, scales_ld = _rows("scales", scales, torch.float32, (T, cols), index)
     elif scales is not None:
         raise ValueError("scales need E4M3 output")
+    else:
+        scales_at = scales_ld = 0
     if sum_out is None and res is not None:
         sum_out = torch.empty((T, d), dtype=dtype, device=x.device)
-    _tensor("res", res, dtype, x.shape, index, False)
-    _tensor("gain", gain, dtype, (d,), index)
-    _tensor("sum_out", sum_out, dtype, x.shape, index, False)
-    _tensor("out", out, out_dtype, x.shape, index, False)
-    args = MoeNormArgs(x.data_ptr(), _ptr(res), _ptr(gain), _ptr(sum_out), out.data_ptr(), _ptr(scales),
-                       _row_stride("x", x), _row_stride("res", res), _row_stride("sum_out", sum_out),
-                       _row_stride("out", out), _row_stride("scales", scales), T, d, group, _DTYPE[dtype],
-                       _DTYPE[out_dtype], eps)
-    _run((_lib or load()).moe_add_rmsnorm, index, _handle(index, stream), (ctypes.byref(args),), "moe_add_rmsnorm")
+    shape = (T, d)
+    res_at, res_ld = _rows("res", res, dtype, shape, index)
+    sum_at, sum_ld = _rows("sum_out", sum_out, dtype, shape, index)
+    out_at, out_ld = _rows("out", out, out_dtype, shape, index)
+    args = _pack_norm(x.data_ptr(), res_at, _whole("gain", gain, dtype, (d,), index), sum_at, out_at, scales_at,
+                      _row_stride("x", x), res_ld, sum_ld, out_ld, scales_ld, T, d, group, _DTYPE[dtype],
+                      _DTYPE[out_dtype], eps)
+    _run(_entry(1), index, _handle(index, stream), (args,), "moe_add_rmsnorm")
     return out, sum_out, scales
 
 
@@ -577,18 +632,13 @@ def _linear_w4(fmt, x, q, s, g, z, x_scales, bias, out, out_dtype, stream):
             raise ValueError(f"s: type {s_type} is not supported")
     if group < 1 or K % group:
         raise ValueError("s: one scale per group of columns expected")
-    _tensor("q", q, torch.uint8, (N, K // 2), index)
-    _tensor("s", s, s_type, (N, K // group), index)
-    _tensor("g", g, torch.float32, (1,), index)
-    _tensor("zeros", z, torch.uint8, (N, K // group), index)
-    _tensor("bias", bias, torch.float32, (N,), index)
-    x_group = 0
+    x_group = xs_at = xs_ld = 0
     if x.dtype == torch.float8_e4m3fn:
         if x_scales is None or x_scales.dim() != 2 or not x_scales.shape[1] or K % x_scales.shape[1]:
             raise ValueError("E4M3 x needs x_scales [M, groups]")
         cols = x_scales.shape[1]
         x_group = K // cols if cols > 1 else 0
-        _tensor("x_scales", x_scales, torch.float32, (M, cols), index, False)
+        xs_at, xs_ld = _rows("x_scales", x_scales, torch.float32, (M, cols), index)
     elif x_scales is not None:
         raise ValueError("x_scales belong to E4M3 x")
     if out is None:
@@ -598,12 +648,13 @@ def _linear_w4(fmt, x, q, s, g, z, x_scales, bias, out, out_dtype, stream):
         raise ValueError("out_dtype and out differ")
     if out.dtype not in _FLOATS:
         raise ValueError(f"out: type {out.dtype} is not supported")
-    _tensor("out", out, out.dtype, (M, N), index, False)
-    args = MoeW4Args(fmt, M, N, K, group, q.data_ptr(), s.data_ptr(), _DTYPE.get(s_type, 0), _ptr(g), _ptr(z),
-                     x.data_ptr(), _DTYPE[x.dtype], _row_stride("x", x), _ptr(x_scales),
-                     _row_stride("x_scales", x_scales), x_group, _ptr(bias), out.data_ptr(), _DTYPE[out.dtype],
-                     _row_stride("out", out))
-    _run((_lib or load()).moe_linear_w4, index, _handle(index, stream), (ctypes.byref(args),), "moe_linear_w4")
+    out_at, out_ld = _rows("out", out, out.dtype, (M, N), index)
+    args = _pack_w4(fmt, M, N, K, group, _whole("q", q, torch.uint8, (N, K // 2), index),
+                    _whole("s", s, s_type, (N, K // group), index), _DTYPE.get(s_type, 0),
+                    _whole("g", g, torch.float32, (1,), index), _whole("zeros", z, torch.uint8, (N, K // group), index),
+                    x.data_ptr(), _DTYPE[x.dtype], _row_stride("x", x), xs_at, xs_ld, x_group,
+                    _whole("bias", bias, torch.float32, (N,), index), out_at, _DTYPE[out.dtype], out_ld)
+    _run(_entry(2), index, _handle(index, stream), (args,), "moe_linear_w4")
     return out
 
 
