@@ -400,6 +400,7 @@ _GROUP_RULE = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 
 # The argument structures as bytes, in a quarter of the time that a ctypes structure takes to fill.
 _PACK = {MoeRouteDesc: struct.Struct("@iiiPiiiif4x"), MoeNormArgs: struct.Struct("@6P5q5if"),
@@ -561,7 +562,10 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
         # scratch from torch's allocator on the stream the kernels run on: every stream and captured graph has its own
         # (without a tensor around it, which costs as much as the two launches)
         size = need.value
-        ws = torch.cuda.caching_allocator_alloc(size, index, st)
+        if _raw_alloc is not None and index == _device():
+            ws = _raw_alloc(size, st)                          # what the next does, without its change of device
+        else:
+            ws = torch.cuda.caching_allocator_alloc(size, index, st)
     try:
         _run(entry, index, st, (desc, logits.data_ptr(), _DTYPE[logits.dtype], row_stride, T,
                                 *[None if t is None else t.data_ptr() for t in recs], ws, size), "moe_route_logits")
