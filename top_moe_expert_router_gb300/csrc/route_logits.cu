@@ -271,13 +271,13 @@ __device__ __forceinline__ int rank_of(uint32_t key, int n, int lane) {
 // Errors. Sigmoid by the fast exponential and reciprocal: the exponent's
 // relative error of (2 + 1.2 |l|) 2^-23 enters the score times p (1 - p), at
 // most 0.64 * 2^-23; with the sum's and the reciprocal's roundings under
-// 2.2 * 2^-23: 2^-21 is allowed. Softmax: likewise t exp(-t) of a term's
-// argument, and about 25 roundings of the sum: 2^-18 of the largest score 1 / z
-// is allowed, and for one expert own_err of that: relative to its score p =
-// exp(-t) / z, its term's (2 + 1.2 t) 2^-23, z's (a mean of the same over the
-// terms, under 10 * 2^-23 for 512 of them, and 25 roundings) and those of the
-// quotient: under (27 + 1.2 t) 2^-23 of p. The bias adds a rounding of 2^-24 of
-// the sum.
+// 2.2 * 2^-23: 2^-21 is allowed. Softmax, relative to a score p = exp(-t) / z, t
+// its logit's distance from the largest: its term's (2 + 1.2 t) 2^-23 and the
+// rounding of t, 0.5 t 2^-23; z's, a mean of the same over the terms (t weighted
+// with exp(-t) is at most 3.9 for 512 of them: 8.7 * 2^-23) and 25 roundings; the
+// quotient's 2 * 2^-23: under (26 + 1.7 t) 2^-23. own_err allows (32 + 1.9 t)
+// 2^-23, and 2^-18 / z is above that for every t. The bias adds a rounding of
+// 2^-24 of the sum.
 template <int EPL>
 __device__ __forceinline__ float score_lane(const RouteArgs &a, const float (&l)[EPL], float lmax, int e0, bool scored,
                                             float (&c)[EPL]) {
@@ -324,7 +324,7 @@ __device__ __forceinline__ float score_lane(const RouteArgs &a, const float (&l)
 
 __device__ __forceinline__ float own_err(const RouteArgs &a, float err, float l, float lmax) {
     const float t = lmax - l;
-    return a.sigmoid ? err : err * __expf(-t) * (1.f + 0.04f * t) + 1e-37f;
+    return a.sigmoid ? err : err * __expf(-t) * (1.f + 0.06f * t) + 1e-37f;
 }
 
 // The best (a.top2: two best) of every group, with the lpg lanes of a group (a
