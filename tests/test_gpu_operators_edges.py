@@ -1,0 +1,58 @@
+"""The operators around the layer at the ends of their ranges, each against a
+plain implementation in 64 bits: scores of very different sizes, rows of
+subnormals, far scales, side streams, captured graphs, waits that run out, and
+the layer with a router of its own in its other forms."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_operators import DT, INF, call_w4, check_norm, check_route, check_w4, gen, make_layer, make_w4, ref_experts
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+def held_back(E, k, groups, base, step, small, seed):
+    """Tokens whose picks are experts of score e^small, their biases `step` apart from `base` on, and one expert of half
+    the softmax's sum that its bias holds back to among them: its score has an error in 32 bits that no other has."""
+    rng, T = np.random.RandomState(seed), 64
+    logits, bias = np.full((T, E), -30.0), np.full(E, -1.0)
+    some = rng.permutation(E // 2 if groups > 1 else E)        # within the groups that are kept
+    big, other, few = some[0], some[1], some[2:k + 4]
+    logits[:, big] = (np.arange(T) - T // 2) * 2e-8            # p moves by 5e-9 from token to token
+    logits[:, other] = 0.0                                     # the other half of the sum, never chosen
+    logits[:, few] = small + 0.1 * rng.randn(len(few))
+    logits = logits.astype(np.float32)
+    p = np.exp(logits[0].astype(np.float64))
+    bias[few] = base + step * (1 + rng.permutation(len(few)))
+    bias[big] = base + step * (1 + rng.uniform(0, len(few))) - p[big] / p.sum()
+    return torch.from_numpy(logits).cuda(), torch.from_numpy(bias.astype(np.float32)).cuda()
+
+
+@pytest.mark.parametrize("E,k,groups", [(32, 2, 1), (32, 4, 4), (100, 6, 1), (256, 8, 1), (256, 8, 4), (512, 16, 8)])
+@pytest.mark.parametrize("base,step,small", [(0.0, 1e-8, -20.7), (1e-3, 1.5e-9, -16.1), (0.0, 4e-8, -18.0)])
+def test_route_softmax_scores_with_errors_of_other_sizes(gpu_lib, E, k, groups, base, step, small):
+    for seed in range(8):
+        logits, bias = held_back(E, k, groups, base, step, small, seed)
+        opt = dict(score="softmax", bias=bias, n_groups=groups, topk_groups=max(1, groups // 2))
+        check_route(gpu_lib.route_logits(logits, k, **opt), logits, k, **opt)
+    many = logits.repeat(5, 1)                                 # the choice in a launch of its own
+    check_route(gpu_lib.route_logits(many, k, **opt), many, k, **opt)
+
+
+@pytest.mark.parametrize("E,k", [(64, 8), (256, 8), (455, 11)])
+def test_route_softmax_biases_that_level_the_scores(gpu_lib, E, k):
+    """Biases of -p and a little noise: the order turns on the noise, the errors on p."""
+    rng = np.random.RandomState(E)
+    for noise in (1e-6, 1e-7):
+        logits = rng.randn(200, E) * 1e-7
+        logits += np.where(np.arange(E) == E // 3, 6.0, rng.randn(E) * 2)
+        logits = logits.astype(np.float32)
+        p = np.exp(logits[0].astype(np.float64) - logits[0].max())
+        bias = torch.from_numpy((rng.uniform(0, noise, E) - p / p.sum()).astype(np.float32)).cuda()
+        logits = torch.from_numpy(logits).cuda()
+        check_route(gpu_lib.route_logits(logits, k, bias=bias), logits, k, bias=bias)
