@@ -56,3 +56,53 @@ def test_route_softmax_biases_that_level_the_scores(gpu_lib, E, k):
         bias = torch.from_numpy((rng.uniform(0, noise, E) - p / p.sum()).astype(np.float32)).cuda()
         logits = torch.from_numpy(logits).cuda()
         check_route(gpu_lib.route_logits(logits, k, bias=bias), logits, k, bias=bias)
+
+
+# ---------------------------------------------------------------------------
+# norm
+# ---------------------------------------------------------------------------
+def check_scaled(moe, x, gain, eps, group=0):
+    """check_norm's E4M3 half with the scale 1 where max|y| / 448 is no normal float."""
+    out, _, scales = moe.add_rmsnorm(x, None, gain, eps=eps, out_dtype=torch.float8_e4m3fn, group=group)
+    T, d = x.shape
+    n, rel = group or d, 64 * 2.0 ** -24                       # rel: as in check_norm
+    ms = x.double().square().mean(1, keepdim=True) + eps
+    y = torch.where(ms == 0, 0.0, x.double() / ms.sqrt()) * (1.0 if gain is None else gain.double())
+    want = y.view(T, d // n, n).abs().amax(2) / 448
+    want = torch.where(want < 2.0 ** -126, 1.0, want)
+    assert ((scales.double() - want).abs() <= want * rel).all()
+    v = (y.view(T, d // n, n) / want[:, :, None]).view(T, d)
+    tol = (v.abs() * (2.0 ** -4 + 2 * rel)).clamp_min(2.0 ** -10 * (1 + 1e-5))
+    assert ((out.float().double() - v).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("d", [64, 1000, 1002, 4099, 8192, 16384])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_norm_of_rows_at_the_ends_of_the_range(gpu_lib, d, dt, e4m3):
+    """Rows of subnormals, single tiny elements among zeros, rows of the largest values, an eps that leaves the range when
+    it is scaled."""
+    g, fi = gen(d), torch.finfo(DT[dt])
+    least = fi.smallest_normal * fi.eps
+    x = torch.zeros(10, d, device="cuda")
+    x[0] = least
+    x[1, d // 3] = least
+    x[2, d - 1] = fi.smallest_normal * 16
+    x[3] = torch.randint(-40, 41, (d,), generator=g, device="cuda") * least
+    x[4] = torch.randn(d, generator=g, device="cuda") * fi.smallest_normal * 4
+    x[5] = fi.max
+    x[6, 0] = fi.max
+    x[7] = torch.randn(d, generator=g, device="cuda") * fi.smallest_normal * 2.0 ** 20
+    x[8] = torch.randn(d, generator=g, device="cuda") * 1e-6
+    x[9, 1] = 1.0
+    x = x.to(DT[dt])
+    gain = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(DT[dt])
+    for eps in (0.0, 2.0 ** -140, 1e-35, 1e34):
+        if e4m3:
+            check_scaled(gpu_lib, x, None, eps)
+            check_scaled(gpu_lib, x, gain, eps)
+            if d % 64 == 0:
+                check_scaled(gpu_lib, x, gain, eps, 64)
+        else:
+            check_norm(gpu_lib, x, None, None, eps=eps)
+            check_norm(gpu_lib, x, torch.zeros_like(x), gain, eps=eps)

@@ -220,9 +220,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) add_rmsnorm_kernel(Norm
         }
         ss = row_reduce<TPR, false>(ss, part, buf);
         float m = fmaf(ss, inv_d, a.eps);
-        float pre = 1.f;
         if (!(m > 1e-30f && m < 1e33f)) {
-            // squares that leave fp32's range: the row by its largest element first
+            // squares, or an eps, at the ends of fp32's range: the row is first scaled by the power of two that takes
+            // the larger of its largest element and sqrt(eps) near 1 (a row of 2^-149 to 2^-23), and its root is
+            // taken of the scaled values: neither the factor nor the reciprocal root leaves the range
             float big = 0.f;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
@@ -230,22 +231,23 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) add_rmsnorm_kernel(Norm
                 for (int i = 0; i < V; ++i) big = max_nan(big, fabsf(s[v][i]));
             big = row_reduce<TPR, true>(big, part, buf);
             if (big > 0.f && big < INFINITY) {
-                const int ex = min(max(ilogbf(big), -100), 126);
-                pre = scalbnf(1.f, -ex);         // a power of two: exact
+                int ex = ilogbf(big);
+                if (a.eps > 0.f) ex = max(ex, ilogbf(a.eps) >> 1);
+                const float pre = scalbnf(1.f, -min(max(ex, -126), 126));
                 float q = 0.f;
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const float u = s[v][i] * pre;
-                        q = fmaf(u, u, q);
+                        s[v][i] *= pre;
+                        q = fmaf(s[v][i], s[v][i], q);
                     }
                 q = row_reduce<TPR, false>(q, part, buf);
                 m = q * inv_d + a.eps * pre * pre;
             }
         }
         // a row of zeros with eps = 0 stays zero
-        const float r = m == 0.f ? 0.f : pre * rsqrtf(m);
+        const float r = m == 0.f ? 0.f : rsqrtf(m);
         if (!PF) fetch_gain();
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
