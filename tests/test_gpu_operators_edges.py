@@ -106,3 +106,57 @@ def test_norm_of_rows_at_the_ends_of_the_range(gpu_lib, d, dt, e4m3):
         else:
             check_norm(gpu_lib, x, None, None, eps=eps)
             check_norm(gpu_lib, x, torch.zeros_like(x), gain, eps=eps)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit products
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("M", [1, 3, 12])
+@pytest.mark.parametrize("fmt,group", [("nvfp4", 16), ("int4", 64)])
+def test_products_that_feed_each_other(gpu_lib, fmt, group, M):
+    """Short products in a row, each started before the one that writes its tokens ends: eagerly and in a replayed graph
+    with changing tokens, against calls with a wait between them."""
+    moe, g, n = gpu_lib, gen(52), 448
+    ws = [make_w4(fmt, n, n, group, True, "bf16", g)[0] for _ in range(6)]
+    if fmt == "nvfp4":
+        ws = [(q, s, gs / 60) for q, s, gs in ws]
+    else:
+        ws = [(q, (s.float() / 60).to(s.dtype), z) for q, s, z in ws]
+    wide = [make_w4(fmt, 1024, 1024, group, True, "bf16", g)[0] for _ in range(2)]
+    x = torch.randn(M, n, generator=g, device="cuda").to(torch.bfloat16)
+    x8 = torch.randn(M, 1024, generator=g, device="cuda").to(torch.bfloat16)
+    bufs = [torch.zeros(M, n, dtype=torch.bfloat16, device="cuda") for _ in ws]
+    outs = [torch.zeros(M, 1024, device="cuda") for _ in wide]
+
+    def chain(wait):
+        y = x
+        for w, b in zip(ws, bufs):
+            y = call_w4(moe, fmt, y, w, out=b)
+            if wait:
+                torch.cuda.synchronize()
+        u, _, sc = moe.add_rmsnorm(x8, out_dtype=torch.float8_e4m3fn, group=128)
+        for w, o in zip(wide, outs):
+            if wait:
+                torch.cuda.synchronize()
+            call_w4(moe, fmt, u, w, x_scales=sc, bias=outs[0][0] if o is not outs[0] else None, out=o)
+
+    def got():
+        torch.cuda.synchronize()
+        return [b.clone() for b in bufs + outs]
+
+    chain(True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(False)
+    for i in range(30):
+        x.copy_(torch.randn(M, n, generator=gen(100 + i), device="cuda"))
+        x8.copy_(torch.randn(M, 1024, generator=gen(200 + i), device="cuda"))
+        chain(True)
+        want = got()
+        assert all(torch.isfinite(v.float()).all() for v in want)
+        for run in (lambda: chain(False), graph.replay):
+            for b in bufs + outs:
+                b.zero_()
+            run()
+            for a, b in zip(got(), want):
+                assert torch.equal(a, b)

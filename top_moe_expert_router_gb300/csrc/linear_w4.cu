@@ -98,21 +98,25 @@ __device__ __forceinline__ void widen_int4(uint32_t w, uint32_t m0, uint32_t m1,
     o[3] = hfma2((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, m1);
 }
 
+// Every global load here is an ordinary one: the kernel may be on the SMs before
+// the one that writes its x (or scales, or bias) has ended, and the path for data
+// that is constant while a kernel runs is not ordered by the wait for that end.
+
 // Eight elements of x as they are loaded (E4M3: two words).
 template <typename T>
 __device__ __forceinline__ uint4 load_x8(const T *p, bool vec) {
     uint32_t u[4] = {0u, 0u, 0u, 0u};
     if constexpr (sizeof(T) == 1) {
         if (vec) {
-            const uint2 v = __ldg((const uint2 *)p);
+            const uint2 v = *(const uint2 *)p;
             return make_uint4(v.x, v.y, 0u, 0u);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j >> 2] |= (uint32_t)__ldg(p + j) << (8 * (j & 3));
+        for (int j = 0; j < 8; ++j) u[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
     } else {
-        if (vec) return __ldg((const uint4 *)p);
+        if (vec) return *(const uint4 *)p;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j >> 1] |= (uint32_t)__ldg(p + j) << (16 * (j & 1));
+        for (int j = 0; j < 8; ++j) u[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
@@ -151,7 +155,7 @@ __device__ __forceinline__ void stage_x_type(const W4Args &a, uint4 *xh, float *
             sc[u] = 1.f;
             if (XT == MOE_T_E4M3 && j == 0 && in) {
                 const int gb = kb0 + kb;
-                sc[u] = __ldg(a.xs + (int64_t)(m0 + m) * a.xs_ld + (a.xgroup == 128 ? gb : gb * 128 / a.xgroup));
+                sc[u] = a.xs[(int64_t)(m0 + m) * a.xs_ld + (a.xgroup == 128 ? gb : gb * 128 / a.xgroup)];
             }
             m += dm;
             kb += dk;
@@ -276,10 +280,10 @@ __device__ __forceinline__ void load_scales(const W4Args &a, int row, int kb, in
         const size_t r = min(row + 8 * jj + g, a.N - 1);
         if constexpr (NVFP4) {
             const int k = min(128 * kb + 32 * t, a.K - 32);
-            s.v[j] = __ldg((const uint16_t *)((const uint8_t *)a.s + r * (a.K / 16) + (k >> 4)));
+            s.v[j] = *(const uint16_t *)((const uint8_t *)a.s + r * (a.K / 16) + (k >> 4));
         } else {
             const int ng = a.K / G, gi = min(kb * S::per_row + item % S::per_row, ng - 1);
-            s.v[j] = __ldg((const uint16_t *)a.s + r * ng + gi) | (a.z ? (uint32_t)__ldg(a.z + r * ng + gi) : 8u) << 16;
+            s.v[j] = ((const uint16_t *)a.s)[r * ng + gi] | (a.z ? (uint32_t)a.z[r * ng + gi] : 8u) << 16;
         }
     }
 }
@@ -380,7 +384,7 @@ __device__ __forceinline__ void store_tile(const W4Args &a, const float *sums, i
         float v = 0.f;
         for (int p = 0; p < parts; ++p) v += at[2 * p * own * mp] + at[(2 * p + 1) * own * mp];
         v *= gs;
-        if (a.bias) v += __ldg(a.bias + n);
+        if (a.bias) v += a.bias[n];
         const int64_t o = (int64_t)(m0 + m) * a.y_ld + n;
         if (a.y_type == MOE_T_F32) ((float *)a.y)[o] = v;
         else if (a.y_type == MOE_T_BF16) ((__nv_bfloat16 *)a.y)[o] = __float2bfloat16_rn(v);
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, CPS) linear_w4_kernel(const __grid_c
                                                     : (wrow + (lane & 7)) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
     const uint32_t scale_at = kCodes<MT> + (wrow + g) * 16 + 8 * b + 2 * t;
     const uint32_t ring = smem_u32(smem), x_at = smem_u32(xh) + b * 4 * ps * 16, xs_at = smem_u32(xsc) + b * mt * 4;
-    const float gs = NVFP4 ? __ldg(a.g) : 1.f;
+    const float gs = NVFP4 ? *a.g : 1.f;
     Scales<MT, NVFP4, G> sc;                     // loaded by the lanes one stage ahead unless they come with it
     if (!TS) load_scales<MT, NVFP4, G>(a, blockIdx.y * kR + wrow, 2 * s0 + b, lane, sc);
     bool staged = false;
