@@ -160,3 +160,27 @@ def test_products_that_feed_each_other(gpu_lib, fmt, group, M):
             run()
             for a, b in zip(got(), want):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("xdt", ["bf16", "e4m3"])
+def test_linear_int4_scales_far_from_one(gpu_lib, group, xdt):
+    """Scales of the weights and of x whose product is no normal float, while the sums are floats."""
+    g = gen(51)
+    M, N, K = 5, 48, 512
+    for far, wide in ((-26, -112), (-40, -105), (20, 90), (-30, 120)):      # sums of about 2^(far + wide + 7)
+        (q, s, z), W = make_w4("int4", N, K, group, True, "bf16", g)
+        s, W = (s.float() * 2.0 ** far).to(torch.bfloat16), W * 2.0 ** far
+        x, xs = torch.randn(M, K, generator=g, device="cuda"), None
+        if xdt == "bf16":
+            x = (x * 2.0 ** wide).to(torch.bfloat16)
+            xd = x.double()
+        else:
+            x, xs = (x * 64).to(torch.float8_e4m3fn), torch.full((M, K // 128), 2.0 ** (wide - 8), device="cuda")
+            xd = x.double() * 2.0 ** (wide - 8)
+        y = gpu_lib.linear_int4(x, q, s, z, x_scales=xs, out_dtype=torch.float32).double()
+        ref, size = xd @ W.t(), xd.abs() @ W.abs().t()
+        # as check_w4, and half a step of the subnormals, 2^-150, for each addition: 4 per 128 columns, 2 per part of K
+        tol = size * (8 * 17 + 4 * (K // 128 + 1) + 16) * 2.0 ** -23 + ref.abs() * 2.0 ** -24
+        tol += (4 * (K // 128) + 2 * 8) * 2.0 ** -150
+        assert ((y - ref).abs() <= tol).all(), (far, wide)

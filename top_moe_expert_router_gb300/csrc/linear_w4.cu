@@ -365,10 +365,11 @@ __device__ __forceinline__ void mul_block(const W4Args &a, uint32_t codes, uint3
         for (int h = 0; h < MT; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                acc[h][n][0] = fmaf(part[h][n][0], NVFP4 ? x0[n] : sf[2 * h] * x0[n], acc[h][n][0]);
-                acc[h][n][1] = fmaf(part[h][n][1], NVFP4 ? x1[n] : sf[2 * h] * x1[n], acc[h][n][1]);
-                acc[h][n][2] = fmaf(part[h][n][2], NVFP4 ? x0[n] : sf[2 * h + 1] * x0[n], acc[h][n][2]);
-                acc[h][n][3] = fmaf(part[h][n][3], NVFP4 ? x1[n] : sf[2 * h + 1] * x1[n], acc[h][n][3]);
+                // (the weights' scale first: its product with x's may leave the range where the sum does not)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[h][n][e] = fmaf(NVFP4 ? part[h][n][e] : part[h][n][e] * sf[2 * h + (e >> 1)], (e & 1) ? x1[n] : x0[n],
+                                        acc[h][n][e]);
             }
     }
 }
