@@ -392,6 +392,17 @@ typedef struct {
 } moe_w4_args;
 moe_status moe_linear_w4(const moe_w4_args *args, void *stream);
 
+/* A product's waits for its weights are bounded (1.5 s). Where one runs out the
+ * call leaves NaN in the rows concerned and sets a bit that belongs to the
+ * device, not to the call. moe_linear_w4_status waits for `stream`, then reads
+ * and clears the current device's: MOE_OK or MOE_ERR_TIMEOUT. Not while the
+ * stream is being captured. */
+moe_status moe_linear_w4_status(void *stream);
+
+/* Test hook: the products launched while hold != 0 copy no weights, so that
+ * their waits run out. No GPU work. */
+moe_status moe_debug_hold_linear_w4(int hold);
+
 moe_status moe_layer_destroy(moe_layer *layer);
 
 const char *moe_status_string(moe_status s);

@@ -184,3 +184,23 @@ def test_linear_int4_scales_far_from_one(gpu_lib, group, xdt):
         tol = size * (8 * 17 + 4 * (K // 128 + 1) + 16) * 2.0 ** -23 + ref.abs() * 2.0 ** -24
         tol += (4 * (K // 128) + 2 * 8) * 2.0 ** -150
         assert ((y - ref).abs() <= tol).all(), (far, wide)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 300, 1152), (3, 39000, 512), (20, 700, 4096)])
+def test_a_product_whose_waits_run_out_says_so(gpu_lib, M, N, K):
+    """One tile and several per CTA, K in one part and in several: NaN in every row, a status, and the next call is right."""
+    moe, g = gpu_lib, gen(53)
+    w, W = make_w4("nvfp4", N, K, 16, False, None, g)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    want = check_w4(moe, "nvfp4", x, w, W).clone()
+    assert moe.linear_w4_status() == moe.MOE_OK
+    moe.hold_linear_w4(True)
+    try:
+        y = moe.linear_nvfp4(x, *w)
+        assert moe.linear_w4_status() == moe.MOE_ERR_TIMEOUT
+    finally:
+        moe.hold_linear_w4(False)
+    assert torch.isnan(y).all()
+    assert moe.linear_w4_status() == moe.MOE_OK          # reading it cleared it
+    assert torch.equal(moe.linear_nvfp4(x, *w), want)
+    assert moe.linear_w4_status() == moe.MOE_OK

@@ -130,6 +130,8 @@ def load(path: str | None = None):
             "moe_layer_set_router": ([vp, ctypes.POINTER(MoeRouteDesc)], st),
             "moe_add_rmsnorm": ([ctypes.POINTER(MoeNormArgs), vp], st),
             "moe_linear_w4": ([ctypes.POINTER(MoeW4Args), vp], st),
+            "moe_linear_w4_status": ([vp], st),
+            "moe_debug_hold_linear_w4": ([i], st),
             "moe_status_string": ([st], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -677,3 +679,14 @@ def linear_int4(x, q, s, zeros=None, *, x_scales=None, bias=None, out=None, out_
     bf16 or f16 with groups of 32, 64 or 128 columns, zeros [N, K/group] uint8 or None for 8 everywhere
     (moe_linear_w4). x and the result as in ``linear_nvfp4``."""
     return _linear_w4(MOE_W4_INT4, x, q, s, None, zeros, x_scales, bias, out, out_dtype, stream)
+
+
+def linear_w4_status(stream=None) -> int:
+    """MOE_ERR_TIMEOUT if a wait of a 4-bit product ran out on the current device since the last call (its rows are then
+    NaN), else MOE_OK (moe_linear_w4_status). Waits for the stream."""
+    return load().moe_linear_w4_status(_stream(stream))
+
+
+def hold_linear_w4(hold: bool):
+    """Test hook: make the waits of the 4-bit products run out, or restore them."""
+    _check(load().moe_debug_hold_linear_w4(1 if hold else 0), "moe_debug_hold_linear_w4")

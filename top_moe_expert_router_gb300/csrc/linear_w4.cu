@@ -42,6 +42,7 @@
 // conflict-free 16-byte read.
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "gemm.cuh"
@@ -396,16 +397,22 @@ __device__ __forceinline__ void store_tile(const W4Args &a, const float *sums, i
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// mbarrier wait that gives up after kWaitLimitNs (or once another warp has)
-// and says so in *bad; the tile's outputs are then NaN.
+// Error bits of the products on a device (moe_linear_w4_status).
+__device__ uint32_t w4_err;
+
+// mbarrier wait that gives up after kWaitLimitNs, or soon after another warp of
+// the CTA has: *bad says so. The tile's outputs are then NaN.
 __device__ __forceinline__ void wait_full(uint64_t *bar, uint32_t parity, volatile int *bad) {
     if (mbar_try_wait(bar, parity)) return;
     const unsigned long long t0 = global_ns();
-    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
-        if ((it & 255u) == 0 && (*bad || global_ns() - t0 > kWaitLimitNs)) {
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if ((it & 7u) == 0 && *bad) return;
+        if ((it & 255u) == 0 && global_ns() - t0 > kWaitLimitNs) {
+            atomicOr(&w4_err, ERRBIT_TIMEOUT);
             *bad = 1;
             return;
         }
+    }
 }
 
 struct Shape {
@@ -415,6 +422,7 @@ struct Shape {
     int ring;       // stages in flight
     int bars;       // offset of the barriers in shared memory
     int vec;
+    int hold;       // test hook: the producers copy nothing
 };
 
 // blockIdx.x: the part of K; .y: the first row tile (then every gridDim.y-th);
@@ -457,9 +465,10 @@ __global__ void __launch_bounds__(kThreads, CPS) linear_w4_kernel(const __grid_c
         // producer: every tile's stages in order; the cluster barrier of a
         // tile is passed before the next one is arrived at
         int i = 0;
+        const int s_end = sh.hold ? s0 : s1;
         for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
             if (lane == 0)
-                for (int st = s0; st < s1; ++st, ++i) {
+                for (int st = s0; st < s_end; ++st, ++i) {
                     const int slot = i % R;
                     if (i >= R) wait_full(&empty[slot], ((i / R) - 1) & 1, bad);
                     if (*bad) break;
@@ -475,6 +484,10 @@ __global__ void __launch_bounds__(kThreads, CPS) linear_w4_kernel(const __grid_c
                 cluster_arrive();
             }
         }
+        // every copy issued must land before the CTA exits (where a wait gave up, nobody else has seen to it)
+        if (lane == 0)
+            for (int j = i > R ? i - R : 0; j < i; ++j) mbar_wait(&full[j % R], (j / R) & 1, &w4_err);
+        __syncwarp();
         if (parts > 1) {
             cluster_wait();
             cluster_arrive();
@@ -587,6 +600,8 @@ __global__ void __launch_bounds__(kThreads, CPS) linear_w4_kernel(const __grid_c
     }
 }
 
+std::atomic<int> w4_hold{0};
+
 bool code_map(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
               bool swizzle) {
     auto enc = get_encode();
@@ -680,6 +695,7 @@ cudaError_t launch_one(const W4Args &a, cudaStream_t st) {
     if (sh.ring > 8) sh.ring = 8;
     const int es = a.x_type == MOE_T_E4M3 ? 1 : 2;
     sh.vec = (uintptr_t)a.x % (8 * es) == 0 && (a.x_ld * es) % (8 * es) == 0;
+    sh.hold = w4_hold.load(std::memory_order_relaxed);
     sh.bars = (sh.ring * kSt + sums + sh.st_pass * xst + 7) / 8 * 8;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(sh.parts, gy, mb);
@@ -714,6 +730,17 @@ cudaError_t launch_fmt(const W4Args &a, cudaStream_t st) {
 }
 
 }  // namespace
+
+void hold_linear_w4(bool hold) { w4_hold.store(hold, std::memory_order_relaxed); }
+
+// Reads and clears the current device's error bits, after `st`'s work.
+cudaError_t linear_w4_errors(cudaStream_t st, uint32_t *bits) {
+    void *at = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&at, w4_err);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, sizeof(*bits), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof(*bits), st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
 
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st) {
     // 32 rows a warp (each x fragment serves two products), where their sums fit in

@@ -93,6 +93,8 @@ constexpr int kW4MaxM = 64;
 constexpr int kW4MaxK = 32768;
 constexpr int kW4MaxN = 1 << 30;
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st);
+cudaError_t linear_w4_errors(cudaStream_t st, uint32_t *bits);
+void hold_linear_w4(bool hold);
 
 #ifdef __CUDACC__
 

@@ -200,4 +200,15 @@ moe_status moe_linear_w4(const moe_w4_args *l, void *stream) {
     return status_of(launch_linear_w4(a, (cudaStream_t)stream));
 }
 
+moe_status moe_linear_w4_status(void *stream) {
+    uint32_t bits = 0;
+    if (linear_w4_errors((cudaStream_t)stream, &bits) != cudaSuccess) return MOE_ERR_CUDA;
+    return bits & ERRBIT_TIMEOUT ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
+moe_status moe_debug_hold_linear_w4(int hold) {
+    hold_linear_w4(hold != 0);
+    return MOE_OK;
+}
+
 }  // extern "C"
