@@ -58,6 +58,23 @@ def test_route_softmax_biases_that_level_the_scores(gpu_lib, E, k):
         check_route(gpu_lib.route_logits(logits, k, bias=bias), logits, k, bias=bias)
 
 
+@pytest.mark.parametrize("row", [(-59.0, -75.0, -88.0, -95.0), (-1.0, -50.0, -87.9, -88.6), (-61.0, -87.5, -100.0, -130.0),
+                                 (3.0, -20.0, -87.0, -88.5), (-87.4, -88.0, -88.7, -89.0)])
+def test_route_sigmoid_weights_far_below_zero(gpu_lib, row):
+    """The quotients of scores that are near or past the end of fp32's range, and those scores themselves."""
+    logits = torch.full((3, 40), -INF, device="cuda")
+    logits[:, 5:9] = torch.tensor(row, device="cuda")
+    l = np.array(row, np.float64)
+    log_p = np.where(l < 0, l, 0.0) - np.log1p(np.exp(-np.abs(l)))
+    rel = np.exp(log_p - log_p[0])
+    for renorm, scale, want in ((True, 1.0, rel / rel.sum()), (False, 2.0 ** 100, np.exp(log_p) * 2.0 ** 100)):
+        r = gpu_lib.route_logits(logits, 4, score="sigmoid", renormalise=renorm, scale=scale)
+        assert r["ids"].tolist() == [[5, 6, 7, 8]] * 3
+        # as check_route; a subnormal score is held in steps of 2^-149, three roundings of it
+        np.testing.assert_allclose(r["w"].cpu().numpy().astype(np.float64), np.tile(want, (3, 1)), rtol=170 * 2.0 ** -24,
+                                   atol=2.0 ** -147 * scale)
+
+
 # ---------------------------------------------------------------------------
 # norm
 # ---------------------------------------------------------------------------

@@ -694,6 +694,12 @@ __device__ __noinline__ int rank_exact(const RouteArgs &a, int64_t row, float lm
     return rank;
 }
 
+// 1 / (1 + exp(-l)) with divisors of 1 to 2 (the fast division gives 0 for one past 2^126).
+__device__ __forceinline__ float sigmoid(float l) {
+    const float e = expf(-fabsf(l));
+    return __fdividef(l < 0.f ? e : 1.f, 1.f + e);
+}
+
 // The weight of a lane's pick (`on`: it is one of the first k).
 template <int EPL>
 __device__ __forceinline__ float pick_weight(const RouteArgs &a, const float (&l)[EPL], float lmax, const Pick &r,
@@ -703,14 +709,16 @@ __device__ __forceinline__ float pick_weight(const RouteArgs &a, const float (&l
         // relative to the largest chosen score: at most 1, and their sum is
         // taken in fixed point, 2^-27, where it is 1 to 16
         const float top = value_of(__reduce_max_sync(kFull, on ? key_of(r.l) : 0u));
-        // sigmoid(l) = exp(l) to within exp(-60) below -60: the quotient is
-        // then that of the exponentials, which does not underflow
+        // of two sigmoids: exp(l - top) (1 + exp(top)) / (1 + exp(l)) for a negative top, where every factor stays in
+        // range however far below zero the logits lie
         if (on)
-            w = a.sigmoid && top >= -60.f ? __fdividef(1.f + expf(-top), 1.f + expf(-r.l)) : expf(r.l - top);
+            w = !a.sigmoid   ? expf(r.l - top)
+                : top < 0.f ? expf(r.l - top) * __fdividef(1.f + expf(top), 1.f + expf(r.l))
+                            : (1.f + expf(-top)) * sigmoid(r.l);
         const uint32_t s = __reduce_add_sync(kFull, __float2uint_rn(w * 0x1p27f));
         w *= __fdividef(0x1p27f, (float)s);
     } else if (a.sigmoid) {
-        if (on) w = __fdividef(1.f, 1.f + expf(-r.l));
+        if (on) w = sigmoid(r.l);
     } else {
         float s = 0.f;
 #pragma unroll
