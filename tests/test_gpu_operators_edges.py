@@ -221,3 +221,19 @@ def test_a_product_whose_waits_run_out_says_so(gpu_lib, M, N, K):
     assert moe.linear_w4_status() == moe.MOE_OK          # reading it cleared it
     assert torch.equal(moe.linear_nvfp4(x, *w), want)
     assert moe.linear_w4_status() == moe.MOE_OK
+
+
+# ---------------------------------------------------------------------------
+# the layer with a router of its own
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("E", [1, 2, 3, 4])
+def test_route_with_its_own_router_keeps_the_expert_outputs(gpu_lib, E):
+    """What the last forward left is there after a route of many tokens, too."""
+    g, T = gen(61), 9728
+    layer, *_ = make_layer(gpu_lib, 256, 128, E, 1, T, g)
+    x = torch.randn(T, 256, generator=g, device="cuda").to(torch.bfloat16)
+    layer.set_router(score="sigmoid")
+    layer.forward(x)
+    want = layer.expert_outputs(T).clone()
+    layer.route(x)
+    assert torch.equal(layer.expert_outputs(T), want)

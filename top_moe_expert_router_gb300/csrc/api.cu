@@ -104,8 +104,8 @@ cudaError_t launch_layer_router(const moe_layer *ly, int T, int nsplit, cudaStre
     a.perm = ws.perm;
     a.pos = ws.pos;
     // 16-bit counts in rows of 8 experts or more: within chunk_base's 32-bit ones from 4 experts on; for fewer, at
-    // most T / 2 bytes of the gathered rows, which are written later
-    a.chunk_cnt = L.E >= 4 ? reinterpret_cast<uint16_t *>(ws.chunk_base) : ws.xperm;
+    // most T / 2 bytes of h (T * k * I elements), which only a forward's experts write, and read, later
+    a.chunk_cnt = reinterpret_cast<uint16_t *>(L.E >= 4 ? (void *)ws.chunk_base : (void *)ws.h);
     a.perm_fill = 0;                    // rows past the last pair are gathered (and never read back)
     a.uniq = ws.uniq;
     a.tile_off = ws.tile_off;
