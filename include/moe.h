@@ -203,7 +203,8 @@ int moe_last_launch_count(const moe_layer *layer);
  * before each of its kernels and one after the last (host-side event objects;
  * no device memory). moe_profile_end waits for those events and writes
  * ms[f * max_kernels + i] = duration of kernel i of recorded forward f, and
- * the counts, then stops recording. */
+ * the counts, then stops recording. The launches of a routing, or of the
+ * grouped GEMMs, count as one kernel; so does a forward that runs in chunks. */
 moe_status moe_profile_begin(moe_layer *layer, int max_forwards);
 moe_status moe_profile_end(moe_layer *layer, float *ms_host, int max_kernels, int *n_forwards,
                            int *n_kernels);

@@ -237,3 +237,20 @@ def test_route_with_its_own_router_keeps_the_expert_outputs(gpu_lib, E):
     want = layer.expert_outputs(T).clone()
     layer.route(x)
     assert torch.equal(layer.expert_outputs(T), want)
+
+
+@pytest.mark.parametrize("d,sizes", [(256, (1, 16)), (320, (3, 16, 40))])
+def test_forwards_with_a_router_are_profiled(gpu_lib, d, sizes):
+    g = gen(62)
+    layer, *_ = make_layer(gpu_lib, d, 128, 64, 4, 64, g)
+    layer.set_router(score="sigmoid")
+    for T in sizes:
+        x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+        layer.forward(x)
+        layer.profile_begin(3)
+        for _ in range(5):
+            layer.forward(x)
+        ms = layer.profile_end()
+        # routing, gate/up, down and combine; a forward in several chunks of tokens as one
+        assert ms.shape == (3, 4 if T <= 16 else 1)
+        assert (ms > 0).all() and (ms < 1000).all()

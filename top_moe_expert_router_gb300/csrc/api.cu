@@ -194,14 +194,20 @@ moe_status forward_impl(moe_layer *ly, const uint16_t *x, const uint16_t *res, u
     }
     // Token chunks of at most tdec tokens run the streaming expert stage; a
     // chunk is a full layer forward (route, experts, combine) of its tokens.
+    // One chunk is recorded by its four steps, several as a whole.
+    const bool one = T <= tdec;
+    prof_mark(ly, 0, st);
     for (int t0 = 0; t0 < T; t0 += tdec) {
         const int n = T - t0 < tdec ? T - t0 : tdec;
         const uint16_t *xc = x + (size_t)t0 * L.d;
         cudaError_t e = launch_routing(ly, xc, n, true, st, &launches);
+        if (one) prof_mark(ly, 1, st);
         if (e == cudaSuccess) e = launch_decode_gateup(L, ly->ws, xc, n, st);
         ++launches;
+        if (one) prof_mark(ly, 2, st);
         if (e == cudaSuccess) e = launch_decode_down(L, ly->ws, xc, n, st);
         ++launches;
+        if (one) prof_mark(ly, 3, st);
         if (e == cudaSuccess)
             e = launch_combine(L, ly->ws, res ? res + (size_t)t0 * L.d : nullptr, out + (size_t)t0 * L.d, n, st);
         ++launches;
@@ -210,7 +216,12 @@ moe_status forward_impl(moe_layer *ly, const uint16_t *x, const uint16_t *res, u
             return MOE_ERR_CUDA;
         }
     }
+    prof_mark(ly, one ? 4 : 1, st);
     ly->last_launches = launches;
+    if (ly->prof_count < ly->prof_max) {
+        ly->prof_nk = one ? 4 : 1;
+        ++ly->prof_count;
+    }
     return MOE_OK;
 }
 
