@@ -254,11 +254,3 @@ def test_forwards_with_a_router_are_profiled(gpu_lib, d, sizes):
         # routing, gate/up, down and combine; a forward in several chunks of tokens as one
         assert ms.shape == (3, 4 if T <= 16 else 1)
         assert (ms > 0).all() and (ms < 1000).all()
-
-
-def test_numbers_that_do_not_fit_are_refused(gpu_lib):
-    x = torch.zeros(4, 64, device="cuda")
-    for call in (lambda: gpu_lib.add_rmsnorm(x, eps=1e39), lambda: gpu_lib.route_logits(x, 2, scale=-1e39),
-                 lambda: gpu_lib.route_logits(x, 2, n_groups=1 << 40)):
-        with pytest.raises(ValueError):
-            call()

@@ -415,7 +415,7 @@ def _packer(cls):
     def packed(*fields):
         try:
             return pack(*fields)
-        except (struct.error, OverflowError) as e:     # an integer, or a float, past its field
+        except struct.error as e:
             raise ValueError(f"{cls.__name__}: {e}") from None
     return packed
 
