@@ -254,3 +254,57 @@ def test_forwards_with_a_router_are_profiled(gpu_lib, d, sizes):
         # routing, gate/up, down and combine; a forward in several chunks of tokens as one
         assert ms.shape == (3, 4 if T <= 16 else 1)
         assert (ms > 0).all() and (ms < 1000).all()
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+def all_calls(moe, g):
+    """(name, call(stream) -> its results), every call that allocates some."""
+    T, d, E = 40, 256, 64
+    layer, *_ = make_layer(moe, d, 128, E, 4, T, g)
+    small = make_layer(moe, d, 128, E, 4, 8, g)[0]
+    stack = moe.MoeStack([small])
+    x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    w, _ = make_w4("nvfp4", 96, d, 16, False, None, g)
+    W = torch.randn(2, 64, d, generator=g, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(600, E, generator=g, device="cuda")
+    return [
+        ("route_logits", lambda st: list(moe.route_logits(logits, 4, stream=st).values())),
+        ("add_rmsnorm", lambda st: list(moe.add_rmsnorm(x, x, out_dtype=torch.float8_e4m3fn, group=64, stream=st))),
+        ("linear_nvfp4", lambda st: [moe.linear_nvfp4(x, *w, stream=st)]),
+        ("rmsnorm", lambda st: [moe.rmsnorm(x, stream=st)]),
+        ("quantize_nvfp4", lambda st: list(moe.quantize_nvfp4(W, stream=st))),
+        ("route", lambda st: list(layer.route(x, stream=st).values())),
+        ("forward", lambda st: [layer.forward(x, stream=st)]),
+        ("route_records", lambda st: list(layer.route_records(T, stream=st).values())),
+        ("expert_outputs", lambda st: [layer.expert_outputs(T, stream=st)]),
+        ("stack", lambda st: [stack.forward(x[:4].contiguous(), stream=st)]),
+    ]
+
+
+def test_results_belong_to_the_stream_they_are_written_on(gpu_lib):
+    """Memory that was freed on the current stream, but is still to be read there, is not what a call on another stream
+    writes its results to."""
+    side = torch.cuda.Stream()
+    for name, call in all_calls(gpu_lib, gen(71)):
+        want = [t.float().clone() for t in call(None)]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        baits = [torch.full((t.numel() * t.element_size(),), 77, dtype=torch.uint8, device="cuda")
+                 for _ in range(3) for t in call(None)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)                   # some 50 ms of the current stream
+        kept = [b + 0 for b in baits]                    # reads the baits after that
+        del baits
+        got = call(side)
+        side.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b)), name
+        torch.cuda.synchronize()
+        assert all((k == 77).all() for k in kept), name
+        segments = {s["address"]: s for s in torch.cuda.memory_snapshot()}
+        for t in got:
+            seg = max(a for a in segments if a <= t.data_ptr())
+            assert segments[seg]["stream"] == side.cuda_stream, name
+        del got

@@ -5,6 +5,11 @@ Argument marshalling only. Every step of the layer runs in the CUDA kernels
 behind the C ABI declared in ``include/moe.h``; PyTorch supplies device
 memory and streams. There is no fallback: if ``libmoe.so`` is missing or no
 GPU is present, the calls raise.
+
+Every call runs on ``stream``, by default the current one. What it allocates for
+its results belongs to that stream, as if the call stood in a
+``torch.cuda.stream(stream)`` block. Its inputs, and buffers handed to it, have to
+be ready there, and to be kept until that work is done.
 """
 from __future__ import annotations
 
@@ -161,6 +166,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call's result, from the memory of the stream that the call writes it on: memory of another stream
+    may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _require_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -222,20 +236,21 @@ class MoeLayer:
     # -- calls ----------------------------------------------------------------
     _RECORDS = ("ids", "w", "counts", "offsets", "perm", "pos")
 
-    def _records(self, T, dev):
+    def _records(self, T, dev, stream):
+        i32 = torch.int32
         return {
-            "ids": torch.empty((T, self.k), dtype=torch.int32, device=dev),
-            "w": torch.empty((T, self.k), dtype=torch.float32, device=dev),
-            "counts": torch.empty(self.E, dtype=torch.int32, device=dev),
-            "offsets": torch.empty(self.E + 1, dtype=torch.int32, device=dev),
-            "perm": torch.empty(T * self.k, dtype=torch.int32, device=dev),
-            "pos": torch.empty((T, self.k), dtype=torch.int32, device=dev),
+            "ids": _empty((T, self.k), i32, dev, stream),
+            "w": _empty((T, self.k), torch.float32, dev, stream),
+            "counts": _empty(self.E, i32, dev, stream),
+            "offsets": _empty(self.E + 1, i32, dev, stream),
+            "perm": _empty(T * self.k, i32, dev, stream),
+            "pos": _empty((T, self.k), i32, dev, stream),
         }
 
     def route(self, x, stream=None):
         _require_cuda(x)
         T = x.shape[0]
-        out = self._records(T, x.device)
+        out = self._records(T, x.device, stream)
         _check(load().moe_route(self._h, _ptr(x), T, *(_ptr(out[n]) for n in self._RECORDS), _stream(stream)),
                "moe_route")
         return out
@@ -243,7 +258,7 @@ class MoeLayer:
     def route_records(self, T, stream=None):
         """The routing records the last forward (or route) of T tokens left in
         the workspace, as that path's own kernels computed them."""
-        out = self._records(T, self.workspace.device)
+        out = self._records(T, self.workspace.device, stream)
         _check(load().moe_debug_route_records(self._h, T, *(_ptr(out[n]) for n in self._RECORDS),
                                               _stream(stream)), "moe_debug_route_records")
         return out
@@ -277,7 +292,7 @@ class MoeLayer:
         _require_cuda(x, out, res)
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
+            out = _empty((T, self.d), torch.bfloat16, x.device, stream)
         if res is None:
             _check(load().moe_forward(self._h, _ptr(x), _ptr(out), T, _stream(stream)), "moe_forward")
         else:
@@ -293,7 +308,7 @@ class MoeLayer:
         return out_host
 
     def expert_outputs(self, T, stream=None):
-        Y = torch.empty((T * self.k, self.d), dtype=torch.float32, device=self.workspace.device)
+        Y = _empty((T * self.k, self.d), torch.float32, self.workspace.device, stream)
         _check(load().moe_debug_expert_outputs(self._h, _ptr(Y), T, _stream(stream)), "moe_debug_expert_outputs")
         return Y
 
@@ -345,7 +360,7 @@ class MoeStack:
         _require_cuda(x, out, layer_out)
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
+            out = _empty((T, self.d), torch.bfloat16, x.device, stream)
         _check(load().moe_stack_forward(self._h, _ptr(x), _ptr(out), T, float(eps), _ptr(layer_out),
                                         _stream(stream)), "moe_stack_forward")
         return out
@@ -373,7 +388,7 @@ def rmsnorm(x, eps=1e-6, out=None, stream=None):
     _require_cuda(x, out)
     T, d = x.shape
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     _check(load().moe_rmsnorm(_ptr(x), _ptr(out), T, d, eps, _stream(stream)), "moe_rmsnorm")
     return out
 
@@ -382,9 +397,9 @@ def quantize_nvfp4(W, stream=None):
     """W [n, rows, K] bf16 on the GPU -> (q [n, rows, K/2] u8, s [n, rows, K/16] u8, g [n] fp32)."""
     _require_cuda(W)
     n, rows, K = W.shape
-    q = torch.empty((n, rows, K // 2), dtype=torch.uint8, device=W.device)
-    s = torch.empty((n, rows, K // 16), dtype=torch.uint8, device=W.device)
-    g = torch.empty(n, dtype=torch.float32, device=W.device)
+    q = _empty((n, rows, K // 2), torch.uint8, W.device, stream)
+    s = _empty((n, rows, K // 16), torch.uint8, W.device, stream)
+    g = _empty(n, torch.float32, W.device, stream)
     _check(load().moe_quantize_nvfp4(_ptr(W), n, rows, K, _ptr(q), _ptr(s), _ptr(g), _stream(stream)),
            "moe_quantize_nvfp4")
     return q, s, g
@@ -537,11 +552,9 @@ def route_logits(logits, top_k, *, score="softmax", bias=None, n_groups=1, topk_
     if bias is not None and bias.get_device() != index:
         raise ValueError(f"bias: on {bias.device}, logits on {logits.device}")
     if out is None:
-        i32 = {"dtype": torch.int32, "device": logits.device}
-        out = {"ids": torch.empty((T, top_k), **i32),
-               "w": torch.empty((T, top_k), dtype=torch.float32, device=logits.device),
-               "counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32),
-               "perm": torch.empty(T * top_k, **i32), "pos": torch.empty((T, top_k), **i32)}
+        shapes = ((T, top_k), (T, top_k), E, E + 1, T * top_k, (T, top_k))
+        out = {n: _empty(shape, dtype, logits.device, stream)
+               for n, dtype, shape in zip(_ROUTE_RECORDS, _ROUTE_TYPES, shapes)}
         recs = [out[n] for n in _ROUTE_RECORDS]
     else:
         recs = [out.get(n) for n in _ROUTE_RECORDS]
@@ -601,18 +614,18 @@ def add_rmsnorm(x, res=None, gain=None, *, eps=1e-6, out_dtype=None, group=0, su
     if group < 0 or (group and (not e4m3 or d % group)):
         raise ValueError("group divides d, and needs E4M3 output")
     if out is None:
-        out = torch.empty((T, d), dtype=out_dtype, device=x.device)
+        out = _empty((T, d), out_dtype, x.device, stream)
     if e4m3:
         cols = d // (group or d) if d else 0
         if scales is None:
-            scales = torch.empty((T, cols), dtype=torch.float32, device=x.device)
+            scales = _empty((T, cols), torch.float32, x.device, stream)
         scales_at, scales_ld = _rows("scales", scales, torch.float32, (T, cols), index)
     elif scales is not None:
         raise ValueError("scales need E4M3 output")
     else:
         scales_at = scales_ld = 0
     if sum_out is None and res is not None:
-        sum_out = torch.empty((T, d), dtype=dtype, device=x.device)
+        sum_out = _empty((T, d), dtype, x.device, stream)
     shape = (T, d)
     res_at, res_ld = _rows("res", res, dtype, shape, index)
     sum_at, sum_ld = _rows("sum_out", sum_out, dtype, shape, index)
@@ -649,7 +662,7 @@ def _linear_w4(fmt, x, q, s, g, z, x_scales, bias, out, out_dtype, stream):
         raise ValueError("x_scales belong to E4M3 x")
     if out is None:
         out_dtype = out_dtype or (torch.bfloat16 if x.dtype == torch.float8_e4m3fn else x.dtype)
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = _empty((M, N), out_dtype, x.device, stream)
     elif out_dtype is not None and out_dtype != out.dtype:
         raise ValueError("out_dtype and out differ")
     if out.dtype not in _FLOATS:
