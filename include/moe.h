@@ -326,7 +326,8 @@ moe_status moe_route_logits(const moe_route_desc *desc, const void *logits, moe_
 /* Makes moe_route and moe_forward* on this layer choose experts as `desc`
  * says, from the layer's own router logits (router_bias included); NULL
  * restores the softmax top-k. E and top_k must be the layer's. desc is copied;
- * its bias must stay valid. Such a forward runs the router, the choice and the
+ * its bias is read by every later call and must stay valid until they are done,
+ * and as long as a graph that captured one is replayed. Such a forward runs the router, the choice and the
  * expert kernels as separate launches. A token left with fewer than top_k
  * experts sets the error word that moe_get_device_status() reports as
  * MOE_ERR_DEVICE, and its output is undefined. Stacks of layers run the

@@ -308,3 +308,66 @@ def test_results_belong_to_the_stream_they_are_written_on(gpu_lib):
             seg = max(a for a in segments if a <= t.data_ptr())
             assert segments[seg]["stream"] == side.cuda_stream, name
         del got
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_a_router_bias_outlives_its_use(gpu_lib, T):
+    """Dropped while another stream is yet to read it, and while a captured graph is replayed."""
+    g, E = gen(72), 64
+    layer, *_ = make_layer(gpu_lib, 256, 128, E, 4, 64, g)
+    x = torch.randn(T, 256, generator=g, device="cuda").to(torch.bfloat16)
+    values = torch.randn(E, generator=g, device="cuda")
+    side = torch.cuda.Stream()
+
+    def spoil():
+        """Whatever memory of the bias's size is free is written over on the current stream."""
+        return [torch.full((E,), -1e3 * i, device="cuda") for i in range(64)]
+
+    layer.set_router(score="sigmoid", bias=values)
+    want = layer.forward(x).clone()
+    torch.cuda.synchronize()
+
+    # another stream
+    layer.set_router(score="sigmoid", bias=values.clone())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    out = layer.forward(x, stream=side)
+    layer.clear_router()
+    spoil()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+    # a graph
+    bias = values.clone()
+    layer.set_router(score="sigmoid", bias=bias)
+    layer.forward(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer.forward(x)
+    layer.set_router(bias=torch.zeros(E, device="cuda"))
+    layer.clear_router()
+    del bias
+    kept = spoil()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    del kept
+
+
+def test_a_router_bias_is_read_not_copied(gpu_lib):
+    g, E = gen(73), 64
+    layer, *_ = make_layer(gpu_lib, 256, 128, E, 4, 64, g)
+    x = torch.randn(5, 256, generator=g, device="cuda").to(torch.bfloat16)
+    a, b = (torch.randn(E, generator=g, device="cuda") for _ in range(2))
+    bias = a.clone()
+    layer.set_router(score="sigmoid", bias=bias)
+    first = layer.route(x)["ids"].clone()
+    bias.copy_(b)
+    second = layer.route(x)["ids"].clone()
+    layer.set_router(score="sigmoid", bias=b)
+    assert torch.equal(layer.route(x)["ids"], second) and not torch.equal(first, second)

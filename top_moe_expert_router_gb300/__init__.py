@@ -232,6 +232,8 @@ class MoeLayer:
                "moe_layer_create")
         self._h = h
         self._desc = desc
+        self._router_bias = None
+        self._captured_biases = []    # those that captured graphs read
 
     # -- calls ----------------------------------------------------------------
     _RECORDS = ("ids", "w", "counts", "offsets", "perm", "pos")
@@ -251,6 +253,7 @@ class MoeLayer:
         _require_cuda(x)
         T = x.shape[0]
         out = self._records(T, x.device, stream)
+        self._use_router_bias(stream)
         _check(load().moe_route(self._h, _ptr(x), T, *(_ptr(out[n]) for n in self._RECORDS), _stream(stream)),
                "moe_route")
         return out
@@ -276,7 +279,10 @@ class MoeLayer:
     def set_router(self, *, score="softmax", bias=None, n_groups=1, topk_groups=1, group_rule="max",
                    renormalise=True, scale=1.0):
         """Choose the layer's experts as ``route_logits`` does, from the layer's own
-        router logits; see ``clear_router``. ``bias``: [E] fp32 CUDA tensor or None."""
+        router logits; see ``clear_router``. ``bias``: [E] fp32 CUDA tensor or None; it is
+        read, not copied, so that changes to its values count from the next call on. A
+        bias that is replaced or cleared stays until what has read it is done, and, where
+        a graph captured a call with it, as long as the layer."""
         desc = _route_desc(self.E, self.k, score, bias, n_groups, topk_groups, group_rule, renormalise, scale)
         if bias is not None and bias.device != self.workspace.device:
             raise ValueError(f"bias: on {bias.device}, the layer on {self.workspace.device}")
@@ -288,11 +294,23 @@ class MoeLayer:
         _check(load().moe_layer_set_router(self._h, None), "moe_layer_set_router")
         self._router_bias = None
 
+    def _use_router_bias(self, stream):
+        """Keeps the bias, should it be dropped, for the work on `stream` that reads it."""
+        bias = self._router_bias
+        if bias is None:
+            return
+        with torch.cuda.stream(stream):             # (None: the current one)
+            if not torch.cuda.is_current_stream_capturing():
+                bias.record_stream(torch.cuda.current_stream())
+            elif not any(b is bias for b in self._captured_biases):
+                self._captured_biases.append(bias)
+
     def forward(self, x, out=None, res=None, stream=None):
         _require_cuda(x, out, res)
         T = x.shape[0]
         if out is None:
             out = _empty((T, self.d), torch.bfloat16, x.device, stream)
+        self._use_router_bias(stream)
         if res is None:
             _check(load().moe_forward(self._h, _ptr(x), _ptr(out), T, _stream(stream)), "moe_forward")
         else:
@@ -303,6 +321,7 @@ class MoeLayer:
     def forward_host(self, x_host, out_host, stream=None):
         """x_host, out_host: CPU tensors [T, d] bf16 (pinned for async copies)."""
         T = x_host.shape[0]
+        self._use_router_bias(stream)
         _check(load().moe_forward_host(self._h, _ptr(x_host), _ptr(out_host), T, _stream(stream)),
                "moe_forward_host")
         return out_host
