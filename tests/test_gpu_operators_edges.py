@@ -371,3 +371,122 @@ def test_a_router_bias_is_read_not_copied(gpu_lib):
     second = layer.route(x)["ids"].clone()
     layer.set_router(score="sigmoid", bias=b)
     assert torch.equal(layer.route(x)["ids"], second) and not torch.equal(first, second)
+
+
+def whole_numbers(T, d, E, g):
+    """Tokens and router weights whose products and sums are exact in any order, so that the layer's logits are the
+    reference's to the bit: ties and all, the choice has to be the same."""
+    x = torch.randint(-2, 3, (T, d), generator=g, device="cuda").float()
+    wr = torch.randint(-1, 2, (E, d), generator=g, device="cuda").float() / 16
+    return x.to(torch.bfloat16), wr.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("form", ["plain", "normed", "interleaved", "nvfp4"])
+@pytest.mark.parametrize("opt", [dict(score="sigmoid", n_groups=8, topk_groups=3, group_rule="top2", scale=2.5),
+                                 dict(score="softmax", renormalise=False), dict(score="softmax", n_groups=4, topk_groups=2)])
+def test_forms_of_the_layer_with_their_own_router(gpu_lib, form, opt):
+    """Normed experts, interleaved rows, 4-bit experts, a bias of the router logits; from host memory too."""
+    moe, g, d, I, E, k = gpu_lib, gen(81), 512, 256, 64, 6
+    _, wr = whole_numbers(1, d, E, g)
+    gate, up = ((0.05 * torch.randn(E, I, d, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2))
+    down = (0.05 * torch.randn(E, d, I, generator=g, device="cuda")).to(torch.bfloat16)
+    lbias = torch.randint(-8, 9, (E,), generator=g, device="cuda").float() / 8
+    kw = dict(top_k=k, max_tokens=300, router_bias=lbias)
+    if form == "interleaved":
+        layer = moe.MoeLayer(wr, w_gate_up=torch.stack((gate, up), 2).contiguous(), w_down=down, **kw)
+    elif form == "nvfp4":
+        layer, _, gate, up, down = make_layer(moe, d, I, E, k, 300, g, "nvfp4")
+        layer = moe.MoeLayer(wr, nvfp4=dict(zip(("q_gate", "s_gate", "g_gate", "q_up", "s_up", "g_up", "q_down", "s_down", "g_down"),
+                                                layer._keep[2:])), **kw)
+    else:
+        layer = moe.MoeLayer(wr, w_gate=gate, w_up=up, w_down=down, expert_out_norm=form == "normed", **kw)
+    bias = 0.2 * torch.randn(E, generator=g, device="cuda")
+    layer.set_router(bias=bias, **opt)
+    for T in (1, 8, 16, 17, 32, 33, 300):
+        x, _ = whole_numbers(T, d, E, g)
+        logits = (x.double() @ wr.double().t() + lbias.double()).float()
+        r = layer.route(x)
+        check_route(r, logits, k, bias=bias, **opt)
+        y = layer.forward(x)
+        left = layer.route_records(T) if T <= 16 or d % 256 == 0 else r
+        for n in r:
+            assert torch.equal(left[n], r[n]), n
+        host = torch.empty(T, d, dtype=torch.bfloat16).pin_memory()
+        layer.forward_host(x.cpu().pin_memory(), host)
+        assert torch.equal(host, y.cpu())
+        assert layer.device_status() == moe.MOE_OK
+        ids, w = r["ids"].long(), r["w"]
+        if form == "normed":
+            ref = torch.zeros(T, d, dtype=torch.float64, device="cuda")
+            one = torch.ones(T, 1, device="cuda")
+            for j in range(k):
+                e = ref_experts(x, ids[:, j:j + 1], one, gate, up, down)
+                ref += w[:, j:j + 1].double() * e / (e.square().mean(1, keepdim=True) + 1e-6).sqrt()
+        else:
+            ref = ref_experts(x, ids, w, gate, up, down)
+        err = (y.double() - ref).abs().amax(1) / ref.abs().amax(1)
+        assert err.max() <= (5e-2 if form == "nvfp4" else 2e-2), (T, err.max())    # the layer's own bars
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+def test_a_router_that_leaves_no_expert_is_reported(gpu_lib, fmt):
+    moe, g = gpu_lib, gen(82)
+    layer, *_ = make_layer(moe, 256, 256, 64, 4, 300, g, fmt)
+    none = torch.full((64,), -INF, device="cuda")
+    for T in (1, 16, 300):
+        x = torch.randn(T, 256, generator=g, device="cuda").to(torch.bfloat16)
+        want = layer.forward(x).clone()
+        layer.set_router(score="softmax", bias=none)
+        r = layer.route(x)
+        assert (r["ids"] == -1).all() and (r["counts"] == 0).all() and (r["offsets"] == 0).all()
+        layer.forward(x)
+        assert layer.device_status() == moe.MOE_ERR_DEVICE
+        layer.clear_router()
+        assert torch.equal(layer.forward(x), want) and layer.device_status() == moe.MOE_OK
+
+
+FIRST_USE = """
+import torch
+import top_moe_expert_router_gb300 as moe
+g = torch.Generator(device="cuda").manual_seed(5)
+def t(*s): return torch.randn(*s, generator=g, device="cuda")
+def u8(*s): return torch.randint(0, 120, s, generator=g, device="cuda", dtype=torch.uint8)
+few, many = t(40, 64), t(700, 300)
+x, res, bias = t(5, 1024).to(torch.bfloat16), t(5, 1024).to(torch.bfloat16), t(64)
+w4 = u8(300, 512), u8(300, 64), torch.full((1,), 1e-4, device="cuda")
+i4 = u8(600, 512), (t(600, 16) / 100).to(torch.float16), u8(600, 16) % 16
+layer = moe.MoeLayer(t(64, 256).to(torch.bfloat16), w_gate=t(64, 128, 256).to(torch.bfloat16) / 16,
+                     w_up=t(64, 128, 256).to(torch.bfloat16) / 16, w_down=t(64, 256, 128).to(torch.bfloat16) / 16, top_k=4, max_tokens=64)
+xl = [t(n, 256).to(torch.bfloat16) for n in (3, 40)]
+layer.set_router(score="sigmoid", bias=bias, n_groups=8, topk_groups=4, group_rule="top2")
+def calls():
+    n8, s, sc = moe.add_rmsnorm(x, res, out_dtype=torch.float8_e4m3fn, group=128)
+    out = [n8.float(), s, sc, moe.linear_nvfp4(n8, *w4, x_scales=sc), moe.linear_int4(x, *i4)]
+    for l in (few, many):
+        out += moe.route_logits(l, 6, score="sigmoid").values()
+    return out + [layer.forward(v) for v in xl]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = calls()
+for _ in range(2):
+    for h in held:
+        h.zero_()
+    graph.replay()
+torch.cuda.synchronize()
+got = [h.clone() for h in held]
+for a, b in zip(got, calls(), strict=True):
+    assert torch.equal(a, b)
+assert layer.device_status() == moe.MOE_OK
+print("same")
+"""
+
+
+def test_first_use_of_every_operator_inside_a_capture():
+    """A process whose first call of each operator, and of a layer with a router, is a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_USE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
