@@ -327,10 +327,12 @@ moe_status moe_route_logits(const moe_route_desc *desc, const void *logits, moe_
  * says, from the layer's own router logits (router_bias included); NULL
  * restores the softmax top-k. E and top_k must be the layer's. desc is copied;
  * its bias is read by every later call and must stay valid until they are done,
- * and as long as a graph that captured one is replayed. Such a forward runs the router, the choice and the
- * expert kernels as separate launches. A token left with fewer than top_k
- * experts sets the error word that moe_get_device_status() reports as
- * MOE_ERR_DEVICE, and its output is undefined. Stacks of layers run the
+ * and as long as a graph that captured one is replayed. Such a forward runs
+ * the router, the choice and the expert kernels as separate launches, up to 16
+ * tokens those of the split decode whatever moe_set_decode_path says (slower
+ * than the single launch, the more so the more tokens). A token left with fewer
+ * than top_k experts sets the error word that moe_get_device_status() reports
+ * as MOE_ERR_DEVICE, and its output is undefined. Stacks of layers run the
  * softmax top-k only: moe_stack_create and moe_stack_forward return
  * MOE_ERR_UNSUPPORTED while one of their layers has a router set. */
 moe_status moe_layer_set_router(moe_layer *layer, const moe_route_desc *desc);
@@ -340,8 +342,9 @@ moe_status moe_layer_set_router(moe_layer *layer, const moe_route_desc *desc);
  *   y = s / sqrt(mean(s^2) + eps) * gain
  * out_type = type: out = round(y). out_type = MOE_T_E4M3: for every `group`
  * columns (0: the whole row) scale = max|y| / 448 (1 where that is no normal
- * float: a group of zeros) and out = E4M3(y / scale). fp32 arithmetic; the norm
- * is of the rounded sum, as moe_rmsnorm after moe_forward_residual. A row of
+ * float: a group of zeros) and out = E4M3(y / scale). fp32 arithmetic, roots and
+ * quotients within a few 2^-24: where y / scale is the middle between two codes
+ * (bf16 and f16 inputs meet it exactly), either may be stored. The norm is of the rounded sum, as moe_rmsnorm after moe_forward_residual. A row of
  * zeros gives zeros (eps = 0 included); a row with an infinity or NaN gives what
  * the formula does, zeros and NaN, and no other row is touched. sum, or out of
  * the inputs' type, may be the same buffer as x or res, with the same stride;
@@ -369,8 +372,10 @@ moe_status moe_add_rmsnorm(const moe_norm_args *args, void *stream);
  *     s [N, K/group] bf16 or f16, z [N, K/group] bytes, NULL: 8 everywhere.
  * x [M, K] is bf16, f16, or E4M3 with scales x_scales [M, K/x_group], x_group
  * a multiple of 128 or 0 (one scale per token), as moe_add_rmsnorm writes
- * them. y [M, N] is bf16, f16 or fp32. Products and sums are fp32; more than 32
- * tokens read the weights twice. K a multiple of 32 and of the group,
+ * them. y [M, N] is bf16, f16 or fp32. Weights enter the products exactly, as do
+ * f16 and E4M3 x; bf16 x is held relative to the largest finite element of each
+ * 128 columns, to 2^-39 of it (exactly down to 2^-29). Products and sums are
+ * fp32, NVFP4's in units of g; more than 32 tokens read the weights twice. K a multiple of 32 and of the group,
  * K <= 32768, N <= 2^30; q 16-byte aligned, s 2-byte aligned; y overlaps no input. */
 typedef enum { MOE_W4_NVFP4 = 0, MOE_W4_INT4 = 1 } moe_w4_fmt;
 typedef struct {

@@ -1,7 +1,9 @@
 // decode.cu — the split streaming expert stage (two launches per chunk of at
-// most 16 tokens), used for NVFP4 batches of more than 16 tokens, which the
-// bf16 grouped GEMMs of the prefill path do not take. The single-launch layer
-// kernel (decode_fused.cuh) covers every batch of at most 16 tokens.
+// most 16 tokens): for layers whose d or I the grouped GEMMs' tiles do not
+// divide, beyond 16 tokens, and for layers with a router of their own
+// (moe_layer_set_router) up to 16, since the single-launch layer kernels
+// (decode_fused.cuh, decode_mma.cuh) that take all other small batches have the
+// softmax top-k built in.
 //
 // Decode-sized chunks are bound by streaming weights from HBM, not by matmul
 // speed, and fetching weights ahead of the compute that needs them hides the

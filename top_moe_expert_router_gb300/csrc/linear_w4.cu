@@ -16,7 +16,7 @@
 // f16 and E4M3 is exact in f16; x in bf16 is scaled by a power of two per
 // token and 128 columns so that the block's largest element lies in [2^14,
 // 2^15): elements down to 2^-29 of the largest keep all their bits, smaller
-// ones lose at most 2^-40 of it. Products and sums are fp32; an INT4 group's
+// ones lose at most 2^-39 of it. Products and sums are fp32; an INT4 group's
 // sum is multiplied by its scale, a 128-column block's by x's, in fp32.
 //
 // Structure. A CTA takes tiles of 64 or 128 rows: a producer warp streams their
@@ -25,13 +25,13 @@
 // x is read once for two products). K is split over a cluster of up to 8 CTAs
 // where there are few tiles; their sums meet in distributed shared memory, added
 // in rank order. What bounds it: the large sizes, about 18 instructions per 256
-// weights that issue in 52 % of the slots while the ring, three stages beside x,
-// keeps DRAM 61 % busy; the small ones, staging x and joining the parts.
+// weights that issue in 51 % of the slots while the ring, three stages beside x,
+// keeps DRAM 60 % busy; the small ones, staging x and joining the parts.
 // Measured on the way (131072 x 4096 NVFP4, 4 tokens, 45 us of stream): loads
 // into registers one block ahead 92 us (waiting for one block's load waited
 // for later ones too), two batches of four blocks in turn 70 us, a ring of
 // 16-byte asynchronous copies 88 us (the L1's tag and data cycles: 82 % busy);
-// now 60 us. 256-row tiles on one CTA of 16 warps took 63 us, pairs of CTAs that
+// now 61 us. 256-row tiles on one CTA of 16 warps took 63 us, pairs of CTAs that
 // share a run of tiles, to end together, 64 us.
 //
 // The k order inside a 128-column block is free as long as both operands use
