@@ -344,7 +344,8 @@ moe_status moe_layer_set_router(moe_layer *layer, const moe_route_desc *desc);
  * columns (0: the whole row) scale = max|y| / 448 (1 where that is no normal
  * float: a group of zeros) and out = E4M3(y / scale). fp32 arithmetic, roots and
  * quotients within a few 2^-24: where y / scale is the middle between two codes
- * (bf16 and f16 inputs meet it exactly), either may be stored. The norm is of the rounded sum, as moe_rmsnorm after moe_forward_residual. A row of
+ * (bf16 and f16 inputs meet it exactly), either may be stored. The norm is of
+ * the rounded sum, as moe_rmsnorm after moe_forward_residual. A row of
  * zeros gives zeros (eps = 0 included); a row with an infinity or NaN gives what
  * the formula does, zeros and NaN, and no other row is touched. sum, or out of
  * the inputs' type, may be the same buffer as x or res, with the same stride;
@@ -375,8 +376,9 @@ moe_status moe_add_rmsnorm(const moe_norm_args *args, void *stream);
  * them. y [M, N] is bf16, f16 or fp32. Weights enter the products exactly, as do
  * f16 and E4M3 x; bf16 x is held relative to the largest finite element of each
  * 128 columns, to 2^-39 of it (exactly down to 2^-29). Products and sums are
- * fp32, NVFP4's in units of g; more than 32 tokens read the weights twice. K a multiple of 32 and of the group,
- * K <= 32768, N <= 2^30; q 16-byte aligned, s 2-byte aligned; y overlaps no input. */
+ * fp32, NVFP4's in units of g; more than 32 tokens read the weights twice. K a
+ * multiple of 32 and of the group, K <= 32768, N <= 2^30; q 16-byte aligned, s
+ * 2-byte aligned; y overlaps no input. */
 typedef enum { MOE_W4_NVFP4 = 0, MOE_W4_INT4 = 1 } moe_w4_fmt;
 typedef struct {
     moe_w4_fmt fmt;

@@ -402,19 +402,22 @@ __device__ __forceinline__ uint32_t in_kept_groups(const RouteArgs &a, bool kept
     return in;
 }
 
-// The largest upper end of the scores below `bound`, of the experts that `in` says (a lane's bits); -inf where there
-// are none. One copy of the code: few tokens come here.
+// The largest upper end of the scores of the experts that `in` says (a lane's bits) less the gathered ones (`id`, one a
+// lane or -1); -inf where there are none. One copy of the code: few tokens come here.
 template <int EPL>
-__device__ __noinline__ float upper_end_below(const RouteArgs &a, int64_t row, float lmax, int lane, uint32_t bound,
-                                              uint32_t in) {
+__device__ __noinline__ float upper_end_of_rest(const RouteArgs &a, int64_t row, float lmax, int lane, uint32_t in, int id,
+                                                int n) {
     float l[EPL], c[EPL];
     load_clean<EPL>(a, row, lane * EPL, l);
     const float err = score_lane<EPL>(a, l, lmax, lane * EPL, true, c);
+    for (int j = 0; j < n; ++j) {
+        const int i = __shfl_sync(kFull, id, j) - lane * EPL;
+        if (i >= 0 && i < EPL) in &= ~(1u << i);
+    }
     float hi = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        if (((in >> i) & 1u) && c[i] > -INFINITY && key_of(c[i]) < bound)
-            hi = fmaxf(hi, c[i] + own_err(a, err, l[i], lmax) + 0x1p-22f * fabsf(c[i]));
+        if (((in >> i) & 1u) && c[i] > -INFINITY) hi = fmaxf(hi, c[i] + own_err(a, err, l[i], lmax) + 0x1p-22f * fabsf(c[i]));
     return value_of(__reduce_max_sync(kFull, key_of(hi)));
 }
 
@@ -505,7 +508,7 @@ __device__ __forceinline__ Pick choose_fast(const RouteArgs &a, const float (&l)
             if (!a.sigmoid && !within) {
                 const float lo = one && r.rank < a.k ? v - (own + 0x1p-22f * fabsf(v)) : INFINITY;
                 within = value_of(__reduce_min_sync(kFull, key_of(lo))) >
-                         upper_end_below<EPL>(a, row, lmax, lane, bound, in);
+                         upper_end_of_rest<EPL>(a, row, lmax, lane, in, r.id, n);
                 near |= !within;
             }
         }
