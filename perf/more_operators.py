@@ -106,10 +106,15 @@ def _codes(r):
     return code[..., 0::2] | (code[..., 1::2] << 4)
 
 
+def _power(e):
+    """2 ** e of whole numbers e in [-127, 127], as the bits of a float."""
+    return torch.where(e > -127, (e + 127) << 23, 1 << 22).to(torch.int32).view(torch.float32)
+
+
 def _row_scale(x):
     """The smallest power of two g with max|x| / (6 * 448) <= g, 1 for a row of zeros."""
     m, e = torch.frexp(x.abs().amax(-1) / (6 * 448))
-    return torch.where(m > 0, torch.ldexp(torch.ones_like(m), torch.where(m == 0.5, e - 1, e).clamp_min(-100)), 1.0)
+    return torch.where(m > 0, _power(torch.where(m == 0.5, e - 1, e).clamp_min(-100)), 1.0)
 
 
 def _quantise(x, fmt, g=None):
@@ -122,7 +127,7 @@ def _quantise(x, fmt, g=None):
     else:
         e = (torch.frexp(top).exponent - 3).clamp(-127, 127)
         e = torch.where(top > 0, e, -127)
-        unit, s = torch.ldexp(torch.ones_like(top), e), (e + 127).to(torch.uint8)
+        unit, s = _power(e), (e + 127).to(torch.uint8)
     r = torch.where(unit[..., None] > 0, b / unit[..., None], 0.0)
     return _codes(r.flatten(-2)), s
 
@@ -134,7 +139,7 @@ def _values(q, s, g, fmt):
     if fmt == "nvfp4":
         unit = s.view(torch.float8_e4m3fn).float() * g[..., None]
     else:
-        unit = torch.ldexp(torch.ones(s.shape, device=s.device), s.int() - 127)
+        unit = _power(s.int() - 127)
     return (v * unit[..., None]).flatten(-2)
 
 
