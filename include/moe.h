@@ -273,7 +273,8 @@ moe_status moe_stack_destroy(moe_stack *stack);
 
 /* ---------------------------------------------------------------------------
  * Operators around the layer: routing from logits, the residual addition and
- * norm in front of it, and products with 4-bit weights. They keep no state:
+ * norm in front of it, products with 4-bit weights, 4-bit floats and their
+ * products, and products grouped by expert. They keep no state:
  * calls on different streams may overlap as long as their buffers (and, for
  * moe_route_logits, their workspaces) differ, and all of them can be captured
  * into a graph. Strides count elements, and rows may lie further apart than
@@ -411,6 +412,112 @@ moe_status moe_linear_w4_status(void *stream);
 /* Test hook: the products launched while hold != 0 copy no weights, so that
  * their waits run out. No GPU work. */
 moe_status moe_debug_hold_linear_w4(int hold);
+
+/* Microscaled 4-bit floats: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ * sign), two to a byte, the low nibble holding the lower index, and scales:
+ *   MOE_FP4_NVFP4: an E4M3 byte s per 16 columns and an fp32 g per row (or
+ *     matrix); a code stands for e2m1 * s * g;
+ *   MOE_FP4_MXFP4: a byte s per 32 columns, the power of two 2^(s - 127), 255
+ *     NaN; a code stands for e2m1 * 2^(s - 127).
+ * moe_quantize_nvfp4 writes the first, g one per matrix. */
+typedef enum { MOE_FP4_NVFP4 = 0, MOE_FP4_MXFP4 = 1 } moe_fp4_fmt;
+
+/* Rows to 4-bit floats. v = x, or silu(x) * up in fp32 with up; rows given:
+ * row r of the result is that of x (and up) at rows[r], and stays as it is
+ * where rows[r] lies outside [0, T), as perm of the routing does past its end.
+ *   NVFP4: g = the smallest power of two >= max|v of the row| / 2688, at least
+ *     2^-100, 1 for a row of zeros; s = E4M3(max|v of the block| / 6 / g);
+ *     codes E2M1(v / (s g)), 0 where s is 0.
+ *   MXFP4: s = floor(log2 max|v of the block|) - 2, clamped to [-127, 127], as
+ *     s + 127, 0 for a block of zeros; codes E2M1(v / 2^s), saturating.
+ * Nearest, ties to even, of exact quotients (with up: of the fp32 v, whose
+ * silu is within 2^-21). A row (NVFP4) or block (MXFP4) that holds an infinity
+ * or NaN gets codes 0 and NaN as g (255 as s): everything computed from it is
+ * NaN. K a multiple of 64, K <= 32768; q 16-byte, s 4-byte aligned, both
+ * without gaps between rows. No output overlaps an input. */
+typedef struct {
+    moe_fp4_fmt fmt;
+    moe_dtype type;      /* of x and up: bf16 or f16 */
+    const void *x;       /* [T, K] */
+    const void *up;      /* [T, K] or NULL */
+    int64_t x_stride, up_stride;
+    const int32_t *rows; /* [R], or NULL: R = T, in order */
+    int T, R, K;
+    uint8_t *q;          /* [R, K/2] */
+    uint8_t *s;          /* [R, K/16] or [R, K/32] */
+    float *g;            /* NVFP4: [R] */
+} moe_quantize_fp4_args;
+moe_status moe_quantize_fp4(const moe_quantize_fp4_args *args, void *stream);
+
+/* What codes and scales stand for, in fp32 and rounded once to bf16, f16 or
+ * fp32. g (NVFP4): [R], or one for all rows, or NULL (1). Alignment and limits
+ * as above. */
+typedef struct {
+    moe_fp4_fmt fmt;
+    moe_dtype type;      /* of out */
+    const uint8_t *q, *s;
+    const float *g;
+    int g_rows;          /* nonzero: g holds one scale a row */
+    int R, K;
+    void *out;           /* [R, K] */
+    int64_t out_stride;
+} moe_dequantize_fp4_args;
+moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *args, void *stream);
+
+/* Products of rows grouped by expert, y[r] = W[e] x[r] + bias[e] for the rows
+ * offsets[e] <= r < offsets[e+1] (device, int32, ascending, as the routing
+ * writes them); rows before offsets[0] and from offsets[groups] on are left as
+ * they are, and no offset leads outside [0, M). offsets NULL (groups = 1): one
+ * matrix for all M rows. Products and sums are fp32. No row of x reaches another row's
+ * result: an infinity or NaN stays in its row. y is bf16, f16 or fp32 and
+ * overlaps no input. groups <= 512, M and N <= 2^24, groups * N < 2^31.
+ *
+ * moe_grouped_linear: x and W of one type, bf16 or f16; K a multiple of 8, x
+ * 16-byte aligned with a stride that is a multiple of 8, W [groups, N, K]
+ * 16-byte aligned.
+ * moe_linear_fp4: x and W in 4-bit floats of one format, as above, K as there;
+ * block products and their scales are exact, sums fp32, and g of x and W
+ * multiply them. */
+typedef struct {
+    moe_dtype type;
+    int groups, M, N, K;
+    const int32_t *offsets;
+    const void *x;       /* [M, K] */
+    int64_t x_stride;
+    const void *w;       /* [groups, N, K] */
+    const float *bias;   /* [groups, N] fp32 or NULL */
+    void *y;             /* [M, N] */
+    moe_dtype y_type;
+    int64_t y_stride;
+} moe_grouped_linear_args;
+moe_status moe_grouped_linear(const moe_grouped_linear_args *args, void *stream);
+
+typedef struct {
+    moe_fp4_fmt fmt;
+    int groups, M, N, K;
+    const int32_t *offsets;
+    const uint8_t *xq, *xs;  /* [M, K/2], [M, K/16 or K/32] */
+    const float *xg;         /* NVFP4: [M] or NULL (1) */
+    const uint8_t *wq, *ws;  /* [groups, N, K/2], [groups, N, K/16 or K/32] */
+    const float *wg;         /* NVFP4: [groups], with wg_cols [groups, N], or NULL (1) */
+    int wg_cols;
+    const float *bias;       /* [groups, N] fp32 or NULL */
+    void *y;                 /* [M, N] */
+    moe_dtype y_type;
+    int64_t y_stride;
+} moe_linear_fp4_args;
+moe_status moe_linear_fp4(const moe_linear_fp4_args *args, void *stream);
+
+/* The waits inside these products are bounded (1.5 s). Where one runs out the
+ * call leaves NaN in the rows concerned and sets a bit that belongs to the
+ * device, not to the call. moe_products_status waits for `stream`, then reads
+ * and clears the current device's: MOE_OK or MOE_ERR_TIMEOUT. Not while the
+ * stream is being captured. */
+moe_status moe_products_status(void *stream);
+
+/* Test hook: the products launched while hold != 0 copy no operands, so that
+ * their waits run out. No GPU work. */
+moe_status moe_debug_hold_products(int hold);
 
 moe_status moe_layer_destroy(moe_layer *layer);
 

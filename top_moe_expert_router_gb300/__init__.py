@@ -33,6 +33,7 @@ MOE_T_BF16, MOE_T_F16, MOE_T_F32, MOE_T_E4M3 = range(4)
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 MOE_W4_NVFP4, MOE_W4_INT4 = 0, 1
+MOE_FP4_NVFP4, MOE_FP4_MXFP4 = 0, 1
 MOE_DECODE_AUTO, MOE_DECODE_CUDA_CORES, MOE_DECODE_TENSOR_CORES = 0, 1, 2
 
 
@@ -82,6 +83,42 @@ class MoeW4Args(ctypes.Structure):
         ("z", ctypes.c_void_p), ("x", ctypes.c_void_p), ("x_type", ctypes.c_int), ("x_stride", ctypes.c_int64),
         ("x_scales", ctypes.c_void_p), ("x_scales_stride", ctypes.c_int64), ("x_group", ctypes.c_int),
         ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_type", ctypes.c_int), ("y_stride", ctypes.c_int64),
+    ]
+
+
+class MoeQuantizeFp4Args(ctypes.Structure):
+    _fields_ = [
+        ("fmt", ctypes.c_int), ("type", ctypes.c_int), ("x", ctypes.c_void_p), ("up", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64), ("up_stride", ctypes.c_int64), ("rows", ctypes.c_void_p),
+        ("T", ctypes.c_int), ("R", ctypes.c_int), ("K", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("g", ctypes.c_void_p),
+    ]
+
+
+class MoeDequantizeFp4Args(ctypes.Structure):
+    _fields_ = [
+        ("fmt", ctypes.c_int), ("type", ctypes.c_int), ("q", ctypes.c_void_p), ("s", ctypes.c_void_p),
+        ("g", ctypes.c_void_p), ("g_rows", ctypes.c_int), ("R", ctypes.c_int), ("K", ctypes.c_int),
+        ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+    ]
+
+
+class MoeGroupedLinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("type", ctypes.c_int), ("groups", ctypes.c_int), ("M", ctypes.c_int), ("N", ctypes.c_int),
+        ("K", ctypes.c_int), ("offsets", ctypes.c_void_p), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_type", ctypes.c_int),
+        ("y_stride", ctypes.c_int64),
+    ]
+
+
+class MoeLinearFp4Args(ctypes.Structure):
+    _fields_ = [
+        ("fmt", ctypes.c_int), ("groups", ctypes.c_int), ("M", ctypes.c_int), ("N", ctypes.c_int),
+        ("K", ctypes.c_int), ("offsets", ctypes.c_void_p), ("xq", ctypes.c_void_p), ("xs", ctypes.c_void_p),
+        ("xg", ctypes.c_void_p), ("wq", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("wg", ctypes.c_void_p),
+        ("wg_cols", ctypes.c_int), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_type", ctypes.c_int),
+        ("y_stride", ctypes.c_int64),
     ]
 
 
@@ -137,6 +174,12 @@ def load(path: str | None = None):
             "moe_linear_w4": ([ctypes.POINTER(MoeW4Args), vp], st),
             "moe_linear_w4_status": ([vp], st),
             "moe_debug_hold_linear_w4": ([i], st),
+            "moe_quantize_fp4": ([ctypes.POINTER(MoeQuantizeFp4Args), vp], st),
+            "moe_dequantize_fp4": ([ctypes.POINTER(MoeDequantizeFp4Args), vp], st),
+            "moe_grouped_linear": ([ctypes.POINTER(MoeGroupedLinearArgs), vp], st),
+            "moe_linear_fp4": ([ctypes.POINTER(MoeLinearFp4Args), vp], st),
+            "moe_products_status": ([vp], st),
+            "moe_debug_hold_products": ([i], st),
             "moe_status_string": ([st], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -440,7 +483,9 @@ _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 
 # The argument structures as bytes, in a quarter of the time that a ctypes structure takes to fill.
 _PACK = {MoeRouteDesc: struct.Struct("@iiiPiiiif4x"), MoeNormArgs: struct.Struct("@6P5q5if"),
-         MoeW4Args: struct.Struct("@5iPPiPPPiqPqiPPiq")}
+         MoeW4Args: struct.Struct("@5iPPiPPPiqPqiPPiq"), MoeQuantizeFp4Args: struct.Struct("@iiPPqqPiiiPPP"),
+         MoeDequantizeFp4Args: struct.Struct("@iiPPPiiiPq"), MoeGroupedLinearArgs: struct.Struct("@5iPPqPPPiq"),
+         MoeLinearFp4Args: struct.Struct("@5i7PiPPiq")}
 
 
 def _packer(cls):
@@ -454,17 +499,19 @@ def _packer(cls):
     return packed
 
 
-_pack_route, _pack_norm, _pack_w4 = (_packer(s) for s in (MoeRouteDesc, MoeNormArgs, MoeW4Args))
+_pack_route, _pack_norm, _pack_w4, _pack_quant, _pack_dequant, _pack_grouped, _pack_fp4 = (_packer(s) for s in _PACK)
+_ENTRIES = ("moe_route_logits", "moe_add_rmsnorm", "moe_linear_w4", "moe_quantize_fp4", "moe_dequantize_fp4",
+            "moe_grouped_linear", "moe_linear_fp4")
 _entries = None
 
 
 def _entry(i):
-    """route_logits', add_rmsnorm's or linear_w4's C entry, which takes its structure as bytes."""
+    """The C entry _ENTRIES[i], which takes its structure as bytes."""
     global _entries
     if _entries is None:
         lib = load()
-        fns = [lib["moe_route_logits"], lib["moe_add_rmsnorm"], lib["moe_linear_w4"]]    # objects of their own
-        for fn, typed in zip(fns, (lib.moe_route_logits, lib.moe_add_rmsnorm, lib.moe_linear_w4)):
+        fns = [lib[name] for name in _ENTRIES]                # objects of their own
+        for fn, typed in zip(fns, (getattr(lib, name) for name in _ENTRIES)):
             fn.argtypes = [ctypes.c_char_p, *typed.argtypes[1:]]
             fn.restype = typed.restype
         _entries = fns
@@ -722,3 +769,203 @@ def linear_w4_status(stream=None) -> int:
 def hold_linear_w4(hold: bool):
     """Test hook: make the waits of the 4-bit products run out, or restore them."""
     _check(load().moe_debug_hold_linear_w4(1 if hold else 0), "moe_debug_hold_linear_w4")
+
+
+# -- 4-bit floats, and products by expert ----------------------------------------
+_HALFS = (torch.bfloat16, torch.float16)
+_FP4 = {"nvfp4": (MOE_FP4_NVFP4, 16), "mxfp4": (MOE_FP4_MXFP4, 32)}
+
+
+def _fp4_fmt(name, q, s):
+    """The format of a matrix in 4-bit floats, by its columns a scale, and its K."""
+    if q.dim() < 2 or s.dim() != q.dim():
+        raise ValueError(f"{name}: codes [.., K/2] and scales [.., K/16] or [.., K/32] expected")
+    K = 2 * q.shape[-1]
+    if s.shape[-1] * 16 == K:
+        return MOE_FP4_NVFP4, K
+    if s.shape[-1] * 32 == K:
+        return MOE_FP4_MXFP4, K
+    raise ValueError(f"{name}: one scale per 16 (NVFP4) or 32 (MXFP4) columns expected")
+
+
+def quantize_fp4(x, fmt="nvfp4", *, up=None, rows=None, out=None, stream=None):
+    """Rows [T, K] (bf16 or f16) to microscaled 4-bit floats (moe_quantize_fp4) -> (q, s, g): codes [R, K/2] uint8, the
+    low nibble first, and scales. ``fmt`` "nvfp4": s [R, K/16] E4M3 bytes and a power of two g [R] fp32 per row;
+    "mxfp4": s [R, K/32] biased exponents, g None.
+
+    With ``up`` [T, K] silu(x) * up is quantised. ``rows`` [R] int32 gathers: row r is that of x at rows[r], and is not
+    written where rows[r] is no row of x (as in the routing's perm past its end). ``out``: (q, s, g) to write to. K is a
+    multiple of 64.
+    """
+    index = _input("x", x, _HALFS)
+    if fmt not in _FP4:
+        raise ValueError(f"fmt is one of {sorted(_FP4)}")
+    code, block = _FP4[fmt]
+    T, K = x.shape
+    if K % 64:
+        raise ValueError("K must be a multiple of 64")
+    R, rows_at = T, 0
+    if rows is not None:
+        if rows.dim() != 1:
+            raise ValueError("rows must be 1-D")
+        R = rows.shape[0]
+        rows_at = _whole("rows", rows, torch.int32, (R,), index)
+    if out is None:
+        q = _empty((R, K // 2), torch.uint8, x.device, stream)
+        s = _empty((R, K // block), torch.uint8, x.device, stream)
+        g = _empty(R, torch.float32, x.device, stream) if block == 16 else None
+    else:
+        q, s, g = out
+        if (g is None) != (block == 32):
+            raise ValueError("out: g belongs to nvfp4")
+    up_at, up_ld = _rows("up", up, x.dtype, (T, K), index)
+    args = _pack_quant(code, _DTYPE[x.dtype], x.data_ptr(), up_at, _row_stride("x", x), up_ld, rows_at, T, R, K,
+                       _whole("q", q, torch.uint8, (R, K // 2), index),
+                       _whole("s", s, torch.uint8, (R, K // block), index), _whole("g", g, torch.float32, (R,), index))
+    _run(_entry(3), index, _handle(index, stream), (args,), "moe_quantize_fp4")
+    return q, s, g
+
+
+def dequantize_fp4(q, s, g=None, *, dtype=None, out=None, stream=None):
+    """What 4-bit floats stand for (moe_dequantize_fp4): q [R, K/2] and s [R, K/16] (NVFP4, with g [R] or [1] fp32) or
+    [R, K/32] (MXFP4) -> [R, K] bf16 (default), f16 or fp32."""
+    index = _input("q", q, (torch.uint8,))
+    code, K = _fp4_fmt("q, s", q, s)
+    R = q.shape[0]
+    if out is None:
+        out = _empty((R, K), dtype or torch.bfloat16, q.device, stream)
+    elif dtype is not None and dtype != out.dtype:
+        raise ValueError("dtype and out differ")
+    if out.dtype not in _FLOATS:
+        raise ValueError(f"out: type {out.dtype} is not supported")
+    if g is not None and code == MOE_FP4_MXFP4:
+        raise ValueError("g belongs to NVFP4")
+    per_row = g is not None and g.numel() != 1
+    out_at, out_ld = _rows("out", out, out.dtype, (R, K), index)
+    args = _pack_dequant(code, _DTYPE[out.dtype], _whole("q", q, torch.uint8, (R, K // 2), index),
+                         _whole("s", s, torch.uint8, (R, s.shape[1]), index),
+                         _whole("g", g, torch.float32, (R if per_row else 1,), index), 1 if per_row else 0, R, K, out_at,
+                         out_ld)
+    _run(_entry(4), index, _handle(index, stream), (args,), "moe_dequantize_fp4")
+    return out
+
+
+def _offsets(offsets, E, index):
+    return _whole("offsets", offsets, torch.int32, (E + 1,), index)
+
+
+def _result(out, out_dtype, default, M, N, device, index, stream):
+    """The result of a product: the tensor, its address and row stride."""
+    if out is None:
+        out = _empty((M, N), out_dtype or default, device, stream)
+    elif out_dtype is not None and out_dtype != out.dtype:
+        raise ValueError("out_dtype and out differ")
+    if out.dtype not in _FLOATS:
+        raise ValueError(f"out: type {out.dtype} is not supported")
+    return out, *_rows("out", out, out.dtype, (M, N), index)
+
+
+def grouped_linear(x, w, offsets, *, bias=None, out=None, out_dtype=None, stream=None):
+    """x[r] W[e]^T + bias[e] for the rows offsets[e] <= r < offsets[e+1] of every expert e (moe_grouped_linear).
+
+    x [M, K] and w [E, N, K] share one type (bf16 or f16), offsets [E+1] int32 on the device as ``route_logits`` gives
+    them, bias [E, N] fp32 or None. The result [M, N] is bf16, f16 or fp32 (default: x's type); rows of no expert are not
+    written. K and x's row stride are multiples of 8, E <= 512.
+    """
+    index = _input("x", x, _HALFS)
+    M, K = x.shape
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, K]")
+    E, N = w.shape[0], w.shape[1]
+    out, out_at, out_ld = _result(out, out_dtype, x.dtype, M, N, x.device, index, stream)
+    args = _pack_grouped(_DTYPE[x.dtype], E, M, N, K, _offsets(offsets, E, index), x.data_ptr(), _row_stride("x", x),
+                         _whole("w", w, x.dtype, (E, N, K), index), _whole("bias", bias, torch.float32, (E, N), index),
+                         out_at, _DTYPE[out.dtype], out_ld)
+    _run(_entry(5), index, _handle(index, stream), (args,), "moe_grouped_linear")
+    return out
+
+
+def _linear_fp4(x, q, s, g, offsets, bias, out, out_dtype, stream):
+    grouped = offsets is not None
+    code, K = _fp4_fmt("q, s", q, s)
+    if q.dim() != (3 if grouped else 2):
+        raise ValueError("q must be [E, N, K/2] with offsets, [N, K/2] without")
+    E, N = (q.shape[0] if grouped else 1), q.shape[-2]
+    lead = q.shape[:-1]
+    mx = code == MOE_FP4_MXFP4
+    codes = not isinstance(x, torch.Tensor)
+    xq, xs, xg = x if codes else (x, None, None)
+    index = _input("x", xq, (torch.uint8,) if codes else _HALFS)
+    M = xq.shape[0]
+    if mx and (g is not None or xg is not None):
+        raise ValueError("g belongs to NVFP4")
+    if not codes and xq.shape[1] != K:
+        raise ValueError(f"x: {K} columns expected, got {xq.shape[1]}")
+    cols = g is not None and g.dim() == (2 if grouped else 1) and g.shape[-1] == N and (grouped or N > 1)
+    g_at = _whole("g", g, torch.float32, lead if cols else (E,), index)
+    q_at = _whole("q", q, torch.uint8, (*lead, K // 2), index)
+    s_at = _whole("s", s, torch.uint8, (*lead, s.shape[-1]), index)
+    b_at = _whole("bias", bias, torch.float32, lead, index)
+    off_at = _offsets(offsets, E, index) if grouped else 0
+    out, out_at, out_ld = _result(out, out_dtype, torch.bfloat16 if codes else x.dtype, M, N, xq.device, index, stream)
+    st = _handle(index, stream)
+    tail = (q_at, s_at, g_at, 1 if cols else 0, b_at, out_at, _DTYPE[out.dtype], out_ld)
+    if codes:
+        args = _pack_fp4(code, E, M, N, K, off_at, _whole("x codes", xq, torch.uint8, (M, K // 2), index),
+                         _whole("x scales", xs, torch.uint8, (M, s.shape[-1]), index),
+                         _whole("x g", xg, torch.float32, (M,), index), *tail)
+        _run(_entry(6), index, st, (args,), "moe_linear_fp4")
+        return out
+    if M == 0 or K % 64:                                       # refused below, or nothing to do
+        _run(_entry(6), index, st, (_pack_fp4(code, E, M, N, K, off_at, 0, 0, 0, *tail),), "moe_linear_fp4")
+        return out
+    x_ld = _row_stride("x", xq)
+    # the tokens' codes and scales in memory of the stream that the kernels run on: every stream and captured graph has
+    # its own
+    n_q, n_s = M * K // 2, (M * s.shape[-1] + 15) // 16 * 16
+    size = n_q + n_s + (0 if mx else 4 * M)
+    if _raw_alloc is not None and index == _device():
+        ws = _raw_alloc(size, st)
+    else:
+        ws = torch.cuda.caching_allocator_alloc(size, index, st)
+    try:
+        ws_g = 0 if mx else ws + n_q + n_s
+        quant = _pack_quant(code, _DTYPE[xq.dtype], xq.data_ptr(), 0, x_ld, 0, 0, M, M, K, ws, ws + n_q, ws_g)
+        _run(_entry(3), index, st, (quant,), "moe_quantize_fp4")
+        args = _pack_fp4(code, E, M, N, K, off_at, ws, ws + n_q, ws_g, *tail)
+        _run(_entry(6), index, st, (args,), "moe_linear_fp4")
+    finally:
+        torch.cuda.caching_allocator_delete(ws)
+    return out
+
+
+def linear_fp4(x, q, s, g=None, *, bias=None, out=None, out_dtype=None, stream=None):
+    """x W^T + bias with both operands in microscaled 4-bit floats, on the tensor cores' 4-bit path (moe_linear_fp4).
+
+    W: q [N, K/2] and s [N, K/16] with g [1] or [N] fp32 (NVFP4, as ``quantize_nvfp4`` or ``quantize_fp4`` write them),
+    or s [N, K/32] (MXFP4). x: (q, s, g) as ``quantize_fp4`` returns them, in W's format, or [M, K] in bf16 or f16, which
+    is then quantised so. bias [N] fp32 or None. The result [M, N] is bf16, f16 or fp32 (default: x's type, bf16 for
+    codes). K is a multiple of 64.
+    """
+    return _linear_fp4(x, q, s, g, None, bias, out, out_dtype, stream)
+
+
+def grouped_linear_fp4(x, q, s, g, offsets, *, bias=None, out=None, out_dtype=None, stream=None):
+    """``grouped_linear`` with both operands in microscaled 4-bit floats (moe_linear_fp4): q [E, N, K/2] and s
+    [E, N, K/16] with g [E] or [E, N] fp32 (NVFP4), or s [E, N, K/32] and g None (MXFP4); x as in ``linear_fp4``, bias
+    [E, N] fp32 or None."""
+    if offsets is None:
+        raise ValueError("offsets are needed")
+    return _linear_fp4(x, q, s, g, offsets, bias, out, out_dtype, stream)
+
+
+def products_status(stream=None) -> int:
+    """MOE_ERR_TIMEOUT if a wait of ``linear_fp4``, ``grouped_linear`` or ``grouped_linear_fp4`` ran out on the current
+    device since the last call (the rows concerned are then NaN), else MOE_OK (moe_products_status). Waits for the
+    stream."""
+    return load().moe_products_status(_stream(stream))
+
+
+def hold_products(hold: bool):
+    """Test hook: make the waits of those products run out, or restore them."""
+    _check(load().moe_debug_hold_products(1 if hold else 0), "moe_debug_hold_products")

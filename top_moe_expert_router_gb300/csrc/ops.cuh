@@ -1,7 +1,9 @@
 // ops.cuh — arguments and launchers of the operators around the expert layer:
 // routing from logits (route_logits.cu), residual + RMSNorm with an 8-bit
-// output (norm_quant.cu) and products with 4-bit weights (linear_w4.cu). Their
-// C entries are in ops_api.cu.
+// output (norm_quant.cu), products with 4-bit weights (linear_w4.cu), 4-bit
+// floats (quant_fp4.cu) and products of two such matrices (linear_fp4.cu), and
+// products grouped by expert (grouped_linear.cu, linear_fp4.cu). Their C entries
+// are in ops_api.cu.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -95,6 +97,59 @@ constexpr int kW4MaxN = 1 << 30;
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st);
 cudaError_t linear_w4_errors(cudaStream_t st, uint32_t *bits);
 void hold_linear_w4(bool hold);
+
+// Microscaled 4-bit floats (quant_fp4.cu): two e2m1 codes to a byte, the low
+// nibble first; NVFP4: an E4M3 scale per 16 and a second, fp32 scale; MXFP4: a
+// power of two per 32, as its biased exponent.
+struct QuantFp4Args {
+    const void *x, *up;      // [T, K] of `type`; up may be null
+    int64_t x_ld, up_ld;
+    const int32_t *rows;     // [R] or null (R == T)
+    int T, R, K;
+    uint8_t *q, *s;          // [R, K/2], [R, K/16 or K/32]
+    float *g;                // [R] (NVFP4)
+    moe_dtype type;
+    bool nvfp4;
+    bool vec;                // rows of x (and up) may be read as 32-byte vectors (set by the launcher)
+};
+struct DequantFp4Args {
+    const uint8_t *q, *s;
+    const float *g;          // NVFP4: [R] or [1]; null: 1
+    bool g_rows;
+    int R, K;
+    void *out;               // [R, K]
+    int64_t out_ld;
+    moe_dtype type;
+    bool nvfp4;
+    bool vec;                // rows of out may be written as 32-byte vectors (set by the launcher)
+};
+constexpr int kFp4MaxK = 32768;
+cudaError_t launch_quantize_fp4(QuantFp4Args a, cudaStream_t st);
+cudaError_t launch_dequantize_fp4(DequantFp4Args a, cudaStream_t st);
+
+// Products of rows grouped by expert (products.cuh).
+constexpr int kProdMaxGroups = 512;
+constexpr int kProdMaxRows = 1 << 24;
+struct ProdArgs {
+    int groups;
+    const int32_t *offsets;  // [groups + 1], or null: one group of all M rows
+    int M, N, K;
+    bool bf16;               // 16-bit operands: bf16, else f16
+    const uint8_t *xs, *ws;  // 4-bit operands: block scales of x [M] and of the weights [groups, N]
+    const float *xg;         // [M] or null
+    const float *wg;         // [groups], or [groups, N] with wg_cols, or null
+    bool wg_cols;
+    const float *bias;       // [groups, N] or null
+    void *y;                 // [M, N]
+    int64_t y_ld;
+    moe_dtype y_type;
+    int s_copy;              // bytes that the scales' alignment lets one copy take (set by the launcher)
+    int hold;                // test hook (set by the launcher)
+};
+cudaError_t launch_grouped_linear(const ProdArgs &a, const void *x, int64_t x_ld, const void *w, cudaStream_t st);
+cudaError_t launch_linear_fp4(ProdArgs a, bool nvfp4, const uint8_t *xq, const uint8_t *wq, cudaStream_t st);
+cudaError_t products_errors(cudaStream_t st, uint32_t *bits);
+void hold_products(bool hold);
 
 #ifdef __CUDACC__
 

@@ -47,6 +47,23 @@ bool misaligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1u)) !=
 int type_size(moe_dtype t) { return t == MOE_T_F32 ? 4 : t == MOE_T_E4M3 ? 1 : 2; }
 bool is_float_type(moe_dtype t) { return t == MOE_T_BF16 || t == MOE_T_F16 || t == MOE_T_F32; }
 moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+bool is_half_type(moe_dtype t) { return t == MOE_T_BF16 || t == MOE_T_F16; }
+
+// What the products of both operand types have in common; MOE_OK with M == 0 asks for nothing.
+moe_status check_product(int groups, int M, int N, int K, const int32_t *offsets, const float *bias, const void *y,
+                         moe_dtype y_type, int64_t y_stride) {
+    if (groups < 1 || M < 0 || N < 1 || K < 1 || (!offsets && groups != 1)) return MOE_ERR_INVALID_ARG;
+    if (!is_float_type(y_type) || groups > kProdMaxGroups || M > kProdMaxRows || N > kProdMaxRows ||
+        (int64_t)groups * N > INT32_MAX)
+        return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    // tiles are counted in 32 bits
+    if (((int64_t)M / 32 + groups) * ((N + 127) / 128) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (!y || misaligned(offsets, 4) || misaligned(bias, 4) || misaligned(y, (unsigned)type_size(y_type)) ||
+        y_stride < N)
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
 
 }  // namespace
 
@@ -198,6 +215,121 @@ moe_status moe_linear_w4(const moe_w4_args *l, void *stream) {
     a.x_type = l->x_type;
     a.y_type = l->y_type;
     return status_of(launch_linear_w4(a, (cudaStream_t)stream));
+}
+
+moe_status moe_quantize_fp4(const moe_quantize_fp4_args *n, void *stream) {
+    if (!n || n->T < 0 || n->R < 0 || n->K < 1 || (!n->rows && n->R != n->T)) return MOE_ERR_INVALID_ARG;
+    if ((n->fmt != MOE_FP4_NVFP4 && n->fmt != MOE_FP4_MXFP4) || !is_half_type(n->type) || n->K % 64 ||
+        n->K > kFp4MaxK)
+        return MOE_ERR_UNSUPPORTED;
+    const bool nvfp4 = n->fmt == MOE_FP4_NVFP4;
+    if (n->R == 0) return MOE_OK;
+    if (!n->q || !n->s || (nvfp4 && !n->g) || (!n->x && n->T)) return MOE_ERR_INVALID_ARG;
+    if (misaligned(n->x, 2) || misaligned(n->up, 2) || misaligned(n->rows, 4) || misaligned(n->q, 16) ||
+        misaligned(n->s, 4) || misaligned(n->g, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (n->x_stride < n->K || (n->up && n->up_stride < n->K)) return MOE_ERR_INVALID_ARG;
+    QuantFp4Args a{};
+    a.x = n->x;
+    a.up = n->up;
+    a.x_ld = n->x_stride;
+    a.up_ld = n->up_stride;
+    a.rows = n->rows;
+    a.T = n->T;
+    a.R = n->R;
+    a.K = n->K;
+    a.q = n->q;
+    a.s = n->s;
+    a.g = n->g;
+    a.type = n->type;
+    a.nvfp4 = nvfp4;
+    return status_of(launch_quantize_fp4(a, (cudaStream_t)stream));
+}
+
+moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *n, void *stream) {
+    if (!n || n->R < 0 || n->K < 1) return MOE_ERR_INVALID_ARG;
+    if ((n->fmt != MOE_FP4_NVFP4 && n->fmt != MOE_FP4_MXFP4) || !is_float_type(n->type) || n->K % 64 ||
+        n->K > kFp4MaxK)
+        return MOE_ERR_UNSUPPORTED;
+    if (n->R == 0) return MOE_OK;
+    if (!n->q || !n->s || !n->out || misaligned(n->q, 16) || misaligned(n->s, 4) || misaligned(n->g, 4) ||
+        misaligned(n->out, (unsigned)type_size(n->type)) || n->out_stride < n->K)
+        return MOE_ERR_INVALID_ARG;
+    DequantFp4Args a{};
+    a.q = n->q;
+    a.s = n->s;
+    a.g = n->g;
+    a.g_rows = n->g_rows != 0;
+    a.R = n->R;
+    a.K = n->K;
+    a.out = n->out;
+    a.out_ld = n->out_stride;
+    a.type = n->type;
+    a.nvfp4 = n->fmt == MOE_FP4_NVFP4;
+    return status_of(launch_dequantize_fp4(a, (cudaStream_t)stream));
+}
+
+moe_status moe_grouped_linear(const moe_grouped_linear_args *l, void *stream) {
+    if (!l) return MOE_ERR_INVALID_ARG;
+    const moe_status s = check_product(l->groups, l->M, l->N, l->K, l->offsets, l->bias, l->y, l->y_type, l->y_stride);
+    if (s != MOE_OK) return s;
+    if (!is_half_type(l->type) || l->K % 8) return MOE_ERR_UNSUPPORTED;
+    if (l->M == 0) return MOE_OK;
+    if (!l->x || !l->w || misaligned(l->x, 16) || misaligned(l->w, 16) || l->x_stride < l->K || l->x_stride % 8)
+        return MOE_ERR_INVALID_ARG;
+    ProdArgs a{};
+    a.groups = l->groups;
+    a.offsets = l->offsets;
+    a.M = l->M;
+    a.N = l->N;
+    a.K = l->K;
+    a.bf16 = l->type == MOE_T_BF16;
+    a.bias = l->bias;
+    a.y = l->y;
+    a.y_ld = l->y_stride;
+    a.y_type = l->y_type;
+    return status_of(launch_grouped_linear(a, l->x, l->x_stride, l->w, (cudaStream_t)stream));
+}
+
+moe_status moe_linear_fp4(const moe_linear_fp4_args *l, void *stream) {
+    if (!l) return MOE_ERR_INVALID_ARG;
+    const moe_status s = check_product(l->groups, l->M, l->N, l->K, l->offsets, l->bias, l->y, l->y_type, l->y_stride);
+    if (s != MOE_OK) return s;
+    if ((l->fmt != MOE_FP4_NVFP4 && l->fmt != MOE_FP4_MXFP4) || l->K % 64 || l->K > kFp4MaxK)
+        return MOE_ERR_UNSUPPORTED;
+    if (l->M == 0) return MOE_OK;
+    const bool nvfp4 = l->fmt == MOE_FP4_NVFP4;
+    if (!l->xq || !l->xs || !l->wq || !l->ws || (!nvfp4 && (l->xg || l->wg))) return MOE_ERR_INVALID_ARG;
+    if (misaligned(l->xq, 16) || misaligned(l->wq, 16) || misaligned(l->xs, 4) || misaligned(l->ws, 4) ||
+        misaligned(l->xg, 4) || misaligned(l->wg, 4))
+        return MOE_ERR_INVALID_ARG;
+    ProdArgs a{};
+    a.groups = l->groups;
+    a.offsets = l->offsets;
+    a.M = l->M;
+    a.N = l->N;
+    a.K = l->K;
+    a.xs = l->xs;
+    a.ws = l->ws;
+    a.xg = l->xg;
+    a.wg = l->wg;
+    a.wg_cols = l->wg_cols != 0;
+    a.bias = l->bias;
+    a.y = l->y;
+    a.y_ld = l->y_stride;
+    a.y_type = l->y_type;
+    return status_of(launch_linear_fp4(a, nvfp4, l->xq, l->wq, (cudaStream_t)stream));
+}
+
+moe_status moe_products_status(void *stream) {
+    uint32_t bits = 0;
+    if (products_errors((cudaStream_t)stream, &bits) != cudaSuccess) return MOE_ERR_CUDA;
+    return bits & ERRBIT_TIMEOUT ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
+moe_status moe_debug_hold_products(int hold) {
+    hold_products(hold != 0);
+    return MOE_OK;
 }
 
 moe_status moe_linear_w4_status(void *stream) {

@@ -1,0 +1,516 @@
+// products.cuh — y[r] = W[e(r)] x[r] + b[e(r)]: products of rows that are grouped
+// by expert (or belong to one matrix) on the 5th-generation tensor cores, with
+// operands in 16 bits (grouped_linear.cu) or in microscaled 4-bit floats
+// (linear_fp4.cu).
+//
+// The weights are the M = 128 operand of tcgen05.mma and the rows of a group the
+// N operand, in steps of 16 up to TN: a group of 5 rows costs 16, not 128, which
+// is what ragged groups and decode batches need, and a tile of weights is read
+// once for up to TN rows. Both operands are K-major tiles of 128-byte rows (64
+// columns of 16 bits, 256 of 4) brought by TMA through a ring; accumulators in
+// tensor memory, two of them, so that one tile is stored while the next is
+// summed. Tiles are dealt to persistent CTAs in an order that the offsets on the
+// device determine: group by group, in bands of 12 weight tiles, so that the
+// CTAs running at a time share weight and row tiles in L2.
+//
+// Warps: 0 TMA, 1 MMA (owns the tensor memory), 2..5 epilogue, and for 4-bit
+// operands 6..9, which bring the block scales into tensor memory: the layout
+// there is lane r % 32, column r / 32 for row r, four scale bytes of one MMA
+// (K = 64) to a column, the same in all four lane quarters.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "gemm.cuh"
+#include "ops.cuh"
+
+namespace moe {
+
+enum { PROD_16 = 0, PROD_NVFP4 = 1, PROD_MXFP4 = 2 };
+
+constexpr int kProdRows = 128;           // weight rows of a tile
+constexpr int kProdBand = 12;            // weight tiles of a band
+constexpr uint32_t kProdABytes = kProdRows * 128;
+
+bool products_held();                    // test hook: copy no operands
+
+#ifdef __CUDACC__
+
+// Error bits of this device's products (of one translation unit).
+static __device__ uint32_t prod_err;
+
+// Reads and clears the bits of the current device, after `st`'s work.
+static inline cudaError_t prod_take_errors(cudaStream_t st, uint32_t *bits) {
+    void *at = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&at, prod_err);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, sizeof(*bits), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof(*bits), st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
+template <int KIND, int TN>
+struct ProdShape {
+    static constexpr bool kFp4 = KIND != PROD_16;
+    static constexpr int kBox = TN < 64 ? TN : 64;           // rows of one TMA copy of x
+    static constexpr uint32_t kStage = kProdABytes + TN * 128;
+    static constexpr int kScaleBytes = KIND == PROD_NVFP4 ? 16 : 8;  // a row's scales of one stage
+    static constexpr int kScaleRows = kProdRows + TN;
+    static constexpr int kAhead = kFp4 ? 5 : 0;              // stages of scales in flight
+    static constexpr uint32_t kScales = kFp4 ? (kAhead + 1) * kScaleRows * kScaleBytes : 0;
+    static constexpr uint32_t kMeta = kProdMaxGroups * 12 + 16 + 512;  // group tables, barriers
+    static constexpr int kStages = (int)((227 * 1024 - 1024 - kMeta - kScales) / kStage) < 10
+                                       ? (int)((227 * 1024 - 1024 - kMeta - kScales) / kStage) : 10;
+    static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kMeta;
+    static constexpr int kThreads = kFp4 ? 320 : 192;
+    // tensor memory: two accumulators, then two buffers of scales (16 columns for
+    // the weights, kBCols for each of the four MMAs of a stage for x)
+    static constexpr int kBCols = TN > 128 ? 8 : 4;
+    static constexpr uint32_t kScaleCols = 16 + 4 * kBCols;
+    static constexpr uint32_t kScaleAt = 2 * TN;
+    static_assert(!kFp4 || kScaleAt + 2 * kScaleCols <= kTmemCols, "tensor memory");
+    static_assert(2 * TN <= (int)kTmemCols, "tensor memory");
+};
+
+__device__ __forceinline__ void mma_f16_kind(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    mma_bf16(d, a, b, idesc, acc);               // bf16 or f16 by the descriptor
+}
+
+template <int KIND>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        uint32_t acc) {
+    if constexpr (KIND == PROD_NVFP4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Asynchronous copy of n bytes to shared memory; zeros where `in` is false.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(in ? N : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The groups as the tiles need them, in shared memory.
+struct ProdGroups {
+    int32_t *start;          // [groups + 1] first tile of each group
+    int32_t *row0, *rows;    // [groups]
+};
+
+struct ProdTile {
+    int g, w, row0, rows;    // group, weight tile, first row and rows (up to TN)
+};
+
+// Walks a CTA's tiles in order.
+template <int TN>
+struct ProdWalk {
+    int tile, g;
+    __device__ __forceinline__ explicit ProdWalk(int first) : tile(first), g(0) {}
+    __device__ __forceinline__ ProdTile at(const ProdGroups &gr, int nw) {
+        while (gr.start[g + 1] <= tile) ++g;
+        const int local = tile - gr.start[g], rows = gr.rows[g], nt = (rows + TN - 1) / TN;
+        const int band = local / (kProdBand * nt), r = local - band * (kProdBand * nt);
+        const int bw = min(kProdBand, nw - band * kProdBand), t = r / bw;
+        ProdTile p;
+        p.g = g;
+        p.w = band * kProdBand + r - t * bw;
+        p.row0 = gr.row0[g] + t * TN;
+        p.rows = min(TN, rows - t * TN);
+        return p;
+    }
+};
+
+// Fills the tables; every thread of the CTA. -> the number of tiles
+template <int TN>
+__device__ __forceinline__ int prod_groups(const ProdArgs &a, const ProdGroups &gr, int nw) {
+    for (int g = threadIdx.x; g < a.groups; g += blockDim.x) {
+        // whatever the offsets hold, no row outside [0, M) is touched
+        int lo = 0, hi = a.M;
+        if (a.offsets) {
+            lo = min(max(a.offsets[g], 0), a.M);
+            hi = min(max(a.offsets[g + 1], lo), a.M);
+        }
+        gr.row0[g] = lo;
+        gr.rows[g] = hi - lo;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int per = (a.groups + 31) / 32, g0 = min(a.groups, (int)threadIdx.x * per), g1 = min(a.groups, g0 + per);
+        int sum = 0;
+        for (int g = g0; g < g1; ++g) sum += (gr.rows[g] + TN - 1) / TN * nw;
+        int end = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, end, o);
+            if ((int)threadIdx.x >= o) end += v;
+        }
+        int at = end - sum;
+        for (int g = g0; g < g1; ++g) {
+            gr.start[g] = at;
+            at += (gr.rows[g] + TN - 1) / TN * nw;
+        }
+        if (threadIdx.x == 31) gr.start[a.groups] = end;
+    }
+    __syncthreads();
+    return gr.start[a.groups];
+}
+
+__device__ __forceinline__ void store_as(void *y, int64_t at, moe_dtype t, float v) {
+    if (t == MOE_T_BF16)
+        ((__nv_bfloat16 *)y)[at] = __float2bfloat16_rn(v);
+    else if (t == MOE_T_F16)
+        ((__half *)y)[at] = __float2half_rn(v);
+    else
+        ((float *)y)[at] = v;
+}
+
+// One tile's rows: this thread owns column n of y and walks the rows.
+template <bool FP4>
+__device__ __forceinline__ void prod_store(const ProdArgs &a, const ProdTile &t, uint32_t tbase, int n, bool failed) {
+    const int lane = threadIdx.x & 31;
+    const bool mine = n < a.N;
+    const float b = a.bias && mine ? a.bias[(int64_t)t.g * a.N + n] : 0.f;
+    float cs = 1.f;
+    if (FP4 && a.wg && mine) cs = a.wg[a.wg_cols ? (int64_t)t.g * a.N + n : t.g];
+    int64_t at = (int64_t)t.row0 * a.y_ld + n;
+#pragma unroll 1
+    for (int c0 = 0; c0 < t.rows; c0 += 16) {
+        uint32_t v[16];
+        if (!failed) {
+            tmem_ld16(tbase + c0, v);
+            tmem_ld_wait();
+        }
+        float rs = 1.f;
+        if (FP4 && a.xg) rs = a.xg[t.row0 + min(c0 + (lane & 15), t.rows - 1)];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float o = failed ? __int_as_float(0x7FFFFFFF) : __uint_as_float(v[i]);
+            if (FP4) o *= cs * __shfl_sync(0xFFFFFFFFu, rs, i);
+            if (mine && c0 + i < t.rows) store_as(a.y, at, a.y_type, o + b);
+            at += a.y_ld;
+        }
+    }
+}
+
+template <int KIND, int TN>
+__global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const ProdArgs a) {
+    using S = ProdShape<KIND, TN>;
+    constexpr int NS = S::kStages;
+    constexpr int kStageK = KIND == PROD_16 ? 64 : 256, kMmaK = kStageK / 4;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t base_u32 = smem_u32(smem_raw);
+    unsigned char *smem = smem_raw + (((base_u32 + 1023u) & ~1023u) - base_u32);
+    unsigned char *scales = smem + NS * S::kStage;
+    unsigned char *meta = scales + S::kScales;
+    uint64_t *full = reinterpret_cast<uint64_t *>(meta), *empty = full + NS;
+    uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 2, *done = sempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    ProdGroups gr;
+    gr.start = reinterpret_cast<int32_t *>(meta + 512);
+    gr.row0 = gr.start + kProdMaxGroups + 1;
+    gr.rows = gr.row0 + kProdMaxGroups;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t *err = &prod_err;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 128);
+            mbar_init(&sfull[b], 128);
+            mbar_init(&sempty[b], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+    pdl_wait();                                  // what earlier kernels write is read from here on
+    const int nw = (a.N + kProdRows - 1) / kProdRows;
+    tc_fence_before();
+    const int ntiles = prod_groups<TN>(a, gr, nw);
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int nst = (a.K + kStageK - 1) / kStageK;
+
+    if (warp == 0) {
+        // ------------------------------- TMA producer -------------------------------
+        if (lane == 0 && !a.hold) {
+            int it = 0;
+            bool ok = true;
+            ProdWalk<TN> walk(blockIdx.x);
+            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x) {
+                const ProdTile t = walk.at(gr, nw);
+                const int wrow = t.g * a.N + t.w * kProdRows;
+                const int loads = (t.rows + S::kBox - 1) / S::kBox;
+                for (int kb = 0; kb < nst; ++kb, ++it) {
+                    const int slot = it % NS;
+                    if (!mbar_wait_or_abort(&empty[slot], ((it / NS) & 1) ^ 1, err, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char *st = smem + (size_t)slot * S::kStage;
+                    mbar_arrive_expect_tx(&full[slot], kProdABytes + loads * S::kBox * 128);
+                    const int k = kb * (KIND == PROD_16 ? 64 : 128);  // elements of the maps
+                    tma_load_2d(st, &tmW, k, wrow, &full[slot]);
+                    for (int j = 0; j < loads; ++j)
+                        tma_load_2d(st + kProdABytes + j * (S::kBox * 128), &tmX, k, t.row0 + j * S::kBox, &full[slot]);
+                }
+            }
+            // every load issued must land before the CTA exits
+            for (int j = (it > NS ? it - NS : 0); j < it; ++j) mbar_wait(&full[j % NS], (j / NS) & 1, err);
+        }
+    } else if (warp == 1) {
+        // -------------------------------- MMA issuer --------------------------------
+        if (lane == 0) {
+            int it = 0, lt = 0;
+            bool ok = true;
+            ProdWalk<TN> walk(blockIdx.x);
+            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x, ++lt) {
+                const ProdTile t = walk.at(gr, nw);
+                const uint32_t n16 = (uint32_t)(t.rows + 15) / 16;
+                uint32_t idesc;
+                if constexpr (S::kFp4)
+                    idesc = (1u << 7) | (1u << 10) | (n16 << 18) | (KIND == PROD_MXFP4 ? 1u << 23 : 0u) |
+                            ((uint32_t)(kProdRows >> 7) << 27);
+                else
+                    idesc = (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u) | (n16 << 18) |
+                            ((uint32_t)(kProdRows >> 4) << 24);
+                const int b = lt & 1;
+                if (!mbar_wait_or_abort(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)(b * TN);
+                for (int kb = 0; kb < nst; ++kb, ++it) {
+                    const int slot = it % NS;
+                    if (!mbar_wait_or_abort(&full[slot], (it / NS) & 1, err, abort_flag) ||
+                        (S::kFp4 && !mbar_wait_or_abort(&sfull[it & 1], (it >> 1) & 1, err, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + (size_t)slot * S::kStage);
+                    const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + kProdABytes);
+                    const int nk = min(4, (a.K - kb * kStageK + kMmaK - 1) / kMmaK);
+                    const uint32_t sc = tmem_base + S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
+                    for (int kk = 0; kk < nk; ++kk) {
+                        const uint64_t o = (uint64_t)(2 * kk);
+                        if constexpr (S::kFp4)
+                            mma_fp4<KIND>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, (kb | kk) != 0);
+                        else
+                            mma_f16_kind(d, ad + o, bd + o, idesc, (kb | kk) != 0);
+                    }
+                    mma_commit(&empty[slot]);    // free once these MMAs have read it
+                    if (S::kFp4) mma_commit(&sempty[it & 1]);
+                }
+                if (!ok) break;
+                mma_commit(&tfull[b]);
+            }
+            mma_commit(done);
+            mbar_wait(done, 0, err);
+        }
+    } else if (warp < 6) {
+        // --------------------------------- epilogue ---------------------------------
+        const int q = warp & 3;                  // TMEM lane quarter of this warp
+        int lt = 0;
+        ProdWalk<TN> walk(blockIdx.x);
+        for (; walk.tile < ntiles; walk.tile += gridDim.x, ++lt) {
+            const ProdTile t = walk.at(gr, nw);
+            const int b = lt & 1;
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&tfull[b], (lt >> 1) & 1, err, abort_flag));
+            tc_fence_after();
+            prod_store<S::kFp4>(a, t, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN),
+                                t.w * kProdRows + q * 32 + lane, !ok);
+            tc_fence_before();
+            mbar_arrive(&tempty[b]);
+        }
+    } else if constexpr (S::kFp4) {
+        // ---------------------------------- scales ----------------------------------
+        constexpr int SB = S::kScaleBytes, D = S::kAhead, NB = (TN + 127) / 128;
+        const int t = threadIdx.x - 192, q = warp & 3;
+        const int pitch = a.K / (KIND == PROD_NVFP4 ? 16 : 32);   // bytes of a row's scales
+        const uint32_t ring = smem_u32(scales);
+        const int64_t wrows = (int64_t)a.groups * a.N;
+        ProdWalk<TN> ahead(blockIdx.x), walk(blockIdx.x);
+        const uint8_t *src[1 + NB];
+        bool in[1 + NB];
+        int akb = 0, issued = 0;
+        auto place = [&]() {                     // the rows of this thread in the tile ahead
+            if (ahead.tile >= ntiles) return;
+            const ProdTile p = ahead.at(gr, nw);
+            const int64_t wr = (int64_t)p.g * a.N + p.w * kProdRows + t;
+            in[0] = wr < wrows;
+            src[0] = a.ws + (in[0] ? wr : 0) * pitch;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int r = t + 128 * j;
+                in[1 + j] = r < p.rows;
+                src[1 + j] = a.xs + (int64_t)(in[1 + j] ? p.row0 + r : 0) * pitch;
+            }
+        };
+        auto issue = [&]() {                     // one stage; an empty group of copies past the end
+            if (ahead.tile < ntiles) {
+                const uint32_t slot = ring + (uint32_t)(issued % (D + 1)) * (S::kScaleRows * SB);
+                const int k0 = akb * SB;
+#pragma unroll
+                for (int j = 0; j <= NB; ++j) {
+                    const int r = j ? kProdRows + t + 128 * (j - 1) : t;
+                    if (r >= S::kScaleRows) break;
+                    const uint32_t dst = slot + r * SB;
+                    if (SB == 16 && a.s_copy == 16) {
+                        cp_async<16>(dst, src[j] + k0, in[j] && k0 < pitch);
+                    } else if (a.s_copy >= 8) {
+#pragma unroll
+                        for (int o = 0; o < SB; o += 8)
+                            cp_async<8>(dst + o, src[j] + min(k0 + o, pitch - 8), in[j] && k0 + o < pitch);
+                    } else if (a.s_copy >= 4) {
+#pragma unroll
+                        for (int o = 0; o < SB; o += 4)
+                            cp_async<4>(dst + o, src[j] + min(k0 + o, pitch - 4), in[j] && k0 + o < pitch);
+                    } else {
+#pragma unroll
+                        for (int o = 0; o < SB; ++o) {
+                            const uint32_t v = in[j] && k0 + o < pitch ? src[j][k0 + o] : 0u;
+                            asm volatile("st.shared.b8 [%0], %1;" ::"r"(dst + o), "r"(v) : "memory");
+                        }
+                    }
+                }
+                ++issued;
+                if (++akb == nst) {
+                    akb = 0;
+                    ahead.tile += gridDim.x;
+                    place();
+                }
+            }
+            cp_async_commit();
+        };
+        place();
+        for (int i = 0; i < D; ++i) issue();
+        int it = 0;
+        bool ok = true;
+        for (; walk.tile < ntiles; walk.tile += gridDim.x) {
+            for (int kb = 0; kb < nst; ++kb, ++it) {
+                cp_async_wait<D - 1>();
+                named_bar(1, 128);               // the stage's scales are there for all four warps
+                const unsigned char *slot = scales + (size_t)(it % (D + 1)) * (S::kScaleRows * SB);
+                uint32_t va[16], vb[4 * S::kBCols];
+                auto words = [&](int row, uint32_t w[4]) {
+                    if constexpr (KIND == PROD_NVFP4) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(slot + row * SB);
+                        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                    } else {                     // two scales a column
+                        const uint2 v = *reinterpret_cast<const uint2 *>(slot + row * SB);
+                        w[0] = v.x & 0xFFFFu, w[1] = v.x >> 16, w[2] = v.y & 0xFFFFu, w[3] = v.y >> 16;
+                    }
+                };
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t w[4];
+                    words(32 * m + lane, w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) va[4 * j + m] = w[j];
+                }
+#pragma unroll
+                for (int m = 0; m < S::kBCols; ++m) {
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
+                    if (32 * m < TN) words(kProdRows + 32 * m + lane, w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
+                }
+                // (a warp whose wait failed goes on to meet the others at the barrier, without work)
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&sempty[it & 1], ((it >> 1) & 1) ^ 1, err, abort_flag));
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t to = tmem_base + ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
+                    tmem_st16(to, va);
+                    tmem_st16(to + 16, vb);
+                    if constexpr (S::kBCols == 8) tmem_st16(to + 32, vb + 16);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&sfull[it & 1]);
+                }
+                issue();                         // over the slot that all read before the barrier above
+            }
+        }
+        cp_async_wait<0>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+#endif  // __CUDACC__
+
+// Host: 2-D map of rows of `row_bytes`, `pitch` bytes apart, in boxes of 128 bytes x box_rows with the 128-byte swizzle.
+bool make_tmap_rows(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t row_bytes, uint64_t pitch,
+                    uint32_t box_rows, bool two_byte);
+int device_sms();
+
+#ifdef __CUDACC__
+// x: rows x_pitch bytes apart; w: [groups * N] rows without gaps.
+template <int KIND, int TN>
+cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, const void *w, cudaStream_t st) {
+    using S = ProdShape<KIND, TN>;
+    static std::atomic<uint64_t> attr_set{0};
+    const auto kern = product_kernel<KIND, TN>;
+    cudaError_t e = set_smem_limit_once((const void *)kern, (int)S::kSmem, attr_set);
+    if (e != cudaSuccess) return e;
+    ProdArgs a = a0;
+    a.hold = products_held();
+    const uint64_t row = KIND == PROD_16 ? (uint64_t)a.K * 2 : (uint64_t)a.K / 2;
+    CUtensorMap tw, tx;
+    if (!make_tmap_rows(&tw, w, (uint64_t)a.groups * a.N, row, row, kProdRows, KIND == PROD_16) ||
+        !make_tmap_rows(&tx, x, a.M, row, a.M > 1 ? x_pitch : row, S::kBox, KIND == PROD_16))
+        return cudaErrorInvalidValue;
+    const int64_t nw = (a.N + kProdRows - 1) / kProdRows;
+    // a tile of every group may be ragged
+    const int64_t most = ((int64_t)a.M / TN + (a.groups < a.M ? a.groups : a.M)) * nw;
+    const int sms = device_sms();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
+}
+#endif
+
+}  // namespace moe

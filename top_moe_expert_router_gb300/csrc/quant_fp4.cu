@@ -1,0 +1,323 @@
+// quant_fp4.cu — rows of 16-bit values to microscaled 4-bit floats and back.
+//
+//   v = x, or silu(x) * up                                    (fp32)
+//   NVFP4: g = the smallest power of two >= max|v_row| / 2688 (6 * 448),
+//          s = E4M3(max|v_block| / 6 / g), blocks of 16, code = E2M1(v / (s g))
+//   MXFP4: s = 2^(floor(log2 max|v_block|) - 2), blocks of 32, code = E2M1(v / s)
+// Bound by memory: 2 bytes in and 0.56 (0.53) out an element.
+//
+// A thread holds 16 elements (half a block of MXFP4), a warp or a CTA of 256 a
+// row, so that a row is read once, from memory to registers, and its maximum is
+// known before its codes are formed.
+//
+// Rounding. Codes and scales are those of exact quotients. g and MXFP4's scales
+// are powers of two; max / 6 by a product with fp32's 1/6 is exact wherever the
+// quotient is the middle between two E4M3 values (checked for all of them), and
+// elsewhere further from it than the product's error: values of 16 bits have 11
+// significant bits, E4M3's middles 5. v / s, s an E4M3 value, is v h + v l
+// with h + l = 1/s to 48 bits: rounded once it meets the middles between codes
+// exactly (v h alone misses them for s of 13/8, 14/8, 15/8).
+#include <cuda_fp4.h>
+
+#include "ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kQThreads = 256;
+
+__device__ __forceinline__ void load32(const void *p, bool vec, uint32_t v[8]) {
+    if (vec) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(p));
+    } else {
+        const uint16_t *h = (const uint16_t *)p;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 widen(uint32_t u) {
+    if (BF16) return make_float2(bf16lo(u), bf16hi(u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// Two values to two codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+}
+
+// The largest magnitude of a thread's 16 elements as the bits of a float (an
+// infinity or NaN stays above every finite one).
+template <bool BF16, bool UP>
+__device__ __forceinline__ uint32_t top_bits(const uint32_t x[8], const float v[16]) {
+    if constexpr (UP) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        return m;
+    } else {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x[i] & 0x7FFF7FFFu);
+        m = max(m & 0xFFFFu, m >> 16);
+        if (BF16) return m << 16;
+        return m >= 0x7C00u ? 0x7F800000u : __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    }
+}
+
+// PER: units of 16 elements of a thread. ROW: threads of a row, 32 or 256.
+template <bool BF16, bool NVFP4, bool UP, int ROW, int PER>
+__global__ void __launch_bounds__(kQThreads) quantize_fp4_kernel(const QuantFp4Args a) {
+    __shared__ uint32_t part[kQThreads / 32];
+    pdl_wait();
+    const int tid = threadIdx.x % ROW, units = a.K / 16;
+    const int r = blockIdx.x * (kQThreads / ROW) + threadIdx.x / ROW;
+    if (r >= a.R) return;
+    int t = r;
+    if (a.rows) {
+        t = a.rows[r];
+        if ((unsigned)t >= (unsigned)a.T) return;           // the row stays as it is
+    }
+    const uint16_t *x = (const uint16_t *)a.x + (int64_t)t * a.x_ld;
+    const uint16_t *up = UP ? (const uint16_t *)a.up + (int64_t)t * a.up_ld : nullptr;
+    uint32_t xv[PER][8], uv[UP ? PER : 1][8], top[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        const int u = tid + p * ROW;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xv[p][i] = 0u;
+        if (u < units) load32(x + u * 16, a.vec, xv[p]);
+        if constexpr (UP) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) uv[p][i] = 0u;
+            if (u < units) load32(up + u * 16, a.vec, uv[p]);
+        }
+    }
+    float v[UP ? PER : 1][16];
+    uint32_t big = 0u;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        if constexpr (UP) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = widen<BF16>(xv[p][i]), w = widen<BF16>(uv[p][i]);
+                v[p][2 * i] = __fdividef(f.x, 1.f + __expf(-f.x)) * w.x;
+                v[p][2 * i + 1] = __fdividef(f.y, 1.f + __expf(-f.y)) * w.y;
+            }
+        }
+        top[p] = top_bits<BF16, UP>(xv[p], v[UP ? p : 0]);
+        big = max(big, top[p]);
+    }
+    float g = 1.f, inv_g = 1.f;
+    if constexpr (NVFP4) {
+        big = __reduce_max_sync(0xFFFFFFFFu, big);
+        if constexpr (ROW > 32) {
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = big;
+            __syncthreads();
+            big = part[0];
+#pragma unroll
+            for (int i = 1; i < ROW / 32; ++i) big = max(big, part[i]);
+        }
+        const bool finite = big < 0x7F800000u;
+        if (big && finite) {
+            const uint32_t q = __float_as_uint(__fdiv_rn(__uint_as_float(big), 2688.f));
+            const uint32_t e = max((q >> 23) + ((q & 0x7FFFFFu) != 0u), 27u);   // at least 2^-100
+            g = __uint_as_float(e << 23);
+            inv_g = __uint_as_float((254u - e) << 23);
+        }
+        if (!finite) inv_g = 0.f;                           // zeros, and NaN as the row's scale
+        if (tid == 0) a.g[r] = finite ? g : __int_as_float(0x7FFFFFFF);
+    }
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        const int u = tid + p * ROW;
+        float hi, lo = 0.f, pre = inv_g;
+        uint32_t s;
+        if constexpr (NVFP4) {
+            const float t6 = inv_g > 0.f ? __uint_as_float(top[p]) * inv_g * (1.f / 6.f) : 0.f;
+            s = __nv_cvt_float_to_fp8(t6, __NV_SATFINITE, __NV_E4M3);
+            const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s, __NV_E4M3);
+            const float sf = __half2float(*reinterpret_cast<const __half *>(&hr));
+            hi = sf > 0.f ? __frcp_rn(sf) : 0.f;
+            lo = fmaf(-hi, sf, 1.f) * hi;
+            if (!(sf > 0.f)) lo = pre = 0.f;
+        } else {
+            const uint32_t m = max(top[p], __shfl_xor_sync(0xFFFFFFFFu, top[p], 1));
+            const bool finite = m < 0x7F800000u;
+            // floor(log2 m) - 2 as a biased exponent, subnormal m among them, at least 0
+            int e = m >= 0x00800000u ? (int)(m >> 23) - 2 : 0;
+            e = max(e, 0);
+            s = !finite ? 255u : m ? (uint32_t)e : 0u;
+            hi = 0.f;
+            pre = finite ? __uint_as_float(e == 0 ? 0x7F000000u : (uint32_t)(254 - e) << 23) : 0.f;
+        }
+        uint32_t c[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            c[h] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 f;
+                if constexpr (UP)
+                    f = make_float2(v[p][8 * h + 2 * i], v[p][8 * h + 2 * i + 1]);
+                else
+                    f = widen<BF16>(xv[p][4 * h + i]);
+                f.x = pre > 0.f ? f.x * pre : 0.f;
+                f.y = pre > 0.f ? f.y * pre : 0.f;
+                if constexpr (NVFP4) {
+                    f.x = fmaf(f.x, hi, f.x * lo);
+                    f.y = fmaf(f.y, hi, f.y * lo);
+                }
+                c[h] |= e2m1x2(f.x, f.y) << (8 * i);
+            }
+        }
+        if (u < units) {
+            *reinterpret_cast<uint2 *>(a.q + (int64_t)r * (a.K / 2) + u * 8) = make_uint2(c[0], c[1]);
+            if (NVFP4)
+                a.s[(int64_t)r * units + u] = (uint8_t)s;
+            else if ((u & 1) == 0)
+                a.s[(int64_t)r * (units / 2) + u / 2] = (uint8_t)s;
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t v[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// A thread turns units of 16 codes of its row into values.
+template <typename T, bool NVFP4, int ROW>
+__global__ void __launch_bounds__(kQThreads) dequantize_fp4_kernel(const DequantFp4Args a) {
+    pdl_wait();
+    const int tid = threadIdx.x % ROW, units = a.K / 16;
+    const int r = blockIdx.x * (kQThreads / ROW) + threadIdx.x / ROW;
+    if (r >= a.R) return;
+    const float g = NVFP4 && a.g ? a.g[a.g_rows ? r : 0] : 1.f;
+    T *out = (T *)a.out + (int64_t)r * a.out_ld;
+#pragma unroll 4
+    for (int u = tid; u < units; u += ROW) {
+        const uint2 c = *reinterpret_cast<const uint2 *>(a.q + (int64_t)r * (a.K / 2) + u * 8);
+        float unit;
+        if constexpr (NVFP4) {
+            const __half_raw hr = __nv_cvt_fp8_to_halfraw(a.s[(int64_t)r * units + u], __NV_E4M3);
+            unit = __half2float(*reinterpret_cast<const __half *>(&hr)) * g;
+        } else {
+            const uint32_t s = a.s[(int64_t)r * (units / 2) + u / 2];
+            unit = __uint_as_float(s == 0 ? 0x00400000u : s == 255u ? 0x7FFFFFFFu : s << 23);
+        }
+        uint32_t h[8];
+        e2m1x8_to_f16x2(c.x, h);
+        e2m1x8_to_f16x2(c.y, h + 4);
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 w = widen<false>(h[i]);
+            f[2 * i] = w.x * unit;
+            f[2 * i + 1] = w.y * unit;
+        }
+        if constexpr (sizeof(T) == 4) {
+            if (a.vec) {
+                uint32_t o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f[i]);
+                store32(out + u * 16, o);
+                store32(out + u * 16 + 8, o + 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) out[u * 16 + i] = f[i];
+            }
+        } else {
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+            if (a.vec) {
+                store32(out + u * 16, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ((uint16_t *)out)[u * 16 + i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
+
+template <typename A>
+cudaError_t launch(void (*kern)(const A), const A &a, int rows, int row_threads, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    const int per = kQThreads / row_threads;
+    cfg.gridDim = dim3((unsigned)((rows + (int64_t)per - 1) / per));
+    cfg.blockDim = dim3(kQThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <bool BF16, bool NVFP4, bool UP>
+cudaError_t launch_quant(const QuantFp4Args &a, cudaStream_t st) {
+    const int units = a.K / 16;
+#define MOE_Q(ROW, PER) return launch(quantize_fp4_kernel<BF16, NVFP4, UP, ROW, PER>, a, a.R, ROW, st)
+    if (units <= 32) MOE_Q(32, 1);
+    if (units <= 64) MOE_Q(32, 2);
+    if (units <= 128) MOE_Q(32, 4);
+    if (units <= 256) MOE_Q(256, 1);
+    if (units <= 512) MOE_Q(256, 2);
+    if (units <= 1024) MOE_Q(256, 4);
+    MOE_Q(256, 8);
+#undef MOE_Q
+}
+
+bool aligned32(const void *p, int64_t ld_bytes, int rows) {
+    return ((uintptr_t)p | (rows > 1 ? (uintptr_t)ld_bytes : 0)) % 32 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_fp4(QuantFp4Args a, cudaStream_t st) {
+    a.vec = aligned32(a.x, 2 * a.x_ld, a.T) && (!a.up || aligned32(a.up, 2 * a.up_ld, a.T));
+    const bool bf = a.type == MOE_T_BF16;
+    if (a.nvfp4) {
+        if (a.up) return bf ? launch_quant<true, true, true>(a, st) : launch_quant<false, true, true>(a, st);
+        return bf ? launch_quant<true, true, false>(a, st) : launch_quant<false, true, false>(a, st);
+    }
+    if (a.up) return bf ? launch_quant<true, false, true>(a, st) : launch_quant<false, false, true>(a, st);
+    return bf ? launch_quant<true, false, false>(a, st) : launch_quant<false, false, false>(a, st);
+}
+
+template <typename T>
+static cudaError_t launch_dequant(const DequantFp4Args &a, cudaStream_t st) {
+    if (a.K <= 2048)
+        return a.nvfp4 ? launch(dequantize_fp4_kernel<T, true, 32>, a, a.R, 32, st)
+                       : launch(dequantize_fp4_kernel<T, false, 32>, a, a.R, 32, st);
+    return a.nvfp4 ? launch(dequantize_fp4_kernel<T, true, 256>, a, a.R, 256, st)
+                   : launch(dequantize_fp4_kernel<T, false, 256>, a, a.R, 256, st);
+}
+
+cudaError_t launch_dequantize_fp4(DequantFp4Args a, cudaStream_t st) {
+    a.vec = aligned32(a.out, a.out_ld * (a.type == MOE_T_F32 ? 4 : 2), a.R);
+    if (a.type == MOE_T_BF16) return launch_dequant<__nv_bfloat16>(a, st);
+    if (a.type == MOE_T_F16) return launch_dequant<__half>(a, st);
+    return launch_dequant<float>(a, st);
+}
+
+}  // namespace moe
