@@ -14,8 +14,8 @@
 // CTAs running at a time share weight and row tiles in L2.
 //
 // Warps: 0 TMA, 1 MMA (owns the tensor memory), 2..5 epilogue, and for 4-bit
-// operands 6..9, which bring the block scales into tensor memory: the layout
-// there is lane r % 32, column r / 32 for row r, four scale bytes of one MMA
+// operands 10..13, which bring the block scales to shared memory, and 6..9, which
+// bring them from there to tensor memory: the layout there is lane r % 32, column r / 32 for row r, four scale bytes of one MMA
 // (K = 64) to a column, the same in all four lane quarters.
 #pragma once
 
@@ -55,15 +55,16 @@ struct ProdShape {
     static constexpr bool kFp4 = KIND != PROD_16;
     static constexpr int kBox = TN < 64 ? TN : 64;           // rows of one TMA copy of x
     static constexpr uint32_t kStage = kProdABytes + TN * 128;
-    static constexpr int kScaleBytes = KIND == PROD_NVFP4 ? 16 : 8;  // a row's scales of one stage
+    // scales come two stages at a time: a row's 32 (16) bytes are one sector
+    static constexpr int kPairBytes = KIND == PROD_NVFP4 ? 32 : 16;
     static constexpr int kScaleRows = kProdRows + TN;
-    static constexpr int kAhead = kFp4 ? 5 : 0;              // stages of scales in flight
-    static constexpr uint32_t kScales = kFp4 ? (kAhead + 1) * kScaleRows * kScaleBytes : 0;
+    static constexpr int kPairs = kFp4 ? 3 : 0;              // such pairs of stages in the ring
+    static constexpr uint32_t kScales = kFp4 ? kPairs * kScaleRows * kPairBytes : 0;
     static constexpr uint32_t kMeta = kProdMaxGroups * 12 + 16 + 512;  // group tables, barriers
-    static constexpr int kStages = (int)((227 * 1024 - 1024 - kMeta - kScales) / kStage) < 10
-                                       ? (int)((227 * 1024 - 1024 - kMeta - kScales) / kStage) : 10;
+    static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales) / kStage);
+    static constexpr int kStages = kRoom < 10 ? kRoom : 10;
     static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kMeta;
-    static constexpr int kThreads = kFp4 ? 320 : 192;
+    static constexpr int kThreads = kFp4 ? 448 : 192;
     // tensor memory: two accumulators, then two buffers of scales (16 columns for
     // the weights, kBCols for each of the four MMAs of a stage for x)
     static constexpr int kBCols = TN > 128 ? 8 : 4;
@@ -73,27 +74,78 @@ struct ProdShape {
     static_assert(2 * TN <= (int)kTmemCols, "tensor memory");
 };
 
-__device__ __forceinline__ void mma_f16_kind(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    mma_bf16(d, a, b, idesc, acc);               // bf16 or f16 by the descriptor
+// One lane of a warp whose 32 lanes are here. The roles that issue TMA copies and
+// MMAs run as whole warps, with the instructions predicated on that lane: their
+// operands then stay in uniform registers, where the instructions want them. One
+// lane alone in a branch moves each operand there first: an MMA of 64 columns or
+// fewer took 116 cycles so and takes 55, a stage of four with its wait 465 and 250.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
+__device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+        : "memory");
 }
 
 template <int KIND>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                        uint32_t acc) {
+                                        uint32_t acc, uint32_t on) {
     if constexpr (KIND == PROD_NVFP4)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(on)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(on)
             : "memory");
+}
+
+__device__ __forceinline__ void commit_on(uint64_t *bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+
+__device__ __forceinline__ void expect_on(uint64_t *bar, uint32_t bytes, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(on)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_on(uint32_t dst, const CUtensorMap *tm, int x, int y, uint64_t *bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(on)
+        : "memory");
+}
+
+// A wait of a whole warp, with one answer for its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *err, volatile int *abort) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, parity, err, abort));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) {
@@ -112,9 +164,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool in)
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(in ? N : 0)
                  : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Arrives at `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // The groups as the tiles need them, in shared memory.
 struct ProdGroups {
@@ -229,7 +282,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
     unsigned char *scales = smem + NS * S::kStage;
     unsigned char *meta = scales + S::kScales;
     uint64_t *full = reinterpret_cast<uint64_t *>(meta), *empty = full + NS;
-    uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 2, *done = sempty + 2;
+    uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 2;
+    uint64_t *lfull = sempty + 2, *lempty = lfull + 4, *done = lempty + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     ProdGroups gr;
@@ -250,6 +304,10 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
             mbar_init(&sfull[b], 128);
             mbar_init(&sempty[b], 1);
         }
+        for (int b = 0; b < S::kPairs; ++b) {
+            mbar_init(&lfull[b], 128);
+            mbar_init(&lempty[b], 128);
+        }
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -262,10 +320,12 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int nst = (a.K + kStageK - 1) / kStageK;
+    const uint32_t tiles = smem_u32(smem);
 
     if (warp == 0) {
         // ------------------------------- TMA producer -------------------------------
-        if (lane == 0 && !a.hold) {
+        if (!a.hold) {
+            const uint32_t on = elect_lane();
             int it = 0;
             bool ok = true;
             ProdWalk<TN> walk(blockIdx.x);
@@ -275,16 +335,16 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
                 const int loads = (t.rows + S::kBox - 1) / S::kBox;
                 for (int kb = 0; kb < nst; ++kb, ++it) {
                     const int slot = it % NS;
-                    if (!mbar_wait_or_abort(&empty[slot], ((it / NS) & 1) ^ 1, err, abort_flag)) {
+                    if (!warp_wait(&empty[slot], ((it / NS) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    unsigned char *st = smem + (size_t)slot * S::kStage;
-                    mbar_arrive_expect_tx(&full[slot], kProdABytes + loads * S::kBox * 128);
+                    const uint32_t st = tiles + slot * S::kStage;
+                    expect_on(&full[slot], kProdABytes + loads * S::kBox * 128, on);
                     const int k = kb * (KIND == PROD_16 ? 64 : 128);  // elements of the maps
-                    tma_load_2d(st, &tmW, k, wrow, &full[slot]);
+                    tma_on(st, &tmW, k, wrow, &full[slot], on);
                     for (int j = 0; j < loads; ++j)
-                        tma_load_2d(st + kProdABytes + j * (S::kBox * 128), &tmX, k, t.row0 + j * S::kBox, &full[slot]);
+                        tma_on(st + kProdABytes + j * (S::kBox * 128), &tmX, k, t.row0 + j * S::kBox, &full[slot], on);
                 }
             }
             // every load issued must land before the CTA exits
@@ -292,52 +352,53 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
         }
     } else if (warp == 1) {
         // -------------------------------- MMA issuer --------------------------------
-        if (lane == 0) {
-            int it = 0, lt = 0;
-            bool ok = true;
-            ProdWalk<TN> walk(blockIdx.x);
-            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x, ++lt) {
-                const ProdTile t = walk.at(gr, nw);
-                const uint32_t n16 = (uint32_t)(t.rows + 15) / 16;
-                uint32_t idesc;
-                if constexpr (S::kFp4)
-                    idesc = (1u << 7) | (1u << 10) | (n16 << 18) | (KIND == PROD_MXFP4 ? 1u << 23 : 0u) |
-                            ((uint32_t)(kProdRows >> 7) << 27);
-                else
-                    idesc = (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u) | (n16 << 18) |
-                            ((uint32_t)(kProdRows >> 4) << 24);
-                const int b = lt & 1;
-                if (!mbar_wait_or_abort(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(b * TN);
-                for (int kb = 0; kb < nst; ++kb, ++it) {
-                    const int slot = it % NS;
-                    if (!mbar_wait_or_abort(&full[slot], (it / NS) & 1, err, abort_flag) ||
-                        (S::kFp4 && !mbar_wait_or_abort(&sfull[it & 1], (it >> 1) & 1, err, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + (size_t)slot * S::kStage);
-                    const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + kProdABytes);
-                    const int nk = min(4, (a.K - kb * kStageK + kMmaK - 1) / kMmaK);
-                    const uint32_t sc = tmem_base + S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
-                    for (int kk = 0; kk < nk; ++kk) {
-                        const uint64_t o = (uint64_t)(2 * kk);
-                        if constexpr (S::kFp4)
-                            mma_fp4<KIND>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, (kb | kk) != 0);
-                        else
-                            mma_f16_kind(d, ad + o, bd + o, idesc, (kb | kk) != 0);
-                    }
-                    mma_commit(&empty[slot]);    // free once these MMAs have read it
-                    if (S::kFp4) mma_commit(&sempty[it & 1]);
+        const uint32_t on = elect_lane();
+        int it = 0, lt = 0;
+        bool ok = true;
+        ProdWalk<TN> walk(blockIdx.x);
+        for (; walk.tile < ntiles && ok; walk.tile += gridDim.x, ++lt) {
+            const uint32_t n16 = __shfl_sync(0xFFFFFFFFu, (uint32_t)(walk.at(gr, nw).rows + 15) / 16, 0);
+            uint32_t idesc;
+            if constexpr (S::kFp4)
+                idesc = (1u << 7) | (1u << 10) | (n16 << 18) | (KIND == PROD_MXFP4 ? 1u << 23 : 0u) |
+                        ((uint32_t)(kProdRows >> 7) << 27);
+            else
+                idesc = (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u) | (n16 << 18) |
+                        ((uint32_t)(kProdRows >> 4) << 24);
+            const int b = lt & 1;
+            if (!warp_wait(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t d = (uint32_t)(b * TN);       // (all columns are this CTA's: they begin at 0)
+            for (int kb = 0; kb < nst; ++kb, ++it) {
+                const int slot = it % NS;
+                if (!warp_wait(&full[slot], (it / NS) & 1, err, abort_flag) ||
+                    (S::kFp4 && !warp_wait(&sfull[it & 1], (it >> 1) & 1, err, abort_flag))) {
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
-                mma_commit(&tfull[b]);
+                tc_fence_after();
+                const uint32_t sa = tiles + slot * S::kStage;
+                const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + kProdABytes);
+                const int left = a.K - kb * kStageK;
+                const uint32_t sc = S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (kk * kMmaK >= left) break;       // the last stage may be shorter
+                    const uint64_t o = (uint64_t)(2 * kk);
+                    const uint32_t acc = kk ? 1u : (uint32_t)(kb != 0);
+                    if constexpr (S::kFp4)
+                        mma_fp4<KIND>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, acc, on);
+                    else
+                        mma_16(d, ad + o, bd + o, idesc, acc, on);
+                }
+                commit_on(&empty[slot], on);             // free once these MMAs have read it
+                if (S::kFp4) commit_on(&sempty[it & 1], on);
             }
-            mma_commit(done);
-            mbar_wait(done, 0, err);
+            if (!ok) break;
+            commit_on(&tfull[b], on);
         }
+        commit_on(done, on);
+        mbar_wait(done, 0, err);
     } else if (warp < 6) {
         // --------------------------------- epilogue ---------------------------------
         const int q = warp & 3;                  // TMEM lane quarter of this warp
@@ -346,111 +407,61 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
         for (; walk.tile < ntiles; walk.tile += gridDim.x, ++lt) {
             const ProdTile t = walk.at(gr, nw);
             const int b = lt & 1;
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&tfull[b], (lt >> 1) & 1, err, abort_flag));
+            const bool ok = warp_wait(&tfull[b], (lt >> 1) & 1, err, abort_flag);
             tc_fence_after();
-            prod_store<S::kFp4>(a, t, tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN),
+            prod_store<S::kFp4>(a, t, ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN),
                                 t.w * kProdRows + q * 32 + lane, !ok);
             tc_fence_before();
             mbar_arrive(&tempty[b]);
         }
     } else if constexpr (S::kFp4) {
-        // ---------------------------------- scales ----------------------------------
-        constexpr int SB = S::kScaleBytes, D = S::kAhead, NB = (TN + 127) / 128;
-        const int t = threadIdx.x - 192, q = warp & 3;
-        const int pitch = a.K / (KIND == PROD_NVFP4 ? 16 : 32);   // bytes of a row's scales
-        const uint32_t ring = smem_u32(scales);
-        const int64_t wrows = (int64_t)a.groups * a.N;
-        ProdWalk<TN> ahead(blockIdx.x), walk(blockIdx.x);
-        const uint8_t *src[1 + NB];
-        bool in[1 + NB];
-        int akb = 0, issued = 0;
-        auto place = [&]() {                     // the rows of this thread in the tile ahead
-            if (ahead.tile >= ntiles) return;
-            const ProdTile p = ahead.at(gr, nw);
-            const int64_t wr = (int64_t)p.g * a.N + p.w * kProdRows + t;
-            in[0] = wr < wrows;
-            src[0] = a.ws + (in[0] ? wr : 0) * pitch;
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int r = t + 128 * j;
-                in[1 + j] = r < p.rows;
-                src[1 + j] = a.xs + (int64_t)(in[1 + j] ? p.row0 + r : 0) * pitch;
-            }
-        };
-        auto issue = [&]() {                     // one stage; an empty group of copies past the end
-            if (ahead.tile < ntiles) {
-                const uint32_t slot = ring + (uint32_t)(issued % (D + 1)) * (S::kScaleRows * SB);
-                const int k0 = akb * SB;
-#pragma unroll
-                for (int j = 0; j <= NB; ++j) {
-                    const int r = j ? kProdRows + t + 128 * (j - 1) : t;
-                    if (r >= S::kScaleRows) break;
-                    const uint32_t dst = slot + r * SB;
-                    if (SB == 16 && a.s_copy == 16) {
-                        cp_async<16>(dst, src[j] + k0, in[j] && k0 < pitch);
-                    } else if (a.s_copy >= 8) {
-#pragma unroll
-                        for (int o = 0; o < SB; o += 8)
-                            cp_async<8>(dst + o, src[j] + min(k0 + o, pitch - 8), in[j] && k0 + o < pitch);
-                    } else if (a.s_copy >= 4) {
-#pragma unroll
-                        for (int o = 0; o < SB; o += 4)
-                            cp_async<4>(dst + o, src[j] + min(k0 + o, pitch - 4), in[j] && k0 + o < pitch);
-                    } else {
-#pragma unroll
-                        for (int o = 0; o < SB; ++o) {
-                            const uint32_t v = in[j] && k0 + o < pitch ? src[j][k0 + o] : 0u;
-                            asm volatile("st.shared.b8 [%0], %1;" ::"r"(dst + o), "r"(v) : "memory");
+        constexpr int PB = S::kPairBytes, SB = PB / 2, NP = S::kPairs, kHalf = S::kScaleRows * PB;
+        const int npair = (nst + 1) / 2;
+        if (warp < 10) {
+            // ------------------------- scales to tensor memory --------------------------
+            const int q = warp & 3;
+            int it = 0, pr = 0;
+            bool ok = true;
+            ProdWalk<TN> walk(blockIdx.x);
+            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x) {
+                for (int kb = 0; kb < nst; ++kb, ++it) {
+                    const int half = kb & 1;
+                    if (!half && !warp_wait(&lfull[pr % NP], (pr / NP) & 1, err, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const unsigned char *ring = scales + (pr % NP) * kHalf;
+                    uint32_t va[16], vb[4 * S::kBCols];
+                    auto words = [&](int row, uint32_t w[4]) {
+                        if constexpr (KIND == PROD_NVFP4) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(ring + row * PB + 16 * (half ^ ((row >> 2) & 1)));
+                            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                        } else {                 // two scales a column
+                            const uint2 v = *reinterpret_cast<const uint2 *>(ring + row * PB + 8 * half);
+                            w[0] = v.x & 0xFFFFu, w[1] = v.x >> 16, w[2] = v.y & 0xFFFFu, w[3] = v.y >> 16;
                         }
+                    };
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t w[4];
+                        words(32 * m + lane, w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) va[4 * j + m] = w[j];
                     }
-                }
-                ++issued;
-                if (++akb == nst) {
-                    akb = 0;
-                    ahead.tile += gridDim.x;
-                    place();
-                }
-            }
-            cp_async_commit();
-        };
-        place();
-        for (int i = 0; i < D; ++i) issue();
-        int it = 0;
-        bool ok = true;
-        for (; walk.tile < ntiles; walk.tile += gridDim.x) {
-            for (int kb = 0; kb < nst; ++kb, ++it) {
-                cp_async_wait<D - 1>();
-                named_bar(1, 128);               // the stage's scales are there for all four warps
-                const unsigned char *slot = scales + (size_t)(it % (D + 1)) * (S::kScaleRows * SB);
-                uint32_t va[16], vb[4 * S::kBCols];
-                auto words = [&](int row, uint32_t w[4]) {
-                    if constexpr (KIND == PROD_NVFP4) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(slot + row * SB);
-                        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                    } else {                     // two scales a column
-                        const uint2 v = *reinterpret_cast<const uint2 *>(slot + row * SB);
-                        w[0] = v.x & 0xFFFFu, w[1] = v.x >> 16, w[2] = v.y & 0xFFFFu, w[3] = v.y >> 16;
+#pragma unroll
+                    for (int m = 0; m < S::kBCols; ++m) {
+                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+                        if (32 * m < TN) words(kProdRows + 32 * m + lane, w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
                     }
-                };
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    uint32_t w[4];
-                    words(32 * m + lane, w);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) va[4 * j + m] = w[j];
-                }
-#pragma unroll
-                for (int m = 0; m < S::kBCols; ++m) {
-                    uint32_t w[4] = {0u, 0u, 0u, 0u};
-                    if (32 * m < TN) words(kProdRows + 32 * m + lane, w);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
-                }
-                // (a warp whose wait failed goes on to meet the others at the barrier, without work)
-                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&sempty[it & 1], ((it >> 1) & 1) ^ 1, err, abort_flag));
-                if (ok) {
+                    if (half || kb + 1 == nst) mbar_arrive(&lempty[pr++ % NP]);   // (its words are in registers)
+                    if (!warp_wait(&sempty[it & 1], ((it >> 1) & 1) ^ 1, err, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
-                    const uint32_t to = tmem_base + ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
+                    const uint32_t to = ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
                     tmem_st16(to, va);
                     tmem_st16(to + 16, vb);
                     if constexpr (S::kBCols == 8) tmem_st16(to + 32, vb + 16);
@@ -458,10 +469,60 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
                     tc_fence_before();
                     mbar_arrive(&sfull[it & 1]);
                 }
-                issue();                         // over the slot that all read before the barrier above
             }
+        } else {
+            // --------------------------- scales to shared memory ------------------------
+            const int t = threadIdx.x - 320;
+            const int pitch = a.K / (KIND == PROD_NVFP4 ? 16 : 32);  // bytes of a row's scales
+            const uint32_t ring = smem_u32(scales);
+            const int64_t wrows = (int64_t)a.groups * a.N;
+            const int copy = a.s_copy < 16 ? a.s_copy : 16;
+            const int shift = 31 - __clz(PB / copy);  // log2 of the chunks of a row and pair of stages
+            int pr = 0;
+            bool ok = true;
+            ProdWalk<TN> walk(blockIdx.x);
+            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x) {
+                const ProdTile p = walk.at(gr, nw);
+                const int64_t wrow = (int64_t)p.g * a.N + p.w * kProdRows;
+                const int rows = kProdRows + (p.rows + 31) / 32 * 32;
+                for (int i = 0; i < npair; ++i, ++pr) {
+                    if (!warp_wait(&lempty[pr % NP], ((pr / NP) & 1) ^ 1, err, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t to = ring + (pr % NP) * kHalf;
+                    // the chunks of a row by neighbouring threads: whole sectors
+                    for (int c = t; c < rows << shift; c += 128) {
+                        const int row = c >> shift, off = (c - (row << shift)) * copy, k = i * PB + off;
+                        const uint8_t *src;
+                        bool in;
+                        if (row < kProdRows) {
+                            in = wrow + row < wrows;
+                            src = a.ws + (in ? wrow + row : 0) * pitch;
+                        } else {
+                            in = row - kProdRows < p.rows;
+                            src = a.xs + (int64_t)(in ? p.row0 + row - kProdRows : 0) * pitch;
+                        }
+                        in = in && k < pitch;
+                        src += in ? k : 0;
+                        const uint32_t dst = to + row * PB + (KIND == PROD_NVFP4 ? off ^ (((row >> 2) & 1) * SB) : off);
+                        if (copy == 16)
+                            cp_async<16>(dst, src, in);
+                        else if (copy == 8)
+                            cp_async<8>(dst, src, in);
+                        else if (copy == 4)
+                            cp_async<4>(dst, src, in);
+                        else
+                            asm volatile("st.shared.b8 [%0], %1;" ::"r"(dst), "r"(in ? (uint32_t)*src : 0u) : "memory");
+                    }
+                    if (copy >= 4)
+                        cp_async_arrive(&lfull[pr % NP]);
+                    else
+                        mbar_arrive(&lfull[pr % NP]);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
-        cp_async_wait<0>();
     }
     tc_fence_before();
     __syncthreads();
