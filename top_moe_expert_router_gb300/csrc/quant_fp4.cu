@@ -6,7 +6,7 @@
 //   MXFP4: s = 2^(floor(log2 max|v_block|) - 2), blocks of 32, code = E2M1(v / s)
 // Bound by memory: 2 bytes in and 0.56 (0.53) out an element.
 //
-// A thread holds 16 elements (half a block of MXFP4), a warp or a CTA of 256 a
+// A thread holds units of 16 elements (half a block of MXFP4), a warp or a CTA a
 // row, so that a row is read once, from memory to registers, and its maximum is
 // known before its codes are formed.
 //
@@ -24,7 +24,8 @@
 namespace moe {
 namespace {
 
-constexpr int kQThreads = 256;
+constexpr int kQThreads = 256;        // of a CTA that dequantises
+constexpr int kManyRows = 4 * 152;    // rows enough for a warp each to fill the GPU
 
 __device__ __forceinline__ void load32(const void *p, bool vec, uint32_t v[8]) {
     if (vec) {
@@ -68,13 +69,33 @@ __device__ __forceinline__ uint32_t top_bits(const uint32_t x[8], const float v[
     }
 }
 
-// PER: units of 16 elements of a thread. ROW: threads of a row, 32 or 256.
-template <bool BF16, bool NVFP4, bool UP, int ROW, int PER>
-__global__ void __launch_bounds__(kQThreads) quantize_fp4_kernel(const QuantFp4Args a) {
-    __shared__ uint32_t part[kQThreads / 32];
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 o;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(o.x), "=f"(o.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return o;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 o;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(o.x), "=f"(o.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return o;
+}
+
+// PER: units of 16 elements of a thread. ROW: threads of a row; THREADS of a CTA.
+template <bool BF16, bool NVFP4, bool UP, int ROW, int PER, int THREADS>
+__global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Args a) {
+    static_assert(ROW == 32 || ROW == THREADS, "a row is a warp's or a CTA's");
+    __shared__ uint32_t part[THREADS / 32];
     pdl_wait();
     const int tid = threadIdx.x % ROW, units = a.K / 16;
-    const int r = blockIdx.x * (kQThreads / ROW) + threadIdx.x / ROW;
+    const int r = blockIdx.x * (THREADS / ROW) + threadIdx.x / ROW;
     if (r >= a.R) return;
     int t = r;
     if (a.rows) {
@@ -112,6 +133,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp4_kernel(const QuantFp4A
         big = max(big, top[p]);
     }
     float g = 1.f, inv_g = 1.f;
+    bool finite = true, far = false;
     if constexpr (NVFP4) {
         big = __reduce_max_sync(0xFFFFFFFFu, big);
         if constexpr (ROW > 32) {
@@ -121,38 +143,49 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp4_kernel(const QuantFp4A
 #pragma unroll
             for (int i = 1; i < ROW / 32; ++i) big = max(big, part[i]);
         }
-        const bool finite = big < 0x7F800000u;
+        finite = big < 0x7F800000u;
         if (big && finite) {
             const uint32_t q = __float_as_uint(__fdiv_rn(__uint_as_float(big), 2688.f));
             const uint32_t e = max((q >> 23) + ((q & 0x7FFFFFu) != 0u), 27u);   // at least 2^-100
+            far = e > 127u + 80u;
             g = __uint_as_float(e << 23);
             inv_g = __uint_as_float((254u - e) << 23);
         }
-        if (!finite) inv_g = 0.f;                           // zeros, and NaN as the row's scale
         if (tid == 0) a.g[r] = finite ? g : __int_as_float(0x7FFFFFFF);
+        if (!finite) {                                      // zeros, and NaN as the row's scale
+#pragma unroll
+            for (int p = 0; p < PER; ++p) {
+                const int u = tid + p * ROW;
+                if (u >= units) continue;
+                *reinterpret_cast<uint2 *>(a.q + (int64_t)r * (a.K / 2) + u * 8) = make_uint2(0u, 0u);
+                a.s[(int64_t)r * units + u] = 0u;
+            }
+            return;
+        }
     }
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const int u = tid + p * ROW;
-        float hi, lo = 0.f, pre = inv_g;
+        float2 hi, lo;
         uint32_t s;
+        bool none;                                          // codes 0 whatever the elements
         if constexpr (NVFP4) {
-            const float t6 = inv_g > 0.f ? __uint_as_float(top[p]) * inv_g * (1.f / 6.f) : 0.f;
-            s = __nv_cvt_float_to_fp8(t6, __NV_SATFINITE, __NV_E4M3);
+            s = __nv_cvt_float_to_fp8(__uint_as_float(top[p]) * inv_g * (1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
             const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s, __NV_E4M3);
             const float sf = __half2float(*reinterpret_cast<const __half *>(&hr));
-            hi = sf > 0.f ? __frcp_rn(sf) : 0.f;
-            lo = fmaf(-hi, sf, 1.f) * hi;
-            if (!(sf > 0.f)) lo = pre = 0.f;
+            none = s == 0u;
+            const float h = __frcp_rn(sf), l = fmaf(-h, sf, 1.f) * h;
+            // 1/g is a power of two: the products are exact, but where l would leave the range of normal numbers
+            hi.x = hi.y = far ? h : h * inv_g;
+            lo.x = lo.y = far ? l : l * inv_g;
         } else {
             const uint32_t m = max(top[p], __shfl_xor_sync(0xFFFFFFFFu, top[p], 1));
-            const bool finite = m < 0x7F800000u;
-            // floor(log2 m) - 2 as a biased exponent, subnormal m among them, at least 0
-            int e = m >= 0x00800000u ? (int)(m >> 23) - 2 : 0;
-            e = max(e, 0);
-            s = !finite ? 255u : m ? (uint32_t)e : 0u;
-            hi = 0.f;
-            pre = finite ? __uint_as_float(e == 0 ? 0x7F000000u : (uint32_t)(254 - e) << 23) : 0.f;
+            none = m >= 0x7F800000u;
+            // floor(log2 m) - 2 as a biased exponent, at least 0 (subnormal m among them)
+            const int e = max((int)(m >> 23) - 2, 0);
+            s = none ? 255u : (uint32_t)e;
+            hi.x = hi.y = __uint_as_float((uint32_t)(254 - e) << 23);
+            lo = hi;
         }
         uint32_t c[2];
 #pragma unroll
@@ -165,14 +198,15 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp4_kernel(const QuantFp4A
                     f = make_float2(v[p][8 * h + 2 * i], v[p][8 * h + 2 * i + 1]);
                 else
                     f = widen<BF16>(xv[p][4 * h + i]);
-                f.x = pre > 0.f ? f.x * pre : 0.f;
-                f.y = pre > 0.f ? f.y * pre : 0.f;
                 if constexpr (NVFP4) {
-                    f.x = fmaf(f.x, hi, f.x * lo);
-                    f.y = fmaf(f.y, hi, f.y * lo);
+                    if (far) f = mul2(f, make_float2(inv_g, inv_g));
+                    f = fma2(f, hi, mul2(f, lo));
+                } else {
+                    f = mul2(f, hi);
                 }
                 c[h] |= e2m1x2(f.x, f.y) << (8 * i);
             }
+            if (none) c[h] = 0u;
         }
         if (u < units) {
             *reinterpret_cast<uint2 *>(a.q + (int64_t)r * (a.K / 2) + u * 8) = make_uint2(c[0], c[1]);
@@ -259,11 +293,11 @@ __global__ void __launch_bounds__(kQThreads) dequantize_fp4_kernel(const Dequant
 }
 
 template <typename A>
-cudaError_t launch(void (*kern)(const A), const A &a, int rows, int row_threads, cudaStream_t st) {
+cudaError_t launch(void (*kern)(const A), const A &a, int rows, int row_threads, int threads, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    const int per = kQThreads / row_threads;
+    const int per = threads / row_threads;
     cfg.gridDim = dim3((unsigned)((rows + (int64_t)per - 1) / per));
-    cfg.blockDim = dim3(kQThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -273,17 +307,34 @@ cudaError_t launch(void (*kern)(const A), const A &a, int rows, int row_threads,
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+// Many rows: a warp each, up to 4096 columns (2048 with up), so that loads, maxima
+// and codes of different rows overlap without a barrier. Few rows: as many threads
+// for one as it has units.
 template <bool BF16, bool NVFP4, bool UP>
 cudaError_t launch_quant(const QuantFp4Args &a, cudaStream_t st) {
     const int units = a.K / 16;
-#define MOE_Q(ROW, PER) return launch(quantize_fp4_kernel<BF16, NVFP4, UP, ROW, PER>, a, a.R, ROW, st)
-    if (units <= 32) MOE_Q(32, 1);
-    if (units <= 64) MOE_Q(32, 2);
-    if (units <= 128) MOE_Q(32, 4);
-    if (units <= 256) MOE_Q(256, 1);
-    if (units <= 512) MOE_Q(256, 2);
-    if (units <= 1024) MOE_Q(256, 4);
-    MOE_Q(256, 8);
+#define MOE_Q(ROW, PER, THREADS) \
+    return launch(quantize_fp4_kernel<BF16, NVFP4, UP, ROW, PER, THREADS>, a, a.R, ROW, THREADS, st)
+    if (a.R > kManyRows) {
+        if (units <= 32) MOE_Q(32, 1, 128);
+        if (units <= 64) MOE_Q(32, 2, 128);
+        if (units <= 96) MOE_Q(32, 3, 128);
+        if (units <= 128) MOE_Q(32, 4, 128);
+        if (!UP && units <= 192) MOE_Q(32, 6, 128);
+        if (!UP && units <= 256) MOE_Q(32, 8, 128);
+        if (units <= 256) MOE_Q(128, 2, 128);
+        if (units <= 384) MOE_Q(128, 3, 128);
+        if (units <= 512) MOE_Q(128, 4, 128);
+    } else {
+        if (units <= 32) MOE_Q(32, 1, 128);
+        if (units <= 128) MOE_Q(128, 1, 128);
+        if (units <= 256) MOE_Q(256, 1, 256);
+        if (units <= 512) MOE_Q(256, 2, 256);
+    }
+    if (units <= 768) MOE_Q(256, 3, 256);
+    if (units <= 1024) MOE_Q(256, 4, 256);
+    if (units <= 1536) MOE_Q(512, 3, 512);
+    MOE_Q(512, 4, 512);
 #undef MOE_Q
 }
 
@@ -307,10 +358,10 @@ cudaError_t launch_quantize_fp4(QuantFp4Args a, cudaStream_t st) {
 template <typename T>
 static cudaError_t launch_dequant(const DequantFp4Args &a, cudaStream_t st) {
     if (a.K <= 2048)
-        return a.nvfp4 ? launch(dequantize_fp4_kernel<T, true, 32>, a, a.R, 32, st)
-                       : launch(dequantize_fp4_kernel<T, false, 32>, a, a.R, 32, st);
-    return a.nvfp4 ? launch(dequantize_fp4_kernel<T, true, 256>, a, a.R, 256, st)
-                   : launch(dequantize_fp4_kernel<T, false, 256>, a, a.R, 256, st);
+        return a.nvfp4 ? launch(dequantize_fp4_kernel<T, true, 32>, a, a.R, 32, kQThreads, st)
+                       : launch(dequantize_fp4_kernel<T, false, 32>, a, a.R, 32, kQThreads, st);
+    return a.nvfp4 ? launch(dequantize_fp4_kernel<T, true, 256>, a, a.R, 256, kQThreads, st)
+                   : launch(dequantize_fp4_kernel<T, false, 256>, a, a.R, 256, kQThreads, st);
 }
 
 cudaError_t launch_dequantize_fp4(DequantFp4Args a, cudaStream_t st) {
