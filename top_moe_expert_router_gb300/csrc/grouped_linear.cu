@@ -51,7 +51,8 @@ cudaError_t launch_grouped_linear(const ProdArgs &a, const void *x, int64_t x_ld
     const int per = a.M / (a.groups < a.M ? a.groups : a.M);     // rows of a group, all of them used
     if (a.M <= 32 || per <= 16) return launch_product<PROD_16, 32>(a, x, 2 * x_ld, w, st);
     if (per <= 64) return launch_product<PROD_16, 128>(a, x, 2 * x_ld, w, st);
-    return launch_product<PROD_16, 256>(a, x, 2 * x_ld, w, st);
+    if (a.N <= 128) return launch_product<PROD_16, 256>(a, x, 2 * x_ld, w, st);
+    return launch_product<PROD_16, 256, 2>(a, x, 2 * x_ld, w, st);
 }
 
 }  // namespace moe

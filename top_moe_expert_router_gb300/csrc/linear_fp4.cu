@@ -15,7 +15,8 @@ static cudaError_t launch_kind(const ProdArgs &a, const uint8_t *xq, const uint8
     const int64_t pitch = a.K / 2;
     const int per = a.M / (a.groups < a.M ? a.groups : a.M);     // rows of a group, all of them used
     if (a.M <= 32 || per <= 16) return launch_product<KIND, 32>(a, xq, pitch, wq, st);
-    return launch_product<KIND, 192>(a, xq, pitch, wq, st);
+    if (a.N <= 128) return launch_product<KIND, 192>(a, xq, pitch, wq, st);
+    return launch_product<KIND, 192, 2>(a, xq, pitch, wq, st);
 }
 
 cudaError_t launch_linear_fp4(ProdArgs a, bool nvfp4, const uint8_t *xq, const uint8_t *wq, cudaStream_t st) {

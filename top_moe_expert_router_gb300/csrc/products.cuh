@@ -50,11 +50,14 @@ static inline cudaError_t prod_take_errors(cudaStream_t st, uint32_t *bits) {
     return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
-template <int KIND, int TN>
+// CG: CTAs of a tile, 1 or 2 (a pair, 256 weight rows)
+template <int KIND, int TN, int CG>
 struct ProdShape {
     static constexpr bool kFp4 = KIND != PROD_16;
-    static constexpr int kBox = TN < 64 ? TN : 64;           // rows of one TMA copy of x
-    static constexpr uint32_t kStage = kProdABytes + TN * 128;
+    static constexpr int kShare = TN / CG;                   // rows of x in a CTA's shared memory
+    static constexpr int kBox = kShare % 64 ? 32 : 64;       // rows of one TMA copy of x
+    static constexpr int kStep = 16 * CG;                    // the N of an MMA is a multiple
+    static constexpr uint32_t kStage = kProdABytes + kShare * 128;
     // scales come two stages at a time: a row's 32 (16) bytes are one sector
     static constexpr int kPairBytes = KIND == PROD_NVFP4 ? 32 : 16;
     static constexpr int kScaleRows = kProdRows + TN;
@@ -85,44 +88,89 @@ __device__ __forceinline__ uint32_t elect_lane() {
     return e;
 }
 
+#define MOE_MMA_16(CGS)                                                        \
+    asm volatile(                                                              \
+        "{\n\t.reg .pred p, q;\n\t"                                        \
+        "setp.ne.b32 p, %4, 0;\n\t"                                          \
+        "setp.ne.b32 q, %5, 0;\n\t"                                          \
+        "@q tcgen05.mma.cta_group::" CGS ".kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), \
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)                          \
+        : "memory")
+#define MOE_MMA_FP4(CGS, KINDS)                                                \
+    asm volatile(                                                              \
+        "{\n\t.reg .pred p, q;\n\t"                                        \
+        "setp.ne.b32 p, %6, 0;\n\t"                                          \
+        "setp.ne.b32 q, %7, 0;\n\t"                                          \
+        "@q tcgen05.mma.cta_group::" CGS "." KINDS " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), \
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(on)        \
+        : "memory")
+
+template <int CG>
 __device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
-        : "memory");
+    if constexpr (CG == 1)
+        MOE_MMA_16("1");
+    else
+        MOE_MMA_16("2");
 }
 
-template <int KIND>
+template <int KIND, int CG>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                         uint32_t acc, uint32_t on) {
-    if constexpr (KIND == PROD_NVFP4)
+    if constexpr (KIND == PROD_NVFP4 && CG == 1)
+        MOE_MMA_FP4("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (KIND == PROD_NVFP4)
+        MOE_MMA_FP4("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (CG == 1)
+        MOE_MMA_FP4("1", "kind::mxf4.block_scale.scale_vec::2X");
+    else
+        MOE_MMA_FP4("2", "kind::mxf4.block_scale.scale_vec::2X");
+}
+#undef MOE_MMA_16
+#undef MOE_MMA_FP4
+
+// Arrives at `bar`, with CG = 2 at that of both CTAs, once the MMAs so far are done.
+template <int CG>
+__device__ __forceinline__ void commit_on(uint64_t *bar, uint32_t on) {
+    if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "setp.ne.b32 q, %7, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(on)
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+            "r"(on)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "setp.ne.b32 q, %7, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(on)
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+                smem_u32(bar)),
+            "r"(on), "h"((uint16_t)3)
             : "memory");
 }
 
-__device__ __forceinline__ void commit_on(uint64_t *bar, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(on)
-        : "memory");
+// The address of this CTA's shared word in the CTA of rank 0.
+__device__ __forceinline__ uint32_t in_leader(const void *p) {
+    uint32_t o;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(o) : "r"(smem_u32(p)));
+    return o;
+}
+
+// One arrival of the warp, whose lanes' work so far it covers, at the leader's barrier.
+template <int CG>
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) != 0) return;
+    if constexpr (CG == 1)
+        mbar_arrive(bar);
+    else
+        // what this orders between the CTAs lies in tensor memory, by the fences beside it; an arrival and a wait that
+        // ordered memory across the cluster would empty the L1 each time (8192 x 16384 x 8192 NVFP4: 1158 us)
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_leader(bar)) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void expect_on(uint64_t *bar, uint32_t bytes, uint32_t on) {
@@ -134,18 +182,60 @@ __device__ __forceinline__ void expect_on(uint64_t *bar, uint32_t bytes, uint32_
         : "memory");
 }
 
-__device__ __forceinline__ void tma_on(uint32_t dst, const CUtensorMap *tm, int x, int y, uint64_t *bar, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(on)
-        : "memory");
+// `bar`: an address in the cluster's shared memory (with CG = 2 the leader's).
+template <int CG>
+__device__ __forceinline__ void tma_on(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar, uint32_t on) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "r"(on)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "r"(on)
+            : "memory");
 }
 
-// A wait of a whole warp, with one answer for its lanes.
+template <int CG>
+__device__ __forceinline__ void prod_tmem_alloc(uint32_t *slot) {
+    if constexpr (CG == 1) {
+        tmem_alloc(slot, kTmemCols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void prod_tmem_free(uint32_t at) {
+    if constexpr (CG == 1)
+        tmem_dealloc(at, kTmemCols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(kTmemCols) : "memory");
+}
+
+// A bounded wait of a whole warp, with one answer for its lanes: false once the limit has passed or another warp of the
+// CTA gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *err, volatile int *abort) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, parity, err, abort));
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        if ((it & 255u) == 0) {
+            const bool late = global_ns() - t0 > kWaitLimitNs;
+            if (late) {
+                atomicOr(err, ERRBIT_TIMEOUT);
+                *abort = 1;
+            }
+            if (__any_sync(0xFFFFFFFFu, late || *abort)) return false;
+        }
+    }
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) {
@@ -270,10 +360,10 @@ __device__ __forceinline__ void prod_store(const ProdArgs &a, const ProdTile &t,
     }
 }
 
-template <int KIND, int TN>
-__global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
+template <int KIND, int TN, int CG>
+__global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const ProdArgs a) {
-    using S = ProdShape<KIND, TN>;
+    using S = ProdShape<KIND, TN, CG>;
     constexpr int NS = S::kStages;
     constexpr int kStageK = KIND == PROD_16 ? 64 : 256, kMmaK = kStageK / 4;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -300,23 +390,26 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 128);
-            mbar_init(&sfull[b], 128);
+            mbar_init(&tempty[b], 4 * CG);
+            mbar_init(&sfull[b], 4 * CG);
             mbar_init(&sempty[b], 1);
         }
         for (int b = 0; b < S::kPairs; ++b) {
             mbar_init(&lfull[b], 128);
-            mbar_init(&lempty[b], 128);
+            mbar_init(&lempty[b], 4);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+    if (warp == 1) prod_tmem_alloc<CG>(tmem_slot);
     pdl_wait();                                  // what earlier kernels write is read from here on
-    const int nw = (a.N + kProdRows - 1) / kProdRows;
+    // this CTA's rank in its pair; a pair walks the tiles as one
+    const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1), first = (int)blockIdx.x / CG, step = (int)gridDim.x / CG;
+    const int nw = (a.N + CG * kProdRows - 1) / (CG * kProdRows);
     tc_fence_before();
     const int ntiles = prod_groups<TN>(a, gr, nw);
+    if constexpr (CG == 2) cluster_sync_all();   // the barriers of both are ready
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int nst = (a.K + kStageK - 1) / kStageK;
@@ -328,11 +421,12 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
             const uint32_t on = elect_lane();
             int it = 0;
             bool ok = true;
-            ProdWalk<TN> walk(blockIdx.x);
-            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x) {
+            ProdWalk<TN> walk(first);
+            for (; walk.tile < ntiles && ok; walk.tile += step) {
                 const ProdTile t = walk.at(gr, nw);
-                const int wrow = t.g * a.N + t.w * kProdRows;
-                const int loads = (t.rows + S::kBox - 1) / S::kBox;
+                const int wrow = t.g * a.N + (t.w * CG + rank) * kProdRows;
+                const int share = CG == 1 ? t.rows : (t.rows + S::kStep - 1) / S::kStep * 16, row0 = t.row0 + rank * share;
+                const int loads = (share + S::kBox - 1) / S::kBox;
                 for (int kb = 0; kb < nst; ++kb, ++it) {
                     const int slot = it % NS;
                     if (!warp_wait(&empty[slot], ((it / NS) & 1) ^ 1, err, abort_flag)) {
@@ -340,31 +434,33 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
                         break;
                     }
                     const uint32_t st = tiles + slot * S::kStage;
-                    expect_on(&full[slot], kProdABytes + loads * S::kBox * 128, on);
+                    // (of both CTAs, where the leader counts them)
+                    if (rank == 0) expect_on(&full[slot], CG * (kProdABytes + loads * S::kBox * 128), on);
+                    const uint32_t bar = CG == 1 ? smem_u32(&full[slot]) : in_leader(&full[slot]);
                     const int k = kb * (KIND == PROD_16 ? 64 : 128);  // elements of the maps
-                    tma_on(st, &tmW, k, wrow, &full[slot], on);
+                    tma_on<CG>(st, &tmW, k, wrow, bar, on);
                     for (int j = 0; j < loads; ++j)
-                        tma_on(st + kProdABytes + j * (S::kBox * 128), &tmX, k, t.row0 + j * S::kBox, &full[slot], on);
+                        tma_on<CG>(st + kProdABytes + j * (S::kBox * 128), &tmX, k, row0 + j * S::kBox, bar, on);
                 }
             }
-            // every load issued must land before the CTA exits
-            for (int j = (it > NS ? it - NS : 0); j < it; ++j) mbar_wait(&full[j % NS], (j / NS) & 1, err);
+            // every load issued must land before the CTA exits (a pair's are counted, and waited for, by the leader)
+            for (int j = rank ? it : it > NS ? it - NS : 0; j < it; ++j) mbar_wait(&full[j % NS], (j / NS) & 1, err);
         }
     } else if (warp == 1) {
+        if (rank == 0) {
         // -------------------------------- MMA issuer --------------------------------
         const uint32_t on = elect_lane();
         int it = 0, lt = 0;
         bool ok = true;
-        ProdWalk<TN> walk(blockIdx.x);
-        for (; walk.tile < ntiles && ok; walk.tile += gridDim.x, ++lt) {
-            const uint32_t n16 = __shfl_sync(0xFFFFFFFFu, (uint32_t)(walk.at(gr, nw).rows + 15) / 16, 0);
-            uint32_t idesc;
+        ProdWalk<TN> walk(first);
+        for (; walk.tile < ntiles && ok; walk.tile += step, ++lt) {
+            // N in units of 8 (from bit 17), M in units of 16 (from bit 24; of 128 from bit 27)
+            const uint32_t n8 = __shfl_sync(0xFFFFFFFFu, (uint32_t)((walk.at(gr, nw).rows + S::kStep - 1) / S::kStep * (S::kStep / 8)), 0);
+            uint32_t idesc = (n8 << 17) | ((uint32_t)(CG * kProdRows >> 4) << 24);
             if constexpr (S::kFp4)
-                idesc = (1u << 7) | (1u << 10) | (n16 << 18) | (KIND == PROD_MXFP4 ? 1u << 23 : 0u) |
-                        ((uint32_t)(kProdRows >> 7) << 27);
+                idesc |= (1u << 7) | (1u << 10) | (KIND == PROD_MXFP4 ? 1u << 23 : 0u);
             else
-                idesc = (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u) | (n16 << 18) |
-                        ((uint32_t)(kProdRows >> 4) << 24);
+                idesc |= (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u);
             const int b = lt & 1;
             if (!warp_wait(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
             tc_fence_after();
@@ -387,32 +483,33 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
                     const uint64_t o = (uint64_t)(2 * kk);
                     const uint32_t acc = kk ? 1u : (uint32_t)(kb != 0);
                     if constexpr (S::kFp4)
-                        mma_fp4<KIND>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, acc, on);
+                        mma_fp4<KIND, CG>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, acc, on);
                     else
-                        mma_16(d, ad + o, bd + o, idesc, acc, on);
+                        mma_16<CG>(d, ad + o, bd + o, idesc, acc, on);
                 }
-                commit_on(&empty[slot], on);             // free once these MMAs have read it
-                if (S::kFp4) commit_on(&sempty[it & 1], on);
+                commit_on<CG>(&empty[slot], on);             // free once these MMAs have read it
+                if (S::kFp4) commit_on<CG>(&sempty[it & 1], on);
             }
             if (!ok) break;
-            commit_on(&tfull[b], on);
+            commit_on<CG>(&tfull[b], on);
         }
-        commit_on(done, on);
+        commit_on<CG>(done, on);
         mbar_wait(done, 0, err);
+        }
     } else if (warp < 6) {
         // --------------------------------- epilogue ---------------------------------
         const int q = warp & 3;                  // TMEM lane quarter of this warp
         int lt = 0;
-        ProdWalk<TN> walk(blockIdx.x);
-        for (; walk.tile < ntiles; walk.tile += gridDim.x, ++lt) {
+        ProdWalk<TN> walk(first);
+        for (; walk.tile < ntiles; walk.tile += step, ++lt) {
             const ProdTile t = walk.at(gr, nw);
             const int b = lt & 1;
             const bool ok = warp_wait(&tfull[b], (lt >> 1) & 1, err, abort_flag);
             tc_fence_after();
             prod_store<S::kFp4>(a, t, ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN),
-                                t.w * kProdRows + q * 32 + lane, !ok);
+                                (t.w * CG + rank) * kProdRows + q * 32 + lane, !ok);
             tc_fence_before();
-            mbar_arrive(&tempty[b]);
+            warp_arrive<CG>(&tempty[b]);
         }
     } else if constexpr (S::kFp4) {
         constexpr int PB = S::kPairBytes, SB = PB / 2, NP = S::kPairs, kHalf = S::kScaleRows * PB;
@@ -422,8 +519,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
             const int q = warp & 3;
             int it = 0, pr = 0;
             bool ok = true;
-            ProdWalk<TN> walk(blockIdx.x);
-            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x) {
+            ProdWalk<TN> walk(first);
+            for (; walk.tile < ntiles && ok; walk.tile += step) {
                 for (int kb = 0; kb < nst; ++kb, ++it) {
                     const int half = kb & 1;
                     if (!half && !warp_wait(&lfull[pr % NP], (pr / NP) & 1, err, abort_flag)) {
@@ -455,7 +552,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
                     }
-                    if (half || kb + 1 == nst) mbar_arrive(&lempty[pr++ % NP]);   // (its words are in registers)
+                    if (half || kb + 1 == nst) warp_arrive<1>(&lempty[pr++ % NP]);  // (its words are in registers)
                     if (!warp_wait(&sempty[it & 1], ((it >> 1) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
@@ -467,7 +564,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
                     if constexpr (S::kBCols == 8) tmem_st16(to + 32, vb + 16);
                     tmem_st_wait();
                     tc_fence_before();
-                    mbar_arrive(&sfull[it & 1]);
+                    warp_arrive<CG>(&sfull[it & 1]);
                 }
             }
         } else {
@@ -480,10 +577,10 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
             const int shift = 31 - __clz(PB / copy);  // log2 of the chunks of a row and pair of stages
             int pr = 0;
             bool ok = true;
-            ProdWalk<TN> walk(blockIdx.x);
-            for (; walk.tile < ntiles && ok; walk.tile += gridDim.x) {
+            ProdWalk<TN> walk(first);
+            for (; walk.tile < ntiles && ok; walk.tile += step) {
                 const ProdTile p = walk.at(gr, nw);
-                const int64_t wrow = (int64_t)p.g * a.N + p.w * kProdRows;
+                const int64_t wrow = (int64_t)p.g * a.N + (int64_t)(p.w * CG + rank) * kProdRows;
                 const int rows = kProdRows + (p.rows + 31) / 32 * 32;
                 for (int i = 0; i < npair; ++i, ++pr) {
                     if (!warp_wait(&lempty[pr % NP], ((pr / NP) & 1) ^ 1, err, abort_flag)) {
@@ -526,9 +623,15 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // neither CTA of a pair leaves, or frees its tensor memory, while the other may still reach it
+    if constexpr (CG == 2) {
+        if (rank && warp == 1) mbar_wait(done, 0, err);      // the leader's last arrival here
+        __syncwarp();
+        cluster_sync_all();
+    }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        prod_tmem_free<CG>(tmem_base);
     }
 }
 
@@ -541,11 +644,11 @@ int device_sms();
 
 #ifdef __CUDACC__
 // x: rows x_pitch bytes apart; w: [groups * N] rows without gaps.
-template <int KIND, int TN>
+template <int KIND, int TN, int CG = 1>
 cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, const void *w, cudaStream_t st) {
-    using S = ProdShape<KIND, TN>;
+    using S = ProdShape<KIND, TN, CG>;
     static std::atomic<uint64_t> attr_set{0};
-    const auto kern = product_kernel<KIND, TN>;
+    const auto kern = product_kernel<KIND, TN, CG>;
     cudaError_t e = set_smem_limit_once((const void *)kern, (int)S::kSmem, attr_set);
     if (e != cudaSuccess) return e;
     ProdArgs a = a0;
@@ -555,21 +658,25 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     if (!make_tmap_rows(&tw, w, (uint64_t)a.groups * a.N, row, row, kProdRows, KIND == PROD_16) ||
         !make_tmap_rows(&tx, x, a.M, row, a.M > 1 ? x_pitch : row, S::kBox, KIND == PROD_16))
         return cudaErrorInvalidValue;
-    const int64_t nw = (a.N + kProdRows - 1) / kProdRows;
+    const int64_t nw = (a.N + CG * kProdRows - 1) / (CG * kProdRows);
     // a tile of every group may be ragged
     const int64_t most = ((int64_t)a.M / TN + (a.groups < a.M ? a.groups : a.M)) * nw;
     const int sms = device_sms();
     if (sms < 1) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.gridDim = dim3((unsigned)(most < sms / CG ? most : sms / CG) * CG);
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CG == 1 ? 1 : 2;
     return cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
 }
 #endif
