@@ -13,9 +13,9 @@
 // device determine: group by group, in bands of 12 weight tiles, so that the
 // CTAs running at a time share weight and row tiles in L2.
 //
-// Warps: 0 TMA, 1 MMA (owns the tensor memory), 2..5 epilogue, and for 4-bit
-// operands 10..13, which bring the block scales to shared memory, and 6..9, which
-// bring them from there to tensor memory: the layout there is lane r % 32, column r / 32 for row r, four scale bytes of one MMA
+// Warps: 0 TMA, 1 MMA (owns the tensor memory), 2..9 epilogue, and for 4-bit
+// operands 18 and 19, which bring the block scales to shared memory, and 10..17,
+// which bring them from there to tensor memory: the layout there is lane r % 32, column r / 32 for row r, four scale bytes of one MMA
 // (K = 64) to a column, the same in all four lane quarters.
 #pragma once
 
@@ -58,16 +58,17 @@ struct ProdShape {
     static constexpr int kBox = kShare % 64 ? 32 : 64;       // rows of one TMA copy of x
     static constexpr int kStep = 16 * CG;                    // the N of an MMA is a multiple
     static constexpr uint32_t kStage = kProdABytes + kShare * 128;
-    // scales come two stages at a time: a row's 32 (16) bytes are one sector
-    static constexpr int kPairBytes = KIND == PROD_NVFP4 ? 32 : 16;
+    // scales come four stages at a time, 64 (32) bytes of a row
+    static constexpr int kQuadBytes = KIND == PROD_NVFP4 ? 64 : 32;
     static constexpr int kScaleRows = kProdRows + TN;
-    static constexpr int kPairs = kFp4 ? 3 : 0;              // such pairs of stages in the ring
-    static constexpr uint32_t kScales = kFp4 ? kPairs * kScaleRows * kPairBytes : 0;
+    static constexpr int kQuads = kFp4 ? 2 : 0;              // such quads of stages in the ring
+    static constexpr uint32_t kScales = kFp4 ? kQuads * kScaleRows * kQuadBytes : 0;
+    static constexpr int kScaleBox = TN % 64 ? 32 : 64;      // rows of one TMA copy of x's scales
     static constexpr uint32_t kMeta = kProdMaxGroups * 12 + 16 + 512;  // group tables, barriers
     static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales) / kStage);
     static constexpr int kStages = kRoom < 10 ? kRoom : 10;
     static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kMeta;
-    static constexpr int kThreads = kFp4 ? 448 : 192;
+    static constexpr int kThreads = kFp4 ? 640 : 320;
     // tensor memory: two accumulators, then two buffers of scales (16 columns for
     // the weights, kBCols for each of the four MMAs of a stage for x)
     static constexpr int kBCols = TN > 128 ? 8 : 4;
@@ -323,46 +324,88 @@ __device__ __forceinline__ int prod_groups(const ProdArgs &a, const ProdGroups &
     return gr.start[a.groups];
 }
 
-__device__ __forceinline__ void store_as(void *y, int64_t at, moe_dtype t, float v) {
-    if (t == MOE_T_BF16)
-        ((__nv_bfloat16 *)y)[at] = __float2bfloat16_rn(v);
-    else if (t == MOE_T_F16)
-        ((__half *)y)[at] = __float2half_rn(v);
-    else
-        ((float *)y)[at] = v;
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t v[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
 }
 
-// One tile's rows: this thread owns column n of y and walks the rows.
-template <bool FP4>
-__device__ __forceinline__ void prod_store(const ProdArgs &a, const ProdTile &t, uint32_t tbase, int n, bool failed) {
-    const int lane = threadIdx.x & 31;
-    const bool mine = n < a.N;
-    const float b = a.bias && mine ? a.bias[(int64_t)t.g * a.N + n] : 0.f;
-    float cs = 1.f;
-    if (FP4 && a.wg && mine) cs = a.wg[a.wg_cols ? (int64_t)t.g * a.N + n : t.g];
-    int64_t at = (int64_t)t.row0 * a.y_ld + n;
-#pragma unroll 1
-    for (int c0 = 0; c0 < t.rows; c0 += 16) {
-        uint32_t v[16];
-        if (!failed) {
-            tmem_ld16(tbase + c0, v);
-            tmem_ld_wait();
-        }
-        float rs = 1.f;
-        if (FP4 && a.xg) rs = a.xg[t.row0 + min(c0 + (lane & 15), t.rows - 1)];
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half rounded(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float rounded(float v) { return v; }
+
+// What a tile's results are multiplied by and added to, read before they are waited for: this thread's column (scale
+// and bias), and the scales of rows lane, lane + 32, ...
+template <bool FP4, int TN>
+struct ProdScales {
+    float col, bias, row[FP4 ? TN / 32 : 1];
+    __device__ __forceinline__ ProdScales(const ProdArgs &a, const ProdTile &t, int n) : col(1.f), bias(0.f) {
+        const bool mine = n < a.N;
+        if (a.bias && mine) bias = a.bias[(int64_t)t.g * a.N + n];
+        if constexpr (FP4) {
+            if (a.wg && mine) col = a.wg[a.wg_cols ? (int64_t)t.g * a.N + n : t.g];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float o = failed ? __int_as_float(0x7FFFFFFF) : __uint_as_float(v[i]);
-            if (FP4) o *= cs * __shfl_sync(0xFFFFFFFFu, rs, i);
-            if (mine && c0 + i < t.rows) store_as(a.y, at, a.y_type, o + b);
-            at += a.y_ld;
+            for (int j = 0; j < TN / 32; ++j) {
+                const int r = 32 * j + (threadIdx.x & 31);
+                row[j] = a.xg && r < t.rows ? a.xg[t.row0 + r] : 1.f;
+            }
+        }
+    }
+};
+
+// A tile's rows: this thread owns column n of y and walks the rows, 32 accumulator columns at a time, every other 32
+// (from `half` on).
+template <bool FP4, int TN, typename T>
+__device__ __forceinline__ void prod_store(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, TN> &sc, uint32_t tbase,
+                                           int n, int half, bool failed) {
+    const bool mine = n < a.N;
+    T *y = (T *)a.y + (int64_t)t.row0 * a.y_ld + n;
+#pragma unroll
+    for (int j = 0; j < TN / 32; ++j) {
+        if (32 * j >= t.rows) break;
+        if ((j & 1) != half) {
+            if (j + 1 < TN / 32) y += 32 * a.y_ld;
+            continue;
+        }
+        uint32_t v[32];
+        tmem_ld32(tbase + 32 * j, v);
+        tmem_ld_wait();
+        if constexpr (FP4) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) * (sc.col * __shfl_sync(0xFFFFFFFFu, sc.row[j], i)));
+        }
+        const int rows = t.rows - 32 * j;
+        if (mine && !failed && rows >= 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                *y = rounded<T>(__uint_as_float(v[i]) + sc.bias);
+                y += a.y_ld;
+            }
+        } else if (mine) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (i < rows) *y = rounded<T>(failed ? __int_as_float(0x7FFFFFFF) : __uint_as_float(v[i]) + sc.bias);
+                y += a.y_ld;
+            }
         }
     }
 }
 
 template <int KIND, int TN, int CG>
 __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const ProdArgs a) {
+    product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ CUtensorMap tmWS, const __grid_constant__ CUtensorMap tmXS, const ProdArgs a) {
     using S = ProdShape<KIND, TN, CG>;
     constexpr int NS = S::kStages;
     constexpr int kStageK = KIND == PROD_16 ? 64 : 256, kMmaK = kStageK / 4;
@@ -373,7 +416,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     unsigned char *meta = scales + S::kScales;
     uint64_t *full = reinterpret_cast<uint64_t *>(meta), *empty = full + NS;
     uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 2;
-    uint64_t *lfull = sempty + 2, *lempty = lfull + 4, *done = lempty + 4;
+    uint64_t *lfull = sempty + 2, *lempty = lfull + 2, *done = lempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     ProdGroups gr;
@@ -390,13 +433,13 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 4 * CG);
+            mbar_init(&tempty[b], 8 * CG);
             mbar_init(&sfull[b], 4 * CG);
             mbar_init(&sempty[b], 1);
         }
-        for (int b = 0; b < S::kPairs; ++b) {
-            mbar_init(&lfull[b], 128);
-            mbar_init(&lempty[b], 4);
+        for (int b = 0; b < S::kQuads; ++b) {
+            mbar_init(&lfull[b], a.s_copy >= 16 ? 1 : 64);
+            mbar_init(&lempty[b], 8);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -496,45 +539,59 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         commit_on<CG>(done, on);
         mbar_wait(done, 0, err);
         }
-    } else if (warp < 6) {
+    } else if (warp < 10) {
         // --------------------------------- epilogue ---------------------------------
-        const int q = warp & 3;                  // TMEM lane quarter of this warp
+        const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter of this warp, its share of the columns
         int lt = 0;
         ProdWalk<TN> walk(first);
         for (; walk.tile < ntiles; walk.tile += step, ++lt) {
             const ProdTile t = walk.at(gr, nw);
             const int b = lt & 1;
+            const int n = (t.w * CG + rank) * kProdRows + q * 32 + lane;
+            const ProdScales<S::kFp4, TN> sc(a, t, n);
             const bool ok = warp_wait(&tfull[b], (lt >> 1) & 1, err, abort_flag);
             tc_fence_after();
-            prod_store<S::kFp4>(a, t, ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN),
-                                (t.w * CG + rank) * kProdRows + q * 32 + lane, !ok);
+            const uint32_t at = ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
+            if (a.y_type == MOE_T_BF16)
+                prod_store<S::kFp4, TN, __nv_bfloat16>(a, t, sc, at, n, half, !ok);
+            else if (a.y_type == MOE_T_F16)
+                prod_store<S::kFp4, TN, __half>(a, t, sc, at, n, half, !ok);
+            else
+                prod_store<S::kFp4, TN, float>(a, t, sc, at, n, half, !ok);
             tc_fence_before();
             warp_arrive<CG>(&tempty[b]);
         }
     } else if constexpr (S::kFp4) {
-        constexpr int PB = S::kPairBytes, SB = PB / 2, NP = S::kPairs, kHalf = S::kScaleRows * PB;
-        const int npair = (nst + 1) / 2;
-        if (warp < 10) {
+        constexpr int QB = S::kQuadBytes, SB = QB / 4, NQ = S::kQuads, kSlot = S::kScaleRows * QB;
+        const int nquad = (nst + 3) / 4;
+        // 16-byte pieces of a row lie in the order of TMA's 64-byte (32-byte) swizzle: rows read together are then on
+        // different banks
+        auto swizzled = [](int row, int off) { return off ^ (QB == 64 ? ((row >> 1) & 3) << 4 : ((row >> 2) & 1) << 4); };
+        if (warp < 18) {
             // ------------------------- scales to tensor memory --------------------------
-            const int q = warp & 3;
-            int it = 0, pr = 0;
+            // (two groups of four warps, one for each buffer in tensor memory)
+            const int q = warp & 3, group = (warp - 10) >> 2;
+            int it = 0, qr = 0;
             bool ok = true;
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
-                for (int kb = 0; kb < nst; ++kb, ++it) {
-                    const int half = kb & 1;
-                    if (!half && !warp_wait(&lfull[pr % NP], (pr / NP) & 1, err, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const unsigned char *ring = scales + (pr % NP) * kHalf;
+                for (int kb = 0; kb < nst && ok; kb += 4, ++qr) {
+                  if (!warp_wait(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
+                      ok = false;
+                      break;
+                  }
+                  const unsigned char *ring = scales + (qr % NQ) * kSlot;
+                  const int parts = min(4, nst - kb);
+                  for (int part = 0; part < parts; ++part, ++it) {
+                    if ((it & 1) != group) continue;
                     uint32_t va[16], vb[4 * S::kBCols];
                     auto words = [&](int row, uint32_t w[4]) {
+                        const unsigned char *at = ring + row * QB + swizzled(row, part * SB);
                         if constexpr (KIND == PROD_NVFP4) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(ring + row * PB + 16 * (half ^ ((row >> 2) & 1)));
+                            const uint4 v = *reinterpret_cast<const uint4 *>(at);
                             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
                         } else {                 // two scales a column
-                            const uint2 v = *reinterpret_cast<const uint2 *>(ring + row * PB + 8 * half);
+                            const uint2 v = *reinterpret_cast<const uint2 *>(at);
                             w[0] = v.x & 0xFFFFu, w[1] = v.x >> 16, w[2] = v.y & 0xFFFFu, w[3] = v.y >> 16;
                         }
                     };
@@ -552,7 +609,6 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
                     }
-                    if (half || kb + 1 == nst) warp_arrive<1>(&lempty[pr++ % NP]);  // (its words are in registers)
                     if (!warp_wait(&sempty[it & 1], ((it >> 1) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
@@ -565,32 +621,61 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     warp_arrive<CG>(&sfull[it & 1]);
+                  }
+                  warp_arrive<1>(&lempty[qr % NQ]);
                 }
             }
+        } else if (a.s_copy >= 16) {
+            // ----------------------- scales to shared memory, by TMA --------------------
+            if (warp == 18 && !a.hold) {
+                const uint32_t on = elect_lane(), ring = smem_u32(scales);
+                int qr = 0;
+                bool ok = true;
+                ProdWalk<TN> walk(first);
+                for (; walk.tile < ntiles && ok; walk.tile += step) {
+                    const ProdTile p = walk.at(gr, nw);
+                    const int wrow = p.g * a.N + (p.w * CG + rank) * kProdRows;
+                    const int loads = (p.rows + S::kScaleBox - 1) / S::kScaleBox;
+                    for (int i = 0; i < nquad; ++i, ++qr) {
+                        uint64_t *bar = &lfull[qr % NQ];
+                        if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t to = ring + (qr % NQ) * kSlot;
+                        expect_on(bar, (kProdRows + loads * S::kScaleBox) * QB, on);
+                        tma_on<CG>(to, &tmWS, i * QB, wrow, smem_u32(bar), on);
+                        for (int j = 0; j < loads; ++j)
+                            tma_on<CG>(to + (kProdRows + j * S::kScaleBox) * QB, &tmXS, i * QB, p.row0 + j * S::kScaleBox,
+                                       smem_u32(bar), on);
+                    }
+                }
+                for (int j = qr > NQ ? qr - NQ : 0; j < qr; ++j) mbar_wait(&lfull[j % NQ], (j / NQ) & 1, err);
+            }
         } else {
-            // --------------------------- scales to shared memory ------------------------
-            const int t = threadIdx.x - 320;
+            // ------------- scales to shared memory, where their rows are not aligned -----
+            const int t = threadIdx.x - 18 * 32;
             const int pitch = a.K / (KIND == PROD_NVFP4 ? 16 : 32);  // bytes of a row's scales
             const uint32_t ring = smem_u32(scales);
             const int64_t wrows = (int64_t)a.groups * a.N;
-            const int copy = a.s_copy < 16 ? a.s_copy : 16;
-            const int shift = 31 - __clz(PB / copy);  // log2 of the chunks of a row and pair of stages
-            int pr = 0;
+            const int copy = a.s_copy;
+            const int shift = 31 - __clz(QB / copy);  // log2 of the pieces of a row and quad of stages
+            int qr = 0;
             bool ok = true;
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
                 const ProdTile p = walk.at(gr, nw);
                 const int64_t wrow = (int64_t)p.g * a.N + (int64_t)(p.w * CG + rank) * kProdRows;
                 const int rows = kProdRows + (p.rows + 31) / 32 * 32;
-                for (int i = 0; i < npair; ++i, ++pr) {
-                    if (!warp_wait(&lempty[pr % NP], ((pr / NP) & 1) ^ 1, err, abort_flag)) {
+                for (int i = 0; i < nquad; ++i, ++qr) {
+                    if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t to = ring + (pr % NP) * kHalf;
-                    // the chunks of a row by neighbouring threads: whole sectors
-                    for (int c = t; c < rows << shift; c += 128) {
-                        const int row = c >> shift, off = (c - (row << shift)) * copy, k = i * PB + off;
+                    const uint32_t to = ring + (qr % NQ) * kSlot;
+                    // the pieces of a row by neighbouring threads: whole sectors
+                    for (int c = t; c < rows << shift; c += 64) {
+                        const int row = c >> shift, off = (c - (row << shift)) * copy, k = i * QB + off;
                         const uint8_t *src;
                         bool in;
                         if (row < kProdRows) {
@@ -602,10 +687,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                         }
                         in = in && k < pitch;
                         src += in ? k : 0;
-                        const uint32_t dst = to + row * PB + (KIND == PROD_NVFP4 ? off ^ (((row >> 2) & 1) * SB) : off);
-                        if (copy == 16)
-                            cp_async<16>(dst, src, in);
-                        else if (copy == 8)
+                        const uint32_t dst = to + row * QB + swizzled(row, off);
+                        if (copy == 8)
                             cp_async<8>(dst, src, in);
                         else if (copy == 4)
                             cp_async<4>(dst, src, in);
@@ -613,9 +696,9 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                             asm volatile("st.shared.b8 [%0], %1;" ::"r"(dst), "r"(in ? (uint32_t)*src : 0u) : "memory");
                     }
                     if (copy >= 4)
-                        cp_async_arrive(&lfull[pr % NP]);
+                        cp_async_arrive(&lfull[qr % NQ]);
                     else
-                        mbar_arrive(&lfull[pr % NP]);
+                        mbar_arrive(&lfull[qr % NQ]);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -640,6 +723,9 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
 // Host: 2-D map of rows of `row_bytes`, `pitch` bytes apart, in boxes of 128 bytes x box_rows with the 128-byte swizzle.
 bool make_tmap_rows(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t row_bytes, uint64_t pitch,
                     uint32_t box_rows, bool two_byte);
+// The same of bytes, in boxes of box_bytes (64 or 32) with the swizzle of that width, rows without gaps.
+bool make_tmap_scales(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes,
+                      uint32_t box_rows);
 int device_sms();
 
 #ifdef __CUDACC__
@@ -658,6 +744,14 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     if (!make_tmap_rows(&tw, w, (uint64_t)a.groups * a.N, row, row, kProdRows, KIND == PROD_16) ||
         !make_tmap_rows(&tx, x, a.M, row, a.M > 1 ? x_pitch : row, S::kBox, KIND == PROD_16))
         return cudaErrorInvalidValue;
+    CUtensorMap tws = tw, txs = tx;
+    if constexpr (S::kFp4) {
+        const uint64_t srow = a.K / (KIND == PROD_NVFP4 ? 16 : 32);
+        if (a.s_copy >= 16 &&
+            (!make_tmap_scales(&tws, a.ws, (uint64_t)a.groups * a.N, srow, S::kQuadBytes, kProdRows) ||
+             !make_tmap_scales(&txs, a.xs, a.M, srow, S::kQuadBytes, S::kScaleBox)))
+            return cudaErrorInvalidValue;
+    }
     const int64_t nw = (a.N + CG * kProdRows - 1) / (CG * kProdRows);
     // a tile of every group may be ragged
     const int64_t most = ((int64_t)a.M / TN + (a.groups < a.M ? a.groups : a.M)) * nw;
@@ -677,7 +771,7 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx, tws, txs, a);
 }
 #endif
 
