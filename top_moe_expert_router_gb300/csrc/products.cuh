@@ -58,16 +58,21 @@ struct ProdShape {
     static constexpr int kBox = kShare % 64 ? 32 : 64;       // rows of one TMA copy of x
     static constexpr int kStep = 16 * CG;                    // the N of an MMA is a multiple
     static constexpr uint32_t kStage = kProdABytes + kShare * 128;
-    // scales come four stages at a time, 64 (32) bytes of a row
-    static constexpr int kQuadBytes = KIND == PROD_NVFP4 ? 64 : 32;
+    // scales come kBatch stages at a time: 32 bytes of a row (of MXFP4 16), a whole sector. (Four stages at a time in two
+    // slots, with one tile stage less: the same time.)
+    static constexpr int kBatch = 2;
+    static constexpr int kBatchBytes = (KIND == PROD_NVFP4 ? 16 : 8) * kBatch;
     static constexpr int kScaleRows = kProdRows + TN;
-    static constexpr int kQuads = kFp4 ? 2 : 0;              // such quads of stages in the ring
-    static constexpr uint32_t kScales = kFp4 ? kQuads * kScaleRows * kQuadBytes : 0;
+    static constexpr int kBatches = kFp4 ? 3 : 0;            // such batches in the ring
+    static constexpr uint32_t kScales = kFp4 ? kBatches * kScaleRows * kBatchBytes : 0;
     static constexpr int kScaleBox = TN % 64 ? 32 : 64;      // rows of one TMA copy of x's scales
+    // results on their way to 16-byte stores: 32 rows x 128 columns of 16 bits for each half of the epilogue's warps
+    static constexpr bool kWide = TN > 32;
+    static constexpr uint32_t kOut = kWide ? 2 * 32 * 256 : 0;
     static constexpr uint32_t kMeta = kProdMaxGroups * 12 + 16 + 512;  // group tables, barriers
-    static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales) / kStage);
+    static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales - kOut) / kStage);
     static constexpr int kStages = kRoom < 10 ? kRoom : 10;
-    static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kMeta;
+    static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kOut + kMeta;
     static constexpr int kThreads = kFp4 ? 640 : 320;
     // tensor memory: two accumulators, then two buffers of scales (16 columns for
     // the weights, kBCols for each of the four MMAs of a stage for x)
@@ -402,6 +407,90 @@ __device__ __forceinline__ void prod_store(const ProdArgs &a, const ProdTile &t,
     }
 }
 
+// 16 lanes x 32 columns of tensor memory: with t the lane of the warp, v[4c], v[4c + 1] are columns 8c + 2 (t % 4) and the
+// next of lane t / 4, v[4c + 2], v[4c + 3] those of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t v[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t rounded2(float a, float b) {
+    const T lo = rounded<T>(a), hi = rounded<T>(b);
+    return (uint32_t)*reinterpret_cast<const uint16_t *>(&lo) | (uint32_t)*reinterpret_cast<const uint16_t *>(&hi) << 16;
+}
+
+// The same for 16-bit results in rows that take 16-byte stores, all 128 columns of the tile inside the matrix: 32 rows at
+// a time are transposed through shared memory, so that a row leaves as 256 adjacent bytes instead of 64 from each warp
+// (4096 x 8192 x 2048 NVFP4: 51 -> 43 us). `stage`: 8 KB of this half of the warps.
+template <bool FP4, int TN, typename T>
+__device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, TN> &sc,
+                                                uint32_t tbase, int n0, int half, bool ok, unsigned char *stage) {
+    const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
+    const uint32_t to = smem_u32(stage);
+    // this thread's four columns of a fragment: 16 l + 8 h + lane / 4 of the warp's 32
+    float col[4], bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        col[i] = FP4 ? __shfl_sync(0xFFFFFFFFu, sc.col, 8 * i + (lane >> 2)) : 1.f;
+        bias[i] = __shfl_sync(0xFFFFFFFFu, sc.bias, 8 * i + (lane >> 2));
+    }
+    // 16-byte pieces of a row are swapped by the row's low bits, against bank conflicts
+    const int mj = lane >> 3, mi = lane & 7;                 // the matrix and row that this lane addresses for stmatrix
+#pragma unroll
+    for (int j = 0; j < TN / 32; ++j) {
+        if (32 * j >= t.rows) break;
+        if ((j & 1) != half) continue;
+        uint32_t v[2][16];
+        tmem_ld_16x32(tbase + 32 * j, v[0]);
+        tmem_ld_16x32(tbase + (16u << 16) + 32 * j, v[1]);
+        tmem_ld_wait();
+        named_bar(2 + half, 128);                            // the rows before have left the stage
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+            float rs[4] = {1.f, 1.f, 1.f, 1.f};
+            if constexpr (FP4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    rs[i] = __shfl_sync(0xFFFFFFFFu, sc.row[j], 8 * (c + (i >> 1)) + 2 * (lane & 3) + (i & 1));
+            }
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                uint32_t m[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                // matrix (c + i / 2, h = i % 2)
+                    const int at = 4 * (c + (i >> 1)) + 2 * (i & 1), k = 2 * l + (i & 1);
+                    float lo = __uint_as_float(v[l][at]), hi = __uint_as_float(v[l][at + 1]);
+                    if constexpr (FP4) {
+                        lo *= col[k] * rs[2 * (i >> 1)];
+                        hi *= col[k] * rs[2 * (i >> 1) + 1];
+                    }
+                    const float none = __int_as_float(0x7FFFFFFF);
+                    m[i] = ok ? rounded2<T>(lo + bias[k], hi + bias[k]) : rounded2<T>(none, none);
+                }
+                const int row = 8 * (c + (mj >> 1)) + mi, piece = 4 * q + 2 * l + (mj & 1);
+                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 to + row * 256 + ((piece ^ (row & 7)) << 4)),
+                             "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
+                             : "memory");
+            }
+        }
+        named_bar(2 + half, 128);
+        const int left = t.rows - 32 * j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * q + 2 * i + (lane >> 4), piece = lane & 15;
+            const uint4 o = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((piece ^ (row & 7)) << 4));
+            if (row < left)
+                *reinterpret_cast<uint4 *>((T *)a.y + (int64_t)(t.row0 + 32 * j + row) * a.y_ld + n0 + 8 * piece) = o;
+        }
+    }
+}
+
 template <int KIND, int TN, int CG>
 __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -413,10 +502,11 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     const uint32_t base_u32 = smem_u32(smem_raw);
     unsigned char *smem = smem_raw + (((base_u32 + 1023u) & ~1023u) - base_u32);
     unsigned char *scales = smem + NS * S::kStage;
-    unsigned char *meta = scales + S::kScales;
+    unsigned char *staged = scales + S::kScales;
+    unsigned char *meta = staged + S::kOut;
     uint64_t *full = reinterpret_cast<uint64_t *>(meta), *empty = full + NS;
     uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 2;
-    uint64_t *lfull = sempty + 2, *lempty = lfull + 2, *done = lempty + 2;
+    uint64_t *lfull = sempty + 2, *lempty = lfull + 4, *done = lempty + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     ProdGroups gr;
@@ -437,7 +527,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             mbar_init(&sfull[b], 4 * CG);
             mbar_init(&sempty[b], 1);
         }
-        for (int b = 0; b < S::kQuads; ++b) {
+        for (int b = 0; b < S::kBatches; ++b) {
             mbar_init(&lfull[b], a.s_copy >= 16 ? 1 : 64);
             mbar_init(&lempty[b], 8);
         }
@@ -547,12 +637,18 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         for (; walk.tile < ntiles; walk.tile += step, ++lt) {
             const ProdTile t = walk.at(gr, nw);
             const int b = lt & 1;
-            const int n = (t.w * CG + rank) * kProdRows + q * 32 + lane;
+            const int n0 = (t.w * CG + rank) * kProdRows, n = n0 + q * 32 + lane;
             const ProdScales<S::kFp4, TN> sc(a, t, n);
             const bool ok = warp_wait(&tfull[b], (lt >> 1) & 1, err, abort_flag);
             tc_fence_after();
             const uint32_t at = ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
-            if (a.y_type == MOE_T_BF16)
+            unsigned char *stage = staged + half * 8192;
+            const bool wide = S::kWide && a.wide && n0 + kProdRows <= a.N;
+            if (wide && a.y_type == MOE_T_BF16)
+                prod_store_wide<S::kFp4, TN, __nv_bfloat16>(a, t, sc, at, n0, half, ok, stage);
+            else if (wide)
+                prod_store_wide<S::kFp4, TN, __half>(a, t, sc, at, n0, half, ok, stage);
+            else if (a.y_type == MOE_T_BF16)
                 prod_store<S::kFp4, TN, __nv_bfloat16>(a, t, sc, at, n, half, !ok);
             else if (a.y_type == MOE_T_F16)
                 prod_store<S::kFp4, TN, __half>(a, t, sc, at, n, half, !ok);
@@ -562,11 +658,11 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             warp_arrive<CG>(&tempty[b]);
         }
     } else if constexpr (S::kFp4) {
-        constexpr int QB = S::kQuadBytes, SB = QB / 4, NQ = S::kQuads, kSlot = S::kScaleRows * QB;
-        const int nquad = (nst + 3) / 4;
-        // 16-byte pieces of a row lie in the order of TMA's 64-byte (32-byte) swizzle: rows read together are then on
+        constexpr int QB = S::kBatchBytes, G = S::kBatch, SB = QB / G, NQ = S::kBatches, kSlot = S::kScaleRows * QB;
+        const int nbatch = (nst + G - 1) / G;
+        // the 16-byte halves of 32-byte rows lie in the order of TMA's 32-byte swizzle: rows read together are then on
         // different banks
-        auto swizzled = [](int row, int off) { return off ^ (QB == 64 ? ((row >> 1) & 3) << 4 : ((row >> 2) & 1) << 4); };
+        auto swizzled = [](int row, int off) { return QB == 32 ? off ^ ((row >> 2) & 1) << 4 : off; };
         if (warp < 18) {
             // ------------------------- scales to tensor memory --------------------------
             // (two groups of four warps, one for each buffer in tensor memory)
@@ -575,13 +671,13 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             bool ok = true;
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
-                for (int kb = 0; kb < nst && ok; kb += 4, ++qr) {
+                for (int kb = 0; kb < nst && ok; kb += G, ++qr) {
                   if (!warp_wait(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
                       ok = false;
                       break;
                   }
                   const unsigned char *ring = scales + (qr % NQ) * kSlot;
-                  const int parts = min(4, nst - kb);
+                  const int parts = min(G, nst - kb);
                   for (int part = 0; part < parts; ++part, ++it) {
                     if ((it & 1) != group) continue;
                     uint32_t va[16], vb[4 * S::kBCols];
@@ -636,7 +732,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                     const ProdTile p = walk.at(gr, nw);
                     const int wrow = p.g * a.N + (p.w * CG + rank) * kProdRows;
                     const int loads = (p.rows + S::kScaleBox - 1) / S::kScaleBox;
-                    for (int i = 0; i < nquad; ++i, ++qr) {
+                    for (int i = 0; i < nbatch; ++i, ++qr) {
                         uint64_t *bar = &lfull[qr % NQ];
                         if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                             ok = false;
@@ -659,7 +755,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             const uint32_t ring = smem_u32(scales);
             const int64_t wrows = (int64_t)a.groups * a.N;
             const int copy = a.s_copy;
-            const int shift = 31 - __clz(QB / copy);  // log2 of the pieces of a row and quad of stages
+            const int shift = 31 - __clz(QB / copy);  // log2 of the pieces of a row
             int qr = 0;
             bool ok = true;
             ProdWalk<TN> walk(first);
@@ -667,7 +763,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                 const ProdTile p = walk.at(gr, nw);
                 const int64_t wrow = (int64_t)p.g * a.N + (int64_t)(p.w * CG + rank) * kProdRows;
                 const int rows = kProdRows + (p.rows + 31) / 32 * 32;
-                for (int i = 0; i < nquad; ++i, ++qr) {
+                for (int i = 0; i < nbatch; ++i, ++qr) {
                     if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
@@ -723,7 +819,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
 // Host: 2-D map of rows of `row_bytes`, `pitch` bytes apart, in boxes of 128 bytes x box_rows with the 128-byte swizzle.
 bool make_tmap_rows(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t row_bytes, uint64_t pitch,
                     uint32_t box_rows, bool two_byte);
-// The same of bytes, in boxes of box_bytes (64 or 32) with the swizzle of that width, rows without gaps.
+// The same of bytes, in boxes of box_bytes (32, with the swizzle of that width, or 16), rows without gaps.
 bool make_tmap_scales(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes,
                       uint32_t box_rows);
 int device_sms();
@@ -739,6 +835,7 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     if (e != cudaSuccess) return e;
     ProdArgs a = a0;
     a.hold = products_held();
+    a.wide = a.y_type != MOE_T_F32 && (uintptr_t)a.y % 16 == 0 && (a.M == 1 || a.y_ld % 8 == 0);
     const uint64_t row = KIND == PROD_16 ? (uint64_t)a.K * 2 : (uint64_t)a.K / 2;
     CUtensorMap tw, tx;
     if (!make_tmap_rows(&tw, w, (uint64_t)a.groups * a.N, row, row, kProdRows, KIND == PROD_16) ||
@@ -748,8 +845,8 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     if constexpr (S::kFp4) {
         const uint64_t srow = a.K / (KIND == PROD_NVFP4 ? 16 : 32);
         if (a.s_copy >= 16 &&
-            (!make_tmap_scales(&tws, a.ws, (uint64_t)a.groups * a.N, srow, S::kQuadBytes, kProdRows) ||
-             !make_tmap_scales(&txs, a.xs, a.M, srow, S::kQuadBytes, S::kScaleBox)))
+            (!make_tmap_scales(&tws, a.ws, (uint64_t)a.groups * a.N, srow, S::kBatchBytes, kProdRows) ||
+             !make_tmap_scales(&txs, a.xs, a.M, srow, S::kBatchBytes, S::kScaleBox)))
             return cudaErrorInvalidValue;
     }
     const int64_t nw = (a.N + CG * kProdRows - 1) / (CG * kProdRows);
