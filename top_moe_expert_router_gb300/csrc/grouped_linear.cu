@@ -1,6 +1,8 @@
 // grouped_linear.cu — y[r] = W[e(r)] x[r] + b[e(r)] for rows grouped by expert,
 // operands in bf16 or f16 (the kernel: products.cuh), and what the products
 // share on the host.
+#include <stdio.h>
+#include <stdlib.h>
 #include "products.cuh"
 
 namespace moe {
@@ -61,11 +63,15 @@ int device_sms() {
 }
 
 cudaError_t launch_grouped_linear(const ProdArgs &a, const void *x, int64_t x_ld, const void *w, cudaStream_t st) {
-    const int per = a.M / (a.groups < a.M ? a.groups : a.M);     // rows of a group, all of them used
-    if (a.M <= 32 || per <= 16) return launch_product<PROD_16, 32>(a, x, 2 * x_ld, w, st);
-    if (per <= 64) return launch_product<PROD_16, 128>(a, x, 2 * x_ld, w, st);
-    if (a.N <= 128) return launch_product<PROD_16, 256>(a, x, 2 * x_ld, w, st);
-    return launch_product<PROD_16, 256, 2>(a, x, 2 * x_ld, w, st);
+    static const char *env = getenv("MOE_PLAN");
+    int tn = 0, ks = 1, per = a.M / (a.groups < a.M ? a.groups : a.M);
+    if (env) sscanf(env, "%d,%d", &tn, &ks);
+    if (!tn) tn = a.M <= 32 || per <= 16 ? 32 : per <= 64 ? 128 : a.N <= 128 ? 128 : 256;
+    if (tn == 32) return launch_product<PROD_16, 32>(a, x, 2 * x_ld, w, ks, st);
+    if (tn == 64) return launch_product<PROD_16, 64>(a, x, 2 * x_ld, w, ks, st);
+    if (tn == 128) return launch_product<PROD_16, 128>(a, x, 2 * x_ld, w, ks, st);
+    if (tn == 129) return launch_product<PROD_16, 128, 2>(a, x, 2 * x_ld, w, ks, st);
+    return launch_product<PROD_16, 256, 2>(a, x, 2 * x_ld, w, ks, st);
 }
 
 }  // namespace moe

@@ -143,6 +143,7 @@ struct ProdArgs {
     void *y;                 // [M, N]
     int64_t y_ld;
     moe_dtype y_type;
+    int ks;                  // parts of K, each a CTA of a cluster (set by the launcher)
     bool wide;               // y takes 16-byte stores (set by the launcher)
     int s_copy;              // bytes that the scales' alignment lets one copy take (set by the launcher)
     int hold;                // test hook (set by the launcher)

@@ -69,19 +69,27 @@ struct ProdShape {
     // results on their way to 16-byte stores: 32 rows x 128 columns of 16 bits for each half of the epilogue's warps
     static constexpr bool kWide = TN > 32;
     static constexpr uint32_t kOut = kWide ? 2 * 32 * 256 : 0;
-    static constexpr uint32_t kMeta = kProdMaxGroups * 12 + 16 + 512;  // group tables, barriers
-    static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales - kOut) / kStage);
+    // K may be split over a cluster of up to 8 CTAs: the sums that the others bring for this CTA's share of the columns
+    static constexpr bool kSplit = CG == 1 && TN <= 64;
+    static constexpr uint32_t kParts = kSplit ? 480 * TN : 0;    // (ks - 1) TN 4 ceil(32 / ks) floats at most
+    static constexpr uint32_t kMeta = kProdMaxGroups * 16 + 16 + 768;  // group tables, barriers, scratch
+    static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales - kOut - kParts) / kStage);
     static constexpr int kStages = kRoom < 10 ? kRoom : 10;
-    static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kOut + kMeta;
+    static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kOut + kParts + kMeta;
     static constexpr int kThreads = kFp4 ? 640 : 320;
-    // tensor memory: two accumulators, then two buffers of scales (16 columns for
+    // tensor memory: two accumulators, then two or four buffers of scales (16 columns for
     // the weights, kBCols for each of the four MMAs of a stage for x)
     static constexpr int kBCols = TN > 128 ? 8 : 4;
     static constexpr uint32_t kScaleCols = 16 + 4 * kBCols;
     static constexpr uint32_t kScaleAt = 2 * TN;
-    static_assert(!kFp4 || kScaleAt + 2 * kScaleCols <= kTmemCols, "tensor memory");
+    static constexpr int kScaleBufs = kScaleAt + 4 * kScaleCols <= kTmemCols ? 4 : 2;
+    static_assert(!kFp4 || kScaleAt + kScaleBufs * kScaleCols <= kTmemCols, "tensor memory");
     static_assert(2 * TN <= (int)kTmemCols, "tensor memory");
 };
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *tm) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
 
 // One lane of a warp whose 32 lanes are here. The roles that issue TMA copies and
 // MMAs run as whole warps, with the instructions predicated on that lane: their
@@ -226,10 +234,7 @@ __device__ __forceinline__ void prod_tmem_free(uint32_t at) {
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(kTmemCols) : "memory");
 }
 
-// A bounded wait of a whole warp, with one answer for its lanes: false once the limit has passed or another warp of the
-// CTA gave up.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *err, volatile int *abort) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+__device__ __forceinline__ bool warp_wait_loop(uint64_t *bar, uint32_t parity, uint32_t *err, volatile int *abort) {
     const unsigned long long t0 = global_ns();
     for (uint32_t it = 1;; ++it) {
         if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
@@ -242,6 +247,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32
             if (__any_sync(0xFFFFFFFFu, late || *abort)) return false;
         }
     }
+}
+
+static __device__ __noinline__ bool warp_wait_called(uint64_t *bar, uint32_t parity, uint32_t *err, volatile int *abort) {
+    return warp_wait_loop(bar, parity, err, abort);
+}
+
+// A bounded wait of a whole warp, with one answer for its lanes: false once the limit has passed or another warp of the
+// CTA gave up. (CALL: what a wait that is not over at once runs is a function. With two waits a stage, as with 4-bit
+// operands, that is faster: 4096 x 8192 x 8192 NVFP4 105 -> 100 us; with one it is slower: a stage of 16 bits and 32
+// rows 111 -> 142 ns.)
+template <bool CALL = true>
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *err, volatile int *abort) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    return CALL ? warp_wait_called(bar, parity, err, abort) : warp_wait_loop(bar, parity, err, abort);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) {
@@ -265,10 +284,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The groups as the tiles need them, in shared memory.
+// The groups that have rows, as the tiles need them, in shared memory.
 struct ProdGroups {
-    int32_t *start;          // [groups + 1] first tile of each group
-    int32_t *row0, *rows;    // [groups]
+    int32_t *start;          // [n + 1] first tile of each
+    int32_t *row0;           // [n]
+    int32_t *rows, *group;   // [n]
+    int n;
 };
 
 struct ProdTile {
@@ -278,55 +299,83 @@ struct ProdTile {
 // Walks a CTA's tiles in order.
 template <int TN>
 struct ProdWalk {
-    int tile, g;
-    __device__ __forceinline__ explicit ProdWalk(int first) : tile(first), g(0) {}
+    int tile, i;             // i: of the groups with rows
+    __device__ __forceinline__ explicit ProdWalk(int first) : tile(first), i(0) {}
     __device__ __forceinline__ ProdTile at(const ProdGroups &gr, int nw) {
-        while (gr.start[g + 1] <= tile) ++g;
-        const int local = tile - gr.start[g], rows = gr.rows[g], nt = (rows + TN - 1) / TN;
+        if (gr.start[i + 1] <= tile) {           // the last group that starts at or before the tile
+            int lo = i + 1, hi = gr.n;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (gr.start[mid] <= tile)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            i = lo;
+        }
+        const int local = tile - gr.start[i], rows = gr.rows[i], nt = (rows + TN - 1) / TN;
         const int band = local / (kProdBand * nt), r = local - band * (kProdBand * nt);
         const int bw = min(kProdBand, nw - band * kProdBand), t = r / bw;
         ProdTile p;
-        p.g = g;
+        p.g = gr.group[i];
         p.w = band * kProdBand + r - t * bw;
-        p.row0 = gr.row0[g] + t * TN;
+        p.row0 = gr.row0[i] + t * TN;
         p.rows = min(TN, rows - t * TN);
         return p;
     }
 };
 
-// Fills the tables; every thread of the CTA. -> the number of tiles
+// Fills the tables; every thread of the CTA, one or two groups each. -> the number of tiles
 template <int TN>
-__device__ __forceinline__ int prod_groups(const ProdArgs &a, const ProdGroups &gr, int nw) {
-    for (int g = threadIdx.x; g < a.groups; g += blockDim.x) {
-        // whatever the offsets hold, no row outside [0, M) is touched
-        int lo = 0, hi = a.M;
-        if (a.offsets) {
-            lo = min(max(a.offsets[g], 0), a.M);
-            hi = min(max(a.offsets[g + 1], lo), a.M);
-        }
-        gr.row0[g] = lo;
-        gr.rows[g] = hi - lo;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int per = (a.groups + 31) / 32, g0 = min(a.groups, (int)threadIdx.x * per), g1 = min(a.groups, g0 + per);
-        int sum = 0;
-        for (int g = g0; g < g1; ++g) sum += (gr.rows[g] + TN - 1) / TN * nw;
-        int end = sum;
+__device__ __forceinline__ int prod_groups(const ProdArgs &a, ProdGroups &gr, int nw, int32_t *scratch) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    int lo[2], rows[2], tiles[2], sum = 0, used = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, end, o);
-            if ((int)threadIdx.x >= o) end += v;
+    for (int j = 0; j < 2; ++j) {
+        const int g = 2 * t + j;
+        lo[j] = rows[j] = 0;
+        if (g < a.groups) {
+            // whatever the offsets hold, no row outside [0, M) is touched
+            int hi = a.M;
+            if (a.offsets) {
+                lo[j] = min(max(a.offsets[g], 0), a.M);
+                hi = min(max(a.offsets[g + 1], lo[j]), a.M);
+            }
+            rows[j] = hi - lo[j];
         }
-        int at = end - sum;
-        for (int g = g0; g < g1; ++g) {
-            gr.start[g] = at;
-            at += (gr.rows[g] + TN - 1) / TN * nw;
-        }
-        if (threadIdx.x == 31) gr.start[a.groups] = end;
+        tiles[j] = (rows[j] + TN - 1) / TN * nw;
+        sum += tiles[j];
+        used += rows[j] > 0;
     }
+    int end = sum, last = used;                  // inclusive sums over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, end, o), u = __shfl_up_sync(0xFFFFFFFFu, last, o);
+        if (lane >= o) end += v, last += u;
+    }
+    if (lane == 31) scratch[2 * warp] = end, scratch[2 * warp + 1] = last;
     __syncthreads();
-    return gr.start[a.groups];
+    int all = 0, n = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        if (w == warp) end += all, last += n;
+        all += scratch[2 * w];
+        n += scratch[2 * w + 1];
+    }
+    int at = end - sum, i = last - used;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (rows[j] > 0) {
+            gr.start[i] = at;
+            gr.row0[i] = lo[j];
+            gr.rows[i] = rows[j];
+            gr.group[i] = 2 * t + j;
+            at += tiles[j];
+            ++i;
+        }
+    if (t == 0) gr.start[n] = all;
+    gr.n = n;
+    __syncthreads();
+    return all;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t v[32]) {
@@ -491,6 +540,101 @@ __device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTil
     }
 }
 
+// The address of this CTA's shared word in the CTA of the given rank.
+__device__ __forceinline__ uint32_t in_rank(const void *p, int rank) {
+    uint32_t o;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(o) : "r"(smem_u32(p)), "r"(rank));
+    return o;
+}
+
+// One arrival of the warp at the barriers of all other CTAs of the cluster, behind what its lanes wrote there.
+__device__ __forceinline__ void arrive_at_others(uint64_t *bar, int ks, int part) {
+    __syncwarp();
+    const int r = threadIdx.x & 31;
+    if (r < ks && r != part)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_rank(bar, r)) : "memory");
+}
+
+// K split over the ks CTAs of a cluster: each owns a share of the tile's 128 columns, four or a multiple. The sums go to
+// the owners, through distributed shared memory (parts[sender][row][column of the share]), which add them in the order of
+// their ranks and store.
+template <bool FP4, int TN>
+__device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, TN> &sc,
+                                                 uint32_t tbase, int n, int half, bool ok, float *parts, int part,
+                                                 uint64_t *pfull, uint64_t *pempty, int phase, uint32_t *err,
+                                                 volatile int *abort_flag) {
+    const int ks = a.ks, lane = threadIdx.x & 31;
+    const int local = ((threadIdx.x >> 5) & 3) * 32 + lane, share = (32 + ks - 1) / ks * 4;
+    const int owner = ((local / 4 + 1) * ks - 1) / 32, col = local - 32 * owner / ks * 4;
+    static_assert(TN <= 64, "each half of the warps has one chunk of 32 rows");
+    const bool busy = 32 * half < t.rows;        // this half of the warps has rows
+    const int rows = min(32, t.rows - 32 * half);
+    uint32_t v[32];
+    if (busy) {
+        tmem_ld32(tbase + 32 * half, v);
+        tmem_ld_wait();
+    }
+    if (!ok) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0x7FFFFFFFu;
+    }
+    warp_wait(pempty, phase ^ 1, err, abort_flag);           // the owners have read the tile before
+    if (busy && owner != part) {
+        const uint32_t to = in_rank(parts, owner) +
+                            (uint32_t)((((part < owner ? part : part - 1) * TN + 32 * half) * share + col) * 4);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < rows) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + i * share * 4), "r"(v[i]) : "memory");
+    }
+    arrive_at_others(pfull, ks, part);
+    const bool all = warp_wait(pfull, phase, err, abort_flag);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    const bool mine = busy && owner == part;
+    if (mine) {
+        const float *from = parts + 32 * half * share + col;
+        float sum[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+#pragma unroll 1
+        for (int r = 0; r < ks; ++r) {
+            if (r == part) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < rows) sum[i] += from[i * share];
+                from += TN * share;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = all ? __float_as_uint(sum[i]) : 0x7FFFFFFFu;
+    }
+    arrive_at_others(pempty, ks, part);
+    if (!busy) return;
+    if constexpr (FP4) {
+        const float row = half ? sc.row[TN / 32 - 1] : sc.row[0];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(__uint_as_float(v[i]) * (sc.col * __shfl_sync(0xFFFFFFFFu, row, i)));
+    }
+    if (!mine || n >= a.N) return;
+    int64_t at = (int64_t)(t.row0 + 32 * half) * a.y_ld + n;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (i < rows) {
+            const float o = __uint_as_float(v[i]) + sc.bias;
+            if (a.y_type == MOE_T_BF16)
+                ((__nv_bfloat16 *)a.y)[at] = rounded<__nv_bfloat16>(o);
+            else if (a.y_type == MOE_T_F16)
+                ((__half *)a.y)[at] = rounded<__half>(o);
+            else
+                ((float *)a.y)[at] = o;
+        }
+        at += a.y_ld;
+    }
+}
+
 template <int KIND, int TN, int CG>
 __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -503,16 +647,20 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     unsigned char *smem = smem_raw + (((base_u32 + 1023u) & ~1023u) - base_u32);
     unsigned char *scales = smem + NS * S::kStage;
     unsigned char *staged = scales + S::kScales;
-    unsigned char *meta = staged + S::kOut;
+    float *parts = reinterpret_cast<float *>(staged + S::kOut);
+    unsigned char *meta = staged + S::kOut + S::kParts;
     uint64_t *full = reinterpret_cast<uint64_t *>(meta), *empty = full + NS;
-    uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 2;
-    uint64_t *lfull = sempty + 2, *lempty = lfull + 4, *done = lempty + 4;
+    uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 4;
+    uint64_t *lfull = sempty + 4, *lempty = lfull + 4, *pfull = lempty + 4, *pempty = pfull + 1, *done = pempty + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     ProdGroups gr;
-    gr.start = reinterpret_cast<int32_t *>(meta + 512);
+    int32_t *scratch = reinterpret_cast<int32_t *>(meta + 512);
+    gr.start = scratch + 64;
     gr.row0 = gr.start + kProdMaxGroups + 1;
     gr.rows = gr.row0 + kProdMaxGroups;
+    gr.group = gr.rows + kProdMaxGroups;
+    static_assert(kProdMaxGroups <= 2 * S::kThreads, "two groups a thread");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t *err = &prod_err;
@@ -524,6 +672,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 8 * CG);
+        }
+        for (int b = 0; b < S::kScaleBufs; ++b) {
             mbar_init(&sfull[b], 4 * CG);
             mbar_init(&sempty[b], 1);
         }
@@ -531,21 +681,38 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             mbar_init(&lfull[b], a.s_copy >= 16 ? 1 : 64);
             mbar_init(&lempty[b], 8);
         }
+        if (S::kSplit && a.ks > 1) {
+            mbar_init(pfull, 8 * (a.ks - 1));
+            mbar_init(pempty, 8 * (a.ks - 1));
+        }
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) prod_tmem_alloc<CG>(tmem_slot);
+    if (threadIdx.x == 32 * 2) {
+        prefetch_map(&tmW);
+        prefetch_map(&tmX);
+        if (S::kFp4 && a.s_copy >= 16) {
+            prefetch_map(&tmWS);
+            prefetch_map(&tmXS);
+        }
+    }
     pdl_wait();                                  // what earlier kernels write is read from here on
-    // this CTA's rank in its pair; a pair walks the tiles as one
-    const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1), first = (int)blockIdx.x / CG, step = (int)gridDim.x / CG;
+    // the CTAs of a cluster walk the tiles together: a pair as one, or each with its part of K
+    const int ks = S::kSplit ? a.ks : 1, part = S::kSplit ? (int)blockIdx.x % ks : 0;
+    const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1), first = (int)blockIdx.x / (CG * ks), step = (int)gridDim.x / (CG * ks);
     const int nw = (a.N + CG * kProdRows - 1) / (CG * kProdRows);
     tc_fence_before();
-    const int ntiles = prod_groups<TN>(a, gr, nw);
-    if constexpr (CG == 2) cluster_sync_all();   // the barriers of both are ready
+    const int ntiles = prod_groups<TN>(a, gr, nw, scratch);
+    if (CG == 2 || ks > 1) cluster_sync_all();   // the barriers of all are ready
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int nst = (a.K + kStageK - 1) / kStageK;
+    constexpr int NB = S::kScaleBufs;
+    // this CTA's stages, whole batches of scales
+    const int nbt = (nst + S::kBatch - 1) / S::kBatch;
+    const int kb0 = ks == 1 ? 0 : nbt * part / ks * S::kBatch, kb1 = ks == 1 ? nst : min(nst, nbt * (part + 1) / ks * S::kBatch);
     const uint32_t tiles = smem_u32(smem);
 
     if (warp == 0) {
@@ -560,7 +727,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                 const int wrow = t.g * a.N + (t.w * CG + rank) * kProdRows;
                 const int share = CG == 1 ? t.rows : (t.rows + S::kStep - 1) / S::kStep * 16, row0 = t.row0 + rank * share;
                 const int loads = (share + S::kBox - 1) / S::kBox;
-                for (int kb = 0; kb < nst; ++kb, ++it) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int slot = it % NS;
                     if (!warp_wait(&empty[slot], ((it / NS) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
@@ -583,7 +750,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         if (rank == 0) {
         // -------------------------------- MMA issuer --------------------------------
         const uint32_t on = elect_lane();
-        int it = 0, lt = 0;
+        int lt = 0, slot = 0, sb = 0;
+        uint32_t phase = 0, sphase = 0;                  // of the ring's and the scales' barriers
         bool ok = true;
         ProdWalk<TN> walk(first);
         for (; walk.tile < ntiles && ok; walk.tile += step, ++lt) {
@@ -598,31 +766,39 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             if (!warp_wait(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
             tc_fence_after();
             const uint32_t d = (uint32_t)(b * TN);       // (all columns are this CTA's: they begin at 0)
-            for (int kb = 0; kb < nst; ++kb, ++it) {
-                const int slot = it % NS;
-                if (!warp_wait(&full[slot], (it / NS) & 1, err, abort_flag) ||
-                    (S::kFp4 && !warp_wait(&sfull[it & 1], (it >> 1) & 1, err, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            uint32_t acc = 0u;
+            auto stage = [&](int n) {                    // the n MMAs of a stage; n is a constant where it is 4
                 const uint32_t sa = tiles + slot * S::kStage;
                 const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + kProdABytes);
-                const int left = a.K - kb * kStageK;
-                const uint32_t sc = S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
+                const uint32_t sc = S::kScaleAt + (uint32_t)sb * S::kScaleCols;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    if (kk * kMmaK >= left) break;       // the last stage may be shorter
+                    if (kk >= n) break;
                     const uint64_t o = (uint64_t)(2 * kk);
-                    const uint32_t acc = kk ? 1u : (uint32_t)(kb != 0);
                     if constexpr (S::kFp4)
                         mma_fp4<KIND, CG>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, acc, on);
                     else
                         mma_16<CG>(d, ad + o, bd + o, idesc, acc, on);
+                    acc = 1u;
                 }
-                commit_on<CG>(&empty[slot], on);             // free once these MMAs have read it
-                if (S::kFp4) commit_on<CG>(&sempty[it & 1], on);
+                commit_on<CG>(&empty[slot], on);         // free once these MMAs have read it
+                if (S::kFp4) commit_on<CG>(&sempty[sb], on);
+                if (++slot == NS) slot = 0, phase ^= 1u;
+                if (++sb == NB) sb = 0, sphase ^= 1u;
+            };
+            auto wait = [&]() {
+                ok = warp_wait<S::kFp4>(&full[slot], phase, err, abort_flag);
+                if (S::kFp4 && ok) ok = warp_wait(&sfull[sb], sphase, err, abort_flag);
+                tc_fence_after();
+                return ok;
+            };
+            // (the last stage may be shorter)
+            const int whole = min(kb1, a.K / kStageK);
+            for (int kb = kb0; kb < whole; ++kb) {
+                if (!wait()) break;
+                stage(4);
             }
+            if (ok && whole < kb1 && wait()) stage((a.K - whole * kStageK + kMmaK - 1) / kMmaK);
             if (!ok) break;
             commit_on<CG>(&tfull[b], on);
         }
@@ -644,7 +820,16 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             const uint32_t at = ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
             unsigned char *stage = staged + half * 8192;
             const bool wide = S::kWide && a.wide && n0 + kProdRows <= a.N;
-            if (wide && a.y_type == MOE_T_BF16)
+            bool stored = false;
+            if constexpr (S::kSplit) {
+                if (ks > 1) {
+                    prod_store_split<S::kFp4, TN>(a, t, sc, at, n, half, ok, parts, part, pfull, pempty, lt & 1, err, abort_flag);
+                    stored = true;
+                }
+            }
+            if (stored)
+                ;
+            else if (wide && a.y_type == MOE_T_BF16)
                 prod_store_wide<S::kFp4, TN, __nv_bfloat16>(a, t, sc, at, n0, half, ok, stage);
             else if (wide)
                 prod_store_wide<S::kFp4, TN, __half>(a, t, sc, at, n0, half, ok, stage);
@@ -659,30 +844,30 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         }
     } else if constexpr (S::kFp4) {
         constexpr int QB = S::kBatchBytes, G = S::kBatch, SB = QB / G, NQ = S::kBatches, kSlot = S::kScaleRows * QB;
-        const int nbatch = (nst + G - 1) / G;
+        const int b0 = kb0 / G, b1 = (kb1 + G - 1) / G;
         // the 16-byte halves of 32-byte rows lie in the order of TMA's 32-byte swizzle: rows read together are then on
         // different banks
         auto swizzled = [](int row, int off) { return QB == 32 ? off ^ ((row >> 2) & 1) << 4 : off; };
         if (warp < 18) {
             // ------------------------- scales to tensor memory --------------------------
-            // (two groups of four warps, one for each buffer in tensor memory)
+            // (two groups of four warps, for alternate stages)
             const int q = warp & 3, group = (warp - 10) >> 2;
             int it = 0, qr = 0;
             bool ok = true;
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
-                for (int kb = 0; kb < nst && ok; kb += G, ++qr) {
+                for (int kb = kb0; kb < kb1 && ok; kb += G, ++qr) {
                   if (!warp_wait(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
                       ok = false;
                       break;
                   }
                   const unsigned char *ring = scales + (qr % NQ) * kSlot;
-                  const int parts = min(G, nst - kb);
-                  for (int part = 0; part < parts; ++part, ++it) {
+                  const int n = min(G, kb1 - kb);
+                  for (int i = 0; i < n; ++i, ++it) {
                     if ((it & 1) != group) continue;
                     uint32_t va[16], vb[4 * S::kBCols];
                     auto words = [&](int row, uint32_t w[4]) {
-                        const unsigned char *at = ring + row * QB + swizzled(row, part * SB);
+                        const unsigned char *at = ring + row * QB + swizzled(row, i * SB);
                         if constexpr (KIND == PROD_NVFP4) {
                             const uint4 v = *reinterpret_cast<const uint4 *>(at);
                             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
@@ -705,18 +890,18 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
                     }
-                    if (!warp_wait(&sempty[it & 1], ((it >> 1) & 1) ^ 1, err, abort_flag)) {
+                    if (!warp_wait(&sempty[it % NB], ((it / NB) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t to = ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it & 1) * S::kScaleCols;
+                    const uint32_t to = ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it % NB) * S::kScaleCols;
                     tmem_st16(to, va);
                     tmem_st16(to + 16, vb);
                     if constexpr (S::kBCols == 8) tmem_st16(to + 32, vb + 16);
                     tmem_st_wait();
                     tc_fence_before();
-                    warp_arrive<CG>(&sfull[it & 1]);
+                    warp_arrive<CG>(&sfull[it % NB]);
                   }
                   warp_arrive<1>(&lempty[qr % NQ]);
                 }
@@ -732,7 +917,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                     const ProdTile p = walk.at(gr, nw);
                     const int wrow = p.g * a.N + (p.w * CG + rank) * kProdRows;
                     const int loads = (p.rows + S::kScaleBox - 1) / S::kScaleBox;
-                    for (int i = 0; i < nbatch; ++i, ++qr) {
+                    for (int i = b0; i < b1; ++i, ++qr) {
                         uint64_t *bar = &lfull[qr % NQ];
                         if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                             ok = false;
@@ -763,7 +948,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                 const ProdTile p = walk.at(gr, nw);
                 const int64_t wrow = (int64_t)p.g * a.N + (int64_t)(p.w * CG + rank) * kProdRows;
                 const int rows = kProdRows + (p.rows + 31) / 32 * 32;
-                for (int i = 0; i < nbatch; ++i, ++qr) {
+                for (int i = b0; i < b1; ++i, ++qr) {
                     if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
@@ -802,8 +987,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    // neither CTA of a pair leaves, or frees its tensor memory, while the other may still reach it
-    if constexpr (CG == 2) {
+    // no CTA of a cluster leaves, or frees its tensor memory, while another may still reach it
+    if (CG == 2 || ks > 1) {
         if (rank && warp == 1) mbar_wait(done, 0, err);      // the leader's last arrival here
         __syncwarp();
         cluster_sync_all();
@@ -823,11 +1008,12 @@ bool make_tmap_rows(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t r
 bool make_tmap_scales(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes,
                       uint32_t box_rows);
 int device_sms();
+constexpr int kProdDevices = 64;
 
 #ifdef __CUDACC__
 // x: rows x_pitch bytes apart; w: [groups * N] rows without gaps.
 template <int KIND, int TN, int CG = 1>
-cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, const void *w, cudaStream_t st) {
+cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, const void *w, int ks, cudaStream_t st) {
     using S = ProdShape<KIND, TN, CG>;
     static std::atomic<uint64_t> attr_set{0};
     const auto kern = product_kernel<KIND, TN, CG>;
@@ -835,6 +1021,10 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     if (e != cudaSuccess) return e;
     ProdArgs a = a0;
     a.hold = products_held();
+    // (every part has work)
+    constexpr int kBatchK = (KIND == PROD_16 ? 64 : 256) * S::kBatch;
+    const int most_ks = (a.K + kBatchK - 1) / kBatchK;
+    a.ks = !S::kSplit ? 1 : ks < most_ks ? ks : most_ks;
     a.wide = a.y_type != MOE_T_F32 && (uintptr_t)a.y % 16 == 0 && (a.M == 1 || a.y_ld % 8 == 0);
     const uint64_t row = KIND == PROD_16 ? (uint64_t)a.K * 2 : (uint64_t)a.K / 2;
     CUtensorMap tw, tx;
@@ -852,10 +1042,9 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     const int64_t nw = (a.N + CG * kProdRows - 1) / (CG * kProdRows);
     // a tile of every group may be ragged
     const int64_t most = ((int64_t)a.M / TN + (a.groups < a.M ? a.groups : a.M)) * nw;
-    const int sms = device_sms();
-    if (sms < 1) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(most < sms / CG ? most : sms / CG) * CG);
+    const int width = CG * a.ks;                 // CTAs of a cluster
+    cfg.gridDim = dim3(width * 1024);
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = st;
@@ -863,11 +1052,27 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = width;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 1 ? 1 : 2;
+    cfg.numAttrs = width == 1 ? 1 : 2;
+    // no more clusters than the device holds at once (fewer than the SMs suggest: a cluster's CTAs lie in one group of SMs)
+    static std::atomic<int> known[kProdDevices][9];
+    int dev = 0, n = device_sms();
+    if (n < 1 || cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (width > 1) {
+        n = dev < kProdDevices ? known[dev][width].load(std::memory_order_relaxed) : 0;
+        if (n < 1) {
+            cudaLaunchConfig_t ask = cfg;
+            ask.attrs = attr + 1;
+            ask.numAttrs = 1;
+            if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &ask)) != cudaSuccess) return e;
+            if (n < 1) return cudaErrorInvalidConfiguration;
+            if (dev < kProdDevices) known[dev][width].store(n, std::memory_order_relaxed);
+        }
+    }
+    cfg.gridDim = dim3((unsigned)(most < n ? most : n) * width);
     return cudaLaunchKernelEx(&cfg, kern, tw, tx, tws, txs, a);
 }
 #endif

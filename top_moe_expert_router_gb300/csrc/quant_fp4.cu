@@ -93,6 +93,8 @@ template <bool BF16, bool NVFP4, bool UP, int ROW, int PER, int THREADS>
 __global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Args a) {
     static_assert(ROW == 32 || ROW == THREADS, "a row is a warp's or a CTA's");
     __shared__ uint32_t part[THREADS / 32];
+    // the product that reads the codes may set itself up meanwhile; it waits for the end of this kernel before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     pdl_wait();
     const int tid = threadIdx.x % ROW, units = a.K / 16;
     const int r = blockIdx.x * (THREADS / ROW) + threadIdx.x / ROW;
