@@ -4,8 +4,6 @@
 // formed and summed by the tensor cores (kind::mxf4nvf4: E4M3 scales per 16,
 // kind::mxf4: powers of two per 32), in fp32; the second scales of x and W, and
 // the bias, belong to the epilogue.
-#include <stdio.h>
-#include <stdlib.h>
 #include "products.cuh"
 
 namespace moe {
@@ -15,14 +13,11 @@ cudaError_t linear_fp4_errors(cudaStream_t st, uint32_t *bits) { return prod_tak
 template <int KIND>
 static cudaError_t launch_kind(const ProdArgs &a, const uint8_t *xq, const uint8_t *wq, cudaStream_t st) {
     const int64_t pitch = a.K / 2;
-    static const char *env = getenv("MOE_PLAN");
-    int tn = 0, ks = 1, per = a.M / (a.groups < a.M ? a.groups : a.M);
-    if (env) sscanf(env, "%d,%d", &tn, &ks);
-    if (!tn) tn = a.M <= 32 || per <= 16 ? 32 : a.N <= 128 ? 128 : 192;
-    if (tn == 32) return launch_product<KIND, 32>(a, xq, pitch, wq, ks, st);
-    if (tn == 64) return launch_product<KIND, 64>(a, xq, pitch, wq, ks, st);
-    if (tn == 128) return launch_product<KIND, 128>(a, xq, pitch, wq, ks, st);
-    return launch_product<KIND, 192, 2>(a, xq, pitch, wq, ks, st);
+    const ProdPlan p = plan_product(true, a.groups, a.M, a.N, a.K);
+    if (p.rows == 32) return launch_product<KIND, 32>(a, xq, pitch, wq, p.ks, st);
+    if (p.rows == 64) return launch_product<KIND, 64>(a, xq, pitch, wq, 1, st);
+    if (p.rows == 128) return launch_product<KIND, 128>(a, xq, pitch, wq, 1, st);
+    return launch_product<KIND, 192, 2>(a, xq, pitch, wq, 1, st);
 }
 
 cudaError_t launch_linear_fp4(ProdArgs a, bool nvfp4, const uint8_t *xq, const uint8_t *wq, cudaStream_t st) {

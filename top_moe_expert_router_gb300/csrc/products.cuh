@@ -50,6 +50,8 @@ static inline cudaError_t prod_take_errors(cudaStream_t st, uint32_t *bits) {
     return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
+constexpr int kPartRow = 36;               // floats from one column of partial sums to the next: 32 rows, and 4 against bank conflicts
+
 // CG: CTAs of a tile, 1 or 2 (a pair, 256 weight rows)
 template <int KIND, int TN, int CG>
 struct ProdShape {
@@ -70,8 +72,9 @@ struct ProdShape {
     static constexpr bool kWide = TN > 32;
     static constexpr uint32_t kOut = kWide ? 2 * 32 * 256 : 0;
     // K may be split over a cluster of up to 8 CTAs: the sums that the others bring for this CTA's share of the columns
-    static constexpr bool kSplit = CG == 1 && TN <= 64;
-    static constexpr uint32_t kParts = kSplit ? 480 * TN : 0;    // (ks - 1) TN 4 ceil(32 / ks) floats at most
+    // (two tiles' worth: (ks - 1) 4 ceil(32 / ks) columns at most)
+    static constexpr bool kSplit = CG == 1 && TN == 32;
+    static constexpr uint32_t kParts = kSplit ? 2 * 120 * kPartRow * 4 : 0;
     static constexpr uint32_t kMeta = kProdMaxGroups * 16 + 16 + 768;  // group tables, barriers, scratch
     static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales - kOut - kParts) / kStage);
     static constexpr int kStages = kRoom < 10 ? kRoom : 10;
@@ -182,9 +185,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
         asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_leader(bar)) : "memory");
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 __device__ __forceinline__ void expect_on(uint64_t *bar, uint32_t bytes, uint32_t on) {
@@ -257,7 +262,7 @@ static __device__ __noinline__ bool warp_wait_called(uint64_t *bar, uint32_t par
 // CTA gave up. (CALL: what a wait that is not over at once runs is a function. With two waits a stage, as with 4-bit
 // operands, that is faster: 4096 x 8192 x 8192 NVFP4 105 -> 100 us; with one it is slower: a stage of 16 bits and 32
 // rows 111 -> 142 ns.)
-template <bool CALL = true>
+template <bool CALL>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *err, volatile int *abort) {
     if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
     return CALL ? warp_wait_called(bar, parity, err, abort) : warp_wait_loop(bar, parity, err, abort);
@@ -296,33 +301,37 @@ struct ProdTile {
     int g, w, row0, rows;    // group, weight tile, first row and rows (up to TN)
 };
 
+// The tile of the given number; i: its place among the groups, which only grows.
+template <int TN>
+__device__ __forceinline__ ProdTile prod_tile(const ProdGroups &gr, int nw, int tile, int &i) {
+    if (gr.start[i + 1] <= tile) {               // the last group that starts at or before the tile
+        int lo = i + 1, hi = gr.n;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (gr.start[mid] <= tile)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        i = lo;
+    }
+    const int local = tile - gr.start[i], rows = gr.rows[i], nt = (rows + TN - 1) / TN;
+    const int band = local / (kProdBand * nt), r = local - band * (kProdBand * nt);
+    const int bw = min(kProdBand, nw - band * kProdBand), t = r / bw;
+    ProdTile p;
+    p.g = gr.group[i];
+    p.w = band * kProdBand + r - t * bw;
+    p.row0 = gr.row0[i] + t * TN;
+    p.rows = min(TN, rows - t * TN);
+    return p;
+}
+
 // Walks a CTA's tiles in order.
 template <int TN>
 struct ProdWalk {
     int tile, i;             // i: of the groups with rows
     __device__ __forceinline__ explicit ProdWalk(int first) : tile(first), i(0) {}
-    __device__ __forceinline__ ProdTile at(const ProdGroups &gr, int nw) {
-        if (gr.start[i + 1] <= tile) {           // the last group that starts at or before the tile
-            int lo = i + 1, hi = gr.n;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (gr.start[mid] <= tile)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            i = lo;
-        }
-        const int local = tile - gr.start[i], rows = gr.rows[i], nt = (rows + TN - 1) / TN;
-        const int band = local / (kProdBand * nt), r = local - band * (kProdBand * nt);
-        const int bw = min(kProdBand, nw - band * kProdBand), t = r / bw;
-        ProdTile p;
-        p.g = gr.group[i];
-        p.w = band * kProdBand + r - t * bw;
-        p.row0 = gr.row0[i] + t * TN;
-        p.rows = min(TN, rows - t * TN);
-        return p;
-    }
+    __device__ __forceinline__ ProdTile at(const ProdGroups &gr, int nw) { return prod_tile<TN>(gr, nw, tile, i); }
 };
 
 // Fills the tables; every thread of the CTA, one or two groups each. -> the number of tiles
@@ -398,6 +407,21 @@ __device__ __forceinline__ __half rounded(float v) { return __float2half_rn(v); 
 template <>
 __device__ __forceinline__ float rounded(float v) { return v; }
 
+__device__ __forceinline__ void store_one(void *y, int64_t at, moe_dtype t, float v) {
+    if (t == MOE_T_BF16)
+        ((__nv_bfloat16 *)y)[at] = rounded<__nv_bfloat16>(v);
+    else if (t == MOE_T_F16)
+        ((__half *)y)[at] = rounded<__half>(v);
+    else
+        ((float *)y)[at] = v;
+}
+
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t v[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(taddr));
+}
+
 // What a tile's results are multiplied by and added to, read before they are waited for: this thread's column (scale
 // and bias), and the scales of rows lane, lane + 32, ...
 template <bool FP4, int TN>
@@ -452,6 +476,27 @@ __device__ __forceinline__ void prod_store(const ProdArgs &a, const ProdTile &t,
                 if (i < rows) *y = rounded<T>(failed ? __int_as_float(0x7FFFFFFF) : __uint_as_float(v[i]) + sc.bias);
                 y += a.y_ld;
             }
+        }
+    }
+}
+
+// A tile of up to 32 rows, four at a time in a loop that stays one: with a tile or two for a CTA, what the stores take is
+// the time to fetch their code.
+template <bool FP4>
+__device__ __forceinline__ void prod_store_few(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, 32> &sc, uint32_t tbase,
+                                               int n, bool ok) {
+    int64_t at = (int64_t)t.row0 * a.y_ld + n;
+#pragma unroll 1
+    for (int i = 0; i < t.rows; i += 4) {
+        uint32_t v[4];
+        tmem_ld4(tbase + i, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float y = ok ? __uint_as_float(v[k]) : __int_as_float(0x7FFFFFFF);
+            if constexpr (FP4) y *= sc.col * __shfl_sync(0xFFFFFFFFu, sc.row[0], i + k);
+            if (n < a.N && i + k < t.rows) store_one(a.y, at, a.y_type, y + sc.bias);
+            at += a.y_ld;
         }
     }
 }
@@ -547,91 +592,80 @@ __device__ __forceinline__ uint32_t in_rank(const void *p, int rank) {
     return o;
 }
 
-// One arrival of the warp at the barriers of all other CTAs of the cluster, behind what its lanes wrote there.
-__device__ __forceinline__ void arrive_at_others(uint64_t *bar, int ks, int part) {
-    __syncwarp();
-    const int r = threadIdx.x & 31;
-    if (r < ks && r != part)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_rank(bar, r)) : "memory");
+// Four words into the shared memory of another CTA, counted at a barrier there.
+__device__ __forceinline__ void send4(uint32_t to, const uint32_t v[4], uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+                 : "memory");
 }
 
 // K split over the ks CTAs of a cluster: each owns a share of the tile's 128 columns, four or a multiple. The sums go to
-// the owners, through distributed shared memory (parts[sender][row][column of the share]), which add them in the order of
-// their ranks and store.
+// the owners as asynchronous stores that a barrier there counts (parts[sender][column of the share][row]); the owners add
+// them in the order of their ranks and store. Two such buffers by turns: whoever sends a tile's sums has read, as all
+// warps of the CTA have, those of the tile before, so nobody writes where another still reads.
 template <bool FP4, int TN>
 __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, TN> &sc,
-                                                 uint32_t tbase, int n, int half, bool ok, float *parts, int part,
-                                                 uint64_t *pfull, uint64_t *pempty, int phase, uint32_t *err,
-                                                 volatile int *abort_flag) {
-    const int ks = a.ks, lane = threadIdx.x & 31;
-    const int local = ((threadIdx.x >> 5) & 3) * 32 + lane, share = (32 + ks - 1) / ks * 4;
+                                                 uint32_t tbase, int n, bool ok, float *parts, int part, uint64_t *pfull,
+                                                 int lt, uint32_t *err, volatile int *abort_flag) {
+    static_assert(TN == 32, "one chunk of rows");
+    const int ks = a.ks, lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
+    const int local = q * 32 + lane, share = (32 + ks - 1) / ks * 4;
     const int owner = ((local / 4 + 1) * ks - 1) / 32, col = local - 32 * owner / ks * 4;
-    static_assert(TN <= 64, "each half of the warps has one chunk of 32 rows");
-    const bool busy = 32 * half < t.rows;        // this half of the warps has rows
-    const int rows = min(32, t.rows - 32 * half);
-    uint32_t v[32];
-    if (busy) {
-        tmem_ld32(tbase + 32 * half, v);
+    const int quads = (t.rows + 3) / 4;
+    float *buf = parts + (lt & 1) * (120 * kPartRow);
+    uint64_t *bar = pfull + (lt & 1);
+    named_bar(2, 128);                           // the tile before the last has been read from this buffer
+    if (q == 0 && lane == 0) {
+        const int own = (32 * (part + 1) / ks - 32 * part / ks) * 4;
+        mbar_arrive_expect_tx(bar, (uint32_t)((ks - 1) * own * quads * 16));
+    }
+    // four rows at a time in loops that stay loops: this code runs once or twice in a kernel, and what it takes is the
+    // time to fetch it
+    const uint32_t there = in_rank(buf, owner) + (uint32_t)(((part < owner ? part : part - 1) * share + col) * kPartRow * 4);
+    const uint32_t bar_there = in_rank(bar, owner);
+#pragma unroll 1
+    for (int i = 0; i < quads; ++i) {
+        uint32_t v[4];
+        tmem_ld4(tbase + 4 * i, v);
         tmem_ld_wait();
+        if (!ok) v[0] = v[1] = v[2] = v[3] = 0x7FFFFFFFu;
+        if (owner != part) send4(there + 16 * i, v, bar_there);
     }
-    if (!ok) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0x7FFFFFFFu;
-    }
-    warp_wait(pempty, phase ^ 1, err, abort_flag);           // the owners have read the tile before
-    if (busy && owner != part) {
-        const uint32_t to = in_rank(parts, owner) +
-                            (uint32_t)((((part < owner ? part : part - 1) * TN + 32 * half) * share + col) * 4);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < rows) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + i * share * 4), "r"(v[i]) : "memory");
-    }
-    arrive_at_others(pfull, ks, part);
-    const bool all = warp_wait(pfull, phase, err, abort_flag);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    const bool mine = busy && owner == part;
-    if (mine) {
-        const float *from = parts + 32 * half * share + col;
-        float sum[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+    ok &= warp_wait<true>(bar, (lt >> 1) & 1, err, abort_flag);
+    asm volatile(                                // (the same once more, in the scope of the cluster)
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"((lt >> 1) & 1)
+        : "memory");
+    const bool mine = owner == part && n < a.N;
+    int64_t at = (int64_t)t.row0 * a.y_ld + n;
+#pragma unroll 1
+    for (int i = 0; i < quads; ++i) {
+        uint32_t v[4];
+        tmem_ld4(tbase + 4 * i, v);
+        tmem_ld_wait();
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *from = buf + col * kPartRow + 4 * i;
 #pragma unroll 1
         for (int r = 0; r < ks; ++r) {
-            if (r == part) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < rows) sum[i] += from[i * share];
-                from += TN * share;
+            float4 f = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
+            if (r != part) {
+                if (mine) f = *reinterpret_cast<const float4 *>(from);
+                from += share * kPartRow;
             }
+            sum.x += f.x;
+            sum.y += f.y;
+            sum.z += f.z;
+            sum.w += f.w;
         }
+        const float o[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = all ? __float_as_uint(sum[i]) : 0x7FFFFFFFu;
-    }
-    arrive_at_others(pempty, ks, part);
-    if (!busy) return;
-    if constexpr (FP4) {
-        const float row = half ? sc.row[TN / 32 - 1] : sc.row[0];
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] = __float_as_uint(__uint_as_float(v[i]) * (sc.col * __shfl_sync(0xFFFFFFFFu, row, i)));
-    }
-    if (!mine || n >= a.N) return;
-    int64_t at = (int64_t)(t.row0 + 32 * half) * a.y_ld + n;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        if (i < rows) {
-            const float o = __uint_as_float(v[i]) + sc.bias;
-            if (a.y_type == MOE_T_BF16)
-                ((__nv_bfloat16 *)a.y)[at] = rounded<__nv_bfloat16>(o);
-            else if (a.y_type == MOE_T_F16)
-                ((__half *)a.y)[at] = rounded<__half>(o);
-            else
-                ((float *)a.y)[at] = o;
+        for (int k = 0; k < 4; ++k) {
+            float y = ok ? o[k] : __int_as_float(0x7FFFFFFF);
+            if constexpr (FP4) y *= sc.col * __shfl_sync(0xFFFFFFFFu, sc.row[0], 4 * i + k);
+            if (mine && 4 * i + k < t.rows) store_one(a.y, at, a.y_type, y + sc.bias);
+            at += a.y_ld;
         }
-        at += a.y_ld;
     }
 }
 
@@ -651,7 +685,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     unsigned char *meta = staged + S::kOut + S::kParts;
     uint64_t *full = reinterpret_cast<uint64_t *>(meta), *empty = full + NS;
     uint64_t *tfull = empty + NS, *tempty = tfull + 2, *sfull = tempty + 2, *sempty = sfull + 4;
-    uint64_t *lfull = sempty + 4, *lempty = lfull + 4, *pfull = lempty + 4, *pempty = pfull + 1, *done = pempty + 1;
+    uint64_t *lfull = sempty + 4, *lempty = lfull + 4, *pfull = lempty + 4, *done = pfull + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     ProdGroups gr;
@@ -681,9 +715,9 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             mbar_init(&lfull[b], a.s_copy >= 16 ? 1 : 64);
             mbar_init(&lempty[b], 8);
         }
-        if (S::kSplit && a.ks > 1) {
-            mbar_init(pfull, 8 * (a.ks - 1));
-            mbar_init(pempty, 8 * (a.ks - 1));
+        if (S::kSplit) {
+            mbar_init(&pfull[0], 1);
+            mbar_init(&pfull[1], 1);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -705,7 +739,11 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     const int nw = (a.N + CG * kProdRows - 1) / (CG * kProdRows);
     tc_fence_before();
     const int ntiles = prod_groups<TN>(a, gr, nw, scratch);
-    if (CG == 2 || ks > 1) cluster_sync_all();   // the barriers of all are ready
+    // the barriers of all are ready (to partial sums from other CTAs, before those send them)
+    if (CG == 2)
+        cluster_sync_all();
+    else if (ks > 1)
+        cluster_arrive();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int nst = (a.K + kStageK - 1) / kStageK;
@@ -729,7 +767,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                 const int loads = (share + S::kBox - 1) / S::kBox;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int slot = it % NS;
-                    if (!warp_wait(&empty[slot], ((it / NS) & 1) ^ 1, err, abort_flag)) {
+                    if (!warp_wait<S::kFp4>(&empty[slot], ((it / NS) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -763,7 +801,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             else
                 idesc |= (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u);
             const int b = lt & 1;
-            if (!warp_wait(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
+            if (!warp_wait<S::kFp4>(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
             tc_fence_after();
             const uint32_t d = (uint32_t)(b * TN);       // (all columns are this CTA's: they begin at 0)
             uint32_t acc = 0u;
@@ -788,7 +826,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             };
             auto wait = [&]() {
                 ok = warp_wait<S::kFp4>(&full[slot], phase, err, abort_flag);
-                if (S::kFp4 && ok) ok = warp_wait(&sfull[sb], sphase, err, abort_flag);
+                if (S::kFp4 && ok) ok = warp_wait<S::kFp4>(&sfull[sb], sphase, err, abort_flag);
                 tc_fence_after();
                 return ok;
             };
@@ -815,7 +853,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             const int b = lt & 1;
             const int n0 = (t.w * CG + rank) * kProdRows, n = n0 + q * 32 + lane;
             const ProdScales<S::kFp4, TN> sc(a, t, n);
-            const bool ok = warp_wait(&tfull[b], (lt >> 1) & 1, err, abort_flag);
+            const bool ok = warp_wait<S::kFp4>(&tfull[b], (lt >> 1) & 1, err, abort_flag);
             tc_fence_after();
             const uint32_t at = ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
             unsigned char *stage = staged + half * 8192;
@@ -823,9 +861,15 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             bool stored = false;
             if constexpr (S::kSplit) {
                 if (ks > 1) {
-                    prod_store_split<S::kFp4, TN>(a, t, sc, at, n, half, ok, parts, part, pfull, pempty, lt & 1, err, abort_flag);
+                    if (lt == 0) cluster_wait();
+                    // (32 rows are the first four warps')
+                    if (!half) prod_store_split<S::kFp4, TN>(a, t, sc, at, n, ok, parts, part, pfull, lt, err, abort_flag);
                     stored = true;
                 }
+            }
+            if constexpr (TN == 32) {
+                if (!stored && !half) prod_store_few<S::kFp4>(a, t, sc, at, n, ok);
+                stored = true;
             }
             if (stored)
                 ;
@@ -857,7 +901,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
                 for (int kb = kb0; kb < kb1 && ok; kb += G, ++qr) {
-                  if (!warp_wait(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
+                  if (!warp_wait<S::kFp4>(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
                       ok = false;
                       break;
                   }
@@ -890,7 +934,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
                     }
-                    if (!warp_wait(&sempty[it % NB], ((it / NB) & 1) ^ 1, err, abort_flag)) {
+                    if (!warp_wait<S::kFp4>(&sempty[it % NB], ((it / NB) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -919,7 +963,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                     const int loads = (p.rows + S::kScaleBox - 1) / S::kScaleBox;
                     for (int i = b0; i < b1; ++i, ++qr) {
                         uint64_t *bar = &lfull[qr % NQ];
-                        if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
+                        if (!warp_wait<S::kFp4>(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -949,7 +993,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                 const int64_t wrow = (int64_t)p.g * a.N + (int64_t)(p.w * CG + rank) * kProdRows;
                 const int rows = kProdRows + (p.rows + 31) / 32 * 32;
                 for (int i = b0; i < b1; ++i, ++qr) {
-                    if (!warp_wait(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
+                    if (!warp_wait<S::kFp4>(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -991,6 +1035,9 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     if (CG == 2 || ks > 1) {
         if (rank && warp == 1) mbar_wait(done, 0, err);      // the leader's last arrival here
         __syncwarp();
+        // (those that did not wait for the start yet)
+        if (CG == 1 && (warp < 2 || warp >= 10 || first >= ntiles)) cluster_wait();
+        __syncwarp();
         cluster_sync_all();
     }
     if (warp == 1) {
@@ -1009,6 +1056,12 @@ bool make_tmap_scales(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t
                       uint32_t box_rows);
 int device_sms();
 constexpr int kProdDevices = 64;
+
+// What a product runs as: tiles of `rows` rows of x by 128 weight rows, or by 256 on a pair of CTAs; K in ks parts.
+struct ProdPlan {
+    int rows, pair, ks;
+};
+ProdPlan plan_product(bool fp4, int groups, int M, int N, int K);
 
 #ifdef __CUDACC__
 // x: rows x_pitch bytes apart; w: [groups * N] rows without gaps.
