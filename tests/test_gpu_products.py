@@ -295,7 +295,7 @@ LINEAR = [
     # M, N, K
     (1, 1, 64), (1, 4096, 4096), (2, 130, 128), (16, 100, 192), (17, 128, 256), (31, 129, 320), (33, 257, 4160),
     (64, 1000, 512), (129, 384, 448), (191, 96, 1024), (193, 640, 2048), (400, 300, 576), (777, 1111, 768),
-    (5, 70, 32768),
+    (5, 70, 32768), (4096, 4096, 704), (4001, 4090, 448),
 ]
 
 

@@ -22,7 +22,7 @@ static cudaError_t launch_kind(const ProdArgs &a, const uint8_t *xq, const uint8
 
 cudaError_t launch_linear_fp4(ProdArgs a, bool nvfp4, const uint8_t *xq, const uint8_t *wq, cudaStream_t st) {
     const uintptr_t at = (uintptr_t)a.xs | (uintptr_t)a.ws | (uintptr_t)(a.K / (nvfp4 ? 16 : 32));
-    a.s_copy = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : 1;
+    a.s_copy = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 2;
     return nvfp4 ? launch_kind<PROD_NVFP4>(a, xq, wq, st) : launch_kind<PROD_MXFP4>(a, xq, wq, st);
 }
 

@@ -145,7 +145,7 @@ struct ProdArgs {
     moe_dtype y_type;
     int ks;                  // parts of K, each a CTA of a cluster (set by the launcher)
     bool wide;               // y takes 16-byte stores (set by the launcher)
-    int s_copy;              // bytes that the scales' alignment lets one copy take (set by the launcher)
+    int s_copy;              // alignment of the scales' rows: 16, 4 or 2 (set by the launcher)
     int hold;                // test hook (set by the launcher)
 };
 cudaError_t launch_grouped_linear(const ProdArgs &a, const void *x, int64_t x_ld, const void *w, cudaStream_t st);

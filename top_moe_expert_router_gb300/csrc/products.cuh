@@ -66,7 +66,9 @@ struct ProdShape {
     static constexpr int kBatchBytes = (KIND == PROD_NVFP4 ? 16 : 8) * kBatch;
     static constexpr int kScaleRows = kProdRows + TN;
     static constexpr int kBatches = kFp4 ? 3 : 0;            // such batches in the ring
-    static constexpr uint32_t kScales = kFp4 ? kBatches * kScaleRows * kBatchBytes : 0;
+    // (rows that begin on odd words of 16 bits lie 24 bytes apart)
+    static constexpr int kSlotBytes = kScaleRows * (KIND == PROD_NVFP4 ? kBatchBytes : 24);
+    static constexpr uint32_t kScales = kFp4 ? kBatches * kSlotBytes : 0;
     static constexpr int kScaleBox = TN % 64 ? 32 : 64;      // rows of one TMA copy of x's scales
     // results on their way to 16-byte stores: 32 rows x 128 columns of 16 bits for each half of the epilogue's warps
     static constexpr bool kWide = TN > 32;
@@ -278,11 +280,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) 
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Asynchronous copy of n bytes to shared memory; zeros where `in` is false.
+// Asynchronous copy of N bytes to shared memory, of which the first `size` are read and the others zeros.
 template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(in ? N : 0)
-                 : "memory");
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, int size) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(size) : "memory");
 }
 // Arrives at `bar` once this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             warp_arrive<CG>(&tempty[b]);
         }
     } else if constexpr (S::kFp4) {
-        constexpr int QB = S::kBatchBytes, G = S::kBatch, SB = QB / G, NQ = S::kBatches, kSlot = S::kScaleRows * QB;
+        constexpr int QB = S::kBatchBytes, G = S::kBatch, SB = QB / G, NQ = S::kBatches, kSlot = S::kSlotBytes;
         const int b0 = kb0 / G, b1 = (kb1 + G - 1) / G;
         // the 16-byte halves of 32-byte rows lie in the order of TMA's 32-byte swizzle: rows read together are then on
         // different banks
@@ -900,6 +901,12 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             bool ok = true;
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
+                int wrow = 0, xrow = 0;          // whether the tile's first rows of W and x are odd
+                if (KIND == PROD_MXFP4 && a.s_copy <= 2) {
+                    const ProdTile p = walk.at(gr, nw);
+                    wrow = (p.g & a.N & 1);      // (of g N + a multiple of 128)
+                    xrow = p.row0 & 1;           // (behind 128 rows of W)
+                }
                 for (int kb = kb0; kb < kb1 && ok; kb += G, ++qr) {
                   if (!warp_wait<S::kFp4>(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
                       ok = false;
@@ -910,27 +917,34 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                   for (int i = 0; i < n; ++i, ++it) {
                     if ((it & 1) != group) continue;
                     uint32_t va[16], vb[4 * S::kBCols];
-                    auto words = [&](int row, uint32_t w[4]) {
-                        const unsigned char *at = ring + row * QB + swizzled(row, i * SB);
+                    auto words = [&](int row, int first_row, uint32_t w[4]) {
                         if constexpr (KIND == PROD_NVFP4) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(at);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(ring + row * QB + swizzled(row, i * SB));
                             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
                         } else {                 // two scales a column
-                            const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                            uint2 v;
+                            if (a.s_copy > 2) {
+                                v = *reinterpret_cast<const uint2 *>(ring + row * QB + i * SB);
+                            } else {             // an odd row begins in the middle of a word
+                                const uint32_t *at = reinterpret_cast<const uint32_t *>(ring + row * 24 + i * SB);
+                                const int shift = ((first_row + row) & 1) * 16;
+                                v.x = __funnelshift_r(at[0], at[1], shift);
+                                v.y = __funnelshift_r(at[1], at[2], shift);
+                            }
                             w[0] = v.x & 0xFFFFu, w[1] = v.x >> 16, w[2] = v.y & 0xFFFFu, w[3] = v.y >> 16;
                         }
                     };
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
                         uint32_t w[4];
-                        words(32 * m + lane, w);
+                        words(32 * m + lane, wrow, w);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) va[4 * j + m] = w[j];
                     }
 #pragma unroll
                     for (int m = 0; m < S::kBCols; ++m) {
                         uint32_t w[4] = {0u, 0u, 0u, 0u};
-                        if (32 * m < TN) words(kProdRows + 32 * m + lane, w);
+                        if (32 * m < TN) words(kProdRows + 32 * m + lane, xrow, w);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
                     }
@@ -979,51 +993,52 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             }
         } else {
             // ------------- scales to shared memory, where their rows are not aligned -----
-            const int t = threadIdx.x - 18 * 32;
+            // by words, the ones of a row by neighbouring threads (whole sectors). What lies behind a row's end is
+            // read too, but never what lies behind the array's; no MMA uses it.
+            const bool odd = a.s_copy <= 2;      // rows of an odd number of 16-bit words
+            const int per = KIND == PROD_NVFP4 || odd ? 8 : 4, words = KIND == PROD_NVFP4 ? 8 : odd ? 5 : 4;
+            const int t = threadIdx.x - 18 * 32, piece = t % per, r0 = t / per, rstep = 64 / per;
             const int pitch = a.K / (KIND == PROD_NVFP4 ? 16 : 32);  // bytes of a row's scales
-            const uint32_t ring = smem_u32(scales);
-            const int64_t wrows = (int64_t)a.groups * a.N;
-            const int copy = a.s_copy;
-            const int shift = 31 - __clz(QB / copy);  // log2 of the pieces of a row
+            const int to_pitch = odd ? 24 : QB;
+            const uint32_t ring = smem_u32(scales) + r0 * to_pitch + (KIND == PROD_NVFP4 ? swizzled(r0, 4 * piece) : 4 * piece);
+            const int64_t wbytes = (int64_t)a.groups * a.N * pitch, xbytes = (int64_t)a.M * pitch;
             int qr = 0;
             bool ok = true;
+            // rows `row` to row + n of an array of scales, from column byte k on; n a multiple of rstep
+            auto copy = [&](const uint8_t *base, int64_t total, int64_t row, int n, int k, uint32_t to) {
+                int64_t off = ((row + r0) * pitch & ~3ll) + k + 4 * piece;
+                const int64_t last = (row + n) * pitch + k + 4 * words;
+                if (piece >= words) return;
+                if (last <= total) {
+#pragma unroll 8
+                    for (int r = 0; r < n; r += rstep) {
+                        cp_async<4>(to, base + off, 4);
+                        off += (int64_t)rstep * pitch;
+                        to += rstep * to_pitch;
+                    }
+                } else {
+                    for (int r = 0; r < n; r += rstep) {
+                        const int64_t left = total - off;
+                        const int size = left >= 4 ? 4 : left > 0 ? (int)left : 0;
+                        cp_async<4>(to, base + (size ? off : 0), size);
+                        off += (int64_t)rstep * pitch;
+                        to += rstep * to_pitch;
+                    }
+                }
+            };
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
                 const ProdTile p = walk.at(gr, nw);
                 const int64_t wrow = (int64_t)p.g * a.N + (int64_t)(p.w * CG + rank) * kProdRows;
-                const int rows = kProdRows + (p.rows + 31) / 32 * 32;
                 for (int i = b0; i < b1; ++i, ++qr) {
                     if (!warp_wait<S::kFp4>(&lempty[qr % NQ], ((qr / NQ) & 1) ^ 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
                     const uint32_t to = ring + (qr % NQ) * kSlot;
-                    // the pieces of a row by neighbouring threads: whole sectors
-                    for (int c = t; c < rows << shift; c += 64) {
-                        const int row = c >> shift, off = (c - (row << shift)) * copy, k = i * QB + off;
-                        const uint8_t *src;
-                        bool in;
-                        if (row < kProdRows) {
-                            in = wrow + row < wrows;
-                            src = a.ws + (in ? wrow + row : 0) * pitch;
-                        } else {
-                            in = row - kProdRows < p.rows;
-                            src = a.xs + (int64_t)(in ? p.row0 + row - kProdRows : 0) * pitch;
-                        }
-                        in = in && k < pitch;
-                        src += in ? k : 0;
-                        const uint32_t dst = to + row * QB + swizzled(row, off);
-                        if (copy == 8)
-                            cp_async<8>(dst, src, in);
-                        else if (copy == 4)
-                            cp_async<4>(dst, src, in);
-                        else
-                            asm volatile("st.shared.b8 [%0], %1;" ::"r"(dst), "r"(in ? (uint32_t)*src : 0u) : "memory");
-                    }
-                    if (copy >= 4)
-                        cp_async_arrive(&lfull[qr % NQ]);
-                    else
-                        mbar_arrive(&lfull[qr % NQ]);
+                    copy(a.ws, wbytes, wrow, kProdRows, i * QB, to);
+                    copy(a.xs, xbytes, p.row0, (p.rows + 31) / 32 * 32, i * QB, to + kProdRows * to_pitch);
+                    cp_async_arrive(&lfull[qr % NQ]);
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
