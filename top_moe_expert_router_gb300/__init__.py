@@ -776,17 +776,24 @@ _HALFS = (torch.bfloat16, torch.float16)
 _FP4 = {"nvfp4": (MOE_FP4_NVFP4, 16), "mxfp4": (MOE_FP4_MXFP4, 32)}
 
 
-def _fp4_fmt(name, q, s):
-    """The format of a matrix in 4-bit floats, by its columns a scale, and its K."""
-    if q.dim() < 2 or s.dim() != q.dim():
-        raise ValueError(f"{name}: codes [.., K/2] and scales [.., K/16] or [.., K/32] expected")
-    K = 2 * q.shape[-1]
-    if s.shape[-1] * 16 == K:
-        return MOE_FP4_NVFP4, K
-    if s.shape[-1] * 32 == K:
-        return MOE_FP4_MXFP4, K
-    raise ValueError(f"{name}: one scale per 16 (NVFP4) or 32 (MXFP4) columns expected")
+_U8 = torch.uint8
 
+
+def _fp4_fmt(q, s):
+    """Codes [.., K/2] and their scales: the format, by the columns of a scale, K, and the codes' shape."""
+    shape = q.shape
+    if len(shape) < 2 or s.dim() != len(shape):
+        raise ValueError("codes [.., K/2] and scales [.., K/16] or [.., K/32] expected")
+    K, cols = 2 * shape[-1], s.shape[-1]
+    if cols * 16 == K:
+        return MOE_FP4_NVFP4, K, shape
+    if cols * 32 == K:
+        return MOE_FP4_MXFP4, K, shape
+    raise ValueError("one scale per 16 (NVFP4) or 32 (MXFP4) columns expected")
+
+
+# These calls take a few microseconds on the GPU, and most of their time on the host is that of looking at their
+# arguments: what is usual is tested in one condition, and looked at one by one, for the message, where that fails.
 
 def quantize_fp4(x, fmt="nvfp4", *, up=None, rows=None, out=None, stream=None):
     """Rows [T, K] (bf16 or f16) to microscaled 4-bit floats (moe_quantize_fp4) -> (q, s, g): codes [R, K/2] uint8, the
@@ -811,18 +818,24 @@ def quantize_fp4(x, fmt="nvfp4", *, up=None, rows=None, out=None, stream=None):
         R = rows.shape[0]
         rows_at = _whole("rows", rows, torch.int32, (R,), index)
     if out is None:
-        q = _empty((R, K // 2), torch.uint8, x.device, stream)
-        s = _empty((R, K // block), torch.uint8, x.device, stream)
+        q = _empty((R, K // 2), _U8, x.device, stream)
+        s = _empty((R, K // block), _U8, x.device, stream)
         g = _empty(R, torch.float32, x.device, stream) if block == 16 else None
     else:
         q, s, g = out
         if (g is None) != (block == 32):
             raise ValueError("out: g belongs to nvfp4")
-    up_at, up_ld = _rows("up", up, x.dtype, (T, K), index)
-    args = _pack_quant(code, _DTYPE[x.dtype], x.data_ptr(), up_at, _row_stride("x", x), up_ld, rows_at, T, R, K,
-                       _whole("q", q, torch.uint8, (R, K // 2), index),
-                       _whole("s", s, torch.uint8, (R, K // block), index), _whole("g", g, torch.float32, (R,), index))
-    _run(_entry(3), index, _handle(index, stream), (args,), "moe_quantize_fp4")
+        if not (q.dtype is _U8 is s.dtype and q.get_device() == index == s.get_device() and q.is_contiguous()
+                and s.is_contiguous() and q.shape == (R, K // 2) and s.shape == (R, K // block)):
+            _whole("q", q, _U8, (R, K // 2), index)
+            _whole("s", s, _U8, (R, K // block), index)
+    up_at = up_ld = 0
+    if up is not None:
+        up_at, up_ld = _rows("up", up, x.dtype, (T, K), index)
+    args = _pack_quant(code, _DTYPE[x.dtype], x.data_ptr(), up_at, K if x.is_contiguous() else _row_stride("x", x), up_ld,
+                       rows_at, T, R, K, q.data_ptr(), s.data_ptr(),
+                       0 if g is None else _whole("g", g, torch.float32, (R,), index))
+    _run(_entry(3), index, _raw_stream(index) if stream is None else stream.cuda_stream, (args,), "moe_quantize_fp4")
     return q, s, g
 
 
@@ -830,8 +843,7 @@ def dequantize_fp4(q, s, g=None, *, dtype=None, out=None, stream=None):
     """What 4-bit floats stand for (moe_dequantize_fp4): q [R, K/2] and s [R, K/16] (NVFP4, with g [R] or [1] fp32) or
     [R, K/32] (MXFP4) -> [R, K] bf16 (default), f16 or fp32."""
     index = _input("q", q, (torch.uint8,))
-    code, K = _fp4_fmt("q, s", q, s)
-    R = q.shape[0]
+    code, K, (R, _) = _fp4_fmt(q, s)
     if out is None:
         out = _empty((R, K), dtype or torch.bfloat16, q.device, stream)
     elif dtype is not None and dtype != out.dtype:
@@ -840,29 +852,21 @@ def dequantize_fp4(q, s, g=None, *, dtype=None, out=None, stream=None):
         raise ValueError(f"out: type {out.dtype} is not supported")
     if g is not None and code == MOE_FP4_MXFP4:
         raise ValueError("g belongs to NVFP4")
-    per_row = g is not None and g.numel() != 1
+    scales, per_row, g_at = s.shape[1], 0, 0
+    if not (s.dtype is _U8 and s.get_device() == index and q.is_contiguous() and s.is_contiguous() and s.shape[0] == R):
+        _whole("q", q, _U8, (R, K // 2), index)
+        _whole("s", s, _U8, (R, scales), index)
+    if g is not None:
+        per_row = 1 if g.numel() != 1 else 0
+        g_at = _whole("g", g, torch.float32, (R if per_row else 1,), index)
     out_at, out_ld = _rows("out", out, out.dtype, (R, K), index)
-    args = _pack_dequant(code, _DTYPE[out.dtype], _whole("q", q, torch.uint8, (R, K // 2), index),
-                         _whole("s", s, torch.uint8, (R, s.shape[1]), index),
-                         _whole("g", g, torch.float32, (R if per_row else 1,), index), 1 if per_row else 0, R, K, out_at,
-                         out_ld)
-    _run(_entry(4), index, _handle(index, stream), (args,), "moe_dequantize_fp4")
+    args = _pack_dequant(code, _DTYPE[out.dtype], q.data_ptr(), s.data_ptr(), g_at, per_row, R, K, out_at, out_ld)
+    _run(_entry(4), index, _raw_stream(index) if stream is None else stream.cuda_stream, (args,), "moe_dequantize_fp4")
     return out
 
 
 def _offsets(offsets, E, index):
     return _whole("offsets", offsets, torch.int32, (E + 1,), index)
-
-
-def _result(out, out_dtype, default, M, N, device, index, stream):
-    """The result of a product: the tensor, its address and row stride."""
-    if out is None:
-        out = _empty((M, N), out_dtype or default, device, stream)
-    elif out_dtype is not None and out_dtype != out.dtype:
-        raise ValueError("out_dtype and out differ")
-    if out.dtype not in _FLOATS:
-        raise ValueError(f"out: type {out.dtype} is not supported")
-    return out, *_rows("out", out, out.dtype, (M, N), index)
 
 
 def grouped_linear(x, w, offsets, *, bias=None, out=None, out_dtype=None, stream=None):
@@ -876,53 +880,87 @@ def grouped_linear(x, w, offsets, *, bias=None, out=None, out_dtype=None, stream
     M, K = x.shape
     if w.dim() != 3:
         raise ValueError("w must be [E, N, K]")
-    E, N = w.shape[0], w.shape[1]
-    out, out_at, out_ld = _result(out, out_dtype, x.dtype, M, N, x.device, index, stream)
-    args = _pack_grouped(_DTYPE[x.dtype], E, M, N, K, _offsets(offsets, E, index), x.data_ptr(), _row_stride("x", x),
-                         _whole("w", w, x.dtype, (E, N, K), index), _whole("bias", bias, torch.float32, (E, N), index),
-                         out_at, _DTYPE[out.dtype], out_ld)
-    _run(_entry(5), index, _handle(index, stream), (args,), "moe_grouped_linear")
+    E, N, w_cols = w.shape
+    if out is None:
+        out = _empty((M, N), out_dtype or x.dtype, x.device, stream)
+    elif out_dtype is not None and out_dtype != out.dtype:
+        raise ValueError("out_dtype and out differ")
+    if out.dtype not in _FLOATS:
+        raise ValueError(f"out: type {out.dtype} is not supported")
+    out_at, out_ld = _rows("out", out, out.dtype, (M, N), index)
+    if not (w.dtype is x.dtype and w_cols == K and w.get_device() == index and w.is_contiguous()):
+        _whole("w", w, x.dtype, (E, N, K), index)
+    if offsets is None:
+        raise ValueError("offsets are needed")
+    args = _pack_grouped(_DTYPE[x.dtype], E, M, N, K, _offsets(offsets, E, index), x.data_ptr(),
+                         K if x.is_contiguous() else _row_stride("x", x), w.data_ptr(),
+                         0 if bias is None else _whole("bias", bias, torch.float32, (E, N), index), out_at,
+                         _DTYPE[out.dtype], out_ld)
+    _run(_entry(5), index, _raw_stream(index) if stream is None else stream.cuda_stream, (args,), "moe_grouped_linear")
     return out
 
 
 def _linear_fp4(x, q, s, g, offsets, bias, out, out_dtype, stream):
-    grouped = offsets is not None
-    code, K = _fp4_fmt("q, s", q, s)
-    if q.dim() != (3 if grouped else 2):
-        raise ValueError("q must be [E, N, K/2] with offsets, [N, K/2] without")
-    E, N = (q.shape[0] if grouped else 1), q.shape[-2]
-    lead = q.shape[:-1]
+    code, K, shape = _fp4_fmt(q, s)
     mx = code == MOE_FP4_MXFP4
+    scales = K // (32 if mx else 16)
+    if offsets is None:
+        if len(shape) != 2:
+            raise ValueError("q must be [N, K/2], or [E, N, K/2] with offsets")
+        E, N = 1, shape[0]
+        lead = (N,)
+    else:
+        if len(shape) != 3:
+            raise ValueError("q must be [E, N, K/2] with offsets")
+        E, N, _ = shape
+        lead = (E, N)
     codes = not isinstance(x, torch.Tensor)
-    xq, xs, xg = x if codes else (x, None, None)
-    index = _input("x", xq, (torch.uint8,) if codes else _HALFS)
-    M = xq.shape[0]
+    if codes:
+        x, xs, xg = x
+        index = _input("x codes", x, (_U8,))
+    else:
+        xg = None
+        index = _input("x", x, _HALFS)
+    M, x_cols = x.shape
+    if x_cols != (K // 2 if codes else K):
+        raise ValueError(f"x: {K} columns expected, got {2 * x_cols if codes else x_cols}")
     if mx and (g is not None or xg is not None):
         raise ValueError("g belongs to NVFP4")
-    if not codes and xq.shape[1] != K:
-        raise ValueError(f"x: {K} columns expected, got {xq.shape[1]}")
-    cols = g is not None and g.dim() == (2 if grouped else 1) and g.shape[-1] == N and (grouped or N > 1)
-    g_at = _whole("g", g, torch.float32, lead if cols else (E,), index)
-    q_at = _whole("q", q, torch.uint8, (*lead, K // 2), index)
-    s_at = _whole("s", s, torch.uint8, (*lead, s.shape[-1]), index)
-    b_at = _whole("bias", bias, torch.float32, lead, index)
-    off_at = _offsets(offsets, E, index) if grouped else 0
-    out, out_at, out_ld = _result(out, out_dtype, torch.bfloat16 if codes else x.dtype, M, N, xq.device, index, stream)
-    st = _handle(index, stream)
-    tail = (q_at, s_at, g_at, 1 if cols else 0, b_at, out_at, _DTYPE[out.dtype], out_ld)
+    g_at = cols = 0
+    if g is not None:
+        cols = 1 if g.numel() != E else 0
+        g_at = _whole("g", g, torch.float32, lead if cols else (E,), index)
+    if out is None:
+        out = _empty((M, N), out_dtype or (torch.bfloat16 if codes else x.dtype), x.device, stream)
+    elif out_dtype is not None and out_dtype != out.dtype:
+        raise ValueError("out_dtype and out differ")
+    if out.dtype not in _FLOATS:
+        raise ValueError(f"out: type {out.dtype} is not supported")
+    out_at, out_ld = _rows("out", out, out.dtype, (M, N), index)
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    off_at = 0 if offsets is None else _offsets(offsets, E, index)
+    if not (q.dtype is _U8 is s.dtype and q.get_device() == index == s.get_device() and q.is_contiguous()
+            and s.is_contiguous() and s.shape[:-1] == lead):
+        _whole("q", q, _U8, shape, index)
+        _whole("s", s, _U8, (*lead, scales), index)
+    tail = (q.data_ptr(), s.data_ptr(), g_at, cols, 0 if bias is None else _whole("bias", bias, torch.float32, lead, index), out_at,
+            _DTYPE[out.dtype], out_ld)
     if codes:
-        args = _pack_fp4(code, E, M, N, K, off_at, _whole("x codes", xq, torch.uint8, (M, K // 2), index),
-                         _whole("x scales", xs, torch.uint8, (M, s.shape[-1]), index),
-                         _whole("x g", xg, torch.float32, (M,), index), *tail)
+        if not (xs.dtype is _U8 and xs.get_device() == index and x.is_contiguous() and xs.is_contiguous()
+                and xs.shape == (M, scales)):
+            _whole("x codes", x, _U8, (M, K // 2), index)
+            _whole("x scales", xs, _U8, (M, scales), index)
+        args = _pack_fp4(code, E, M, N, K, off_at, x.data_ptr(), xs.data_ptr(),
+                         0 if xg is None else _whole("x g", xg, torch.float32, (M,), index), *tail)
         _run(_entry(6), index, st, (args,), "moe_linear_fp4")
         return out
-    if M == 0 or K % 64:                                       # refused below, or nothing to do
+    if M == 0 or K % 64:                                       # nothing to do, or refused there
         _run(_entry(6), index, st, (_pack_fp4(code, E, M, N, K, off_at, 0, 0, 0, *tail),), "moe_linear_fp4")
         return out
-    x_ld = _row_stride("x", xq)
+    x_ld = K if x.is_contiguous() else _row_stride("x", x)
     # the tokens' codes and scales in memory of the stream that the kernels run on: every stream and captured graph has
     # its own
-    n_q, n_s = M * K // 2, (M * s.shape[-1] + 15) // 16 * 16
+    n_q, n_s = M * K // 2, (M * scales + 15) // 16 * 16
     size = n_q + n_s + (0 if mx else 4 * M)
     if _raw_alloc is not None and index == _device():
         ws = _raw_alloc(size, st)
@@ -930,7 +968,7 @@ def _linear_fp4(x, q, s, g, offsets, bias, out, out_dtype, stream):
         ws = torch.cuda.caching_allocator_alloc(size, index, st)
     try:
         ws_g = 0 if mx else ws + n_q + n_s
-        quant = _pack_quant(code, _DTYPE[xq.dtype], xq.data_ptr(), 0, x_ld, 0, 0, M, M, K, ws, ws + n_q, ws_g)
+        quant = _pack_quant(code, _DTYPE[x.dtype], x.data_ptr(), 0, x_ld, 0, 0, M, M, K, ws, ws + n_q, ws_g)
         _run(_entry(3), index, st, (quant,), "moe_quantize_fp4")
         args = _pack_fp4(code, E, M, N, K, off_at, ws, ws + n_q, ws_g, *tail)
         _run(_entry(6), index, st, (args,), "moe_linear_fp4")

@@ -29,9 +29,12 @@ bool make_tmap_rows(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t r
     cuuint64_t strides[1] = {pitch};
     cuuint32_t box[2] = {128 / es, box_rows};
     cuuint32_t estr[2] = {1, 1};
+    // (rows that do not begin on lines of 128 bytes: what lies beside a box is rarely wanted. 5003 rows by 12 experts of
+    // 2712 x 2712: 83 -> 74 us)
+    const auto promote = pitch % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     return enc(tm, two_byte ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_SWIZZLE_128B, promote,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
