@@ -15,8 +15,8 @@
 // quotient is the middle between two E4M3 values (checked for all of them), and
 // elsewhere further from it than the product's error: values of 16 bits have 11
 // significant bits, E4M3's middles 5. v / s, s an E4M3 value, is v h + v l
-// with h + l = 1/s to 48 bits: rounded once it meets the middles between codes
-// exactly (v h alone misses them for s of 13/8, 14/8, 15/8).
+// with h + l = 1/s to 40 bits or more: rounded once it meets the middles between
+// codes exactly (v h alone misses them for s of 13/8, 14/8, 15/8).
 #include <cuda_fp4.h>
 
 #include "ops.cuh"
@@ -45,9 +45,34 @@ __device__ __forceinline__ float2 widen(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
-// Two values to two codes, the first in the low nibble.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+// Eight values to eight codes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float2 f[4]) {
+    uint32_t o;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(o)
+        : "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y));
+    return o;
+}
+
+// The larger magnitude, NaN where one is, under any sign.
+template <bool BF16>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+    uint32_t o;
+    if (BF16)
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+    return o;
+}
+__device__ __forceinline__ float larger(float a, float b) {
+    float o;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
+    return o;
 }
 
 // The largest magnitude of a thread's 16 elements as the bits of a float (an
@@ -55,15 +80,14 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
 template <bool BF16, bool UP>
 __device__ __forceinline__ uint32_t top_bits(const uint32_t x[8], const float v[16]) {
     if constexpr (UP) {
-        uint32_t m = 0u;
+        float m[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        return m;
+        for (int i = 0; i < 4; ++i) m[i] = larger(larger(v[i], v[i + 4]), larger(v[i + 8], v[i + 12]));
+        return __float_as_uint(larger(larger(m[0], m[1]), larger(m[2], m[3]))) & 0x7FFFFFFFu;
     } else {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x[i] & 0x7FFF7FFFu);
-        m = max(m & 0xFFFFu, m >> 16);
+        const uint32_t m2 = larger2<BF16>(larger2<BF16>(larger2<BF16>(x[0], x[1]), larger2<BF16>(x[2], x[3])),
+                                          larger2<BF16>(larger2<BF16>(x[4], x[5]), larger2<BF16>(x[6], x[7]))) & 0x7FFF7FFFu;
+        const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
         if (BF16) return m << 16;
         return m >= 0x7C00u ? 0x7F800000u : __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
     }
@@ -135,7 +159,7 @@ __global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Arg
         big = max(big, top[p]);
     }
     float g = 1.f, inv_g = 1.f;
-    bool finite = true, far = false;
+    bool finite = true;
     if constexpr (NVFP4) {
         big = __reduce_max_sync(0xFFFFFFFFu, big);
         if constexpr (ROW > 32) {
@@ -149,9 +173,26 @@ __global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Arg
         if (big && finite) {
             const uint32_t q = __float_as_uint(__fdiv_rn(__uint_as_float(big), 2688.f));
             const uint32_t e = max((q >> 23) + ((q & 0x7FFFFFu) != 0u), 27u);   // at least 2^-100
-            far = e > 127u + 80u;
             g = __uint_as_float(e << 23);
             inv_g = __uint_as_float((254u - e) << 23);
+            if (e > 127u + 80u) {
+                // The parts of 1 / (s g) would leave the range of normal numbers: 2^-64 goes to the elements first. (bf16
+                // alone, or a product, is as large. What becomes subnormal has code 0 either way.)
+                inv_g *= 18446744073709551616.f;
+#pragma unroll
+                for (int p = 0; p < PER; ++p) {
+                    top[p] = __float_as_uint(__uint_as_float(top[p]) * 5.421010862427522e-20f);
+                    if constexpr (UP) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[p][i] *= 5.421010862427522e-20f;
+                    } else if constexpr (BF16) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            xv[p][i] = (uint32_t)f32_to_bf16_rn(bf16lo(xv[p][i]) * 5.421010862427522e-20f) |
+                                       (uint32_t)f32_to_bf16_rn(bf16hi(xv[p][i]) * 5.421010862427522e-20f) << 16;
+                    }
+                }
+            }
         }
         if (tid == 0) a.g[r] = finite ? g : __int_as_float(0x7FFFFFFF);
         if (!finite) {                                      // zeros, and NaN as the row's scale
@@ -176,10 +217,11 @@ __global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Arg
             const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s, __NV_E4M3);
             const float sf = __half2float(*reinterpret_cast<const __half *>(&hr));
             none = s == 0u;
-            const float h = __frcp_rn(sf), l = fmaf(-h, sf, 1.f) * h;
-            // 1/g is a power of two: the products are exact, but where l would leave the range of normal numbers
-            hi.x = hi.y = far ? h : h * inv_g;
-            lo.x = lo.y = far ? l : l * inv_g;
+            // h within 2^-22 of 1 / s, l what it lacks; times 1 / g, a power of two
+            float h;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(sf));
+            hi.x = hi.y = h * inv_g;
+            lo.x = lo.y = fmaf(-h, sf, 1.f) * hi.x;
         } else {
             const uint32_t m = max(top[p], __shfl_xor_sync(0xFFFFFFFFu, top[p], 1));
             none = m >= 0x7F800000u;
@@ -192,22 +234,16 @@ __global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Arg
         uint32_t c[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            c[h] = 0u;
+            float2 f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float2 f;
                 if constexpr (UP)
-                    f = make_float2(v[p][8 * h + 2 * i], v[p][8 * h + 2 * i + 1]);
+                    f[i] = make_float2(v[p][8 * h + 2 * i], v[p][8 * h + 2 * i + 1]);
                 else
-                    f = widen<BF16>(xv[p][4 * h + i]);
-                if constexpr (NVFP4) {
-                    if (far) f = mul2(f, make_float2(inv_g, inv_g));
-                    f = fma2(f, hi, mul2(f, lo));
-                } else {
-                    f = mul2(f, hi);
-                }
-                c[h] |= e2m1x2(f.x, f.y) << (8 * i);
+                    f[i] = widen<BF16>(xv[p][4 * h + i]);
+                f[i] = NVFP4 ? fma2(f[i], hi, mul2(f[i], lo)) : mul2(f[i], hi);
             }
+            c[h] = e2m1x8(f);
             if (none) c[h] = 0u;
         }
         if (u < units) {
