@@ -415,8 +415,8 @@ moe_status moe_debug_hold_linear_w4(int hold);
 
 /* Microscaled 4-bit floats: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
  * sign), two to a byte, the low nibble holding the lower index, and scales:
- *   MOE_FP4_NVFP4: an E4M3 byte s per 16 columns and an fp32 g per row (or
- *     matrix); a code stands for e2m1 * s * g;
+ *   MOE_FP4_NVFP4: an E4M3 byte s (not negative) per 16 columns and an fp32 g
+ *     per row (or matrix); a code stands for e2m1 * s * g;
  *   MOE_FP4_MXFP4: a byte s per 32 columns, the power of two 2^(s - 127), 255
  *     NaN; a code stands for e2m1 * 2^(s - 127).
  * moe_quantize_nvfp4 writes the first, g one per matrix. */
@@ -430,8 +430,8 @@ typedef enum { MOE_FP4_NVFP4 = 0, MOE_FP4_MXFP4 = 1 } moe_fp4_fmt;
  *     codes E2M1(v / (s g)), 0 where s is 0.
  *   MXFP4: s = floor(log2 max|v of the block|) - 2, clamped to [-127, 127], as
  *     s + 127, 0 for a block of zeros; codes E2M1(v / 2^s), saturating.
- * Nearest, ties to even, of exact quotients (with up: of the fp32 v, whose
- * silu is within 2^-21). A row (NVFP4) or block (MXFP4) that holds an infinity
+ * Nearest, ties to even, of exact quotients (with up: of the fp32 v, which
+ * is within (5 + 1.2 |x|) 2^-23 of itself). A row (NVFP4) or block (MXFP4) that holds an infinity
  * or NaN gets codes 0 and NaN as g (255 as s): everything computed from it is
  * NaN. K a multiple of 64, K <= 32768; q 16-byte, s 4-byte aligned, both
  * without gaps between rows. No output overlaps an input. */
@@ -467,10 +467,11 @@ moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *args, void *stream)
 /* Products of rows grouped by expert, y[r] = W[e] x[r] + bias[e] for the rows
  * offsets[e] <= r < offsets[e+1] (device, int32, ascending, as the routing
  * writes them); rows before offsets[0] and from offsets[groups] on are left as
- * they are, and no offset leads outside [0, M). offsets NULL (groups = 1): one
+ * they are, and no offset leads outside [0, M) (where offsets run backwards, what
+ * rows hold is undefined). offsets NULL (groups = 1): one
  * matrix for all M rows. Products and sums are fp32. No row of x reaches another row's
  * result: an infinity or NaN stays in its row. y is bf16, f16 or fp32 and
- * overlaps no input. groups <= 512, M and N <= 2^24, groups * N < 2^31.
+ * overlaps no input. groups <= 512, M, N and K <= 2^24, groups * N < 2^31.
  *
  * moe_grouped_linear: x and W of one type, bf16 or f16; K a multiple of 8, x
  * 16-byte aligned with a stride that is a multiple of 8, W [groups, N, K]

@@ -295,7 +295,8 @@ LINEAR = [
     # M, N, K
     (1, 1, 64), (1, 4096, 4096), (2, 130, 128), (16, 100, 192), (17, 128, 256), (31, 129, 320), (33, 257, 4160),
     (64, 1000, 512), (129, 384, 448), (191, 96, 1024), (193, 640, 2048), (400, 300, 576), (777, 1111, 768),
-    (5, 70, 32768), (4096, 4096, 704), (4001, 4090, 448),
+    (5, 70, 32768), (4096, 4096, 704), (4001, 4090, 448), (3, 4096, 4096), (30, 512, 8192), (20, 900, 3136), (500, 4096, 4096),
+    (1000, 4096, 1088),
 ]
 
 
@@ -362,6 +363,10 @@ GROUPS = [
     ([1], 1, 8), ([5], 130, 72), ([0, 3, 0, 0, 1, 0], 100, 64), ([1] * 8, 1536, 4096), ([16, 17, 31, 32, 33], 384, 200),
     ([0] * 255 + [7], 96, 320), ([130, 1, 0, 300, 64, 65], 257, 448), ([513, 0, 255, 256, 257], 200, 136),
     ([3] * 512, 64, 64), ([0, 0, 0], 128, 128), ([40] * 12, 1000, 1016), ([900, 30], 640, 2048),
+    # sums in parts: one tile a cluster, several parts, a last part that is shorter
+    ([3], 384, 4096), ([32], 260, 2040), ([9], 4096, 4096),
+    # tiles of 64 and 128 rows, pairs of CTAs
+    ([200], 4096, 1024), ([60, 0, 70], 1024, 1024), ([500, 300], 2048, 512), ([1000], 4096, 640), ([257, 511, 700], 2000, 1032),
 ]
 
 
@@ -428,7 +433,7 @@ def test_grouped_rows_left_alone(gpu_lib):
     assert (kept == -3).all()
     xq = gpu_lib.quantize_fp4(x)
     q, s, gs = gpu_lib.quantize_nvfp4(w)
-    for bad in ([-9, 3, 2 ** 30, 2 ** 31 - 1, 5], [80, 20, 10, 200, 90], [-2 ** 31, -5, -1, 0, 0]):
+    for bad in ([-9, 3, 2 ** 30, 2 ** 31 - 1, 5], [80, 20, 10, 200, 90], [0, 90, 0, 90, 0], [-2 ** 31, -5, -1, 0, 0]):
         off = torch.tensor(bad, dtype=torch.int32, device="cuda")
         buf.fill_(-3.0)
         gpu_lib.grouped_linear(x, w, off, out=y)
@@ -536,29 +541,63 @@ def test_streams_and_graphs(gpu_lib):
     assert gpu_lib.products_status() == gpu_lib.MOE_OK
 
 
-def test_waits_that_run_out(gpu_lib):
+@pytest.mark.parametrize("counts,N,K", [([20, 0, 300], 300, 320), ([3, 0, 5], 300, 4096), ([700, 0, 900], 2056, 768)])
+def test_waits_that_run_out(gpu_lib, counts, N, K):
     """Products that copy no operands: NaN in their rows and only there, the status says so once, and the next call is as
-    before."""
+    before. (Tiles of one CTA, sums in parts, pairs of CTAs.)"""
     g = gen(14)
-    counts, N, K = [20, 0, 300], 300, 320
     off = offsets_of(counts, first=2)
-    x, w = randn(g, 330, K).to(torch.bfloat16), randn(g, 3, N, K).to(torch.bfloat16)
+    end = 2 + sum(counts)
+    M = end + 8
+    x, w = randn(g, M, K).to(torch.bfloat16), randn(g, 3, N, K).to(torch.bfloat16)
     ws = [v.view(3, N, *v.shape[1:]) for v in gpu_lib.quantize_fp4(w.view(3 * N, K))]
     xq = gpu_lib.quantize_fp4(x)
     for call in (lambda o: gpu_lib.grouped_linear(x, w, off, out=o),
                  lambda o: gpu_lib.grouped_linear_fp4(xq, *ws, off, out=o)):
-        good = call(torch.full((330, N), 5.0, dtype=torch.bfloat16, device="cuda"))
-        held = torch.full((330, N), 5.0, dtype=torch.bfloat16, device="cuda")
+        good = call(torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda"))
+        held = torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")
         gpu_lib.hold_products(True)
         try:
             call(held)
             torch.cuda.synchronize()
         finally:
             gpu_lib.hold_products(False)
-        assert torch.isnan(held[2:322]).all() and (held[:2] == 5).all() and (held[322:] == 5).all()
+        assert torch.isnan(held[2:end]).all() and (held[:2] == 5).all() and (held[end:] == 5).all()
         assert gpu_lib.products_status() == gpu_lib.MOE_ERR_TIMEOUT
         assert gpu_lib.products_status() == gpu_lib.MOE_OK
-        assert torch.equal(call(torch.full((330, N), 5.0, dtype=torch.bfloat16, device="cuda")), good)
+        assert torch.equal(call(torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")), good)
+
+
+FIRST_USE = """
+import torch
+import top_moe_expert_router_gb300 as moe
+g = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn(40, 512, generator=g, device="cuda").to(torch.bfloat16)
+w = (0.1 * torch.randn(3, 300, 512, generator=g, device="cuda")).to(torch.bfloat16)
+off = torch.tensor([0, 10, 10, 40], dtype=torch.int32, device="cuda")
+def calls():
+    q, s, gs = moe.quantize_fp4(w.view(900, 512))
+    q, s, gs = q.view(3, 300, 256), s.view(3, 300, 32), gs.view(3, 300)
+    return (moe.dequantize_fp4(*moe.quantize_fp4(x, "mxfp4")), moe.grouped_linear(x, w, off),
+            moe.grouped_linear_fp4(x, q, s, gs, off), moe.linear_fp4(x, q[1], s[1], gs[1]))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+print("same" if all(torch.equal(a, b) for a, b in zip(got, calls())) else "different")
+"""
+
+
+def test_first_use_of_every_operator_inside_a_capture():
+    """A process whose first call of each operator is a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_USE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------------------

@@ -72,7 +72,7 @@ BOTH = [
 
 @pytest.mark.parametrize("kw,want", BOTH + [
     (dict(type=F32), UNS), (dict(x=None), BAD), (dict(w=None), BAD), (dict(x=P + 8), BAD), (dict(w=P + 8), BAD),
-    (dict(x_stride=504), BAD), (dict(x_stride=516), BAD),
+    (dict(x_stride=504), BAD), (dict(x_stride=516), BAD), (dict(K=(1 << 24) + 8, x_stride=1 << 25), UNS),
 ])
 def test_grouped_linear_arguments_rejected(lib, kw, want):
     assert lib.moe_grouped_linear(_grouped(**kw), None) == want

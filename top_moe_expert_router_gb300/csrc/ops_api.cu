@@ -53,7 +53,7 @@ bool is_half_type(moe_dtype t) { return t == MOE_T_BF16 || t == MOE_T_F16; }
 moe_status check_product(int groups, int M, int N, int K, const int32_t *offsets, const float *bias, const void *y,
                          moe_dtype y_type, int64_t y_stride) {
     if (groups < 1 || M < 0 || N < 1 || K < 1 || (!offsets && groups != 1)) return MOE_ERR_INVALID_ARG;
-    if (!is_float_type(y_type) || groups > kProdMaxGroups || M > kProdMaxRows || N > kProdMaxRows ||
+    if (!is_float_type(y_type) || groups > kProdMaxGroups || M > kProdMaxRows || N > kProdMaxRows || K > kProdMaxRows ||
         (int64_t)groups * N > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;

@@ -13,10 +13,23 @@
 // device determine: group by group, in bands of 12 weight tiles, so that the
 // CTAs running at a time share weight and row tiles in L2.
 //
+// With few rows and few tiles K is split over a cluster of CTAs, whose sums meet
+// in distributed shared memory; with many rows a pair of CTAs shares a tile of
+// 256 weight rows (cta_group::2), each with half of the rows of x in its shared
+// memory.
+//
 // Warps: 0 TMA, 1 MMA (owns the tensor memory), 2..9 epilogue, and for 4-bit
 // operands 18 and 19, which bring the block scales to shared memory, and 10..17,
-// which bring them from there to tensor memory: the layout there is lane r % 32, column r / 32 for row r, four scale bytes of one MMA
-// (K = 64) to a column, the same in all four lane quarters.
+// which bring them from there to tensor memory: the layout there is lane r % 32,
+// column r / 32 for row r, the scale bytes of one MMA (K = 64) in a column, the
+// same in all four lane quarters.
+//
+// What bounds it: with few rows, or ragged groups, the stream of the weights
+// (32768 rows by 256 experts of 1536 x 4096: bf16 530 us, NVFP4 165 us, 1.00 and
+// 0.96 of the copy rate); with many, 16 bits: the MMAs (4096 x 8192 x 4096 bf16
+// 131 us, 2.10 PFLOP/s); 4 bits: shared memory, through which a stage's 28 KB of
+// operands pass twice and its 5 KB of scales five times (4096 x 8192 x 8192 NVFP4
+// 100 us, 5.5 PFLOP/s; without the scales 80 us, without the stores too 72).
 #pragma once
 
 #include <cuda.h>
@@ -50,7 +63,8 @@ static inline cudaError_t prod_take_errors(cudaStream_t st, uint32_t *bits) {
     return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
-constexpr int kPartRow = 36;               // floats from one column of partial sums to the next: 32 rows, and 4 against bank conflicts
+// Floats from one column of partial sums to the next: 32 rows, and 4 against bank conflicts.
+constexpr int kPartRow = 36;
 
 // CG: CTAs of a tile, 1 or 2 (a pair, 256 weight rows)
 template <int KIND, int TN, int CG>
@@ -73,11 +87,11 @@ struct ProdShape {
     // results on their way to 16-byte stores: 32 rows x 128 columns of 16 bits for each half of the epilogue's warps
     static constexpr bool kWide = TN > 32;
     static constexpr uint32_t kOut = kWide ? 2 * 32 * 256 : 0;
-    // K may be split over a cluster of up to 8 CTAs: the sums that the others bring for this CTA's share of the columns
+    // K may be split over a cluster of CTAs (up to 8): the sums that the others bring for this CTA's share of the columns
     // (two tiles' worth: (ks - 1) 4 ceil(32 / ks) columns at most)
     static constexpr bool kSplit = CG == 1 && TN == 32;
     static constexpr uint32_t kParts = kSplit ? 2 * 120 * kPartRow * 4 : 0;
-    static constexpr uint32_t kMeta = kProdMaxGroups * 16 + 16 + 768;  // group tables, barriers, scratch
+    static constexpr uint32_t kMeta = kProdMaxGroups * 16 + 16 + 512 + 256;  // group tables, barriers, scratch of 64 words
     static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales - kOut - kParts) / kStage);
     static constexpr int kStages = kRoom < 10 ? kRoom : 10;
     static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kOut + kParts + kMeta;
@@ -335,11 +349,13 @@ struct ProdWalk {
     __device__ __forceinline__ ProdTile at(const ProdGroups &gr, int nw) { return prod_tile<TN>(gr, nw, tile, i); }
 };
 
-// Fills the tables; every thread of the CTA, one or two groups each. -> the number of tiles
+// Fills the tables; every thread of the CTA, one or two groups each. -> the number of tiles, 0 where offsets that run
+// backwards make them more than can be counted
 template <int TN>
 __device__ __forceinline__ int prod_groups(const ProdArgs &a, ProdGroups &gr, int nw, int32_t *scratch) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    int lo[2], rows[2], tiles[2], sum = 0, used = 0;
+    int lo[2], rows[2], tiles[2], used = 0;
+    long long sum = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int g = 2 * t + j;
@@ -357,24 +373,31 @@ __device__ __forceinline__ int prod_groups(const ProdArgs &a, ProdGroups &gr, in
         sum += tiles[j];
         used += rows[j] > 0;
     }
-    int end = sum, last = used;                  // inclusive sums over the threads
+    long long end = sum;
+    int last = used;                             // inclusive sums over the threads
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, end, o), u = __shfl_up_sync(0xFFFFFFFFu, last, o);
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, end, o);
+        const int u = __shfl_up_sync(0xFFFFFFFFu, last, o);
         if (lane >= o) end += v, last += u;
     }
-    if (lane == 31) scratch[2 * warp] = end, scratch[2 * warp + 1] = last;
+    if (lane == 31) {
+        reinterpret_cast<long long *>(scratch)[warp] = end;
+        scratch[40 + warp] = last;
+    }
     __syncthreads();
-    int all = 0, n = 0;
+    long long all = 0;
+    int n = 0;
     for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         if (w == warp) end += all, last += n;
-        all += scratch[2 * w];
-        n += scratch[2 * w + 1];
+        all += reinterpret_cast<const long long *>(scratch)[w];
+        n += scratch[40 + w];
     }
-    int at = end - sum, i = last - used;
+    if (all > 0x7FFFFFFF) all = n = 0;
+    int at = (int)(end - sum), i = last - used;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        if (rows[j] > 0) {
+        if (rows[j] > 0 && n) {
             gr.start[i] = at;
             gr.row0[i] = lo[j];
             gr.rows[i] = rows[j];
@@ -382,10 +405,10 @@ __device__ __forceinline__ int prod_groups(const ProdArgs &a, ProdGroups &gr, in
             at += tiles[j];
             ++i;
         }
-    if (t == 0) gr.start[n] = all;
+    if (t == 0) gr.start[n] = (int)all;
     gr.n = n;
     __syncthreads();
-    return all;
+    return (int)all;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t v[32]) {
@@ -786,63 +809,63 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             for (int j = rank ? it : it > NS ? it - NS : 0; j < it; ++j) mbar_wait(&full[j % NS], (j / NS) & 1, err);
         }
     } else if (warp == 1) {
-        if (rank == 0) {
         // -------------------------------- MMA issuer --------------------------------
-        const uint32_t on = elect_lane();
-        int lt = 0, slot = 0, sb = 0;
-        uint32_t phase = 0, sphase = 0;                  // of the ring's and the scales' barriers
-        bool ok = true;
-        ProdWalk<TN> walk(first);
-        for (; walk.tile < ntiles && ok; walk.tile += step, ++lt) {
-            // N in units of 8 (from bit 17), M in units of 16 (from bit 24; of 128 from bit 27)
-            const uint32_t n8 = __shfl_sync(0xFFFFFFFFu, (uint32_t)((walk.at(gr, nw).rows + S::kStep - 1) / S::kStep * (S::kStep / 8)), 0);
-            uint32_t idesc = (n8 << 17) | ((uint32_t)(CG * kProdRows >> 4) << 24);
-            if constexpr (S::kFp4)
-                idesc |= (1u << 7) | (1u << 10) | (KIND == PROD_MXFP4 ? 1u << 23 : 0u);
-            else
-                idesc |= (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u);
-            const int b = lt & 1;
-            if (!warp_wait<S::kFp4>(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
-            tc_fence_after();
-            const uint32_t d = (uint32_t)(b * TN);       // (all columns are this CTA's: they begin at 0)
-            uint32_t acc = 0u;
-            auto stage = [&](int n) {                    // the n MMAs of a stage; n is a constant where it is 4
-                const uint32_t sa = tiles + slot * S::kStage;
-                const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + kProdABytes);
-                const uint32_t sc = S::kScaleAt + (uint32_t)sb * S::kScaleCols;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if (kk >= n) break;
-                    const uint64_t o = (uint64_t)(2 * kk);
-                    if constexpr (S::kFp4)
-                        mma_fp4<KIND, CG>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, acc, on);
-                    else
-                        mma_16<CG>(d, ad + o, bd + o, idesc, acc, on);
-                    acc = 1u;
-                }
-                commit_on<CG>(&empty[slot], on);         // free once these MMAs have read it
-                if (S::kFp4) commit_on<CG>(&sempty[sb], on);
-                if (++slot == NS) slot = 0, phase ^= 1u;
-                if (++sb == NB) sb = 0, sphase ^= 1u;
-            };
-            auto wait = [&]() {
-                ok = warp_wait<S::kFp4>(&full[slot], phase, err, abort_flag);
-                if (S::kFp4 && ok) ok = warp_wait<S::kFp4>(&sfull[sb], sphase, err, abort_flag);
+        if (rank == 0) {
+            const uint32_t on = elect_lane();
+            int lt = 0, slot = 0, sb = 0;
+            uint32_t phase = 0, sphase = 0;                  // of the ring's and the scales' barriers
+            bool ok = true;
+            ProdWalk<TN> walk(first);
+            for (; walk.tile < ntiles && ok; walk.tile += step, ++lt) {
+                // N in units of 8 (from bit 17), M in units of 16 (from bit 24; of 128 from bit 27)
+                const uint32_t n8 = __shfl_sync(0xFFFFFFFFu, (uint32_t)((walk.at(gr, nw).rows + S::kStep - 1) / S::kStep * (S::kStep / 8)), 0);
+                uint32_t idesc = (n8 << 17) | ((uint32_t)(CG * kProdRows >> 4) << 24);
+                if constexpr (S::kFp4)
+                    idesc |= (1u << 7) | (1u << 10) | (KIND == PROD_MXFP4 ? 1u << 23 : 0u);
+                else
+                    idesc |= (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u);
+                const int b = lt & 1;
+                if (!warp_wait<S::kFp4>(&tempty[b], ((lt >> 1) & 1) ^ 1, err, abort_flag)) break;
                 tc_fence_after();
-                return ok;
-            };
-            // (the last stage may be shorter)
-            const int whole = min(kb1, a.K / kStageK);
-            for (int kb = kb0; kb < whole; ++kb) {
-                if (!wait()) break;
-                stage(4);
+                const uint32_t d = (uint32_t)(b * TN);       // (all columns are this CTA's: they begin at 0)
+                uint32_t acc = 0u;
+                auto stage = [&](int n) {                    // the n MMAs of a stage; n is a constant where it is 4
+                    const uint32_t sa = tiles + slot * S::kStage;
+                    const uint64_t ad = smem_desc_sw128(sa), bd = smem_desc_sw128(sa + kProdABytes);
+                    const uint32_t sc = S::kScaleAt + (uint32_t)sb * S::kScaleCols;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk >= n) break;
+                        const uint64_t o = (uint64_t)(2 * kk);
+                        if constexpr (S::kFp4)
+                            mma_fp4<KIND, CG>(d, ad + o, bd + o, idesc, sc + 4 * kk, sc + 16 + S::kBCols * kk, acc, on);
+                        else
+                            mma_16<CG>(d, ad + o, bd + o, idesc, acc, on);
+                        acc = 1u;
+                    }
+                    commit_on<CG>(&empty[slot], on);         // free once these MMAs have read it
+                    if (S::kFp4) commit_on<CG>(&sempty[sb], on);
+                    if (++slot == NS) slot = 0, phase ^= 1u;
+                    if (++sb == NB) sb = 0, sphase ^= 1u;
+                };
+                auto wait = [&]() {
+                    ok = warp_wait<S::kFp4>(&full[slot], phase, err, abort_flag);
+                    if (S::kFp4 && ok) ok = warp_wait<S::kFp4>(&sfull[sb], sphase, err, abort_flag);
+                    tc_fence_after();
+                    return ok;
+                };
+                // (the last stage may be shorter)
+                const int whole = min(kb1, a.K / kStageK);
+                for (int kb = kb0; kb < whole; ++kb) {
+                    if (!wait()) break;
+                    stage(4);
+                }
+                if (ok && whole < kb1 && wait()) stage((a.K - whole * kStageK + kMmaK - 1) / kMmaK);
+                if (!ok) break;
+                commit_on<CG>(&tfull[b], on);
             }
-            if (ok && whole < kb1 && wait()) stage((a.K - whole * kStageK + kMmaK - 1) / kMmaK);
-            if (!ok) break;
-            commit_on<CG>(&tfull[b], on);
-        }
-        commit_on<CG>(done, on);
-        mbar_wait(done, 0, err);
+            commit_on<CG>(done, on);
+            mbar_wait(done, 0, err);
         }
     } else if (warp < 10) {
         // --------------------------------- epilogue ---------------------------------
@@ -908,60 +931,60 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                     xrow = p.row0 & 1;           // (behind 128 rows of W)
                 }
                 for (int kb = kb0; kb < kb1 && ok; kb += G, ++qr) {
-                  if (!warp_wait<S::kFp4>(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
-                      ok = false;
-                      break;
-                  }
-                  const unsigned char *ring = scales + (qr % NQ) * kSlot;
-                  const int n = min(G, kb1 - kb);
-                  for (int i = 0; i < n; ++i, ++it) {
-                    if ((it & 1) != group) continue;
-                    uint32_t va[16], vb[4 * S::kBCols];
-                    auto words = [&](int row, int first_row, uint32_t w[4]) {
-                        if constexpr (KIND == PROD_NVFP4) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(ring + row * QB + swizzled(row, i * SB));
-                            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                        } else {                 // two scales a column
-                            uint2 v;
-                            if (a.s_copy > 2) {
-                                v = *reinterpret_cast<const uint2 *>(ring + row * QB + i * SB);
-                            } else {             // an odd row begins in the middle of a word
-                                const uint32_t *at = reinterpret_cast<const uint32_t *>(ring + row * 24 + i * SB);
-                                const int shift = ((first_row + row) & 1) * 16;
-                                v.x = __funnelshift_r(at[0], at[1], shift);
-                                v.y = __funnelshift_r(at[1], at[2], shift);
-                            }
-                            w[0] = v.x & 0xFFFFu, w[1] = v.x >> 16, w[2] = v.y & 0xFFFFu, w[3] = v.y >> 16;
-                        }
-                    };
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        uint32_t w[4];
-                        words(32 * m + lane, wrow, w);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) va[4 * j + m] = w[j];
-                    }
-#pragma unroll
-                    for (int m = 0; m < S::kBCols; ++m) {
-                        uint32_t w[4] = {0u, 0u, 0u, 0u};
-                        if (32 * m < TN) words(kProdRows + 32 * m + lane, xrow, w);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
-                    }
-                    if (!warp_wait<S::kFp4>(&sempty[it % NB], ((it / NB) & 1) ^ 1, err, abort_flag)) {
+                    if (!warp_wait<S::kFp4>(&lfull[qr % NQ], (qr / NQ) & 1, err, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t to = ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it % NB) * S::kScaleCols;
-                    tmem_st16(to, va);
-                    tmem_st16(to + 16, vb);
-                    if constexpr (S::kBCols == 8) tmem_st16(to + 32, vb + 16);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    warp_arrive<CG>(&sfull[it % NB]);
-                  }
-                  warp_arrive<1>(&lempty[qr % NQ]);
+                    const unsigned char *ring = scales + (qr % NQ) * kSlot;
+                    const int n = min(G, kb1 - kb);
+                    for (int i = 0; i < n; ++i, ++it) {
+                        if ((it & 1) != group) continue;
+                        uint32_t va[16], vb[4 * S::kBCols];
+                        auto words = [&](int row, int first_row, uint32_t w[4]) {
+                            if constexpr (KIND == PROD_NVFP4) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(ring + row * QB + swizzled(row, i * SB));
+                                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                            } else {                 // two scales a column
+                                uint2 v;
+                                if (a.s_copy > 2) {
+                                    v = *reinterpret_cast<const uint2 *>(ring + row * QB + i * SB);
+                                } else {             // an odd row begins in the middle of a word
+                                    const uint32_t *at = reinterpret_cast<const uint32_t *>(ring + row * 24 + i * SB);
+                                    const int shift = ((first_row + row) & 1) * 16;
+                                    v.x = __funnelshift_r(at[0], at[1], shift);
+                                    v.y = __funnelshift_r(at[1], at[2], shift);
+                                }
+                                w[0] = v.x & 0xFFFFu, w[1] = v.x >> 16, w[2] = v.y & 0xFFFFu, w[3] = v.y >> 16;
+                            }
+                        };
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            uint32_t w[4];
+                            words(32 * m + lane, wrow, w);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) va[4 * j + m] = w[j];
+                        }
+#pragma unroll
+                        for (int m = 0; m < S::kBCols; ++m) {
+                            uint32_t w[4] = {0u, 0u, 0u, 0u};
+                            if (32 * m < TN) words(kProdRows + 32 * m + lane, xrow, w);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) vb[S::kBCols * j + m] = w[j];
+                        }
+                        if (!warp_wait<S::kFp4>(&sempty[it % NB], ((it / NB) & 1) ^ 1, err, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t to = ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it % NB) * S::kScaleCols;
+                        tmem_st16(to, va);
+                        tmem_st16(to + 16, vb);
+                        if constexpr (S::kBCols == 8) tmem_st16(to + 32, vb + 16);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        warp_arrive<CG>(&sfull[it % NB]);
+                    }
+                    warp_arrive<1>(&lempty[qr % NQ]);
                 }
             }
         } else if (a.s_copy >= 16) {
