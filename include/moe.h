@@ -478,7 +478,7 @@ moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *args, void *stream)
  * 16-byte aligned.
  * moe_linear_fp4: x and W in 4-bit floats of one format, as above, K as there;
  * block products and their scales are exact, sums fp32, and g of x and W
- * multiply them. */
+ * multiply them. With x the rows are first quantised as moe_quantize_fp4 does. */
 typedef struct {
     moe_dtype type;
     int groups, M, N, K;
@@ -497,8 +497,11 @@ typedef struct {
     moe_fp4_fmt fmt;
     int groups, M, N, K;
     const int32_t *offsets;
-    const uint8_t *xq, *xs;  /* [M, K/2], [M, K/16 or K/32] */
-    const float *xg;         /* NVFP4: [M] or NULL (1) */
+    const void *x;           /* NULL, or [M, K] to be quantised first, into xq, xs and xg */
+    int64_t x_stride;
+    moe_dtype x_type;        /* bf16 or f16 */
+    uint8_t *xq, *xs;        /* [M, K/2], [M, K/16 or K/32] */
+    float *xg;               /* NVFP4: [M] or, without x, NULL (1) */
     const uint8_t *wq, *ws;  /* [groups, N, K/2], [groups, N, K/16 or K/32] */
     const float *wg;         /* NVFP4: [groups], with wg_cols [groups, N], or NULL (1) */
     int wg_cols;

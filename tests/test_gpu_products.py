@@ -334,6 +334,40 @@ def test_linear_fp4_second_scales(gpu_lib):
                                                                      out_dtype=torch.float16))
 
 
+def test_no_rows_and_refusals(gpu_lib):
+    x = torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda")
+    q, s, gs = gpu_lib.quantize_fp4(torch.ones(70, 128, dtype=torch.bfloat16, device="cuda"))
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert gpu_lib.linear_fp4(x, q, s, gs).shape == (0, 70)
+    assert gpu_lib.linear_fp4((q[:0], s[:0], gs[:0]), q, s, gs).shape == (0, 70)
+    assert gpu_lib.grouped_linear_fp4(x, q[None], s[None], None, off).shape == (0, 70)
+    assert gpu_lib.grouped_linear(x, torch.ones(1, 70, 128, dtype=torch.bfloat16, device="cuda"), off).shape == (0, 70)
+    assert gpu_lib.dequantize_fp4(q[:0], s[:0], gs[:0]).shape == (0, 128)
+    x = torch.ones(3, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gpu_lib.MoeError):                     # K no multiple of 64
+        gpu_lib.linear_fp4(x[:, :32], q[:, :16].contiguous(), s[:, :2].contiguous(), gs)
+    with pytest.raises(gpu_lib.MoeError):                     # x not 16-byte aligned
+        gpu_lib.grouped_linear(x[:, 1:121], torch.ones(1, 70, 120, dtype=torch.bfloat16, device="cuda"), off)
+    for call in (lambda: gpu_lib.linear_fp4(x, q, s, gs[:3]), lambda: gpu_lib.linear_fp4(x, q, s, gs.half()),
+                 lambda: gpu_lib.linear_fp4(x[:, :64], q, s, gs), lambda: gpu_lib.linear_fp4(x.float(), q, s, gs),
+                 lambda: gpu_lib.linear_fp4(x, q, s[:60], gs), lambda: gpu_lib.linear_fp4(x, q, s, gs, bias=gs[:9]),
+                 lambda: gpu_lib.linear_fp4(x, q, s, gs, out_dtype=torch.float64), lambda: gpu_lib.linear_fp4(x, q[::2], s[::2], None),
+                 lambda: gpu_lib.linear_fp4((q, s[:, :4], None), q, s, gs), lambda: gpu_lib.quantize_fp4(x[:, :96]),
+                 lambda: gpu_lib.quantize_fp4(x, "fp4"), lambda: gpu_lib.quantize_fp4(x, up=x[:2]),
+                 lambda: gpu_lib.quantize_fp4(x, out=(q, s, gs)), lambda: gpu_lib.quantize_fp4(x, rows=off.long()),
+                 lambda: gpu_lib.dequantize_fp4(q, s, gs[:7]), lambda: gpu_lib.dequantize_fp4(q, s.cpu(), gs),
+                 lambda: gpu_lib.grouped_linear(x, x[None], off[:1]), lambda: gpu_lib.grouped_linear(x, x[None].half(), off),
+                 lambda: gpu_lib.grouped_linear(x, x[None], off, out=x.to(torch.float64)),
+                 lambda: gpu_lib.grouped_linear_fp4(x, q[None], s[None], gs, off.long())):
+        with pytest.raises(ValueError):
+            call()
+    # g of one column each, where there are as many matrices as that makes scales
+    w = gpu_lib.quantize_fp4(torch.ones(4, 128, dtype=torch.bfloat16, device="cuda"))
+    off = torch.tensor([0, 1, 1, 2, 3], dtype=torch.int32, device="cuda")
+    y = gpu_lib.grouped_linear_fp4(x, w[0][:, None], w[1][:, None], w[2][:, None], off)
+    assert torch.equal(y, gpu_lib.grouped_linear_fp4(x, w[0][:, None], w[1][:, None], w[2], off))
+
+
 def test_linear_fp4_exact_sums(gpu_lib):
     """Small whole numbers: every product and sum is exact, so every result is too, whatever the order."""
     g = gen(5)

@@ -57,7 +57,7 @@ def _grouped(**kw):
 
 
 def _fp4(**kw):
-    return _with(moe.MoeLinearFp4Args(moe.MOE_FP4_NVFP4, 8, 64, 256, 512, P, P, P, P, P, P, P, 0, P, P, BF16, 256), kw)
+    return _with(moe.MoeLinearFp4Args(moe.MOE_FP4_NVFP4, 8, 64, 256, 512, P, None, 512, BF16, P, P, P, P, P, P, 0, P, P, BF16, 256), kw)
 
 
 BOTH = [
@@ -83,6 +83,7 @@ def test_grouped_linear_arguments_rejected(lib, kw, want):
     (dict(wq=None), BAD), (dict(ws=None), BAD), (dict(xq=P + 8), BAD), (dict(wq=P + 8), BAD), (dict(xs=P + 2), BAD),
     (dict(ws=P + 1), BAD), (dict(xg=P + 2), BAD), (dict(wg=P + 2), BAD),
     (dict(fmt=moe.MOE_FP4_MXFP4), BAD),                                # second scales belong to NVFP4
+    (dict(x=P, x_type=F32), UNS), (dict(x=P + 1), BAD), (dict(x=P, x_stride=511), BAD), (dict(x=P, xg=None), BAD),
 ])
 def test_linear_fp4_arguments_rejected(lib, kw, want):
     assert lib.moe_linear_fp4(_fp4(**kw), None) == want

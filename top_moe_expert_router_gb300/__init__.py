@@ -115,8 +115,8 @@ class MoeGroupedLinearArgs(ctypes.Structure):
 class MoeLinearFp4Args(ctypes.Structure):
     _fields_ = [
         ("fmt", ctypes.c_int), ("groups", ctypes.c_int), ("M", ctypes.c_int), ("N", ctypes.c_int),
-        ("K", ctypes.c_int), ("offsets", ctypes.c_void_p), ("xq", ctypes.c_void_p), ("xs", ctypes.c_void_p),
-        ("xg", ctypes.c_void_p), ("wq", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("wg", ctypes.c_void_p),
+        ("K", ctypes.c_int), ("offsets", ctypes.c_void_p), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+        ("x_type", ctypes.c_int), ("xq", ctypes.c_void_p), ("xs", ctypes.c_void_p), ("xg", ctypes.c_void_p), ("wq", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("wg", ctypes.c_void_p),
         ("wg_cols", ctypes.c_int), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_type", ctypes.c_int),
         ("y_stride", ctypes.c_int64),
     ]
@@ -480,12 +480,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None) or torch.cuda.caching_allocator_delete
 
 # The argument structures as bytes, in a quarter of the time that a ctypes structure takes to fill.
 _PACK = {MoeRouteDesc: struct.Struct("@iiiPiiiif4x"), MoeNormArgs: struct.Struct("@6P5q5if"),
          MoeW4Args: struct.Struct("@5iPPiPPPiqPqiPPiq"), MoeQuantizeFp4Args: struct.Struct("@iiPPqqPiiiPPP"),
          MoeDequantizeFp4Args: struct.Struct("@iiPPPiiiPq"), MoeGroupedLinearArgs: struct.Struct("@5iPPqPPPiq"),
-         MoeLinearFp4Args: struct.Struct("@5i7PiPPiq")}
+         MoeLinearFp4Args: struct.Struct("@5iPPqi6PiPPiq")}
 
 
 def _packer(cls):
@@ -505,8 +506,8 @@ _ENTRIES = ("moe_route_logits", "moe_add_rmsnorm", "moe_linear_w4", "moe_quantiz
 _entries = None
 
 
-def _entry(i):
-    """The C entry _ENTRIES[i], which takes its structure as bytes."""
+def _load_entries():
+    """The C entries _ENTRIES, which take their structures as bytes."""
     global _entries
     if _entries is None:
         lib = load()
@@ -515,7 +516,11 @@ def _entry(i):
             fn.argtypes = [ctypes.c_char_p, *typed.argtypes[1:]]
             fn.restype = typed.restype
         _entries = fns
-    return _entries[i]
+    return _entries
+
+
+def _entry(i):
+    return (_entries or _load_entries())[i]
 
 
 def _addr(t):
@@ -774,9 +779,7 @@ def hold_linear_w4(hold: bool):
 # -- 4-bit floats, and products by expert ----------------------------------------
 _HALFS = (torch.bfloat16, torch.float16)
 _FP4 = {"nvfp4": (MOE_FP4_NVFP4, 16), "mxfp4": (MOE_FP4_MXFP4, 32)}
-
-
-_U8 = torch.uint8
+_U8, _F32 = torch.uint8, torch.float32
 
 
 def _fp4_fmt(q, s):
@@ -794,6 +797,7 @@ def _fp4_fmt(q, s):
 
 # These calls take a few microseconds on the GPU, and most of their time on the host is that of looking at their
 # arguments: what is usual is tested in one condition, and looked at one by one, for the message, where that fails.
+
 
 def quantize_fp4(x, fmt="nvfp4", *, up=None, rows=None, out=None, stream=None):
     """Rows [T, K] (bf16 or f16) to microscaled 4-bit floats (moe_quantize_fp4) -> (q, s, g): codes [R, K/2] uint8, the
@@ -834,8 +838,8 @@ def quantize_fp4(x, fmt="nvfp4", *, up=None, rows=None, out=None, stream=None):
         up_at, up_ld = _rows("up", up, x.dtype, (T, K), index)
     args = _pack_quant(code, _DTYPE[x.dtype], x.data_ptr(), up_at, K if x.is_contiguous() else _row_stride("x", x), up_ld,
                        rows_at, T, R, K, q.data_ptr(), s.data_ptr(),
-                       0 if g is None else _whole("g", g, torch.float32, (R,), index))
-    _run(_entry(3), index, _raw_stream(index) if stream is None else stream.cuda_stream, (args,), "moe_quantize_fp4")
+                       0 if g is None else _whole("g", g, _F32, (R,), index))
+    _run1(3, index, args, stream)
     return q, s, g
 
 
@@ -858,11 +862,31 @@ def dequantize_fp4(q, s, g=None, *, dtype=None, out=None, stream=None):
         _whole("s", s, _U8, (R, scales), index)
     if g is not None:
         per_row = 1 if g.numel() != 1 else 0
-        g_at = _whole("g", g, torch.float32, (R if per_row else 1,), index)
-    out_at, out_ld = _rows("out", out, out.dtype, (R, K), index)
+        g_at = _whole("g", g, _F32, (R if per_row else 1,), index)
+    out_at, out_ld = _result_rows(out, R, K, index)
     args = _pack_dequant(code, _DTYPE[out.dtype], q.data_ptr(), s.data_ptr(), g_at, per_row, R, K, out_at, out_ld)
-    _run(_entry(4), index, _raw_stream(index) if stream is None else stream.cuda_stream, (args,), "moe_dequantize_fp4")
+    _run1(4, index, args, stream)
     return out
+
+
+def _result_rows(out, rows, cols, index):
+    """The address of a result and the elements from one of its rows to the next, its shape and device checked."""
+    if out.is_contiguous() and out.get_device() == index and out.shape == (rows, cols):
+        return out.data_ptr(), cols
+    return _rows("out", out, out.dtype, (rows, cols), index)
+
+
+def _run1(i, index, args, stream):
+    """C entry i with its packed arguments on `stream` (None: the current one) of device `index`."""
+    fn = (_entries or _load_entries())[i]
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _device():
+        status = fn(args, st)
+    else:
+        with torch.cuda.device(index):
+            status = fn(args, st)
+    if status != MOE_OK:
+        raise MoeError(status, _ENTRIES[i])
 
 
 def _offsets(offsets, E, index):
@@ -887,16 +911,16 @@ def grouped_linear(x, w, offsets, *, bias=None, out=None, out_dtype=None, stream
         raise ValueError("out_dtype and out differ")
     if out.dtype not in _FLOATS:
         raise ValueError(f"out: type {out.dtype} is not supported")
-    out_at, out_ld = _rows("out", out, out.dtype, (M, N), index)
+    out_at, out_ld = _result_rows(out, M, N, index)
     if not (w.dtype is x.dtype and w_cols == K and w.get_device() == index and w.is_contiguous()):
         _whole("w", w, x.dtype, (E, N, K), index)
     if offsets is None:
         raise ValueError("offsets are needed")
     args = _pack_grouped(_DTYPE[x.dtype], E, M, N, K, _offsets(offsets, E, index), x.data_ptr(),
                          K if x.is_contiguous() else _row_stride("x", x), w.data_ptr(),
-                         0 if bias is None else _whole("bias", bias, torch.float32, (E, N), index), out_at,
-                         _DTYPE[out.dtype], out_ld)
-    _run(_entry(5), index, _raw_stream(index) if stream is None else stream.cuda_stream, (args,), "moe_grouped_linear")
+                         0 if bias is None else _whole("bias", bias, _F32, (E, N), index), out_at, _DTYPE[out.dtype],
+                         out_ld)
+    _run1(5, index, args, stream)
     return out
 
 
@@ -904,16 +928,11 @@ def _linear_fp4(x, q, s, g, offsets, bias, out, out_dtype, stream):
     code, K, shape = _fp4_fmt(q, s)
     mx = code == MOE_FP4_MXFP4
     scales = K // (32 if mx else 16)
-    if offsets is None:
-        if len(shape) != 2:
-            raise ValueError("q must be [N, K/2], or [E, N, K/2] with offsets")
-        E, N = 1, shape[0]
-        lead = (N,)
-    else:
-        if len(shape) != 3:
-            raise ValueError("q must be [E, N, K/2] with offsets")
-        E, N, _ = shape
-        lead = (E, N)
+    if len(shape) != (2 if offsets is None else 3):
+        raise ValueError("q must be [N, K/2], or [E, N, K/2] with offsets")
+    lead = shape[:-1]
+    N = lead[-1]
+    E = 1 if offsets is None else lead[0]
     codes = not isinstance(x, torch.Tensor)
     if codes:
         x, xs, xg = x
@@ -928,52 +947,47 @@ def _linear_fp4(x, q, s, g, offsets, bias, out, out_dtype, stream):
         raise ValueError("g belongs to NVFP4")
     g_at = cols = 0
     if g is not None:
-        cols = 1 if g.numel() != E else 0
-        g_at = _whole("g", g, torch.float32, lead if cols else (E,), index)
+        cols = 1 if g.dim() == 2 or (offsets is None and g.numel() != 1) else 0
+        g_at = _whole("g", g, _F32, lead if cols else (E,), index)
     if out is None:
         out = _empty((M, N), out_dtype or (torch.bfloat16 if codes else x.dtype), x.device, stream)
     elif out_dtype is not None and out_dtype != out.dtype:
         raise ValueError("out_dtype and out differ")
-    if out.dtype not in _FLOATS:
+    y_type = _DTYPE.get(out.dtype, MOE_T_E4M3)
+    if y_type == MOE_T_E4M3:
         raise ValueError(f"out: type {out.dtype} is not supported")
-    out_at, out_ld = _rows("out", out, out.dtype, (M, N), index)
-    st = _raw_stream(index) if stream is None else stream.cuda_stream
-    off_at = 0 if offsets is None else _offsets(offsets, E, index)
+    out_at, out_ld = _result_rows(out, M, N, index)
     if not (q.dtype is _U8 is s.dtype and q.get_device() == index == s.get_device() and q.is_contiguous()
             and s.is_contiguous() and s.shape[:-1] == lead):
         _whole("q", q, _U8, shape, index)
         _whole("s", s, _U8, (*lead, scales), index)
-    tail = (q.data_ptr(), s.data_ptr(), g_at, cols, 0 if bias is None else _whole("bias", bias, torch.float32, lead, index), out_at,
-            _DTYPE[out.dtype], out_ld)
+    off_at = 0 if offsets is None else _offsets(offsets, E, index)
+    bias_at = 0 if bias is None else _whole("bias", bias, _F32, lead, index)
     if codes:
         if not (xs.dtype is _U8 and xs.get_device() == index and x.is_contiguous() and xs.is_contiguous()
                 and xs.shape == (M, scales)):
             _whole("x codes", x, _U8, (M, K // 2), index)
             _whole("x scales", xs, _U8, (M, scales), index)
-        args = _pack_fp4(code, E, M, N, K, off_at, x.data_ptr(), xs.data_ptr(),
-                         0 if xg is None else _whole("x g", xg, torch.float32, (M,), index), *tail)
-        _run(_entry(6), index, st, (args,), "moe_linear_fp4")
+        _run1(6, index, _pack_fp4(code, E, M, N, K, off_at, 0, 0, 0, x.data_ptr(), xs.data_ptr(),
+                                  0 if xg is None else _whole("x g", xg, _F32, (M,), index), q.data_ptr(), s.data_ptr(),
+                                  g_at, cols, bias_at, out_at, y_type, out_ld), stream)
         return out
-    if M == 0 or K % 64:                                       # nothing to do, or refused there
-        _run(_entry(6), index, st, (_pack_fp4(code, E, M, N, K, off_at, 0, 0, 0, *tail),), "moe_linear_fp4")
-        return out
-    x_ld = K if x.is_contiguous() else _row_stride("x", x)
     # the tokens' codes and scales in memory of the stream that the kernels run on: every stream and captured graph has
     # its own
-    n_q, n_s = M * K // 2, (M * scales + 15) // 16 * 16
-    size = n_q + n_s + (0 if mx else 4 * M)
+    x_ld = K if x.is_contiguous() else _row_stride("x", x)
+    n_q, n_s = (M * K // 2 + 15) // 16 * 16, (M * scales + 15) // 16 * 16
+    size = n_q + n_s + 4 * M + 16
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
     if _raw_alloc is not None and index == _device():
         ws = _raw_alloc(size, st)
     else:
         ws = torch.cuda.caching_allocator_alloc(size, index, st)
     try:
-        ws_g = 0 if mx else ws + n_q + n_s
-        quant = _pack_quant(code, _DTYPE[x.dtype], x.data_ptr(), 0, x_ld, 0, 0, M, M, K, ws, ws + n_q, ws_g)
-        _run(_entry(3), index, st, (quant,), "moe_quantize_fp4")
-        args = _pack_fp4(code, E, M, N, K, off_at, ws, ws + n_q, ws_g, *tail)
-        _run(_entry(6), index, st, (args,), "moe_linear_fp4")
+        _run1(6, index, _pack_fp4(code, E, M, N, K, off_at, x.data_ptr(), x_ld, _DTYPE[x.dtype], ws, ws + n_q,
+                                  0 if mx else ws + n_q + n_s, q.data_ptr(), s.data_ptr(), g_at, cols, bias_at, out_at,
+                                  y_type, out_ld), stream)
     finally:
-        torch.cuda.caching_allocator_delete(ws)
+        _raw_free(ws)
     return out
 
 

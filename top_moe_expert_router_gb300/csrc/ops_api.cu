@@ -303,6 +303,20 @@ moe_status moe_linear_fp4(const moe_linear_fp4_args *l, void *stream) {
     if (misaligned(l->xq, 16) || misaligned(l->wq, 16) || misaligned(l->xs, 4) || misaligned(l->ws, 4) ||
         misaligned(l->xg, 4) || misaligned(l->wg, 4))
         return MOE_ERR_INVALID_ARG;
+    if (l->x) {
+        moe_quantize_fp4_args n{};
+        n.fmt = l->fmt;
+        n.type = l->x_type;
+        n.x = l->x;
+        n.x_stride = l->x_stride;
+        n.T = n.R = l->M;
+        n.K = l->K;
+        n.q = l->xq;
+        n.s = l->xs;
+        n.g = l->xg;
+        const moe_status q = moe_quantize_fp4(&n, stream);
+        if (q != MOE_OK) return q;
+    }
     ProdArgs a{};
     a.groups = l->groups;
     a.offsets = l->offsets;
