@@ -27,9 +27,13 @@
 // What bounds it: with few rows, or ragged groups, the stream of the weights
 // (32768 rows by 256 experts of 1536 x 4096: bf16 530 us, NVFP4 165 us, 1.00 and
 // 0.96 of the copy rate); with many, 16 bits: the MMAs (4096 x 8192 x 4096 bf16
-// 131 us, 2.10 PFLOP/s); 4 bits: shared memory, through which a stage's 28 KB of
-// operands pass twice and its 5 KB of scales five times (4096 x 8192 x 8192 NVFP4
-// 100 us, 5.5 PFLOP/s; without the scales 80 us, without the stores too 72).
+// 131 us, 2.10 PFLOP/s); 4 bits: issue slots. The warp that issues the MMAs has 200
+// ns for a stage, and shares its scheduler with two that bring scales and two of
+// the epilogue (4096 x 8192 x 8192 NVFP4 98 us, 5.6 PFLOP/s; without the scales 82
+// us, without the stores 88, without both 73, without loads and both 70; without
+// loads alone 96). Tried there: the warps with the scales waiting for the operands
+// too, so that the MMAs take one wait and one commit a stage (110 us), waits that
+// spin (103 to 121 us).
 #pragma once
 
 #include <cuda.h>
@@ -96,12 +100,13 @@ struct ProdShape {
     static constexpr int kStages = kRoom < 10 ? kRoom : 10;
     static constexpr uint32_t kSmem = 1024 + kStages * kStage + kScales + kOut + kParts + kMeta;
     static constexpr int kThreads = kFp4 ? 640 : 320;
-    // tensor memory: two accumulators, then two or four buffers of scales (16 columns for
-    // the weights, kBCols for each of the four MMAs of a stage for x)
-    static constexpr int kBCols = TN > 128 ? 8 : 4;
+    // tensor memory: two accumulators, then up to four buffers of scales (16 columns for the weights, kBCols for each of
+    // the four MMAs of a stage for x)
+    static constexpr int kBCols = TN > 128 ? TN / 32 : 4;
     static constexpr uint32_t kScaleCols = 16 + 4 * kBCols;
     static constexpr uint32_t kScaleAt = 2 * TN;
-    static constexpr int kScaleBufs = kScaleAt + 4 * kScaleCols <= kTmemCols ? 4 : 2;
+    static constexpr int kScaleRoom = (int)((kTmemCols - kScaleAt) / kScaleCols);
+    static constexpr int kScaleBufs = !kFp4 ? 1 : kScaleRoom < 4 ? kScaleRoom : 4;
     static_assert(!kFp4 || kScaleAt + kScaleBufs * kScaleCols <= kTmemCols, "tensor memory");
     static_assert(2 * TN <= (int)kTmemCols, "tensor memory");
 };
@@ -291,6 +296,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) 
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t v[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -940,6 +950,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                     for (int i = 0; i < n; ++i, ++it) {
                         if ((it & 1) != group) continue;
                         uint32_t va[16], vb[4 * S::kBCols];
+                        static_assert(S::kBCols == 4 || S::kBCols == 6, "columns that the stores below cover");
                         auto words = [&](int row, int first_row, uint32_t w[4]) {
                             if constexpr (KIND == PROD_NVFP4) {
                                 const uint4 v = *reinterpret_cast<const uint4 *>(ring + row * QB + swizzled(row, i * SB));
@@ -979,7 +990,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                         const uint32_t to = ((uint32_t)(q * 32) << 16) + S::kScaleAt + (uint32_t)(it % NB) * S::kScaleCols;
                         tmem_st16(to, va);
                         tmem_st16(to + 16, vb);
-                        if constexpr (S::kBCols == 8) tmem_st16(to + 32, vb + 16);
+                        if constexpr (S::kBCols == 6) tmem_st8(to + 32, vb + 16);
                         tmem_st_wait();
                         tc_fence_before();
                         warp_arrive<CG>(&sfull[it % NB]);
