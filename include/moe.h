@@ -519,8 +519,8 @@ moe_status moe_linear_fp4(const moe_linear_fp4_args *args, void *stream);
  * stream is being captured. */
 moe_status moe_products_status(void *stream);
 
-/* Test hook: the products launched while hold != 0 copy no operands, so that
- * their waits run out. No GPU work. */
+/* Test hook: the products launched while hold is 1 copy no operands, so that
+ * their waits run out; while it is 2, every second CTA copies none. No GPU work. */
 moe_status moe_debug_hold_products(int hold);
 
 moe_status moe_layer_destroy(moe_layer *layer);

@@ -399,6 +399,8 @@ GROUPS = [
     ([3] * 512, 64, 64), ([0, 0, 0], 128, 128), ([40] * 12, 1000, 1016), ([900, 30], 640, 2048),
     # sums in parts: one tile a cluster, several parts, a last part that is shorter
     ([3], 384, 4096), ([32], 260, 2040), ([9], 4096, 4096),
+    # ... and more tiles than the clusters that run at a time
+    ([829] + 35 * [1], 100, 8192),
     # tiles of 64 and 128 rows, pairs of CTAs
     ([200], 4096, 1024), ([60, 0, 70], 1024, 1024), ([500, 300], 2048, 512), ([1000], 4096, 640), ([257, 511, 700], 2000, 1032),
 ]
@@ -575,10 +577,11 @@ def test_streams_and_graphs(gpu_lib):
     assert gpu_lib.products_status() == gpu_lib.MOE_OK
 
 
-@pytest.mark.parametrize("counts,N,K", [([20, 0, 300], 300, 320), ([3, 0, 5], 300, 4096), ([700, 0, 900], 2056, 768)])
+@pytest.mark.parametrize("counts,N,K", [([20, 0, 300], 300, 320), ([3, 0, 5], 300, 4096), ([700, 0, 900], 2056, 768),
+                                        ([2000, 0, 2500], 2056, 2048), ([6000, 0, 6500], 1000, 64)])
 def test_waits_that_run_out(gpu_lib, counts, N, K):
     """Products that copy no operands: NaN in their rows and only there, the status says so once, and the next call is as
-    before. (Tiles of one CTA, sums in parts, pairs of CTAs.)"""
+    before. (Tiles of one CTA, sums in parts, pairs of CTAs, and many tiles for each.)"""
     g = gen(14)
     off = offsets_of(counts, first=2)
     end = 2 + sum(counts)
@@ -600,6 +603,39 @@ def test_waits_that_run_out(gpu_lib, counts, N, K):
         assert gpu_lib.products_status() == gpu_lib.MOE_ERR_TIMEOUT
         assert gpu_lib.products_status() == gpu_lib.MOE_OK
         assert torch.equal(call(torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")), good)
+
+
+@pytest.mark.parametrize("counts,N,K,clusters", [
+    ([20, 0, 300], 300, 320, (False, False)), ([3, 0, 5], 300, 4096, (True, True)),
+    ([700, 0, 900], 2056, 768, (True, False)), ([2000, 0, 2500], 2056, 2048, (True, True)),
+    ([829] + 35 * [1], 100, 8192, (True, True))])
+def test_waits_that_run_out_in_every_second_cta(gpu_lib, counts, N, K, clusters):
+    """As above where only every second CTA copies none: what comes out is right or NaN, and NaN throughout where the CTAs
+    of a cluster need each other (of 16-bit operands, of 4-bit ones). Second and last: sums in parts, there with several
+    tiles for a CTA; third and fourth: pairs."""
+    g = gen(15)
+    E, off = len(counts), offsets_of(counts, first=2)
+    end = 2 + sum(counts)
+    M = end + 8
+    x, w = randn(g, M, K).to(torch.bfloat16), randn(g, E, N, K).to(torch.bfloat16)
+    ws = [v.view(E, N, *v.shape[1:]) for v in gpu_lib.quantize_fp4(w.view(E * N, K))]
+    xq = gpu_lib.quantize_fp4(x)
+    for cluster, call in zip(clusters, (lambda o: gpu_lib.grouped_linear(x, w, off, out=o),
+                                        lambda o: gpu_lib.grouped_linear_fp4(xq, *ws, off, out=o))):
+        good = call(torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda"))
+        held = torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")
+        gpu_lib.hold_products(2)
+        try:
+            call(held)
+            torch.cuda.synchronize()
+        finally:
+            gpu_lib.hold_products(0)
+        none = torch.isnan(held)
+        assert none.any() and torch.equal(held[~none], good[~none]) and not none[:2].any() and not none[end:].any()
+        assert none[2:end].all() or not cluster
+        assert gpu_lib.products_status() == gpu_lib.MOE_ERR_TIMEOUT
+        assert torch.equal(call(torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")), good)
+        assert gpu_lib.products_status() == gpu_lib.MOE_OK
 
 
 FIRST_USE = """

@@ -1018,6 +1018,6 @@ def products_status(stream=None) -> int:
     return load().moe_products_status(_stream(stream))
 
 
-def hold_products(hold: bool):
-    """Test hook: make the waits of those products run out, or restore them."""
-    _check(load().moe_debug_hold_products(1 if hold else 0), "moe_debug_hold_products")
+def hold_products(hold: int):
+    """Test hook: make the waits of those products run out (1: in all CTAs, 2: in every second), or restore them (0)."""
+    _check(load().moe_debug_hold_products(int(hold)), "moe_debug_hold_products")

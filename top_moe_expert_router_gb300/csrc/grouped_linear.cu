@@ -6,8 +6,8 @@
 namespace moe {
 
 static std::atomic<int> prod_hold{0};
-bool products_held() { return prod_hold.load(std::memory_order_relaxed) != 0; }
-void hold_products(bool hold) { prod_hold.store(hold, std::memory_order_relaxed); }
+int products_held() { return prod_hold.load(std::memory_order_relaxed); }
+void hold_products(int hold) { prod_hold.store(hold, std::memory_order_relaxed); }
 
 cudaError_t linear_fp4_errors(cudaStream_t st, uint32_t *bits);  // linear_fp4.cu
 

@@ -151,7 +151,7 @@ struct ProdArgs {
 cudaError_t launch_grouped_linear(const ProdArgs &a, const void *x, int64_t x_ld, const void *w, cudaStream_t st);
 cudaError_t launch_linear_fp4(ProdArgs a, bool nvfp4, const uint8_t *xq, const uint8_t *wq, cudaStream_t st);
 cudaError_t products_errors(cudaStream_t st, uint32_t *bits);
-void hold_products(bool hold);
+void hold_products(int hold);
 
 #ifdef __CUDACC__
 

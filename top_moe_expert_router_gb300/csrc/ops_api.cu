@@ -342,7 +342,7 @@ moe_status moe_products_status(void *stream) {
 }
 
 moe_status moe_debug_hold_products(int hold) {
-    hold_products(hold != 0);
+    hold_products(hold);
     return MOE_OK;
 }
 

@@ -51,7 +51,7 @@ constexpr int kProdRows = 128;           // weight rows of a tile
 constexpr int kProdBand = 12;            // weight tiles of a band
 constexpr uint32_t kProdABytes = kProdRows * 128;
 
-bool products_held();                    // test hook: copy no operands
+int products_held();                     // test hook: 1 copy no operands, 2 every second CTA copies none
 
 #ifdef __CUDACC__
 
@@ -637,10 +637,12 @@ __device__ __forceinline__ void send4(uint32_t to, const uint32_t v[4], uint32_t
 // the owners as asynchronous stores that a barrier there counts (parts[sender][column of the share][row]); the owners add
 // them in the order of their ranks and store. Two such buffers by turns: whoever sends a tile's sums has read, as all
 // warps of the CTA have, those of the tile before, so nobody writes where another still reads.
+// `together`: whether this warp still takes part. Once a wait for the others' sums has run out it stays away from the barriers,
+// whose phases no longer fit: arriving at one twice in a phase is undefined.
 template <bool FP4, int TN>
 __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, TN> &sc,
                                                  uint32_t tbase, int n, bool ok, float *parts, int part, uint64_t *pfull,
-                                                 int lt, uint32_t *err, volatile int *abort_flag) {
+                                                 int lt, bool &together, uint32_t *err, volatile int *abort_flag) {
     static_assert(TN == 32, "one chunk of rows");
     const int ks = a.ks, lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
     const int local = q * 32 + lane, share = (32 + ks - 1) / ks * 4;
@@ -649,7 +651,7 @@ __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTi
     float *buf = parts + (lt & 1) * (120 * kPartRow);
     uint64_t *bar = pfull + (lt & 1);
     named_bar(2, 128);                           // the tile before the last has been read from this buffer
-    if (q == 0 && lane == 0) {
+    if (together && q == 0 && lane == 0) {
         const int own = (32 * (part + 1) / ks - 32 * part / ks) * 4;
         mbar_arrive_expect_tx(bar, (uint32_t)((ks - 1) * own * quads * 16));
     }
@@ -663,9 +665,10 @@ __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTi
         tmem_ld4(tbase + 4 * i, v);
         tmem_ld_wait();
         if (!ok) v[0] = v[1] = v[2] = v[3] = 0x7FFFFFFFu;
-        if (owner != part) send4(there + 16 * i, v, bar_there);
+        if (together && owner != part) send4(there + 16 * i, v, bar_there);
     }
-    ok &= warp_wait<true>(bar, (lt >> 1) & 1, err, abort_flag);
+    together = together && warp_wait<true>(bar, (lt >> 1) & 1, err, abort_flag);
+    ok &= together;
     asm volatile(                                // (the same once more, in the scope of the cluster)
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
@@ -722,6 +725,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     uint64_t *lfull = sempty + 4, *lempty = lfull + 4, *pfull = lempty + 4, *done = pfull + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const bool held = a.hold == 1 || (a.hold == 2 && (blockIdx.x & 1));
     ProdGroups gr;
     int32_t *scratch = reinterpret_cast<int32_t *>(meta + 512);
     gr.start = scratch + 64;
@@ -789,7 +793,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------- TMA producer -------------------------------
-        if (!a.hold) {
+        if (!held) {
             const uint32_t on = elect_lane();
             int it = 0;
             bool ok = true;
@@ -816,7 +820,9 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                 }
             }
             // every load issued must land before the CTA exits (a pair's are counted, and waited for, by the leader)
-            for (int j = rank ? it : it > NS ? it - NS : 0; j < it; ++j) mbar_wait(&full[j % NS], (j / NS) & 1, err);
+            // -- one limit for all of them
+            for (int j = rank ? it : it > NS ? it - NS : 0; j < it; ++j)
+                if (!mbar_wait(&full[j % NS], (j / NS) & 1, err)) break;
         }
     } else if (warp == 1) {
         // -------------------------------- MMA issuer --------------------------------
@@ -881,13 +887,15 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         // --------------------------------- epilogue ---------------------------------
         const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter of this warp, its share of the columns
         int lt = 0;
+        bool ok = true;                      // once a wait ran out, phases tell nothing: all later tiles are NaN
+        [[maybe_unused]] bool together = true;
         ProdWalk<TN> walk(first);
         for (; walk.tile < ntiles; walk.tile += step, ++lt) {
             const ProdTile t = walk.at(gr, nw);
             const int b = lt & 1;
             const int n0 = (t.w * CG + rank) * kProdRows, n = n0 + q * 32 + lane;
             const ProdScales<S::kFp4, TN> sc(a, t, n);
-            const bool ok = warp_wait<S::kFp4>(&tfull[b], (lt >> 1) & 1, err, abort_flag);
+            ok = ok && warp_wait<S::kFp4>(&tfull[b], (lt >> 1) & 1, err, abort_flag);
             tc_fence_after();
             const uint32_t at = ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
             unsigned char *stage = staged + half * 8192;
@@ -897,7 +905,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                 if (ks > 1) {
                     if (lt == 0) cluster_wait();
                     // (32 rows are the first four warps')
-                    if (!half) prod_store_split<S::kFp4, TN>(a, t, sc, at, n, ok, parts, part, pfull, lt, err, abort_flag);
+                    if (!half)
+                        prod_store_split<S::kFp4, TN>(a, t, sc, at, n, ok, parts, part, pfull, lt, together, err, abort_flag);
                     stored = true;
                 }
             }
@@ -1000,7 +1009,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             }
         } else if (a.s_copy >= 16) {
             // ----------------------- scales to shared memory, by TMA --------------------
-            if (warp == 18 && !a.hold) {
+            if (warp == 18 && !held) {
                 const uint32_t on = elect_lane(), ring = smem_u32(scales);
                 int qr = 0;
                 bool ok = true;
@@ -1023,7 +1032,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                                        smem_u32(bar), on);
                     }
                 }
-                for (int j = qr > NQ ? qr - NQ : 0; j < qr; ++j) mbar_wait(&lfull[j % NQ], (j / NQ) & 1, err);
+                for (int j = qr > NQ ? qr - NQ : 0; j < qr; ++j)
+                    if (!mbar_wait(&lfull[j % NQ], (j / NQ) & 1, err)) break;
             }
         } else {
             // ------------- scales to shared memory, where their rows are not aligned -----
@@ -1088,6 +1098,10 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         if (CG == 1 && (warp < 2 || warp >= 10 || first >= ntiles)) cluster_wait();
         __syncwarp();
         cluster_sync_all();
+        // where a wait ran out, sums or operands that nobody waited for may still be on their way here: they have 0.1 ms
+        if (*abort_flag)
+            for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 100000ull;) {
+            }
     }
     if (warp == 1) {
         tc_fence_after();
