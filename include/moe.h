@@ -431,10 +431,11 @@ typedef enum { MOE_FP4_NVFP4 = 0, MOE_FP4_MXFP4 = 1 } moe_fp4_fmt;
  *   MXFP4: s = floor(log2 max|v of the block|) - 2, clamped to [-127, 127], as
  *     s + 127, 0 for a block of zeros; codes E2M1(v / 2^s), saturating.
  * Nearest, ties to even, of exact quotients (with up: of the fp32 v, which
- * is within (5 + 1.2 |x|) 2^-23 of itself). A row (NVFP4) or block (MXFP4) that holds an infinity
- * or NaN gets codes 0 and NaN as g (255 as s): everything computed from it is
- * NaN. K a multiple of 64, K <= 32768; q 16-byte, s 4-byte aligned, both
- * without gaps between rows. No output overlaps an input. */
+ * is within (5 + 1.2 |x|) 2^-23 of itself for x > -87.3; below, silu(x) is 0).
+ * A row (NVFP4) or block (MXFP4) that holds an infinity or NaN gets codes 0 and
+ * NaN as g (255 as s): everything computed from it is NaN. K a multiple of 64,
+ * K <= 32768; q 16-byte, s 4-byte aligned, both without gaps between rows. No
+ * output overlaps an input. */
 typedef struct {
     moe_fp4_fmt fmt;
     moe_dtype type;      /* of x and up: bf16 or f16 */

@@ -235,6 +235,22 @@ def test_quantize_silu(gpu_lib, R, K, dtype, fmt):
     assert ((c == 0) | (torch.sign(c) == torch.sign(v))).all()
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quantize_silu_far_below_zero(gpu_lib, dtype, fmt):
+    """silu(x) of x below -87.3, less than 2^-119, is 0 whatever it is multiplied by; just above it is not."""
+    least, most = torch.finfo(DT[dtype]).min, torch.finfo(DT[dtype]).max
+    x = torch.tensor([-87.5, -88.0, -89.0, -100.0, -1000.0, least], device="cuda").repeat_interleave(64).view(6, 64).to(DT[dtype])
+    up = torch.full_like(x, most)
+    assert (gpu_lib.dequantize_fp4(*gpu_lib.quantize_fp4(x, fmt, up=up), dtype=torch.float32) == 0).all()
+    x[:, 5] = -80.0                                          # the largest of its row and block: 6 or 4 times a scale
+    q, s, g = gpu_lib.quantize_fp4(x, fmt, up=up)
+    c = code_values(q)
+    if dtype == "bf16":
+        assert (c[:, 5] <= -4).all()
+    assert (c[:, :5] == 0).all() and (c[:, 6:] == 0).all()
+
+
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 def test_dequantize_every_code_and_scale(gpu_lib, out):
     t = DT[out]
@@ -478,6 +494,13 @@ def test_grouped_rows_left_alone(gpu_lib):
         kept = buf.clone()
         kept[1:M + 1, 5:N + 5] = -3.0
         assert (kept == -3).all()
+    # groups that overlap a thousandfold are more tiles than M rows have: none is taken
+    E, M, N = 512, 512, 256
+    x, w = randn(g, M, 64).to(torch.bfloat16), randn(g, E, N, 64).to(torch.bfloat16)
+    off = torch.tensor([0, M] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    y = torch.full((M, N), -3.0, dtype=torch.float32, device="cuda")
+    gpu_lib.grouped_linear(x, w, off, out=y)
+    assert (y == -3).all()
     assert gpu_lib.products_status() == gpu_lib.MOE_OK
 
 

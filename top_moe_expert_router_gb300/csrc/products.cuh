@@ -360,7 +360,7 @@ struct ProdWalk {
 };
 
 // Fills the tables; every thread of the CTA, one or two groups each. -> the number of tiles, 0 where offsets that run
-// backwards make them more than can be counted
+// backwards make them more than M rows can have: a ragged tile a group and M / TN full ones
 template <int TN>
 __device__ __forceinline__ int prod_groups(const ProdArgs &a, ProdGroups &gr, int nw, int32_t *scratch) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -403,7 +403,7 @@ __device__ __forceinline__ int prod_groups(const ProdArgs &a, ProdGroups &gr, in
         all += reinterpret_cast<const long long *>(scratch)[w];
         n += scratch[40 + w];
     }
-    if (all > 0x7FFFFFFF) all = n = 0;
+    if (all > ((long long)a.M / TN + min(a.groups, a.M)) * nw) all = n = 0;
     int at = (int)(end - sum), i = last - used;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
