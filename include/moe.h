@@ -447,8 +447,17 @@ typedef struct {
     uint8_t *q;          /* [R, K/2] */
     uint8_t *s;          /* [R, K/16] or [R, K/32] */
     float *g;            /* NVFP4: [R] */
+    void *workspace;     /* 16-byte aligned, or NULL */
+    size_t ws_bytes;
 } moe_quantize_fp4_args;
 moe_status moe_quantize_fp4(const moe_quantize_fp4_args *args, void *stream);
+
+/* Bytes of device workspace with which moe_quantize_fp4 is faster, 0 where it
+ * uses none: gathered rows that are many times the tokens take every token's
+ * codes from there. The results are the same without, it needs no
+ * initialisation and carries nothing from one call to the next. Looks at fmt, T,
+ * R, K and whether there are rows and up. No GPU work. */
+moe_status moe_quantize_fp4_workspace_size(const moe_quantize_fp4_args *args, size_t *bytes);
 
 /* What codes and scales stand for, in fp32 and rounded once to bf16, f16 or
  * fp32. g (NVFP4): [R], or one for all rows, or NULL (1). Alignment and limits

@@ -202,6 +202,58 @@ def test_quantize_gather_and_strides(gpu_lib, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("K,with_up", [(4096, False), (4160, False), (4224, True)])
+def test_quantize_rows_many_times_the_tokens(gpu_lib, K, with_up, fmt):
+    """So many rows that tokens are quantised once and copied: the codes of the tokens themselves, rows out of range as
+    they were; also captured, on two streams at once, with scales at any word. (Rows of scales of 16, 4 and 2 bytes.)"""
+    g = gen(K)
+    T, R, n = 37, 8200, BLOCK[fmt]
+    assert R * K >= 1 << 25
+    rows = torch.randint(0, T, (R,), generator=g, device="cuda", dtype=torch.int32)
+    rows[[0, 4000, R - 1]] = torch.tensor([-1, T, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    on = (rows >= 0) & (rows < T)
+    at = rows[on].long()
+    xs = [randn(g, T, K + 16).to(torch.bfloat16)[:, 3:K + 3] for _ in range(3)]
+    xs[1][5, 70] = NAN
+    up = randn(g, T, K).to(torch.bfloat16) if with_up else None
+    want = [gpu_lib.quantize_fp4(x, fmt, up=up) for x in xs]
+
+    def room():
+        s = torch.full((R * (K // n) + 16,), 0xA5, dtype=torch.uint8, device="cuda")[4:4 + R * (K // n)]
+        return (torch.full((R, K // 2), 0xA5, dtype=torch.uint8, device="cuda"), s.view(R, K // n),
+                torch.full((R,), -7.0, device="cuda") if fmt == "nvfp4" else None)
+
+    def same(got, k):
+        for o, w, kept in zip(got, want[k], (0xA5, 0xA5, -7.0)):
+            if o is not None:
+                assert torch.equal(o[on].view(torch.uint8), w[at].view(torch.uint8)) and (o[~on] == kept).all()
+
+    same(gpu_lib.quantize_fp4(xs[0], fmt, up=up, rows=rows, out=room()), 0)
+    new = gpu_lib.quantize_fp4(xs[1], fmt, up=up, rows=rows)
+    assert all(o is None or torch.equal(o[on].view(torch.uint8), w[at].view(torch.uint8)) for o, w in zip(new, want[1]))
+    outs, streams = [room() for _ in range(6)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        gpu_lib.quantize_fp4(xs[i % 3], fmt, up=up, rows=rows, out=o, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        same(o, i % 3)
+    held, graphs = [x.clone() for x in xs[:2]], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gpu_lib.quantize_fp4(held[i], fmt, up=up, rows=rows, out=outs[i])
+        graphs.append(graph)
+    for k in range(3):
+        for i in range(2):
+            held[i].copy_(xs[(k + i) % 3])
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            same(outs[i], (k + i) % 3)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("R,K", [(1, 64), (33, 1536), (5, 4160), (2, 12288)])
 def test_quantize_silu(gpu_lib, R, K, dtype, fmt):

@@ -39,6 +39,22 @@ def test_quantize_arguments_rejected(lib, kw, want):
     assert lib.moe_quantize_fp4(_quant(**kw), None) == want
 
 
+def test_quantize_workspace(lib):
+    """Asked for by rows that are many times the tokens alone; codes, scales in whole 16 bytes, and g of every token."""
+    need = ctypes.c_size_t(7)
+    size = lambda **kw: (lib.moe_quantize_fp4_workspace_size(_quant(**kw), ctypes.byref(need)), need.value)
+    assert size() == (OK, 0) and size(R=1 << 20, rows=None) == (OK, 0) and size(T=1 << 19, R=1 << 20) == (OK, 0)
+    assert size(R=1 << 20, T=3, K=64) == (OK, 3 * 32 + 16 + 12)
+    assert size(R=1 << 20, T=3, K=64, fmt=moe.MOE_FP4_MXFP4) == (OK, 3 * 32 + 16 + 12)
+    assert size(R=1 << 14, T=1 << 12, up=None) == (OK, (1 << 12) * (2048 + 256 + 4))
+    assert size(T=-1)[0] == BAD and size(R=-1)[0] == BAD and size(K=0)[0] == BAD and size(K=65)[0] == UNS and size(fmt=3)[0] == UNS
+    assert lib.moe_quantize_fp4_workspace_size(None, ctypes.byref(need)) == BAD
+    assert lib.moe_quantize_fp4_workspace_size(_quant(), None) == BAD
+    many = dict(R=1 << 20, T=3, K=64, workspace=P)
+    assert lib.moe_quantize_fp4(_quant(**many, ws_bytes=123), None) == BAD
+    assert lib.moe_quantize_fp4(_quant(**{**many, "workspace": P + 8}, ws_bytes=124), None) == BAD
+
+
 def _dequant(**kw):
     return _with(moe.MoeDequantizeFp4Args(moe.MOE_FP4_NVFP4, BF16, P, P, P, 1, 64, 4096, P, 4096), kw)
 

@@ -92,6 +92,7 @@ class MoeQuantizeFp4Args(ctypes.Structure):
         ("x_stride", ctypes.c_int64), ("up_stride", ctypes.c_int64), ("rows", ctypes.c_void_p),
         ("T", ctypes.c_int), ("R", ctypes.c_int), ("K", ctypes.c_int),
         ("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("g", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
     ]
 
 
@@ -175,6 +176,7 @@ def load(path: str | None = None):
             "moe_linear_w4_status": ([vp], st),
             "moe_debug_hold_linear_w4": ([i], st),
             "moe_quantize_fp4": ([ctypes.POINTER(MoeQuantizeFp4Args), vp], st),
+            "moe_quantize_fp4_workspace_size": ([ctypes.POINTER(MoeQuantizeFp4Args), ctypes.POINTER(ctypes.c_size_t)], st),
             "moe_dequantize_fp4": ([ctypes.POINTER(MoeDequantizeFp4Args), vp], st),
             "moe_grouped_linear": ([ctypes.POINTER(MoeGroupedLinearArgs), vp], st),
             "moe_linear_fp4": ([ctypes.POINTER(MoeLinearFp4Args), vp], st),
@@ -484,7 +486,7 @@ _raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None) or 
 
 # The argument structures as bytes, in a quarter of the time that a ctypes structure takes to fill.
 _PACK = {MoeRouteDesc: struct.Struct("@iiiPiiiif4x"), MoeNormArgs: struct.Struct("@6P5q5if"),
-         MoeW4Args: struct.Struct("@5iPPiPPPiqPqiPPiq"), MoeQuantizeFp4Args: struct.Struct("@iiPPqqPiiiPPP"),
+         MoeW4Args: struct.Struct("@5iPPiPPPiqPqiPPiq"), MoeQuantizeFp4Args: struct.Struct("@iiPPqqPiiiPPPPN"),
          MoeDequantizeFp4Args: struct.Struct("@iiPPPiiiPq"), MoeGroupedLinearArgs: struct.Struct("@5iPPqPPPiq"),
          MoeLinearFp4Args: struct.Struct("@5iPPqi6PiPPiq")}
 
@@ -836,10 +838,23 @@ def quantize_fp4(x, fmt="nvfp4", *, up=None, rows=None, out=None, stream=None):
     up_at = up_ld = 0
     if up is not None:
         up_at, up_ld = _rows("up", up, x.dtype, (T, K), index)
-    args = _pack_quant(code, _DTYPE[x.dtype], x.data_ptr(), up_at, K if x.is_contiguous() else _row_stride("x", x), up_ld,
-                       rows_at, T, R, K, q.data_ptr(), s.data_ptr(),
-                       0 if g is None else _whole("g", g, _F32, (R,), index))
-    _run1(3, index, args, stream)
+    values = (code, _DTYPE[x.dtype], x.data_ptr(), up_at, K if x.is_contiguous() else _row_stride("x", x), up_ld,
+              rows_at, T, R, K, q.data_ptr(), s.data_ptr(), 0 if g is None else _whole("g", g, _F32, (R,), index))
+    args = _pack_quant(*values, 0, 0)
+    if R <= T:                                                # (what may take scratch has more rows than tokens)
+        _run1(3, index, args, stream)
+        return q, s, g
+    need = ctypes.c_size_t(0)
+    _check(load().moe_quantize_fp4_workspace_size(MoeQuantizeFp4Args.from_buffer_copy(args), ctypes.byref(need)),
+           "moe_quantize_fp4")
+    if not need.value:
+        _run1(3, index, args, stream)
+        return q, s, g
+    ws = _scratch(need.value, index, stream)
+    try:
+        _run1(3, index, _pack_quant(*values, ws, need.value), stream)
+    finally:
+        _raw_free(ws)
     return q, s, g
 
 
@@ -887,6 +902,15 @@ def _run1(i, index, args, stream):
             status = fn(args, st)
     if status != MOE_OK:
         raise MoeError(status, _ENTRIES[i])
+
+
+def _scratch(size, index, stream):
+    """The address of memory of the stream that a call's kernels run on: every stream and captured graph has its own. For
+    _raw_free, once they are launched."""
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _raw_alloc is not None and index == _device():
+        return _raw_alloc(size, st)                            # what the next does, without its change of device
+    return torch.cuda.caching_allocator_alloc(size, index, st)
 
 
 def _offsets(offsets, E, index):
@@ -972,16 +996,9 @@ def _linear_fp4(x, q, s, g, offsets, bias, out, out_dtype, stream):
                                   0 if xg is None else _whole("x g", xg, _F32, (M,), index), q.data_ptr(), s.data_ptr(),
                                   g_at, cols, bias_at, out_at, y_type, out_ld), stream)
         return out
-    # the tokens' codes and scales in memory of the stream that the kernels run on: every stream and captured graph has
-    # its own
     x_ld = K if x.is_contiguous() else _row_stride("x", x)
     n_q, n_s = (M * K // 2 + 15) // 16 * 16, (M * scales + 15) // 16 * 16
-    size = n_q + n_s + 4 * M + 16
-    st = _raw_stream(index) if stream is None else stream.cuda_stream
-    if _raw_alloc is not None and index == _device():
-        ws = _raw_alloc(size, st)
-    else:
-        ws = torch.cuda.caching_allocator_alloc(size, index, st)
+    ws = _scratch(n_q + n_s + 4 * M + 16, index, stream)
     try:
         _run1(6, index, _pack_fp4(code, E, M, N, K, off_at, x.data_ptr(), x_ld, _DTYPE[x.dtype], ws, ws + n_q,
                                   0 if mx else ws + n_q + n_s, q.data_ptr(), s.data_ptr(), g_at, cols, bias_at, out_at,

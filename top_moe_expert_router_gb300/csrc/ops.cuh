@@ -124,7 +124,17 @@ struct DequantFp4Args {
     bool vec;                // rows of out may be written as 32-byte vectors (set by the launcher)
 };
 constexpr int kFp4MaxK = 32768;
-cudaError_t launch_quantize_fp4(QuantFp4Args a, cudaStream_t st);
+struct GatherFp4Args {
+    const uint8_t *q_from, *s_from;
+    const float *g_from;
+    const int32_t *rows;     // [R]
+    int T, R, q_bytes, s_bytes;
+    uint8_t *q, *s;
+    float *g;                // or null
+};
+// scratch: 16-byte aligned, of at least quantize_fp4_scratch's bytes, or null
+size_t quantize_fp4_scratch(const QuantFp4Args &a);
+cudaError_t launch_quantize_fp4(QuantFp4Args a, uint8_t *scratch, cudaStream_t st);
 cudaError_t launch_dequantize_fp4(DequantFp4Args a, cudaStream_t st);
 
 // Products of rows grouped by expert (products.cuh).

@@ -217,6 +217,20 @@ moe_status moe_linear_w4(const moe_w4_args *l, void *stream) {
     return status_of(launch_linear_w4(a, (cudaStream_t)stream));
 }
 
+moe_status moe_quantize_fp4_workspace_size(const moe_quantize_fp4_args *n, size_t *bytes) {
+    if (!n || !bytes || n->T < 0 || n->R < 0 || n->K < 1) return MOE_ERR_INVALID_ARG;
+    if ((n->fmt != MOE_FP4_NVFP4 && n->fmt != MOE_FP4_MXFP4) || n->K % 64 || n->K > kFp4MaxK) return MOE_ERR_UNSUPPORTED;
+    QuantFp4Args a{};
+    a.up = n->up;
+    a.rows = n->rows;
+    a.T = n->T;
+    a.R = n->R;
+    a.K = n->K;
+    a.nvfp4 = n->fmt == MOE_FP4_NVFP4;
+    *bytes = quantize_fp4_scratch(a);
+    return MOE_OK;
+}
+
 moe_status moe_quantize_fp4(const moe_quantize_fp4_args *n, void *stream) {
     if (!n || n->T < 0 || n->R < 0 || n->K < 1 || (!n->rows && n->R != n->T)) return MOE_ERR_INVALID_ARG;
     if ((n->fmt != MOE_FP4_NVFP4 && n->fmt != MOE_FP4_MXFP4) || !is_half_type(n->type) || n->K % 64 ||
@@ -226,7 +240,7 @@ moe_status moe_quantize_fp4(const moe_quantize_fp4_args *n, void *stream) {
     if (n->R == 0) return MOE_OK;
     if (!n->q || !n->s || (nvfp4 && !n->g) || (!n->x && n->T)) return MOE_ERR_INVALID_ARG;
     if (misaligned(n->x, 2) || misaligned(n->up, 2) || misaligned(n->rows, 4) || misaligned(n->q, 16) ||
-        misaligned(n->s, 4) || misaligned(n->g, 4))
+        misaligned(n->s, 4) || misaligned(n->g, 4) || misaligned(n->workspace, 16))
         return MOE_ERR_INVALID_ARG;
     if (n->x_stride < n->K || (n->up && n->up_stride < n->K)) return MOE_ERR_INVALID_ARG;
     QuantFp4Args a{};
@@ -243,7 +257,8 @@ moe_status moe_quantize_fp4(const moe_quantize_fp4_args *n, void *stream) {
     a.g = n->g;
     a.type = n->type;
     a.nvfp4 = nvfp4;
-    return status_of(launch_quantize_fp4(a, (cudaStream_t)stream));
+    if (n->workspace && n->ws_bytes < quantize_fp4_scratch(a)) return MOE_ERR_INVALID_ARG;
+    return status_of(launch_quantize_fp4(a, (uint8_t *)n->workspace, (cudaStream_t)stream));
 }
 
 moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *n, void *stream) {
