@@ -328,6 +328,21 @@ def test_dequantize_every_code_and_scale(gpu_lib, out):
             assert (buf[:, 67:] == 9).all()
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("R,K", [(1, 64), (3, 1536), (100, 12288), (1300, 1088), (1300, 4160), (1217, 16448), (5000, 64),
+                                 (4865, 4160), (6001, 8256)])
+def test_dequantize_sizes(gpu_lib, R, K, fmt):
+    """Every count of threads a row, and more values than L2 holds; a code times its scales has few enough bits to be exact in
+    bf16 and fp32."""
+    x = randn(gen(R + K), R, K).to(torch.bfloat16)
+    codes = gpu_lib.quantize_fp4(x, fmt)
+    want = values(*codes, fmt)
+    assert torch.equal(gpu_lib.dequantize_fp4(*codes).double(), want)
+    buf = torch.full((R, K + 9), 9.0, device="cuda")
+    assert torch.equal(gpu_lib.dequantize_fp4(*codes, out=buf[:, 1:K + 1]).double(), want)
+    assert (buf[:, 0] == 9).all() and (buf[:, K + 1:] == 9).all()
+
+
 # ---------------------------------------------------------------------------
 # products
 # ---------------------------------------------------------------------------
