@@ -547,9 +547,16 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t v[16]) {
 }
 
 template <typename T>
-__device__ __forceinline__ uint32_t rounded2(float a, float b) {
-    const T lo = rounded<T>(a), hi = rounded<T>(b);
-    return (uint32_t)*reinterpret_cast<const uint16_t *>(&lo) | (uint32_t)*reinterpret_cast<const uint16_t *>(&hi) << 16;
+__device__ __forceinline__ uint32_t rounded2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t rounded2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t rounded2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // The same for 16-bit results in rows that take 16-byte stores, all 128 columns of the tile inside the matrix: 32 rows at
@@ -566,7 +573,10 @@ __device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTil
     for (int i = 0; i < 4; ++i) {
         col[i] = FP4 ? __shfl_sync(0xFFFFFFFFu, sc.col, 8 * i + (lane >> 2)) : 1.f;
         bias[i] = __shfl_sync(0xFFFFFFFFu, sc.bias, 8 * i + (lane >> 2));
+        if (!ok) bias[i] = __int_as_float(0x7FFFFFFF);
     }
+    const int row0 = 8 * q + (lane >> 4), piece0 = lane & 15;  // what it stores: rows row0, row0 + 2, ..
+    T *y = (T *)a.y + (int64_t)(t.row0 + row0) * a.y_ld + n0 + 8 * piece0;
     // 16-byte pieces of a row are swapped by the row's low bits, against bank conflicts
     const int mj = lane >> 3, mi = lane & 7;                 // the matrix and row that this lane addresses for stmatrix
 #pragma unroll
@@ -578,27 +588,29 @@ __device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTil
         tmem_ld_16x32(tbase + (16u << 16) + 32 * j, v[1]);
         tmem_ld_wait();
         named_bar(2 + half, 128);                            // the rows before have left the stage
+        float2 rs[4];                                        // of columns 8 c + 2 (lane % 4) and the next
+        if constexpr (FP4) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                rs[c].x = __shfl_sync(0xFFFFFFFFu, sc.row[j], 8 * c + 2 * (lane & 3));
+                rs[c].y = __shfl_sync(0xFFFFFFFFu, sc.row[j], 8 * c + 2 * (lane & 3) + 1);
+            }
+        }
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
-            float rs[4] = {1.f, 1.f, 1.f, 1.f};
-            if constexpr (FP4) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rs[i] = __shfl_sync(0xFFFFFFFFu, sc.row[j], 8 * (c + (i >> 1)) + 2 * (lane & 3) + (i & 1));
-            }
 #pragma unroll
             for (int l = 0; l < 2; ++l) {
                 uint32_t m[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {                // matrix (c + i / 2, h = i % 2)
-                    const int at = 4 * (c + (i >> 1)) + 2 * (i & 1), k = 2 * l + (i & 1);
-                    float lo = __uint_as_float(v[l][at]), hi = __uint_as_float(v[l][at + 1]);
-                    if constexpr (FP4) {
-                        lo *= col[k] * rs[2 * (i >> 1)];
-                        hi *= col[k] * rs[2 * (i >> 1) + 1];
-                    }
-                    const float none = __int_as_float(0x7FFFFFFF);
-                    m[i] = ok ? rounded2<T>(lo + bias[k], hi + bias[k]) : rounded2<T>(none, none);
+                    const int cc = c + (i >> 1), at = 4 * cc + 2 * (i & 1), k = 2 * l + (i & 1);
+                    float2 o = make_float2(__uint_as_float(v[l][at]), __uint_as_float(v[l][at + 1]));
+                    const float2 b2 = make_float2(bias[k], bias[k]);
+                    if constexpr (FP4)
+                        o = fma2(o, mul2(rs[cc], make_float2(col[k], col[k])), b2);
+                    else
+                        o = fma2(o, make_float2(1.f, 1.f), b2);
+                    m[i] = rounded2<T>(o.x, o.y);
                 }
                 const int row = 8 * (c + (mj >> 1)) + mi, piece = 4 * q + 2 * l + (mj & 1);
                 asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
@@ -608,13 +620,11 @@ __device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTil
             }
         }
         named_bar(2 + half, 128);
-        const int left = t.rows - 32 * j;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = 8 * q + 2 * i + (lane >> 4), piece = lane & 15;
-            const uint4 o = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((piece ^ (row & 7)) << 4));
-            if (row < left)
-                *reinterpret_cast<uint4 *>((T *)a.y + (int64_t)(t.row0 + 32 * j + row) * a.y_ld + n0 + 8 * piece) = o;
+            const int row = row0 + 2 * i;
+            const uint4 o = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((piece0 ^ (row & 7)) << 4));
+            if (32 * j + row < t.rows) *reinterpret_cast<uint4 *>(y + (32 * j + 2 * i) * a.y_ld) = o;
         }
     }
 }

@@ -98,25 +98,6 @@ __device__ __forceinline__ uint32_t top_bits(const uint32_t x[8], const float v[
     }
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 o;
-    asm("{\n\t.reg .b64 x, y, z;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(o.x), "=f"(o.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return o;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 o;
-    asm("{\n\t.reg .b64 x, y, z;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(o.x), "=f"(o.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return o;
-}
-
 // PER: units of 16 elements of a thread. ROW: threads of a row; THREADS of a CTA.
 template <bool BF16, bool NVFP4, bool UP, int ROW, int PER, int THREADS>
 __global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Args a) {
