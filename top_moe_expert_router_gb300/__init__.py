@@ -841,7 +841,7 @@ def quantize_fp4(x, fmt="nvfp4", *, up=None, rows=None, out=None, stream=None):
     values = (code, _DTYPE[x.dtype], x.data_ptr(), up_at, K if x.is_contiguous() else _row_stride("x", x), up_ld,
               rows_at, T, R, K, q.data_ptr(), s.data_ptr(), 0 if g is None else _whole("g", g, _F32, (R,), index))
     args = _pack_quant(*values, 0, 0)
-    if R <= T:                                                # (what may take scratch has more rows than tokens)
+    if R < 2 * T or R * K < 1 << 24:                          # (these never take scratch)
         _run1(3, index, args, stream)
         return q, s, g
     need = ctypes.c_size_t(0)

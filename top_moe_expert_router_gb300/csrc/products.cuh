@@ -27,7 +27,8 @@
 // What bounds it: with few rows, or ragged groups, the stream of the weights
 // (32768 rows by 256 experts of 1536 x 4096: bf16 530 us, NVFP4 165 us, 1.00 and
 // 0.96 of the copy rate); with many, 16 bits: the MMAs (4096 x 8192 x 4096 bf16
-// 131 us, 2.10 PFLOP/s); 4 bits: issue slots. The warp that issues the MMAs has 200
+// 143 us, 1.92 PFLOP/s); 4 bits: issue slots, with short K those of the epilogue (8192
+// x 4096 x 512 NVFP4 28 us, of which 13 pass without results). The warp that issues the MMAs has 200
 // ns for a stage, and shares its scheduler with two that bring scales and two of
 // the epilogue (4096 x 8192 x 8192 NVFP4 98 us, 5.6 PFLOP/s; without the scales 82
 // us, without the stores 88, without both 73, without loads and both 70; without
@@ -90,7 +91,8 @@ struct ProdShape {
     static constexpr int kScaleBox = TN % 64 ? 32 : 64;      // rows of one TMA copy of x's scales
     // results on their way to 16-byte stores: 32 rows x 128 columns of 16 bits for each half of the epilogue's warps
     static constexpr bool kWide = TN > 32;
-    static constexpr uint32_t kOut = kWide ? 2 * 32 * 256 : 0;
+    static constexpr int kOutBufs = kFp4 ? 2 : 1;            // (with 16 bits a stage more is worth more)
+    static constexpr uint32_t kOut = kWide ? kOutBufs * 2 * 32 * 256 : 0;
     // K may be split over a cluster of CTAs (up to 8): the sums that the others bring for this CTA's share of the columns
     // (two tiles' worth: (ks - 1) 4 ceil(32 / ks) columns at most)
     static constexpr bool kSplit = CG == 1 && TN == 32;
@@ -561,12 +563,13 @@ __device__ __forceinline__ uint32_t rounded2<__half>(float lo, float hi) {
 
 // The same for 16-bit results in rows that take 16-byte stores, all 128 columns of the tile inside the matrix: 32 rows at
 // a time are transposed through shared memory, so that a row leaves as 256 adjacent bytes instead of 64 from each warp
-// (4096 x 8192 x 2048 NVFP4: 51 -> 43 us). `stage`: 8 KB of this half of the warps.
+// (4096 x 8192 x 2048 NVFP4: 51 -> 43 us; two values an instruction 38; two buffers by turns, and so one barrier, 36.6).
+// `stage`: 8 KB of this half of the warps, or with 4-bit operands twice that. Rows that begin between 16 bytes gain
+// nothing this way: 23383 rows by 129 experts of 3362 x 272 by shifted pieces 112 us, by elements 76.
 template <bool FP4, int TN, typename T>
 __device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, TN> &sc,
-                                                uint32_t tbase, int n0, int half, bool ok, unsigned char *stage) {
+                                                uint32_t tbase, int n0, int half, bool ok, unsigned char *stage, int &turn) {
     const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
-    const uint32_t to = smem_u32(stage);
     // this thread's four columns of a fragment: 16 l + 8 h + lane / 4 of the warp's 32
     float col[4], bias[4];
 #pragma unroll
@@ -583,11 +586,14 @@ __device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTil
     for (int j = 0; j < TN / 32; ++j) {
         if (32 * j >= t.rows) break;
         if ((j & 1) != half) continue;
+        unsigned char *const buf = FP4 ? stage + turn * 8192 : stage;
+        const uint32_t to = smem_u32(buf);
+        turn ^= 1;
         uint32_t v[2][16];
         tmem_ld_16x32(tbase + 32 * j, v[0]);
         tmem_ld_16x32(tbase + (16u << 16) + 32 * j, v[1]);
         tmem_ld_wait();
-        named_bar(2 + half, 128);                            // the rows before have left the stage
+        if (!FP4) named_bar(2 + half, 128);                  // the rows before have left the buffer
         float2 rs[4];                                        // of columns 8 c + 2 (lane % 4) and the next
         if constexpr (FP4) {
 #pragma unroll
@@ -623,7 +629,7 @@ __device__ __forceinline__ void prod_store_wide(const ProdArgs &a, const ProdTil
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = row0 + 2 * i;
-            const uint4 o = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((piece0 ^ (row & 7)) << 4));
+            const uint4 o = *reinterpret_cast<const uint4 *>(buf + row * 256 + ((piece0 ^ (row & 7)) << 4));
             if (32 * j + row < t.rows) *reinterpret_cast<uint4 *>(y + (32 * j + 2 * i) * a.y_ld) = o;
         }
     }
@@ -897,6 +903,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         // --------------------------------- epilogue ---------------------------------
         const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter of this warp, its share of the columns
         int lt = 0;
+        [[maybe_unused]] int turn = 0;           // of two buffers for results
         bool ok = true;                      // once a wait ran out, phases tell nothing: all later tiles are NaN
         [[maybe_unused]] bool together = true;
         ProdWalk<TN> walk(first);
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             ok = ok && warp_wait<S::kFp4>(&tfull[b], (lt >> 1) & 1, err, abort_flag);
             tc_fence_after();
             const uint32_t at = ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
-            unsigned char *stage = staged + half * 8192;
+            unsigned char *stage = staged + half * (S::kOutBufs * 8192);
             const bool wide = S::kWide && a.wide && n0 + kProdRows <= a.N;
             bool stored = false;
             if constexpr (S::kSplit) {
@@ -927,9 +934,9 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             if (stored)
                 ;
             else if (wide && a.y_type == MOE_T_BF16)
-                prod_store_wide<S::kFp4, TN, __nv_bfloat16>(a, t, sc, at, n0, half, ok, stage);
+                prod_store_wide<S::kFp4, TN, __nv_bfloat16>(a, t, sc, at, n0, half, ok, stage, turn);
             else if (wide)
-                prod_store_wide<S::kFp4, TN, __half>(a, t, sc, at, n0, half, ok, stage);
+                prod_store_wide<S::kFp4, TN, __half>(a, t, sc, at, n0, half, ok, stage, turn);
             else if (a.y_type == MOE_T_BF16)
                 prod_store<S::kFp4, TN, __nv_bfloat16>(a, t, sc, at, n, half, !ok);
             else if (a.y_type == MOE_T_F16)
