@@ -487,8 +487,9 @@ moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *args, void *stream)
  * 16-byte aligned with a stride that is a multiple of 8, W [groups, N, K]
  * 16-byte aligned.
  * moe_linear_fp4: x and W in 4-bit floats of one format, as above, K as there;
- * block products and their scales are exact, sums fp32, and g of x and W
- * multiply them. With x the rows are first quantised as moe_quantize_fp4 does. */
+ * block products and their scales are exact, sums fp32, and the product of x's
+ * and W's g, formed in fp32, multiplies them. With x the rows are first quantised
+ * as moe_quantize_fp4 does. */
 typedef struct {
     moe_dtype type;
     int groups, M, N, K;

@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter of this warp, its share of the columns
         int lt = 0;
         [[maybe_unused]] int turn = 0;           // of two buffers for results
-        bool ok = true;                      // once a wait ran out, phases tell nothing: all later tiles are NaN
+        bool ok = true;                          // once a wait ran out, phases tell nothing: all later tiles are NaN
         [[maybe_unused]] bool together = true;
         ProdWalk<TN> walk(first);
         for (; walk.tile < ntiles; walk.tile += step, ++lt) {
