@@ -1,0 +1,104 @@
+"""Products by expert and 4-bit floats where few tests go: sums that have to be
+exact in 16 bits, and addresses past 32 bits."""
+import pytest
+import torch
+
+from test_gpu_products import BLOCK, DT, check_product, check_quantised, code_values, gen, offsets_of, randn, values
+
+pytestmark = pytest.mark.gpu
+
+
+# counts of each group, N, K: tiles of 32 rows, those with K in parts, of 64 and 128 rows, pairs of CTAs
+EXACT = [([1], 100, 40), ([3, 0, 30], 260, 4096), ([1], 4096, 4096), ([829] + 35 * [1], 100, 8192), ([200], 4096, 1024),
+         ([60, 0, 70], 1024, 1032), ([500, 300], 2048, 520), ([1000], 4096, 640), ([257, 511, 700], 2000, 1032)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts,N,K", EXACT)
+def test_grouped_linear_exact_sums(gpu_lib, counts, N, K, dtype):
+    """Small whole numbers: sums of up to 8192 products of at most 49 stay below 2^24 in magnitude, so every sum of some of
+    them is exact in fp32, and every result is too, whatever the order."""
+    g = gen(N + K + len(counts))
+    E, M = len(counts), sum(counts)
+    assert 49 * K < 1 << 24
+    off = offsets_of(counts)
+    x = torch.randint(-7, 8, (M, K), generator=g, device="cuda").to(DT[dtype])
+    w = torch.randint(-7, 8, (E, N, K), generator=g, device="cuda").to(DT[dtype])
+    bias = torch.randint(-9, 10, (E, N), generator=g, device="cuda").float()
+    y = gpu_lib.grouped_linear(x, w, off, bias=bias, out_dtype=torch.float32)
+    at = 0
+    for e, c in enumerate(counts):
+        want = x[at:at + c].double() @ w[e].double().t() + bias[e].double()
+        assert torch.equal(y[at:at + c].double(), want)
+        at += c
+    assert gpu_lib.products_status() == gpu_lib.MOE_OK
+
+
+@pytest.mark.parametrize("fmt,K", [("nvfp4", 4096), ("nvfp4", 4160), ("mxfp4", 4096), ("mxfp4", 4160)])
+def test_4bit_weights_past_32_bits(gpu_lib, fmt, K):
+    """Codes past 2^32 elements, scales of whole 16 bytes a row (4096 columns) and of words (4160): the first and the last
+    expert, whose weights alone are not 0."""
+    E, N = 270, 4096
+    assert (E - 1) * N * K > 1 << 32
+    g = gen(K)
+    q = torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(E, N, K // BLOCK[fmt], dtype=torch.uint8, device="cuda")
+    gs = torch.ones(E, N, device="cuda") if fmt == "nvfp4" else None
+    for e in (0, E - 1):
+        codes = gpu_lib.quantize_fp4((0.02 * randn(g, N, K)).to(torch.bfloat16), fmt)
+        q[e], s[e] = codes[0], codes[1]
+        if gs is not None:
+            gs[e] = codes[2]
+    for first, last in ((3, 5), (150, 170)):
+        x = gpu_lib.quantize_fp4(randn(g, first + last, K).to(torch.bfloat16), fmt)
+        off = offsets_of([first] + [0] * (E - 2) + [last])
+        y = gpu_lib.grouped_linear_fp4(x, q, s, gs, off)
+        for e, rows in ((0, slice(0, first)), (E - 1, slice(first, first + last))):
+            check_product(y[rows], values(*(None if v is None else v[rows] for v in x), fmt),
+                          values(q[e], s[e], None if gs is None else gs[e], fmt))
+    assert gpu_lib.products_status() == gpu_lib.MOE_OK
+
+
+@pytest.mark.parametrize("M", [70, 150, 400])
+def test_results_past_32_bits(gpu_lib, M):
+    """Rows of y so far apart that its last elements lie past 2^31: tiles of 64 and 128 rows and pairs of CTAs, whole rows of
+    16-byte stores and single elements."""
+    N, K = 4096, 256
+    g = gen(M)
+    x, w = randn(g, M, K).to(torch.bfloat16), (0.1 * randn(g, 1, N, K)).to(torch.bfloat16)
+    off = offsets_of([M])
+    ws = [v.view(1, N, *v.shape[1:]) for v in gpu_lib.quantize_fp4(w[0])]
+    want = gpu_lib.grouped_linear(x, w, off), gpu_lib.grouped_linear_fp4(x, *ws, off)
+    ld = -(-(2 ** 31 + 9) // (M - 1) // 8) * 8
+    buf = torch.empty((M - 1) * ld + N + 8, dtype=torch.bfloat16, device="cuda")
+    assert (M - 1) * ld > 1 << 31
+    for first in (0, 8, 1):
+        y = buf.as_strided((M, N), (ld, 1), first)
+        assert (gpu_lib.grouped_linear(x, w, off, out=y) == want[0]).all()
+        assert (gpu_lib.grouped_linear_fp4(x, *ws, off, out=y) == want[1]).all()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_quantisation_past_32_bits(gpu_lib, fmt):
+    """Tokens, codes and values past 2^31 elements, each row by itself and gathered (from few tokens: by way of their codes):
+    the rows around that border and the last."""
+    K = 4096
+    T = (1 << 31) // K + 700
+    g = gen(5)
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda")
+    for at in range(0, T, 1 << 16):
+        x[at:at + (1 << 16)] = randn(g, min(1 << 16, T - at), K)
+    look = torch.tensor([0, 1, T // 2, T - 702, T - 701, T - 700, T - 699, T - 2, T - 1], device="cuda")
+    pick = lambda t, at: tuple(None if v is None else v[at] for v in t)
+    got = gpu_lib.quantize_fp4(x, fmt)
+    check_quantised(pick(got, look), x[look], fmt)
+    out = gpu_lib.dequantize_fp4(*got)
+    assert torch.equal(out[look].double(), values(*pick(got, look), fmt))
+    del out, got
+    rows = torch.randint(0, T, (T,), generator=g, device="cuda", dtype=torch.int32)
+    rows[look] = torch.arange(T - look.numel(), T, device="cuda", dtype=torch.int32)
+    got = gpu_lib.quantize_fp4(x, fmt, rows=rows)
+    check_quantised(pick(got, look), x[rows[look].long()], fmt)
+    few = rows % 512
+    got = gpu_lib.quantize_fp4(x[:512], fmt, rows=few)
+    check_quantised(pick(got, look), x[few[look].long()], fmt)
