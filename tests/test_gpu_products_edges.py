@@ -1,5 +1,5 @@
 """Products by expert and 4-bit floats where few tests go: sums that have to be
-exact in 16 bits, and addresses past 32 bits."""
+exact in 16 bits, addresses past 32 bits, and how calls end whose waits run out."""
 import pytest
 import torch
 
@@ -102,3 +102,69 @@ def test_quantisation_past_32_bits(gpu_lib, fmt):
     few = rows % 512
     got = gpu_lib.quantize_fp4(x[:512], fmt, rows=few)
     check_quantised(pick(got, look), x[few[look].long()], fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4", "mxfp4"])
+def test_pairs_leave_once_their_copies_have_landed(gpu_lib, fmt):
+    """Pairs of CTAs of which the second copies no operands: waits run out after 1.5 s, and what the first has issued has
+    landed long before. The call takes one such limit, not a second one for copies that nobody issued."""
+    g = gen(21)
+    counts, N, K = [2000, 0, 2500], 2056, 2048
+    off, M = offsets_of(counts), sum(counts)
+    x, w = randn(g, M, K).to(torch.bfloat16), (0.1 * randn(g, 3, N, K)).to(torch.bfloat16)
+    if fmt == "bf16":
+        call = lambda: gpu_lib.grouped_linear(x, w, off)
+    else:
+        xq = gpu_lib.quantize_fp4(x, fmt)
+        ws = [v if v is None else v.view(3, N, *v.shape[1:]) for v in gpu_lib.quantize_fp4(w.view(3 * N, K), fmt)]
+        call = lambda: gpu_lib.grouped_linear_fp4(xq, *ws, off)
+    good = call()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    gpu_lib.hold_products(2)
+    try:
+        start.record()
+        held = call()
+        end.record()
+        torch.cuda.synchronize()
+    finally:
+        gpu_lib.hold_products(0)
+    assert torch.isnan(held).all()
+    assert start.elapsed_time(end) < 2500
+    assert gpu_lib.products_status() == gpu_lib.MOE_ERR_TIMEOUT
+    assert torch.equal(call(), good)
+    assert gpu_lib.products_status() == gpu_lib.MOE_OK
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("counts,N,K,limits", [([3], 384, 4096, 1), ([32], 384, 8192, 1), ([829] + 35 * [1], 100, 8192, 2)])
+def test_parts_leave_once_their_sums_have_landed(gpu_lib, counts, N, K, limits, fmt):
+    """K in parts, where every second CTA copies no operands: at about the time at which it gives up and sends NaN, the others
+    give up waiting for its sums. Whichever comes first, what was sent has landed before a CTA leaves, and nobody waits
+    for what was not. With one tile for a CTA that takes one limit of 1.5 s; with several a CTA that still had the sums of the
+    first waits once more."""
+    g = gen(22)
+    E, off, M = len(counts), offsets_of(counts), sum(counts)
+    x, w = randn(g, M, K).to(torch.bfloat16), (0.1 * randn(g, E, N, K)).to(torch.bfloat16)
+    if fmt == "bf16":
+        call = lambda: gpu_lib.grouped_linear(x, w, off)
+    else:
+        xq = gpu_lib.quantize_fp4(x, fmt)
+        ws = [v.view(E, N, *v.shape[1:]) for v in gpu_lib.quantize_fp4(w.view(E * N, K), fmt)]
+        call = lambda: gpu_lib.grouped_linear_fp4(xq, *ws, off)
+    good = call()
+    for _ in range(2):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        gpu_lib.hold_products(2)
+        try:
+            start.record()
+            held = call()
+            end.record()
+            torch.cuda.synchronize()
+        finally:
+            gpu_lib.hold_products(0)
+        none = torch.isnan(held)
+        assert none.all()
+        assert start.elapsed_time(end) < 1500 * limits + 1000
+        assert gpu_lib.products_status() == gpu_lib.MOE_ERR_TIMEOUT
+    assert torch.equal(call(), good)
+    assert gpu_lib.products_status() == gpu_lib.MOE_OK

@@ -70,6 +70,7 @@ static inline cudaError_t prod_take_errors(cudaStream_t st, uint32_t *bits) {
 
 // Floats from one column of partial sums to the next: 32 rows, and 4 against bank conflicts.
 constexpr int kPartRow = 36;
+constexpr int kNoTile = 0x7FFFFFFF;
 
 // CG: CTAs of a tile, 1 or 2 (a pair, 256 weight rows)
 template <int KIND, int TN, int CG>
@@ -93,9 +94,10 @@ struct ProdShape {
     static constexpr bool kWide = TN > 32;
     static constexpr int kOutBufs = kFp4 ? 2 : 1;            // (with 16 bits a stage more is worth more)
     static constexpr uint32_t kOut = kWide ? kOutBufs * 2 * 32 * 256 : 0;
-    // K may be split over a cluster of CTAs (up to 8): the sums that the others bring for this CTA's share of the columns
-    // (two tiles' worth: (ks - 1) 4 ceil(32 / ks) columns at most)
+    // K may be split over a cluster of CTAs: the sums that the others bring for this CTA's share of the columns
+    // (two tiles' worth: (ks - 1) 4 ceil(32 / ks) columns, with up to 8 parts 120 at most)
     static constexpr bool kSplit = CG == 1 && TN == 32;
+    static constexpr int kMostParts = 8;
     static constexpr uint32_t kParts = kSplit ? 2 * 120 * kPartRow * 4 : 0;
     static constexpr uint32_t kMeta = kProdMaxGroups * 16 + 16 + 512 + 256;  // group tables, barriers, scratch of 64 words
     static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales - kOut - kParts) / kStage);
@@ -642,6 +644,16 @@ __device__ __forceinline__ uint32_t in_rank(const void *p, int rank) {
     return o;
 }
 
+// A word into the shared memory of another CTA of the cluster.
+__device__ __forceinline__ void store_there(uint32_t to, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+}
+
+// Takes bytes that nobody will copy off what a barrier of this CTA waits for.
+__device__ __forceinline__ void complete_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // Four words into the shared memory of another CTA, counted at a barrier there.
 __device__ __forceinline__ void send4(uint32_t to, const uint32_t v[4], uint32_t bar) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
@@ -649,20 +661,26 @@ __device__ __forceinline__ void send4(uint32_t to, const uint32_t v[4], uint32_t
                  : "memory");
 }
 
+// The CTA that adds the sums of the four columns from 4 u on.
+__device__ __forceinline__ int part_owner(int u, int ks) { return ((u + 1) * ks - 1) / 32; }
+
 // K split over the ks CTAs of a cluster: each owns a share of the tile's 128 columns, four or a multiple. The sums go to
 // the owners as asynchronous stores that a barrier there counts (parts[sender][column of the share][row]); the owners add
 // them in the order of their ranks and store. Two such buffers by turns: whoever sends a tile's sums has read, as all
 // warps of the CTA have, those of the tile before, so nobody writes where another still reads.
-// `together`: whether this warp still takes part. Once a wait for the others' sums has run out it stays away from the barriers,
-// whose phases no longer fit: arriving at one twice in a phase is undefined.
+// `lost`: the CTA's tile (lt) whose sums this warp waited for in vain, its limit having passed, or kNoTile. It has sent its own
+// for the tiles up to that one, and from then on stays away from the barriers, whose phases no longer fit: arriving at one
+// twice in a phase is undefined. (Ordinary stores, which the cluster's last barrier would order, take 0.25 to 0.4 us more a
+// tile: 1 x 4096 x 4096 NVFP4 7.9 -> 8.1 us, bf16 8.4 -> 8.7.)
 template <bool FP4, int TN>
 __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTile &t, const ProdScales<FP4, TN> &sc,
                                                  uint32_t tbase, int n, bool ok, float *parts, int part, uint64_t *pfull,
-                                                 int lt, bool &together, uint32_t *err, volatile int *abort_flag) {
+                                                 int lt, int &lost, uint32_t *err, volatile int *abort_flag) {
     static_assert(TN == 32, "one chunk of rows");
+    bool together = lost == kNoTile;
     const int ks = a.ks, lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
     const int local = q * 32 + lane, share = (32 + ks - 1) / ks * 4;
-    const int owner = ((local / 4 + 1) * ks - 1) / 32, col = local - 32 * owner / ks * 4;
+    const int owner = part_owner(local / 4, ks), col = local - 32 * owner / ks * 4;
     const int quads = (t.rows + 3) / 4;
     float *buf = parts + (lt & 1) * (120 * kPartRow);
     uint64_t *bar = pfull + (lt & 1);
@@ -683,7 +701,10 @@ __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTi
         if (!ok) v[0] = v[1] = v[2] = v[3] = 0x7FFFFFFFu;
         if (together && owner != part) send4(there + 16 * i, v, bar_there);
     }
-    together = together && warp_wait<true>(bar, (lt >> 1) & 1, err, abort_flag);
+    if (together && !warp_wait<true>(bar, (lt >> 1) & 1, err, abort_flag)) {
+        together = false;
+        lost = lt;
+    }
     ok &= together;
     asm volatile(                                // (the same once more, in the scope of the cluster)
         "{\n\t.reg .pred p;\n\t"
@@ -722,6 +743,57 @@ __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTi
     }
 }
 
+// A pair some of whose waits ran out: waits, one thread of the leader, until the copies of both CTAs have landed. The
+// leader has issued those of `mine` stages and counted them and the other's on full[], the other of `theirs`. Where one is
+// ahead, the other's share of a stage is taken off what its barrier waits for, or that of the one ahead is added to
+// it. (Neither is ahead by more than the ring: a slot is free once an MMA has read it, which takes both.)
+template <typename S, int TN>
+__device__ __noinline__ void settle_pair(const ProdGroups gr, int nw, int first, int step, int nst, int mine, int theirs,
+                                         uint64_t *full, uint32_t *err) {
+    const int last = max(mine, theirs);
+    for (int j = min(mine, theirs); j < last; ++j) {
+        int i = 0;
+        const ProdTile t = prod_tile<TN>(gr, nw, first + j / nst * step, i);
+        const int share = (t.rows + S::kStep - 1) / S::kStep * 16;
+        const uint32_t bytes = kProdABytes + (share + S::kBox - 1) / S::kBox * S::kBox * 128;
+        uint64_t *bar = &full[j % S::kStages];
+        if (mine > theirs)
+            complete_tx(bar, bytes);
+        else
+            mbar_arrive_expect_tx(bar, bytes);
+    }
+    for (int j = last > S::kStages ? last - S::kStages : 0; j < last; ++j)
+        if (!mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1, err)) break;
+}
+
+// The same for K in parts, where the wait for the sums of tile `lost` ran out, one thread of the warp that expects them: until
+// what the other CTAs have sent has landed here. Of `lost` all was expected, and what nobody sends is taken off. Of the next
+// two tiles what was sent is expected now: others may have had all sums of `lost`, or of the tile after it, but nobody
+// those of a third one, which takes sums that follow a wait for the second, and that wait takes this warp. The tiles
+// before were waited for.
+template <int TN>
+__device__ __noinline__ void settle_parts(const ProdGroups gr, int nw, int first, int step, int ntiles, int ks, int part,
+                                          int lost, volatile const int *sent, uint64_t *pfull, uint32_t *err) {
+    for (int lt = lost; lt < lost + 3 && first + (int64_t)lt * step < ntiles; ++lt) {
+        int i = 0;
+        const int quads = (prod_tile<TN>(gr, nw, first + lt * step, i).rows + 3) / 4;
+        uint32_t all = 0, there = 0;
+        for (int r = 0; r < ks; ++r)
+            for (int u = 0; u < 32 && r != part; ++u)        // four columns, eight of them a warp's
+                if (part_owner(u, ks) == part) {
+                    all += quads * 64;
+                    there += sent[4 * r + u / 8] > lt ? quads * 64 : 0;
+                }
+        if (lt > lost && !there) break;
+        uint64_t *bar = pfull + (lt & 1);
+        if (lt > lost)
+            mbar_arrive_expect_tx(bar, there);
+        else if (all > there)
+            complete_tx(bar, all - there);
+        mbar_wait(bar, (lt >> 1) & 1, err);
+    }
+}
+
 template <int KIND, int TN, int CG>
 __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -741,6 +813,10 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     uint64_t *lfull = sempty + 4, *lempty = lfull + 4, *pfull = lempty + 4, *done = pfull + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    [[maybe_unused]] volatile int *issued = abort_flag + 1;  // in a pair's leader: stages whose copies the other has issued
+    // with K in parts: how many tiles' sums each warp of each other CTA has sent, where one of its waits ran out
+    [[maybe_unused]] volatile int *sent = issued + 1;
+    [[maybe_unused]] int issued_here = 0, lost = kNoTile;
     const bool held = a.hold == 1 || (a.hold == 2 && (blockIdx.x & 1));
     ProdGroups gr;
     int32_t *scratch = reinterpret_cast<int32_t *>(meta + 512);
@@ -749,6 +825,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     gr.rows = gr.row0 + kProdMaxGroups;
     gr.group = gr.rows + kProdMaxGroups;
     static_assert(kProdMaxGroups <= 2 * S::kThreads, "two groups a thread");
+    static_assert((2 * NS + 23) * 8 + (3 + 4 * S::kMostParts) * 4 <= 512, "barriers and words");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t *err = &prod_err;
@@ -778,6 +855,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         fence_barrier_init();
     }
     if (warp == 1) prod_tmem_alloc<CG>(tmem_slot);
+    if (S::kSplit && warp == 3 && lane < 4 * S::kMostParts) sent[lane] = kNoTile;
     if (threadIdx.x == 32 * 2) {
         prefetch_map(&tmW);
         prefetch_map(&tmX);
@@ -809,9 +887,9 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------- TMA producer -------------------------------
+        int it = 0;
         if (!held) {
             const uint32_t on = elect_lane();
-            int it = 0;
             bool ok = true;
             ProdWalk<TN> walk(first);
             for (; walk.tile < ntiles && ok; walk.tile += step) {
@@ -835,10 +913,15 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                         tma_on<CG>(st + kProdABytes + j * (S::kBox * 128), &tmX, k, row0 + j * S::kBox, bar, on);
                 }
             }
-            // every load issued must land before the CTA exits (a pair's are counted, and waited for, by the leader)
-            // -- one limit for all of them
-            for (int j = rank ? it : it > NS ? it - NS : 0; j < it; ++j)
-                if (!mbar_wait(&full[j % NS], (j / NS) & 1, err)) break;
+            // every load issued must land before the CTA exits -- one limit for all of them. (A pair's have where its MMAs
+            // were all issued; where a wait ran out, settle_pair sees to it.)
+            if (CG == 1)
+                for (int j = it > NS ? it - NS : 0; j < it; ++j)
+                    if (!mbar_wait(&full[j % NS], (j / NS) & 1, err)) break;
+        }
+        if (CG == 2) {
+            if (rank && lane == 0) store_there(in_leader((const void *)issued), (uint32_t)it);
+            issued_here = it;
         }
     } else if (warp == 1) {
         // -------------------------------- MMA issuer --------------------------------
@@ -905,7 +988,6 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         int lt = 0;
         [[maybe_unused]] int turn = 0;           // of two buffers for results
         bool ok = true;                          // once a wait ran out, phases tell nothing: all later tiles are NaN
-        [[maybe_unused]] bool together = true;
         ProdWalk<TN> walk(first);
         for (; walk.tile < ntiles; walk.tile += step, ++lt) {
             const ProdTile t = walk.at(gr, nw);
@@ -923,7 +1005,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
                     if (lt == 0) cluster_wait();
                     // (32 rows are the first four warps')
                     if (!half)
-                        prod_store_split<S::kFp4, TN>(a, t, sc, at, n, ok, parts, part, pfull, lt, together, err, abort_flag);
+                        prod_store_split<S::kFp4, TN>(a, t, sc, at, n, ok, parts, part, pfull, lt, lost, err, abort_flag);
                     stored = true;
                 }
             }
@@ -946,6 +1028,8 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
             tc_fence_before();
             warp_arrive<CG>(&tempty[b]);
         }
+        if (S::kSplit && lost != kNoTile && lane < ks && lane != part)
+            store_there(in_rank((const void *)(sent + 4 * part + q), lane), (uint32_t)(lost + 1));
     } else if constexpr (S::kFp4) {
         constexpr int QB = S::kBatchBytes, G = S::kBatch, SB = QB / G, NQ = S::kBatches, kSlot = S::kSlotBytes;
         const int b0 = kb0 / G, b1 = (kb1 + G - 1) / G;
@@ -1114,11 +1198,16 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         // (those that did not wait for the start yet)
         if (CG == 1 && (warp < 2 || warp >= 10 || first >= ntiles)) cluster_wait();
         __syncwarp();
+        if (CG == 2 && threadIdx.x == 0 && *abort_flag) store_there(in_rank((const void *)abort_flag, 1 - rank), 1u);
         cluster_sync_all();
-        // where a wait ran out, sums or operands that nobody waited for may still be on their way here: they have 0.1 ms
-        if (*abort_flag)
-            for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 100000ull;) {
-            }
+        // a wait ran out in one of a pair or both: operands may be on their way to either
+        if (CG == 2 && *abort_flag) {
+            if (rank == 0 && threadIdx.x == 0) settle_pair<S, TN>(gr, nw, first, step, nst, issued_here, *issued, full, err);
+            __syncwarp();
+            cluster_sync_all();
+        }
+        if (S::kSplit && warp == 4 && lane == 0 && lost != kNoTile)
+            settle_parts<TN>(gr, nw, first, step, ntiles, ks, part, lost, sent, pfull, err);
     }
     if (warp == 1) {
         tc_fence_after();
