@@ -405,7 +405,8 @@ moe_status moe_linear_w4(const moe_w4_args *args, void *stream);
 /* A product's waits for its weights are bounded (1.5 s). Where one runs out the
  * call leaves NaN in the rows concerned and sets a bit that belongs to the
  * device, not to the call. moe_linear_w4_status waits for `stream`, then reads
- * and clears the current device's: MOE_OK or MOE_ERR_TIMEOUT. Not while the
+ * and clears the current device's: MOE_OK or MOE_ERR_TIMEOUT. A bit that is set
+ * meanwhile by work on another stream is kept for the next call. Not while the
  * stream is being captured. */
 moe_status moe_linear_w4_status(void *stream);
 
@@ -526,7 +527,8 @@ moe_status moe_linear_fp4(const moe_linear_fp4_args *args, void *stream);
 /* The waits inside these products are bounded (1.5 s). Where one runs out the
  * call leaves NaN in the rows concerned and sets a bit that belongs to the
  * device, not to the call. moe_products_status waits for `stream`, then reads
- * and clears the current device's: MOE_OK or MOE_ERR_TIMEOUT. Not while the
+ * and clears the current device's: MOE_OK or MOE_ERR_TIMEOUT. A bit that is set
+ * meanwhile by work on another stream is kept for the next call. Not while the
  * stream is being captured. */
 moe_status moe_products_status(void *stream);
 

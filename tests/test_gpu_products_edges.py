@@ -168,3 +168,38 @@ def test_parts_leave_once_their_sums_have_landed(gpu_lib, counts, N, K, limits, 
         assert gpu_lib.products_status() == gpu_lib.MOE_ERR_TIMEOUT
     assert torch.equal(call(), good)
     assert gpu_lib.products_status() == gpu_lib.MOE_OK
+
+
+@pytest.mark.parametrize("op", ["grouped_linear", "linear_fp4", "linear_nvfp4"])
+def test_every_wait_that_ran_out_is_reported(gpu_lib, op):
+    """The status is asked for all the time, on another stream, while one call after the other runs out of its waits: whatever
+    the moment at which a bit is set, one of the answers has it."""
+    g = gen(23)
+    x, w = randn(g, 1, 128).to(torch.bfloat16), randn(g, 1, 64, 128).to(torch.bfloat16)
+    hold, status = gpu_lib.hold_products, gpu_lib.products_status
+    side, asks = torch.cuda.Stream(), torch.cuda.Stream()
+    if op == "grouped_linear":
+        call = lambda off=offsets_of([1]): gpu_lib.grouped_linear(x, w, off, stream=side)
+    elif op == "linear_fp4":
+        xq, ws = gpu_lib.quantize_fp4(x), gpu_lib.quantize_fp4(w[0])
+        call = lambda: gpu_lib.linear_fp4(xq, *ws, stream=side)
+    else:
+        q, s, gs = gpu_lib.quantize_nvfp4(w)
+        hold, status = gpu_lib.hold_linear_w4, gpu_lib.linear_w4_status
+        call = lambda: gpu_lib.linear_nvfp4(x, q[0], s[0], gs, stream=side)
+    good = call()
+    torch.cuda.synchronize()
+    assert status(asks) == gpu_lib.MOE_OK
+    for _ in range(8):
+        hold(True)
+        try:
+            y = call()
+        finally:
+            hold(False)
+        answers = []
+        while not side.query():
+            answers.append(status(asks))
+        answers.append(status(asks))
+        assert torch.isnan(y).all() and gpu_lib.MOE_ERR_TIMEOUT in answers
+        assert status(asks) == gpu_lib.MOE_OK
+    assert torch.equal(call(), good)

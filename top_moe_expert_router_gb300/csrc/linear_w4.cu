@@ -736,10 +736,8 @@ void hold_linear_w4(bool hold) { w4_hold.store(hold, std::memory_order_relaxed);
 // Reads and clears the current device's error bits, after `st`'s work.
 cudaError_t linear_w4_errors(cudaStream_t st, uint32_t *bits) {
     void *at = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&at, w4_err);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, sizeof(*bits), cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof(*bits), st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+    const cudaError_t e = cudaGetSymbolAddress(&at, w4_err);
+    return e == cudaSuccess ? take_error_bits((uint32_t *)at, st, bits) : e;
 }
 
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st) {

@@ -96,6 +96,9 @@ constexpr int kW4MaxK = 32768;
 constexpr int kW4MaxN = 1 << 30;
 cudaError_t launch_linear_w4(const W4Args &a, cudaStream_t st);
 cudaError_t linear_w4_errors(cudaStream_t st, uint32_t *bits);
+// Reads a device's error bits and clears those it has read, after `st`'s work: a bit that a kernel on another stream sets
+// meanwhile stays for the next to read.
+cudaError_t take_error_bits(uint32_t *word, cudaStream_t st, uint32_t *bits);
 void hold_linear_w4(bool hold);
 
 // Microscaled 4-bit floats (quant_fp4.cu): two e2m1 codes to a byte, the low

@@ -37,6 +37,17 @@ RouteArgs route_args(const moe_route_desc &d) {
     return a;
 }
 
+static __global__ void clear_bits_kernel(uint32_t *word, uint32_t bits) { atomicAnd(word, ~bits); }
+
+cudaError_t take_error_bits(uint32_t *word, cudaStream_t st, uint32_t *bits) {
+    cudaError_t e = cudaMemcpyAsync(bits, word, sizeof(*bits), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess || !*bits) return e;
+    clear_bits_kernel<<<1, 1, 0, st>>>(word, *bits);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
 }  // namespace moe
 
 namespace {

@@ -62,10 +62,8 @@ static __device__ uint32_t prod_err;
 // Reads and clears the bits of the current device, after `st`'s work.
 static inline cudaError_t prod_take_errors(cudaStream_t st, uint32_t *bits) {
     void *at = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&at, prod_err);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(bits, at, sizeof(*bits), cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof(*bits), st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+    const cudaError_t e = cudaGetSymbolAddress(&at, prod_err);
+    return e == cudaSuccess ? take_error_bits((uint32_t *)at, st, bits) : e;
 }
 
 // Floats from one column of partial sums to the next: 32 rows, and 4 against bank conflicts.
