@@ -203,3 +203,25 @@ def test_every_wait_that_ran_out_is_reported(gpu_lib, op):
         assert torch.isnan(y).all() and gpu_lib.MOE_ERR_TIMEOUT in answers
         assert status(asks) == gpu_lib.MOE_OK
     assert torch.equal(call(), good)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_scales_of_silu_at_the_middles(gpu_lib, dtype):
+    """silu(x) * up where it is exact: x of 32 or more, where 1 + exp(-x) is 1, and so a product of two short values. Block
+    maxima at 6 times every middle between two E4M3 values, and at the products next to it."""
+    t = DT[dtype]
+    xs, ups = [], []
+    for m in range(17, 32, 2):                              # middles m / 16, in three binades
+        for e in (-3, 0, 4):
+            for near in (0.0, 2.0 ** -7, -(2.0 ** -7)):
+                x = torch.zeros(16, device="cuda")
+                up = torch.zeros(16, device="cuda")
+                x[3], up[3] = 32 * m / 16, 6 * 2.0 ** (e - 5) * (1 + near)
+                x[7], up[7] = 48.0, 2.0 ** (e - 6)          # 0.75 and 1 in the same binade
+                xs.append(x)
+                ups.append(up)
+    x, up = torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")
+    x[0], up[0] = 64.0, 42.0                                # 2688: g is 1
+    fill = 4 - len(xs) % 4
+    xs, ups = torch.cat(xs + [x] * fill)[None].to(t), torch.cat(ups + [up] * fill)[None].to(t)
+    check_quantised(gpu_lib.quantize_fp4(xs, up=ups), xs.double() * ups.double(), "nvfp4")

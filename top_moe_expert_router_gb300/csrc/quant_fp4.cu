@@ -12,14 +12,16 @@
 // and its codes copied, where the caller has room for them.
 //
 // Rounding. Codes and scales are those of exact quotients. g and MXFP4's scales
-// are powers of two; max / 6 by a product with fp32's 1/6 is exact wherever the
-// quotient is the middle between two E4M3 values (checked for all of them), and
-// elsewhere further from it than the product's error: values of 16 bits have 11
-// significant bits, E4M3's middles 5. v / s, s an E4M3 value, is v h + v l
+// are powers of two; max / 6 (fp4_scale.h) is a product with fp32's 1/6 where
+// values have 16 bits, and corrected to the nearest float where they are
+// silu(x) * up, of 24 bits. v / s, s an E4M3 value, is v h + v l
 // with h + l = 1/s to 40 bits or more: rounded once it meets the middles between
-// codes exactly (v h alone misses them for s of 13/8, 14/8, 15/8).
+// codes exactly (v h alone misses them for s of 13/8, 14/8, 15/8), and for v of 24
+// bits no others: a unit of v's last place, divided by s < 2, is 8/15 of one of
+// the quotient's or more.
 #include <cuda_fp4.h>
 
+#include "fp4_scale.h"
 #include "ops.cuh"
 
 namespace moe {
@@ -199,7 +201,8 @@ __global__ void __launch_bounds__(THREADS) quantize_fp4_kernel(const QuantFp4Arg
         uint32_t s;
         bool none;                                          // codes 0 whatever the elements
         if constexpr (NVFP4) {
-            s = __nv_cvt_float_to_fp8(__uint_as_float(top[p]) * inv_g * (1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
+            const float scaled = __uint_as_float(top[p]) * inv_g;
+            s = __nv_cvt_float_to_fp8(UP ? fp4_sixth(scaled) : fp4_sixth_of_short(scaled), __NV_SATFINITE, __NV_E4M3);
             const __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s, __NV_E4M3);
             const float sf = __half2float(*reinterpret_cast<const __half *>(&hr));
             none = s == 0u;
