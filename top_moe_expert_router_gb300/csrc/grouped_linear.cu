@@ -98,7 +98,7 @@ ProdPlan plan_product(bool fp4, int groups, int M, int N, int K) {
             ns = ns > mma ? ns : mma;
             ns = ns > 6.3 * kb ? ns : 6.3 * kb;
         }
-        for (int ks = 1; ks <= (s.rows == 32 ? 4 : 1); ++ks) {
+        for (int ks = 1; ks <= (s.rows == 32 ? kMostParts : 1); ++ks) {
             const int slots = 152 / (ctas * ks), part = ((stages + 1) / 2 + ks - 1) / ks * 2;
             if (ks > 1 && (tiles > slots || part * (ks - 1) >= stages)) break;
             const double rounds = tiles <= slots ? 1 : (double)(int64_t)((tiles + slots - 1) / slots);

@@ -69,6 +69,10 @@ static inline cudaError_t prod_take_errors(cudaStream_t st, uint32_t *bits) {
 // Floats from one column of partial sums to the next: 32 rows, and 4 against bank conflicts.
 constexpr int kPartRow = 36;
 constexpr int kNoTile = 0x7FFFFFFF;
+constexpr int kMostParts = 4;            // of K, CTAs of a cluster
+// columns of partial sums that a CTA receives for a tile, at most: of ks parts (ks - 1) 4 ceil(32 / ks)
+constexpr int kPartCols = 96;
+static_assert((kMostParts - 1) * 4 * ((32 + kMostParts - 1) / kMostParts) <= kPartCols, "partial sums");
 
 // CG: CTAs of a tile, 1 or 2 (a pair, 256 weight rows)
 template <int KIND, int TN, int CG>
@@ -92,11 +96,9 @@ struct ProdShape {
     static constexpr bool kWide = TN > 32;
     static constexpr int kOutBufs = kFp4 ? 2 : 1;            // (with 16 bits a stage more is worth more)
     static constexpr uint32_t kOut = kWide ? kOutBufs * 2 * 32 * 256 : 0;
-    // K may be split over a cluster of CTAs: the sums that the others bring for this CTA's share of the columns
-    // (two tiles' worth: (ks - 1) 4 ceil(32 / ks) columns, with up to 8 parts 120 at most)
+    // K may be split over a cluster of CTAs: the sums that the others bring for this CTA's share of the columns, of two tiles
     static constexpr bool kSplit = CG == 1 && TN == 32;
-    static constexpr int kMostParts = 8;
-    static constexpr uint32_t kParts = kSplit ? 2 * 120 * kPartRow * 4 : 0;
+    static constexpr uint32_t kParts = kSplit ? 2 * kPartCols * kPartRow * 4 : 0;
     static constexpr uint32_t kMeta = kProdMaxGroups * 16 + 16 + 512 + 256;  // group tables, barriers, scratch of 64 words
     static constexpr int kRoom = (int)((227 * 1024 - 1024 - kMeta - kScales - kOut - kParts) / kStage);
     static constexpr int kStages = kRoom < 10 ? kRoom : 10;
@@ -680,7 +682,7 @@ __device__ __forceinline__ void prod_store_split(const ProdArgs &a, const ProdTi
     const int local = q * 32 + lane, share = (32 + ks - 1) / ks * 4;
     const int owner = part_owner(local / 4, ks), col = local - 32 * owner / ks * 4;
     const int quads = (t.rows + 3) / 4;
-    float *buf = parts + (lt & 1) * (120 * kPartRow);
+    float *buf = parts + (lt & 1) * (kPartCols * kPartRow);
     uint64_t *bar = pfull + (lt & 1);
     named_bar(2, 128);                           // the tile before the last has been read from this buffer
     if (together && q == 0 && lane == 0) {
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
     gr.rows = gr.row0 + kProdMaxGroups;
     gr.group = gr.rows + kProdMaxGroups;
     static_assert(kProdMaxGroups <= 2 * S::kThreads, "two groups a thread");
-    static_assert((2 * NS + 23) * 8 + (3 + 4 * S::kMostParts) * 4 <= 512, "barriers and words");
+    static_assert((2 * NS + 23) * 8 + (3 + 4 * kMostParts) * 4 <= 512, "barriers and words");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t *err = &prod_err;
@@ -853,7 +855,7 @@ __global__ void __launch_bounds__(ProdShape<KIND, TN, CG>::kThreads, 1)
         fence_barrier_init();
     }
     if (warp == 1) prod_tmem_alloc<CG>(tmem_slot);
-    if (S::kSplit && warp == 3 && lane < 4 * S::kMostParts) sent[lane] = kNoTile;
+    if (S::kSplit && warp == 3 && lane < 4 * kMostParts) sent[lane] = kNoTile;
     if (threadIdx.x == 32 * 2) {
         prefetch_map(&tmW);
         prefetch_map(&tmX);
@@ -1278,7 +1280,7 @@ cudaError_t launch_product(const ProdArgs &a0, const void *x, int64_t x_pitch, c
     cfg.attrs = attr;
     cfg.numAttrs = width == 1 ? 1 : 2;
     // no more clusters than the device holds at once (fewer than the SMs suggest: a cluster's CTAs lie in one group of SMs)
-    static std::atomic<int> known[kProdDevices][9];
+    static std::atomic<int> known[kProdDevices][kMostParts + 1];
     int dev = 0, n = device_sms();
     if (n < 1 || cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (width > 1) {
