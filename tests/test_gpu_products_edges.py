@@ -3,7 +3,7 @@ exact in 16 bits, addresses past 32 bits, and how calls end whose waits run out.
 import pytest
 import torch
 
-from test_gpu_products import BLOCK, DT, check_product, check_quantised, code_values, gen, offsets_of, randn, values
+from test_gpu_products import BLOCK, DT, check_product, check_quantised, gen, offsets_of, power, randn, values
 
 pytestmark = pytest.mark.gpu
 
@@ -225,3 +225,20 @@ def test_scales_of_silu_at_the_middles(gpu_lib, dtype):
     fill = 4 - len(xs) % 4
     xs, ups = torch.cat(xs + [x] * fill)[None].to(t), torch.cat(ups + [up] * fill)[None].to(t)
     check_quantised(gpu_lib.quantize_fp4(xs, up=ups), xs.double() * ups.double(), "nvfp4")
+
+
+@pytest.mark.parametrize("K", [64, 512])
+def test_mxfp4_every_pair_of_scales(gpu_lib, K):
+    """Ones under every pair of scales, 2^-254 to 2^254 together: sums of K equal powers of two, exact where they are normal
+    numbers, infinite above, and below off by what is cut off each term."""
+    r = torch.arange(255, device="cuda")
+    q = torch.full((255, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    x = q, r.to(torch.uint8)[:, None].expand(255, K // 32).contiguous(), None
+    y = gpu_lib.linear_fp4(x, *x, out_dtype=torch.float32).double()
+    e = r[:, None] + r[None, :] - 254 + K.bit_length() - 1
+    want = power(e.clamp(-300, 300))
+    low = e < -126
+    assert torch.equal(y[~low], torch.where(e > 127, torch.inf, want)[~low])
+    assert ((y - want).abs()[low] <= K * 2.0 ** -149).all()
+    none = torch.zeros_like(q), x[1], None                  # nothing but zeros, whatever their scales
+    assert (gpu_lib.linear_fp4(none, *x, out_dtype=torch.float32) == 0).all()
