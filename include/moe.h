@@ -480,7 +480,9 @@ moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *args, void *stream)
  * writes them); rows before offsets[0] and from offsets[groups] on are left as
  * they are, and no offset leads outside [0, M) (where offsets run backwards, what
  * rows hold is undefined). offsets NULL (groups = 1): one
- * matrix for all M rows. Products and sums are fp32. No row of x reaches another row's
+ * matrix for all M rows. Products are exact and sums fp32, as the tensor cores add: cut
+ * toward zero, not rounded (off by 5e-6 of the result at K = 4096 of random operands, less
+ * in proportion for smaller K; rounded sums are off by 1e-7 to 7e-7 there). No row of x reaches another row's
  * result: an infinity or NaN stays in its row. y is bf16, f16 or fp32 and
  * overlaps no input. groups <= 512, M, N and K <= 2^24, groups * N < 2^31.
  *
@@ -488,8 +490,8 @@ moe_status moe_dequantize_fp4(const moe_dequantize_fp4_args *args, void *stream)
  * 16-byte aligned with a stride that is a multiple of 8, W [groups, N, K]
  * 16-byte aligned.
  * moe_linear_fp4: x and W in 4-bit floats of one format, as above, K as there;
- * block products and their scales are exact, sums fp32, and the product of x's
- * and W's g, formed in fp32, multiplies them. With x the rows are first quantised
+ * block products and their scales are exact, and the product of x's
+ * and W's g, formed in fp32, multiplies their sums. With x the rows are first quantised
  * as moe_quantize_fp4 does. */
 typedef struct {
     moe_dtype type;

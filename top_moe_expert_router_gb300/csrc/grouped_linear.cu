@@ -63,8 +63,10 @@ int device_sms() {
     return n;
 }
 
-// The plan with the shortest estimate. The groups' sizes are on the device: as many as there can be are taken to share
-// the rows. Measured, a stage of a tile (K = 64, of 4-bit operands 256) takes
+// The plan with the shortest estimate, for a GB300 (152 SMs, 6.6 TB/s). The groups' sizes are on the device: as many as there
+// can be are taken to share the rows. (Where few of many groups have rows, the tiles are then smaller than theirs would
+// be: 8192 rows of 16 experts of 1536 x 4096, bf16 / NVFP4, 68 / 31 us, told among 256 experts 110 / 54; with 64 experts of
+// 256 150 / 58 for 145 / 50.) Measured, a stage of a tile (K = 64, of 4-bit operands 256) takes
 //   16 bits: 120 ns, or 6.3 ns for every KB that passes through shared memory, or what its MMAs take; a pair's at least 190
 //   4 bits:  215 to 236 ns, a pair's 235 to 313
 // and splitting K costs 2 us. The weights come no faster than from memory, which it takes about 120 CTAs to keep busy; read

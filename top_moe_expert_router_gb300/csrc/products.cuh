@@ -28,11 +28,13 @@
 // (32768 rows by 256 experts of 1536 x 4096: bf16 530 us, NVFP4 165 us, 1.00 and
 // 0.96 of the copy rate); with many, 16 bits: the MMAs (4096 x 8192 x 4096 bf16
 // 143 us, 1.92 PFLOP/s); 4 bits: issue slots, with short K those of the epilogue (8192
-// x 4096 x 512 NVFP4 28 us, of which 13 pass without results). The warp that issues the MMAs has 200
+// x 4096 x 512 NVFP4 28 us, 15 without results). The warp that issues the MMAs has 200
 // ns for a stage, and shares its scheduler with two that bring scales and two of
 // the epilogue (4096 x 8192 x 8192 NVFP4 98 us, 5.6 PFLOP/s; without the scales 82
 // us, without the stores 88, without both 73, without loads and both 70; without
-// loads alone 96). Tried there: the warps with the scales waiting for the operands
+// loads alone 96; MXFP4, which fills as many columns of tensor memory with half of the
+// scales, 105). The MMAs are those of K = 64; sm_103a also has dense ones of K = 96, half as
+// much work again for an instruction, which are not used here. Tried there: the warps with the scales waiting for the operands
 // too, so that the MMAs take one wait and one commit a stage (110 us), waits that
 // spin (103 to 121 us).
 #pragma once
